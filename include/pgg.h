@@ -388,6 +388,96 @@ int pgg_mx_grouped_gemm_clamped(int mode, int fmt, const uint8_t* A, const uint8
                                 void* out2, uint8_t* out_codes, uint8_t* out_scales, int64_t M, int64_t N,
                                 int64_t K, int G, float swiglu_limit, int32_t* err, void* stream);
 
+/* ---------------------------------------------------------------- around the experts: norm, routing, decode */
+
+/* Element types and gate scores of the calls below. */
+typedef enum { PGG_DTYPE_F32 = 0, PGG_DTYPE_BF16 = 1 } pgg_dtype;
+typedef enum { PGG_SCORE_SOFTMAX = 0, PGG_SCORE_SIGMOID = 1 } pgg_score;
+
+/* Longest row of the norm. */
+#define PGG_NORM_MAX_COLS 16384
+
+/* Residual addition, RMS norm and MX operand of the next product, in one pass:
+ *   s = x + residual;  h = bf16(s);  rstd = 1 / sqrt(mean(s^2) + eps);  y = s rstd gamma
+ * in fp32, every output rounded once.
+ *   x [R, C], residual [R, C] or NULL, gamma [C] bf16.
+ *   Outputs, each optional (NULL), at least one given: h [R, C] bf16 (the new residual stream),
+ *   y [R, C] bf16, rstd [R] fp32 (the backward pass reads it), and with fmt PGG_FMT_E4M3 or
+ *   PGG_FMT_E2M1 codes and scales: the row-wise MX quantization of y (the layout and the rule of
+ *   pgg_mx_quantize_rowwise, applied to the fp32 y, not to its bf16 rounding; a block whose amax
+ *   is an fp32 subnormal has scale code 0).  fmt 0: codes and scales are NULL.
+ *   8 <= C <= PGG_NORM_MAX_COLS, C % 8 == 0, with codes C % 32 == 0; eps >= 0.  h may be x or
+ *   residual (in place).  R == 0 is a no-op. */
+int pgg_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t R, int64_t C, float eps,
+                    int fmt, void* h, void* y, uint8_t* codes, uint8_t* scales, float* rstd, void* stream);
+
+/* Bytes of the workspace that pgg_add_rmsnorm_bwd needs, into *bytes. */
+int pgg_add_rmsnorm_bwd_workspace_size(int64_t R, int64_t C, size_t* bytes);
+
+/* Backward pass, with xh = h rstd and u = dy gamma:
+ *   dx = dh + rstd (u - xh mean(u xh)), the gradient of x and of the residual alike;
+ *   dgamma = sum over rows of dy xh, in fp32 and a fixed order.
+ *   dy [R, C], dh [R, C] or NULL (the gradient of h), h [R, C], gamma [C] bf16, rstd [R] fp32;
+ *   dx [R, C] bf16, dgamma [C] fp32.  dx may be dy or dh (in place).  ws: device scratch, 16-byte
+ *   aligned.  R == 0 writes dgamma = 0. */
+int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const void* gamma, const float* rstd,
+                        int64_t R, int64_t C, void* dx, float* dgamma, void* ws, size_t ws_bytes, void* stream);
+
+/* The router: each token's k experts and their weights, what pgg_moe_permute, pgg_moe_combine and
+ * pgg_moe_decode take.
+ *   key_e = logit_e + bias_e (fp32; the bias decides the choice only);
+ *   topk_ids: the k largest keys, largest first, ties to the lowest expert;
+ *   w_j = scale a_j / Z with a = exp(logit - max) or sigmoid(logit); Z = the sum of a over all
+ *   experts (softmax), over the k chosen (renormalize = 1), or 1 (sigmoid without it).
+ * An expert whose key is -inf is masked: it counts in no sum, and where fewer than k are left it
+ * fills the choice with weight 0 (a row that is masked whole has ids 0 .. k-1, weights 0).  A NaN
+ * key ranks as -inf and makes the row's weights NaN; the ids are in range whatever the logits.
+ *   logits [T, E] fp32 or bf16 (dtype), bias [E] fp32 or NULL; topk_ids [T, k] int32, w [T, k]
+ *   fp32.  1 <= E <= 1024, 1 <= k <= min(32, E), T < 2^26. */
+int pgg_moe_route(const void* logits, int dtype, const float* bias, int64_t T, int E, int k, int score,
+                  int renormalize, float scale, int32_t* topk_ids, float* w, void* stream);
+
+/* Gradient of the logits from dw [T, k], the gradient of w (pgg_moe_combine_bwd gives it), at the
+ * experts that pgg_moe_route chose; the other arguments are that call's.  dlogits [T, E] in the
+ * logits' type, fully written: zero outside the choice unless the score is a softmax over all
+ * experts.  An id outside [0, E) has no part; a row with a NaN key gets NaN. */
+int pgg_moe_route_bwd(const void* logits, int dtype, const float* bias, const int32_t* topk_ids, const float* dw,
+                      int64_t T, int E, int k, int score, int renormalize, float scale, void* dlogits,
+                      void* stream);
+
+/* Most tokens of one pgg_moe_decode call. */
+#define PGG_MOE_DECODE_MAX_T 128
+
+/* Bytes of the workspace of the two calls below (fmt 0 for pgg_moe_decode), into *bytes. */
+int pgg_moe_decode_workspace_size(int fmt, int64_t T, int k, int64_t H, int64_t I, int E, size_t* bytes);
+
+/* A whole expert layer for a few tokens (decoding), in two kernels and without a permuted copy:
+ *   out[t] = sum_j w[t, j] W2_e (silu(g) u),  [g; u] = W1_e X[t],  e = topk_ids[t, j]
+ *   X [T, H] bf16; topk_ids [T, k] int32; w [T, k] fp32 or NULL (weight 1); W1 [E, 2I, H] (gate |
+ *   up), W2 [E, H, I] bf16; out [T, H] bf16.  fp32 accumulation; the activation between the two
+ *   products is kept as the sum of two bf16 numbers.  swiglu_limit as in
+ *   pgg_grouped_fc1_swiglu_clamped (0: none).
+ *   0 <= T <= PGG_MOE_DECODE_MAX_T (else PGG_ERR_TOO_LARGE: permute and use the grouped GEMMs),
+ *   1 <= k <= 32, H and I multiples of 8 up to 65536.  A token may name an expert twice.
+ * An id outside [0, E) sets *err = PGG_ERR_BAD_EXPERT and has no part.
+ * ws: device scratch of pgg_moe_decode_workspace_size bytes, 16-byte aligned.  Its first 4096
+ * bytes have to be zero at the first call; every call leaves them zero, so one buffer serves any
+ * number of calls (of any sizes that it is large enough for) on one stream.  Zero them again after
+ * a call that set PGG_ERR_TIMEOUT.  Calls that may overlap need a workspace each. */
+int pgg_moe_decode(const void* X, const int32_t* topk_ids, const float* w, const void* W1, const void* W2, void* out,
+                   int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
+                   int32_t* err, void* stream);
+
+/* The same on MX operands in `fmt`: X row-wise codes [T, H] (e4m3) or [T, H/2] (e2m1) with scales
+ * SX [T, H/32] (pgg_add_rmsnorm or pgg_mx_quantize_rowwise write them; 4-byte aligned); W1 codes
+ * [E*2I, H], W2 codes [E*H, I] with blocked scales (pgg_mx_quantize_rowwise_blocked: the forward
+ * weight operands of pgg_mx_grouped_gemm).  The activation between the products is quantized from
+ * fp32 into MX codes of `fmt`.  H and I are multiples of 128. */
+int pgg_mx_moe_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_t* topk_ids, const float* w,
+                      const uint8_t* W1, const uint8_t* SW1, const uint8_t* W2, const uint8_t* SW2, void* out,
+                      int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
+                      int32_t* err, void* stream);
+
 /* Test hook; the pages have no counterpart.  Runs the forward grouped GEMM --
  * BF16 when fmt == 0 (A = X, B = W, SA and SB unused), else the block-scaled
  * forward in `fmt` (arguments as pgg_mx_grouped_gemm with PGG_MODE_FWD and

@@ -12,6 +12,8 @@ A plain, slow, obviously correct fp64 restatement of what the pages define:
   as "dequantize, then the fp64 grouped GEMM";
 * moe_glue.py -- the single-GPU token permute / combine around the grouped
   GEMM and their backward passes;
+* block.py -- the norm with the residual's addition, the router, and a whole
+  expert layer for a few tokens;
 * fp8.py -- e4m3 tensor-wise current scaling and the FP8 grouped GEMMs.
 
 It shares no code with the CUDA path and imports nothing from it.  Inputs are
@@ -19,4 +21,4 @@ bf16 bit patterns (numpy uint16) or MX byte codes; everything is computed in
 fp64.  Every function is pinned by a `-m "not gpu"` test against brute force,
 closed forms, invariants or hand-derived format values.
 """
-from . import fp8, grouped_gemm, moe_glue, mx  # noqa: F401
+from . import block, fp8, grouped_gemm, moe_glue, mx  # noqa: F401

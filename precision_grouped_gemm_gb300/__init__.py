@@ -15,7 +15,9 @@ from ._binding import (PggError, PAD, FMT_E4M3, FMT_E2M1, MODE_FWD, MODE_DGRAD, 
                        mx_pad_rows,
                        fp8_tensor_scale, fp8_quantize_rowwise, fp8_quantize_colwise, fp8_workspace_size,
                        fp8_grouped_gemm,
-                       moe_permute_workspace_size, moe_permute, moe_combine, moe_combine_bwd)
+                       moe_permute_workspace_size, moe_permute, moe_combine, moe_combine_bwd,
+                       add_rmsnorm, add_rmsnorm_bwd, add_rmsnorm_bwd_workspace_size, moe_route, moe_route_bwd,
+                       moe_decode, mx_moe_decode, moe_decode_workspace, moe_decode_workspace_size)
 
 __all__ = [
     "PggError", "PAD", "FMT_E4M3", "FMT_E2M1", "MODE_FWD", "MODE_DGRAD", "MODE_WGRAD",
@@ -25,5 +27,6 @@ __all__ = [
     "grouped_fc2_dgrad_swiglu_bwd", "mx_quantize_rowwise", "mx_quantize_rowwise_blocked", "mx_quantize_colwise",
     "mx_grouped_gemm", "mx_pad_rows", "fp8_tensor_scale", "fp8_quantize_rowwise", "fp8_quantize_colwise",
     "fp8_workspace_size", "fp8_grouped_gemm", "moe_permute_workspace_size", "moe_permute", "moe_combine",
-    "moe_combine_bwd",
+    "moe_combine_bwd", "add_rmsnorm", "add_rmsnorm_bwd", "add_rmsnorm_bwd_workspace_size", "moe_route",
+    "moe_route_bwd", "moe_decode", "mx_moe_decode", "moe_decode_workspace", "moe_decode_workspace_size",
 ]

@@ -46,6 +46,15 @@ SIGNATURES = {
     "pgg_fp8_grouped_gemm": [_I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I64, _F32, _P,
                              ctypes.c_size_t, _P, _P],
     "pgg_moe_combine_bwd": [_P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _P],
+    "pgg_add_rmsnorm": [_P, _P, _P, _I64, _I64, _F32, _I32, _P, _P, _P, _P, _P, _P],
+    "pgg_add_rmsnorm_bwd_workspace_size": [_I64, _I64, _P],
+    "pgg_add_rmsnorm_bwd": [_P, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P],
+    "pgg_moe_route": [_P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _F32, _P, _P, _P],
+    "pgg_moe_route_bwd": [_P, _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _F32, _P, _P],
+    "pgg_moe_decode_workspace_size": [_I32, _I64, _I32, _I64, _I64, _I32, _P],
+    "pgg_moe_decode": [_P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _F32, _P, ctypes.c_size_t, _P, _P],
+    "pgg_mx_moe_decode": [_I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _F32, _P,
+                          ctypes.c_size_t, _P, _P],
     "pgg_test_stalled_fwd": [_I32, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I64, ctypes.c_uint64, _P, _P],
 }
 
@@ -426,3 +435,193 @@ def moe_combine_bwd(dOut, Ys, pos, w, dYs=None, dw=None, stream=None):
     _check(lib().pgg_moe_combine_bwd(_ptr(dOut), _ptr(Ys), _ptr(pos), _ptr(w), _ptr(dYs), _ptr(dw), T, k, H,
                                      _stream(stream)), "pgg_moe_combine_bwd")
     return dYs, dw
+
+
+def _typed(t, dtype, what, shape=None):
+    if t is not None:
+        if t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must have shape {tuple(shape)}")
+
+
+def _size_of(name, *args):
+    out = ctypes.c_size_t(0)
+    _check(getattr(lib(), name)(*args, ctypes.byref(out)), name)
+    return out.value
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def add_rmsnorm(x, residual, gamma, eps=1e-6, fmt=None, h=None, y=None, codes=None, scales=None, rstd=None,
+                save_y=True, save_rstd=True, stream=None):
+    """s = x + residual (residual may be None), y = s / sqrt(mean(s^2) + eps) * gamma; x [R,C] bf16.
+
+    -> (h = bf16(s), y, codes, scales, rstd): y None with save_y=False, codes / scales (the
+    row-wise MX operand in `fmt`) None without fmt, rstd None with save_rstd=False."""
+    R, C = x.shape
+    bf, dev = torch.bfloat16, x.device
+    f = 0 if fmt is None else _FMT[fmt]
+    if h is None:
+        h = torch.empty((R, C), dtype=bf, device=dev)
+    if y is None and save_y:
+        y = torch.empty((R, C), dtype=bf, device=dev)
+    if f:
+        if codes is None:
+            codes = torch.empty((R, C if f == FMT_E4M3 else C // 2), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((R, C // 32), dtype=torch.uint8, device=dev)
+        _typed(codes, torch.uint8, "codes", (R, C if f == FMT_E4M3 else C // 2))
+        _typed(scales, torch.uint8, "scales", (R, C // 32))
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales need fmt")
+    if rstd is None and save_rstd:
+        rstd = torch.empty((R,), dtype=torch.float32, device=dev)
+    for t, what in ((x, "x"), (residual, "residual"), (h, "h"), (y, "y")):
+        _typed(t, bf, what, (R, C))
+    _typed(gamma, bf, "gamma", (C,))
+    _typed(rstd, torch.float32, "rstd", (R,))
+    _dev(x, residual, gamma, h, y, codes, scales, rstd)
+    _check(lib().pgg_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(gamma), R, C, eps, f, _ptr(h), _ptr(y), _ptr(codes),
+                                 _ptr(scales), _ptr(rstd), _stream(stream)), "pgg_add_rmsnorm")
+    return h, y, codes, scales, rstd
+
+
+def add_rmsnorm_bwd_workspace_size(R: int, C: int) -> int:
+    return _size_of("pgg_add_rmsnorm_bwd_workspace_size", R, C)
+
+
+def add_rmsnorm_bwd(dy, dh, h, gamma, rstd, dx=None, dgamma=None, ws=None, stream=None):
+    """Backward of add_rmsnorm: dy [R,C] bf16, dh the gradient of h (or None), h and rstd as saved
+    -> (dx [R,C] bf16, the gradient of x and of residual, dgamma [C] fp32)."""
+    R, C = dy.shape
+    if dx is None:
+        dx = torch.empty((R, C), dtype=torch.bfloat16, device=dy.device)
+    if dgamma is None:
+        dgamma = torch.empty((C,), dtype=torch.float32, device=dy.device)
+    if ws is None:
+        ws = torch.empty(max(16, add_rmsnorm_bwd_workspace_size(R, C)), dtype=torch.uint8, device=dy.device)
+    for t, what in ((dy, "dy"), (dh, "dh"), (h, "h"), (dx, "dx")):
+        _typed(t, torch.bfloat16, what, (R, C))
+    _typed(gamma, torch.bfloat16, "gamma", (C,))
+    _typed(rstd, torch.float32, "rstd", (R,))
+    _typed(dgamma, torch.float32, "dgamma", (C,))
+    _dev(dy, dh, h, gamma, rstd, dx, dgamma, ws)
+    _check(lib().pgg_add_rmsnorm_bwd(_ptr(dy), _ptr(dh), _ptr(h), _ptr(gamma), _ptr(rstd), R, C, _ptr(dx),
+                                     _ptr(dgamma), _ptr(ws), _nbytes(ws), _stream(stream)), "pgg_add_rmsnorm_bwd")
+    return dx, dgamma
+
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_args(logits, bias, score):
+    if logits.dtype not in _DTYPE:
+        raise ValueError("logits must be float32 or bfloat16")
+    if score not in _SCORE:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    T, E = logits.shape
+    _typed(bias, torch.float32, "bias", (E,))
+    return T, E
+
+
+def moe_route(logits, k, bias=None, score="softmax", renormalize=True, scale=1.0, ids=None, w=None, stream=None):
+    """Top-k routing of gate logits [T,E] (fp32 or bf16) -> (topk_ids [T,k] int32, w [T,k] fp32).
+
+    bias [E] fp32 is added for the choice only (-inf masks an expert); see pgg.h."""
+    T, E = _route_args(logits, bias, score)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if w is None:
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _typed(ids, torch.int32, "ids", (T, k))
+    _typed(w, torch.float32, "w", (T, k))
+    _dev(logits, bias, ids, w)
+    _check(lib().pgg_moe_route(_ptr(logits), _DTYPE[logits.dtype], _ptr(bias), T, E, k, _SCORE[score],
+                               int(renormalize), scale, _ptr(ids), _ptr(w), _stream(stream)), "pgg_moe_route")
+    return ids, w
+
+
+def moe_route_bwd(logits, ids, dw, bias=None, score="softmax", renormalize=True, scale=1.0, dlogits=None,
+                  stream=None):
+    """dlogits [T,E] (the logits' type) from dw [T,k] at the ids of moe_route."""
+    T, E = _route_args(logits, bias, score)
+    k = ids.shape[1]
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _typed(ids, torch.int32, "ids", (T, k))
+    _typed(dw, torch.float32, "dw", (T, k))
+    _typed(dlogits, logits.dtype, "dlogits", (T, E))
+    _dev(logits, bias, ids, dw, dlogits)
+    _check(lib().pgg_moe_route_bwd(_ptr(logits), _DTYPE[logits.dtype], _ptr(bias), _ptr(ids), _ptr(dw), T, E, k,
+                                   _SCORE[score], int(renormalize), scale, _ptr(dlogits), _stream(stream)),
+           "pgg_moe_route_bwd")
+    return dlogits
+
+
+def moe_decode_workspace_size(T: int, k: int, H: int, I: int, E: int, fmt=None) -> int:
+    return _size_of("pgg_moe_decode_workspace_size", 0 if fmt is None else _FMT[fmt], T, k, H, I, E)
+
+
+def moe_decode_workspace(T: int, k: int, H: int, I: int, E: int, fmt=None, device="cuda"):
+    """A zeroed workspace for moe_decode (fmt None) / mx_moe_decode calls of up to these sizes."""
+    return torch.zeros(moe_decode_workspace_size(T, k, H, I, E, fmt), dtype=torch.uint8, device=device)
+
+
+def moe_decode(X, ids, w, W1, W2, out=None, swiglu_limit=0.0, ws=None, err=None, stream=None):
+    """A whole expert layer for T <= 128 tokens: X [T,H] bf16, ids [T,k] int32, w [T,k] fp32 (or None),
+    W1 [E,2I,H], W2 [E,H,I] bf16 -> out [T,H] bf16.  ws: a moe_decode_workspace kept between calls
+    (None: one is made for this call)."""
+    T, H = X.shape
+    E, _, I = W2.shape
+    k = ids.shape[1]
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=X.device)
+    if ws is None:
+        ws = moe_decode_workspace(T, k, H, I, E, None, X.device)
+    _typed(X, torch.bfloat16, "X")
+    _typed(ids, torch.int32, "ids", (T, k))
+    _typed(w, torch.float32, "w", (T, k))
+    _typed(W1, torch.bfloat16, "W1", (E, 2 * I, H))
+    _typed(W2, torch.bfloat16, "W2", (E, H, I))
+    _typed(out, torch.bfloat16, "out", (T, H))
+    _dev(X, ids, w, W1, W2, out, ws, err)
+    _check(lib().pgg_moe_decode(_ptr(X), _ptr(ids), _ptr(w), _ptr(W1), _ptr(W2), _ptr(out), T, k, H, I, E,
+                                swiglu_limit, _ptr(ws), _nbytes(ws), _ptr(err), _stream(stream)), "pgg_moe_decode")
+    return out
+
+
+def mx_moe_decode(fmt, X, SX, ids, w, W1, SW1, W2, SW2, out=None, swiglu_limit=0.0, ws=None, err=None, stream=None):
+    """moe_decode on MX operands: X / SX row-wise codes and scales [T, .] (add_rmsnorm or
+    mx_quantize_rowwise), W1 [E*2I, .] and W2 [E*H, .] codes with blocked scales
+    (mx_quantize_rowwise_blocked)."""
+    f = _FMT[fmt]
+    per = 1 if f == FMT_E4M3 else 2  # elements of a byte
+    T, H = X.shape[0], X.shape[1] * per
+    I = W2.shape[1] * per
+    E = W2.shape[0] // H
+    k = ids.shape[1]
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=X.device)
+    if ws is None:
+        ws = moe_decode_workspace(T, k, H, I, E, f, X.device)
+    u8 = torch.uint8
+    _typed(X, u8, "X")
+    _typed(SX, u8, "SX", (T, H // 32))
+    _typed(ids, torch.int32, "ids", (T, k))
+    _typed(w, torch.float32, "w", (T, k))
+    _typed(W1, u8, "W1", (E * 2 * I, H // per))
+    _typed(W2, u8, "W2", (E * H, I // per))
+    _typed(SW1, u8, "SW1")
+    _typed(SW2, u8, "SW2")
+    if SW1.numel() < E * 2 * I * (H // 32) or SW2.numel() < E * H * (I // 32):
+        raise ValueError("SW1 / SW2 are too small for W1 / W2")
+    _typed(out, torch.bfloat16, "out", (T, H))
+    _dev(X, SX, ids, w, W1, SW1, W2, SW2, out, ws, err)
+    _check(lib().pgg_mx_moe_decode(f, _ptr(X), _ptr(SX), _ptr(ids), _ptr(w), _ptr(W1), _ptr(SW1), _ptr(W2), _ptr(SW2),
+                                   _ptr(out), T, k, H, I, E, swiglu_limit, _ptr(ws), _nbytes(ws), _ptr(err),
+                                   _stream(stream)), "pgg_mx_moe_decode")
+    return out

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpgg.so")
-SOURCES = ["pgg_api.cu", "gemm_bf16.cu", "mx_quant.cu", "gemm_mx.cu", "moe_glue.cu"]
+SOURCES = ["pgg_api.cu", "gemm_bf16.cu", "mx_quant.cu", "gemm_mx.cu", "moe_glue.cu", "norm.cu", "moe_route.cu",
+           "moe_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]
@@ -76,9 +77,10 @@ if __name__ == "__main__":
 # Kernel families with DRAM counters in profiles/traffic.json, and the sources each one's
 # kernels cannot depend on (separate translation units): a family's counters stay valid
 # while the sources it is built from are unchanged.
+_BLOCK = ("block.cuh", "norm.cu", "moe_route.cu", "moe_decode.cu")  # the operators around the grouped GEMMs
 DIGEST_EXCLUDE = {
-    "bf16": ("gemm_mx.cu", "mx_quant.cu", "moe_glue.cu"),    # BF16 grouped GEMM family
-    "mx": ("gemm_bf16.cu", "gemm_bf16.cuh", "moe_glue.cu"),  # block-scaled GEMM + MX quantizers
+    "bf16": ("gemm_mx.cu", "mx_quant.cu", "moe_glue.cu") + _BLOCK,    # BF16 grouped GEMM family
+    "mx": ("gemm_bf16.cu", "gemm_bf16.cuh", "moe_glue.cu") + _BLOCK,  # block-scaled GEMM + MX quantizers
 }
 
 
