@@ -112,16 +112,15 @@ struct Plan {
   int L;        // stages of one item: an (expert, tile) in phase 1, an output tile in phase 2
   int total;    // stages of the launch
   int ctas;     // CTAs that get any
+  int quot, rem;  // total = ctas quot + rem: the first rem CTAs get a stage more
   int stages;   // ring depth
-  int stage_bytes, b_off, sf_off;  // layout of a stage
+  int stage_bytes, b_off, b_piece, sf_off;  // layout of a stage
   int acc_cols, nacc, sf_col0, sf_per;  // tensor memory
-  __device__ __forceinline__ int start(int c) const { return (int)((int64_t)total * c / ctas); }
+  __device__ __forceinline__ int start(int c) const { return c * quot + min(c, rem); }
   // the CTA that stage p belongs to
   __device__ __forceinline__ int owner(int p) const {
-    int c = (int)((int64_t)p * ctas / total);
-    while (start(c + 1) <= p) ++c;
-    while (start(c) > p) --c;
-    return c;
+    const int big = rem * (quot + 1);
+    return p < big ? p / (quot + 1) : rem + (p - big) / quot;
   }
 };
 
@@ -134,6 +133,7 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int n_act, int ma
   const int tiles = (a.rows + 127) / 128;
   const int kb = (a.red + C::kBK - 1) / C::kBK;
   const int bsub = P.ncols * 128 * (PHASE == 2 && FMT == 0 ? 2 : 1);
+  P.b_piece = bsub;
   if (PHASE == 1) {
     P.ns = 1;
     P.nk = kb;
@@ -159,6 +159,8 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int n_act, int ma
   P.L = PHASE == 1 ? P.nk : n_act * P.nk;
   P.total = n_act * tiles * P.nk;
   P.ctas = max(1, min((int)gridDim.x, P.total));
+  P.quot = P.total / P.ctas;
+  P.rem = P.total - P.ctas * P.quot;
   return P;
 }
 
@@ -388,6 +390,9 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     int acc = 0;
     uint32_t acc_phase = 0;
+    // descriptors of stage 0's tiles; an address d bytes further on adds d / 16
+    const uint64_t desc_a = smem_desc(smem0, 16, 1024, kSwizzle128B);
+    const uint64_t desc_b = smem_desc(smem0 + P.b_off, 16, 1024, kSwizzle128B);
     for (int p = p0; p < p1 && !aborted;) {
       const Seg S = seg_at<PHASE>(P, tiles, p, p1);
       const uint32_t n16 = (uint32_t)((s_off[S.slot + 1] - s_off[S.slot] + 15) & ~15);
@@ -401,25 +406,24 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         tc_fence_after();
         if (lane == 0) {
           if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
-          const uint32_t st = smem0 + stage * P.stage_bytes;
-          const uint64_t da = smem_desc(st, 16, 1024, kSwizzle128B);
-          const uint64_t db = smem_desc(st + P.b_off, 16, 1024, kSwizzle128B);
+          const uint64_t so = (uint64_t)(stage * P.stage_bytes) >> 4;
           const uint32_t sf = tmem_base + P.sf_col0 + stage * P.sf_per;
-          const int npiece = PHASE == 1 ? 2 : P.ns;  // phase 1: gate and up; phase 2: K pieces
-          for (int s = 0; s < npiece; ++s) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {  // phase 1: gate and up; phase 2: K pieces
+            if (PHASE == 2 && s == P.ns) break;
             const int kk = PHASE == 1 ? kb : kb * P.ns + s;
             // MMAs of this piece that hold data (an e2m1 K may end inside it; the zero-filled end
             // of a bf16 K adds nothing)
-            const int nmma = min(4, (a.red - kk * C::kBK + C::kPerMma - 1) / C::kPerMma);
-            const uint64_t ad = da + s * (kTileBytes >> 4);
-            const uint64_t bd = db + (PHASE == 1 ? 0 : s * ((P.sf_off - P.b_off) / P.ns >> 4));
+            const int left = a.red - kk * C::kBK;
+            const uint64_t ad = desc_a + so + s * (kTileBytes >> 4);
+            const uint64_t bd = desc_b + so + (PHASE == 1 ? 0 : s * (P.b_piece >> 4));
             const uint32_t dd = PHASE == 1 ? d + s * P.ncols : d;
             const uint32_t sfa = sf + s * C::kSub * 4;
             const uint32_t sfb = sf + (PHASE == 1 ? C::kSub * 8 : (P.ns + s) * C::kSub * 4);
-            const uint32_t fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
+            const bool fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              if (j >= nmma) break;
+              if (j * C::kPerMma >= left) break;
               const uint32_t accum = !(fresh && j == 0);
               if (FMT == 0) {
                 mma_f16(dd, ad + 2 * j, bd + 2 * j, idesc, accum);
@@ -477,38 +481,51 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------------------ the token operand
     if (PHASE == 2) grid_wait();  // A is phase 1's
+    // Thread (r0, j) fetches 16-byte chunk j of rows r0, r0 + 8, ...: chunk j of row r goes to chunk
+    // j ^ (r % 8) of its 128 bytes (the 128-byte swizzle), so its places are 1024 bytes apart.
+    // Rows past n hold leftovers, which only reach accumulator columns that nobody reads.
     const int tid = threadIdx.x - kLoadWarp0 * 32;
+    const int j = tid & 7, r0 = tid >> 3;
+    const uint32_t place = r0 * 128 + ((j ^ r0) << 4);
+    const int natom = a.red >> 7;
+    const int64_t lo_off = PHASE == 2 && FMT == 0 ? a.b_lo - a.b : 0;
     for (int p = p0; p < p1 && !aborted;) {
       const Seg S = seg_at<PHASE>(P, tiles, p, p1);
-      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off, n16 = (n + 15) & ~15;
+      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
+      const uint32_t lo_place = (uint32_t)((n + 15) & ~15) * 128;
+      auto row_of = [&](int r) -> int64_t { return PHASE == 1 ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
+      // the first rows' sources stay in registers over the segment
+      const uint8_t* src0 = a.b + (r0 < n ? row_of(r0) : 0) * a.b_ld + j * 16;
+      const uint8_t* src1 = a.b + (r0 + 8 < n ? row_of(r0 + 8) : 0) * a.b_ld + j * 16;
+      const uint8_t* ssrc = C::kSub ? a.sb + (tid < n ? row_of(tid) : 0) * a.sb_ld : nullptr;
       for (int kb = S.kb0; kb < S.kb1; ++kb) {
         if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
         const uint32_t st = smem0 + stage * P.stage_bytes;
-        for (int s = 0; s < P.ns; ++s) {
+#pragma unroll
+        for (int s = 0; s < PHASE; ++s) {
           const int kk = kb * P.ns + s;
-          if (kk * C::kBK >= a.red) break;
-          const uint32_t sb = st + P.b_off + s * ((P.sf_off - P.b_off) / P.ns);
-          // row r's 16-byte chunk j goes to chunk j ^ (r % 8) of its 128 bytes (the 128-byte swizzle);
-          // rows past n hold leftovers, which only reach accumulator columns that nobody reads
-          const int rows = PHASE == 2 && FMT == 0 ? 2 * n : n;
-          for (int i = tid; i < rows * 8; i += 32 * kLoadWarps) {
-            const int r = i >> 3, j = i & 7;
-            const bool lo = r >= n;
-            const int rr = lo ? n16 + r - n : r, src = lo ? r - n : r;
-            const int64_t row = PHASE == 1 ? s_tok[off + src] : off + src;
-            const int64_t byte = (int64_t)kk * 128 + j * 16;
-            const bool in = byte < a.b_ld;  // past the end of K: zeros
-            cp_async_16(sb + rr * 128 + ((j ^ (rr & 7)) << 4), (lo ? a.b_lo : a.b) + row * a.b_ld + (in ? byte : 0),
-                        in ? 16u : 0u);
-          }
+          if (PHASE == 2 && (s == P.ns || kk * C::kBK >= a.red)) break;
+          const int kbyte = kk * 128;
+          const uint32_t size = kbyte + j * 16 < a.b_ld ? 16u : 0u;  // past the end of K: zeros
+          const int go = size ? kbyte : -j * 16;
+          const uint32_t dst = st + P.b_off + s * P.b_piece + place;
+          auto fetch = [&](const uint8_t* from, uint32_t to) {
+            cp_async_16(to, from + go, size);
+            if (PHASE == 2 && FMT == 0) cp_async_16(to + lo_place, from + lo_off + go, size);
+          };
+          if (r0 < n) fetch(src0, dst);
+          if (r0 + 8 < n) fetch(src1, dst + 1024);
+          for (int r = r0 + 16; r < n; r += 8) fetch(a.b + row_of(r) * a.b_ld + j * 16, dst + (r - r0) * 128);
           if (C::kSub) {
-            const int at0 = kk * C::kSub, natom = a.red >> 7;
+            // row r's 4 scales of a 128-element atom: word 4 (r % 32) + r / 32
             const uint32_t ssf = st + P.sf_off + (PHASE == 1 ? 2 * C::kSub : (P.ns + s) * C::kSub) * 512;
-            for (int i = tid; i < n * C::kSub; i += 32 * kLoadWarps) {
-              const int sub = i / n, r = i - sub * n;
-              if (at0 + sub >= natom) break;
-              const int64_t row = PHASE == 1 ? s_tok[off + r] : off + r;
-              cp_async_4(ssf + sub * 512 + (r & 31) * 16 + (r >> 5) * 4, a.sb + row * a.sb_ld + (at0 + sub) * 4, 4u);
+#pragma unroll
+            for (int sub = 0; sub < C::kSub; ++sub) {
+              const int at = kk * C::kSub + sub;
+              if (at >= natom) break;
+              if (tid < n) cp_async_4(ssf + sub * 512 + (tid & 31) * 16 + (tid >> 5) * 4, ssrc + at * 4, 4u);
+              for (int r = tid + 32 * kLoadWarps; r < n; r += 32 * kLoadWarps)
+                cp_async_4(ssf + sub * 512 + (r & 31) * 16 + (r >> 5) * 4, a.sb + row_of(r) * a.sb_ld + at * 4, 4u);
             }
           }
         }
@@ -541,11 +558,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       if (mine) __threadfence();
       return mine;
     };
-    // partial sums of a CTA's run: its first item (entered in the middle) or its last one
-    auto part_of = [&](int c, int item) {
-      const int which = P.start(c) > item * P.L ? 0 : 1;
-      return a.part + (int64_t)(c * 2 + which) * (PHASE == 1 ? 256 : 128) * ((a.T + 15) & ~15);
-    };
+    // Partial sums of an item: CTA c keeps those of an item that begins in its run (`begins`: it is the
+    // first of the CTAs) apart from those of the item that its run enters in the middle.
+    const int part_sz = (PHASE == 1 ? 256 : 128) * ((a.T + 15) & ~15);
+    auto part_of = [&](int c, bool begins) { return a.part + (int64_t)(c * 2 + begins) * part_sz; };
 
     for (int p = p0; p < p1 && !aborted;) {
       const Seg S = seg_at<PHASE>(P, tiles, p, p1);
@@ -599,7 +615,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
           }
         };
         const bool whole = S.kb0 == 0 && S.kb1 == P.nk;
-        float* mine = part_of(cta, S.item);
+        float* mine = part_of(cta, S.kb0 == 0);
         for (int c0 = 0; c0 < n; c0 += 16) {
           float g[16], u[16];
           tmem_ld16(tb + c0, g);
@@ -625,12 +641,12 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 16; ++c) g[c] = u[c] = 0.0f;
               for (int x = c_first; x <= c_last; ++x) {
-                const float* o = part_of(x, S.item);
+                const float* o = part_of(x, x == c_first) + c0 * 256 + row;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                   if (c0 + c >= n) break;
-                  g[c] += __ldcg(o + (c0 + c) * 256 + row);
-                  u[c] += __ldcg(o + (c0 + c) * 256 + 128 + row);
+                  g[c] += __ldcg(o + c * 256);
+                  u[c] += __ldcg(o + c * 256 + 128);
                 }
               }
               finish(c0, g, u);
@@ -657,25 +673,42 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&tempty[acc]));
         if (p_end == p1 || p_end == item1) {  // this CTA's part of the output tile is complete
-          const bool whole = p0 <= item0 && p_end == item1;
-          bool last = whole;
-          int c_first = cta, c_last = cta;
-          if (!whole) {
-            c_first = P.owner(item0);
-            c_last = P.owner(item1 - 1);
-            float* mine = part_of(cta, S.item);
+          if (p0 <= item0 && p_end == item1) {
+            if (out_row < a.rows)
+              for (int t = 0; t < a.T; ++t)
+                a.out[(int64_t)t * a.rows + out_row] = __float2bfloat16_rn(s_acc[t * 128 + row]);
+          } else {
+            const int c_first = P.owner(item0), c_last = P.owner(item1 - 1);
+            float* mine = part_of(cta, p0 <= item0);
             for (int t = 0; t < a.T; ++t) mine[t * 128 + row] = s_acc[t * 128 + row];
-            last = join(S.item, c_first, c_last);
-          }
-          if (last && out_row < a.rows) {
-            for (int t = 0; t < a.T; ++t) {
-              float v = 0.0f;
-              if (whole) {
-                v = s_acc[t * 128 + row];
-              } else {
-                for (int x = c_first; x <= c_last; ++x) v += __ldcg(part_of(x, S.item) + t * 128 + row);
+            if (join(S.item, c_first, c_last)) {
+              // a warp takes four tokens at a time, a lane four rows of each; eight loads in flight
+              const float4* first = reinterpret_cast<const float4*>(part_of(c_first, true)) + lane;
+              const float4* rest = reinterpret_cast<const float4*>(part_of(0, false)) + lane;
+              const int step = part_sz / 2;  // float4s from a CTA's partial sums to the next CTA's
+              for (int t0 = (warp - 2) * 4; t0 < a.T; t0 += 16) {
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  v[i] = t0 + i < a.T ? __ldcg(first + (t0 + i) * 32) : make_float4(0, 0, 0, 0);
+#pragma unroll 2
+                for (int x = c_first + 1; x <= c_last; ++x) {
+                  const float4* o = rest + (int64_t)x * step;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    if (t0 + i >= a.T) break;
+                    const float4 w4 = __ldcg(o + (t0 + i) * 32);
+                    v[i].x += w4.x; v[i].y += w4.y; v[i].z += w4.z; v[i].w += w4.w;
+                  }
+                }
+                const int r4 = S.tile * 128 + 4 * lane;
+                if (r4 < a.rows)  // rows is a multiple of 8
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    if (t0 + i < a.T)
+                      *reinterpret_cast<uint2*>(a.out + (int64_t)(t0 + i) * a.rows + r4) =
+                          make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
               }
-              a.out[(int64_t)t * a.rows + out_row] = __float2bfloat16_rn(v);
             }
           }
         }
