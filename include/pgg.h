@@ -451,7 +451,7 @@ int pgg_moe_route_bwd(const void* logits, int dtype, const float* bias, const in
 /* Bytes of the workspace of the two calls below (fmt 0 for pgg_moe_decode), into *bytes. */
 int pgg_moe_decode_workspace_size(int fmt, int64_t T, int k, int64_t H, int64_t I, int E, size_t* bytes);
 
-/* A whole expert layer for a few tokens (decoding), in two kernels and without a permuted copy:
+/* A whole expert layer for a few tokens (decoding), in one kernel and without a permuted copy:
  *   out[t] = sum_j w[t, j] W2_e (silu(g) u),  [g; u] = W1_e X[t],  e = topk_ids[t, j]
  *   X [T, H] bf16; topk_ids [T, k] int32; w [T, k] fp32 or NULL (weight 1); W1 [E, 2I, H] (gate |
  *   up), W2 [E, H, I] bf16; out [T, H] bf16.  fp32 accumulation; the activation between the two

@@ -1,4 +1,4 @@
-// A whole expert layer for a few tokens, in two kernels:
+// A whole expert layer for a few tokens, in one kernel of two phases:
 //
 //   phase 1   A[r] = silu(g) u, [g; u] = W1_e x_t     every (expert, token) pair r of the batch
 //   phase 2   out[t] = sum over t's experts e of w_te W2_e A[r]
@@ -10,14 +10,18 @@
 // everything else is small: the kernels are weight streams.  Weights are the MMA's A operand
 // (128 output rows a tile, loaded by TMA), the expert's tokens its B operand (N = tokens rounded
 // up to 16), so a tile is multiplied as it lands in shared memory and no weight passes through a
-// register.  The stages of all tiles of the batch form one sequence that is cut into equal runs,
+// register.  The stages of all tiles of a phase form one sequence that is cut into equal runs,
 // one per CTA, so every SM reads the same number of bytes whatever the routing; a tile that a cut
 // divides is put together from fp32 partial sums by the last of its CTAs to arrive, in CTA order
 // (the result does not depend on which one that is).
 //
+// Between the phases only the warps that fetch A wait for the other CTAs (a cooperative launch
+// makes all of them resident); the weight loads run on into phase 2 and keep the ring full.
+//
 // Every CTA builds the batch's expert list by itself from the ids: a bit per (expert, token), so
 // an expert named twice by a token is computed once and its weights are added up.
 #include <algorithm>
+#include <type_traits>
 
 #include "block.cuh"
 #include "epilogue.cuh"
@@ -41,26 +45,29 @@ struct DecCfg {
   static constexpr int kThreads = 32 * (6 + kCopier + kLoadWarps);
 };
 
+// One matrix of a layer and what the MMAs of its phase read and write.
+struct DecodePhase {
+  int rows;            // output rows per expert: I (phase 1), H (phase 2)
+  int red;             // reduction length: H (phase 1), I (phase 2)
+  const uint8_t* b;    // token operand, row-major: X (phase 1) or A (phase 2)
+  int64_t b_ld;        // bytes of a row
+  const uint8_t* sb;   // its scales, row-major, red / 32 bytes a row
+  const uint8_t* sa;   // the weights' blocked scales
+};
+
 struct DecodeArgs {
   const int32_t* ids;  // [T, k]
   const float* w;      // [T, k] or nullptr
-  int T, k, E;
-  int rows;            // output rows per expert: I (phase 1), H (phase 2)
-  int red;             // reduction length: H (phase 1), I (phase 2)
-  int I;
+  int T, k, E, I;
   float limit;
-  const uint8_t* b;     // token operand: X (phase 1) or A (phase 2), row-major
-  const uint8_t* b_lo;  // phase 2, bf16: the part of A that its bf16 rounding left over
-  int64_t b_ld;         // bytes of a row
-  const uint8_t* sb;    // its scales, row-major, sb_ld bytes a row
-  int64_t sb_ld;
-  const uint8_t* sa;    // the weights' blocked scales
-  uint8_t* act;         // phase 1 output (and act_lo / act_scales)
-  uint8_t* act_lo;
-  uint8_t* act_scales;
-  __nv_bfloat16* out;   // phase 2 output [T, H]
+  DecodePhase ph[2];
+  uint8_t* act;         // A: bf16 (high part), or codes
+  uint8_t* act_lo;      // bf16: what the rounding to the high part left over
+  uint8_t* act_scales;  // MX: row-major scales
+  __nv_bfloat16* out;   // [T, H]
   float* part;          // partial sums: 2 tiles per CTA
-  unsigned* cnt;        // arrivals at a divided tile, by its first CTA; zero between launches
+  unsigned* cnt;        // arrivals at a divided tile by its first CTA, for each phase
+  unsigned* done;       // CTAs that have finished phase 1; [1]: that have left.  All zero between launches
   int ring_bytes;       // shared memory for the stages
   int slots_cap;        // most experts that the batch can name
   int32_t* err;
@@ -96,26 +103,29 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// Wait until the kernels that this launch depends on have completed and their writes are visible
-// (returns at once when it was not launched as their dependent).
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
-// How a launch cuts up its work; every CTA computes the same.
-struct Plan {
+// What both phases share of a launch's cut: the shape of a ring stage and of tensor memory.
+struct Shape {
   int n_act;    // experts that the batch names
   int ncols;    // most tokens of one of them, rounded up to 16
   int ns;       // phase 2: 128-byte K pieces per stage
-  int nk;       // stages of one (expert, tile)
-  int L;        // stages of one item: an (expert, tile) in phase 1, an output tile in phase 2
-  int total;    // stages of the launch
-  int ctas;     // CTAs that get any
-  int quot, rem;  // total = ctas quot + rem: the first rem CTAs get a stage more
-  int stages;   // ring depth
-  int stage_bytes, b_off, b_piece, sf_off;  // layout of a stage
+  int stages, stage_bytes;
   int acc_cols, nacc, sf_col0, sf_per;  // tensor memory
+};
+// One phase's stages, cut into equal runs; every CTA computes the same.
+struct Plan {
+  int tiles;      // 128-row output tiles per expert
+  int nk;         // stages of one (expert, tile)
+  int L;          // stages of one item: an (expert, tile) in phase 1, an output tile in phase 2
+  int total;      // stages of the phase
+  int quot, rem;  // total = ctas quot + rem: the first rem CTAs get a stage more
+  int b_off, b_piece, sf_off;  // layout of a stage: weights, token pieces, scale atoms
+  int p0, p1;     // this CTA's run
   __device__ __forceinline__ int start(int c) const { return c * quot + min(c, rem); }
   // the CTA that stage p belongs to
   __device__ __forceinline__ int owner(int p) const {
@@ -124,43 +134,58 @@ struct Plan {
   }
 };
 
+// Columns (rows of the token operand) of n tokens in phase 2: bf16 keeps the high and the low parts
+// of A next to each other, each rounded up to the 8 rows of a swizzle atom.
+template <int FMT>
+__device__ __forceinline__ int cols2(int n) {
+  return FMT == 0 ? (2 * ((n + 7) & ~7) + 15) & ~15 : (n + 15) & ~15;
+}
+
+template <int FMT>
+__device__ __forceinline__ Shape make_shape(const DecodeArgs& a, int n_act, int max_n) {
+  using C = DecCfg<FMT>;
+  Shape S;
+  S.n_act = n_act;
+  S.ncols = (max_n + 15) & ~15;
+  const int b1 = S.ncols * 128, b2 = cols2<FMT>(max_n) * 128;
+  const int s1 = 2 * kTileBytes + b1 + C::kSub * 3 * 512;
+  const int two = 2 * (kTileBytes + b2 + C::kSub * 1024), one = kTileBytes + b2 + C::kSub * 1024;
+  // phase 2: two K pieces a stage, or one where many tokens would leave fewer than three stages
+  const int st1 = (max(s1, one) + 1023) & ~1023, st2 = (max(s1, two) + 1023) & ~1023;
+  S.ns = a.ring_bytes / st2 >= min(3, a.ring_bytes / st1) ? 2 : 1;
+  S.stage_bytes = S.ns == 2 ? st2 : st1;
+  S.stages = min(kMaxStages, a.ring_bytes / S.stage_bytes);
+  S.acc_cols = max(2 * S.ncols, b2 / 128);
+  S.sf_per = C::kSub * max(12, S.ns * 8);
+  S.nacc = 2 * S.acc_cols + S.stages * S.sf_per <= 512 ? 2 : 1;
+  S.sf_col0 = S.nacc * S.acc_cols;
+  return S;
+}
+
 template <int FMT, int PHASE>
-__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int n_act, int max_n) {
+__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Shape& S, int max_n) {
   using C = DecCfg<FMT>;
   Plan P;
-  P.n_act = n_act;
-  P.ncols = (max_n + 15) & ~15;
-  const int tiles = (a.rows + 127) / 128;
-  const int kb = (a.red + C::kBK - 1) / C::kBK;
-  const int bsub = P.ncols * 128 * (PHASE == 2 && FMT == 0 ? 2 : 1);
-  P.b_piece = bsub;
+  const int kb = (a.ph[PHASE - 1].red + C::kBK - 1) / C::kBK;
+  P.tiles = (a.ph[PHASE - 1].rows + 127) / 128;
   if (PHASE == 1) {
-    P.ns = 1;
     P.nk = kb;
     P.b_off = 2 * kTileBytes;
-    P.sf_off = P.b_off + bsub;
-    P.stage_bytes = (P.sf_off + C::kSub * 3 * 512 + 1023) & ~1023;
-    P.sf_per = C::kSub * 12;
-    P.acc_cols = 2 * P.ncols;
+    P.b_piece = S.ncols * 128;
+    P.sf_off = P.b_off + P.b_piece;
   } else {
-    // two K pieces a stage, or one where many tokens would leave fewer than three stages
-    const int two = (2 * (kTileBytes + bsub + C::kSub * 1024) + 1023) & ~1023;
-    P.ns = a.ring_bytes / two >= 3 ? 2 : 1;
-    P.nk = (kb + P.ns - 1) / P.ns;
-    P.b_off = P.ns * kTileBytes;
-    P.sf_off = P.b_off + P.ns * bsub;
-    P.stage_bytes = (P.sf_off + P.ns * C::kSub * 1024 + 1023) & ~1023;
-    P.sf_per = P.ns * C::kSub * 8;
-    P.acc_cols = P.ncols * (FMT == 0 ? 2 : 1);
+    P.nk = S.ns == 2 ? (kb + 1) >> 1 : kb;
+    P.b_off = S.ns * kTileBytes;
+    P.b_piece = cols2<FMT>(max_n) * 128;
+    P.sf_off = P.b_off + S.ns * P.b_piece;
   }
-  P.stages = min(kMaxStages, a.ring_bytes / max(P.stage_bytes, 1));
-  P.nacc = 2 * P.acc_cols + P.stages * P.sf_per <= 512 ? 2 : 1;
-  P.sf_col0 = P.nacc * P.acc_cols;
-  P.L = PHASE == 1 ? P.nk : n_act * P.nk;
-  P.total = n_act * tiles * P.nk;
-  P.ctas = max(1, min((int)gridDim.x, P.total));
-  P.quot = P.total / P.ctas;
-  P.rem = P.total - P.ctas * P.quot;
+  P.L = PHASE == 1 ? P.nk : S.n_act * P.nk;
+  P.total = S.n_act * P.tiles * P.nk;
+  const int ctas = max(1, min((int)gridDim.x, P.total)), cta = blockIdx.x;
+  P.quot = P.total / ctas;
+  P.rem = P.total - ctas * P.quot;
+  P.p0 = cta < ctas ? P.start(cta) : 0;
+  P.p1 = cta < ctas ? P.start(cta + 1) : 0;
   return P;
 }
 
@@ -170,26 +195,30 @@ struct Seg {
 };
 
 template <int PHASE>
-__device__ __forceinline__ Seg seg_at(const Plan& P, int tiles, int p, int p1) {
+__device__ __forceinline__ Seg seg_at(const Plan& P, int p) {
   Seg s;
   s.item = p / P.L;
   const int q = p - s.item * P.L;
   if (PHASE == 1) {
-    s.slot = s.item / tiles;
-    s.tile = s.item - s.slot * tiles;
+    s.slot = s.item / P.tiles;
+    s.tile = s.item - s.slot * P.tiles;
     s.kb0 = q;
   } else {
     s.tile = s.item;
     s.slot = q / P.nk;
     s.kb0 = q - s.slot * P.nk;
   }
-  s.kb1 = min(P.nk, s.kb0 + (p1 - p));
+  s.kb1 = min(P.nk, s.kb0 + (P.p1 - p));
   return s;
 }
 
-template <int FMT, int PHASE>
+using Phase1 = std::integral_constant<int, 1>;
+using Phase2 = std::integral_constant<int, 2>;
+
+template <int FMT>
 __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
-    moe_decode_kernel(const __grid_constant__ CUtensorMap tmW, const DecodeArgs a) {
+    moe_decode_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW2,
+                      const __grid_constant__ DecodeArgs a) {
   using C = DecCfg<FMT>;
   constexpr int kNT = C::kThreads;
   constexpr int kLoadWarp0 = 6 + C::kCopier;
@@ -209,49 +238,54 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   int* s_last = reinterpret_cast<int*>(s_tmem + 1);
   int* s_scan = s_last + 1;  // [2 * 16]
   float* s_acc = reinterpret_cast<float*>(smem + a.ring_bytes + 512);  // phase 2: [T][128]
-  float* s_w = s_acc + (PHASE == 2 ? a.T * 128 : 0);                    // phase 2: [T k]
-  uint16_t* s_off = reinterpret_cast<uint16_t*>(s_w + (PHASE == 2 ? a.T * a.k : 0));  // [slots + 1]
-  uint16_t* s_exp = s_off + a.slots_cap + 1;                                         // [slots]
-  uint8_t* s_tok = reinterpret_cast<uint8_t*>(s_exp + a.slots_cap);                  // [T k]
+  float* s_w = s_acc + a.T * 128;                                       // [T k]
+  uint16_t* s_off = reinterpret_cast<uint16_t*>(s_w + a.T * a.k);       // [slots + 1]: an expert's first entry
+  uint16_t* s_exp = s_off + a.slots_cap + 1;                            // [slots]
+  uint8_t* s_tok = reinterpret_cast<uint8_t*>(s_exp + a.slots_cap);     // [T k]: the entries' tokens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (PHASE == 1) grid_launch_dependents();
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1 + 32 * kLoadWarps);
-      mbar_init(smem_u32(&empty[s]), 1);
-      mbar_init(smem_u32(&sfull[s]), 1);
+
+  // ---- the batch's experts and their tokens (scratch: the ring, before the first stage lands)
+  const int W = (a.T + 31) / 32;  // mask words per expert
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem);               // [E][W]
+  float* s_wid = reinterpret_cast<float*>(s_mask + a.E * W);          // [T k]: the weights as given
+  int16_t* s_id = reinterpret_cast<int16_t*>(s_wid + a.T * a.k);      // [T k]: the ids, -1 out of range
+  uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_id + a.T * a.k);   // [E]: first entry
+  const int n_ids = a.T * a.k;
+  for (int i = threadIdx.x; i < n_ids; i += kNT) {
+    const int e = __ldg(a.ids + i);
+    const bool ok = e >= 0 && e < a.E;
+    if (!ok && blockIdx.x == 0) set_error(a.err, kErrBadExpert);
+    s_id[i] = (int16_t)(ok ? e : -1);
+    s_wid[i] = a.w ? __ldg(a.w + i) : 1.0f;
+  }
+  for (int i = threadIdx.x; i < a.E * W; i += kNT) s_mask[i] = 0;
+  if (warp == 0) {
+    if (lane < kMaxStages) {
+      mbar_init(smem_u32(&full[lane]), 1 + 32 * kLoadWarps);
+      mbar_init(smem_u32(&empty[lane]), 1);
+      mbar_init(smem_u32(&sfull[lane]), 1);
+    } else if (lane < kMaxStages + 2) {
+      mbar_init(smem_u32(&tfull[lane - kMaxStages]), 1);
+      mbar_init(smem_u32(&tempty[lane - kMaxStages]), 128);
+    } else if (lane == kMaxStages + 2) {
+      mbar_init(smem_u32(drain), 1);
+      mbar_init(smem_u32(cdrain), 1);
+      s_ctl->abort = 0;
+      s_ctl->limit_ns = kWaitTimeoutNs;
+      prefetch_tmap(&tmW1);
+      prefetch_tmap(&tmW2);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&tfull[s]), 1);
-      mbar_init(smem_u32(&tempty[s]), 128);
-    }
-    mbar_init(smem_u32(drain), 1);
-    mbar_init(smem_u32(cdrain), 1);
-    s_ctl->abort = 0;
-    s_ctl->limit_ns = kWaitTimeoutNs;
     fence_mbar_init();
-    prefetch_tmap(&tmW);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
-
-  // ---- the batch's experts and their tokens (scratch: the ring, before the first stage lands)
-  const int W = (a.T + 31) / 32;  // mask words per expert
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem);                  // [E][W]
-  uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_mask + a.E * W);      // [E]: first entry
-  const int n_ids = a.T * a.k;
-  for (int i = threadIdx.x; i < a.E * W; i += kNT) s_mask[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n_ids; i += kNT) {
-    const int e = __ldg(a.ids + i), t = i / a.k;
-    if (e < 0 || e >= a.E) {
-      if (blockIdx.x == 0) set_error(a.err, kErrBadExpert);
-    } else {
-      atomicOr(&s_mask[e * W + (t >> 5)], 1u << (t & 31));
-    }
+    const int t = i / a.k;
+    if (s_id[i] >= 0) atomicOr(&s_mask[s_id[i] * W + (t >> 5)], 1u << (t & 31));
   }
   __syncthreads();
   int n_act, max_n;
@@ -297,92 +331,97 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_ids; i += kNT) {
-    const int e = __ldg(a.ids + i);
-    if (e < 0 || e >= a.E) continue;
+    const int e = s_id[i];
+    if (e < 0) continue;
     const int t = i / a.k, i0 = t * a.k;
     bool first = true;  // the token's first choice of this expert writes the entry
-    for (int j = i0; j < i; ++j) first &= __ldg(a.ids + j) != e;
+    for (int j = i0; j < i; ++j) first &= s_id[j] != e;
     if (!first) continue;
     int r = s_eoff[e];
     for (int q = 0; q < (t >> 5); ++q) r += __popc(s_mask[e * W + q]);
     r += __popc(s_mask[e * W + (t >> 5)] & ((1u << (t & 31)) - 1u));
     s_tok[r] = (uint8_t)t;
-    if (PHASE == 2) {
-      float wt = 0.0f;
-      for (int j = i; j < i0 + a.k; ++j)
-        if (__ldg(a.ids + j) == e) wt += a.w ? __ldg(a.w + j) : 1.0f;
-      s_w[r] = wt;
-    }
+    float wt = 0.0f;
+    for (int j = i; j < i0 + a.k; ++j)
+      if (s_id[j] == e) wt += s_wid[j];
+    s_w[r] = wt;
   }
   fence_proxy_async_smem();  // the ring's scratch use, before its first bulk copies
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
-  const Plan P = make_plan<FMT, PHASE>(a, n_act, max_n);
-  const int tiles = (a.rows + 127) / 128;
+  const Shape H = make_shape<FMT>(a, n_act, max_n);
+  const Plan plan1 = make_plan<FMT, 1>(a, H, max_n), plan2 = make_plan<FMT, 2>(a, H, max_n);
   const int cta = blockIdx.x;
-  const int p0 = cta < P.ctas && P.total ? P.start(cta) : 0;
-  const int p1 = cta < P.ctas && P.total ? P.start(cta + 1) : 0;
   const uint32_t tmem_base = *s_tmem;
   const uint32_t smem0 = smem_u32(smem);
   bool aborted = false;
   int stage = 0;
   uint32_t phase = 0;
   auto advance = [&]() {
-    if (++stage == P.stages) { stage = 0; phase ^= 1u; }
+    if (++stage == H.stages) { stage = 0; phase ^= 1u; }
   };
 
-  if (PHASE == 2 && P.total == 0) {  // no expert is named: the layer's output is zero
-    for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.rows; i += (int64_t)gridDim.x * kNT)
+  if (n_act == 0) {  // no expert is named: the layer's output is zero
+    for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.ph[1].rows; i += (int64_t)gridDim.x * kNT)
       a.out[i] = __float2bfloat16_rn(0.0f);
   }
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights: TMA tiles, bulk scale atoms
+    // The producer runs into phase 2 without waiting: its weights do not depend on phase 1.
     long long issued = 0;
-    for (int p = p0; p < p1 && !aborted;) {
-      const Seg S = seg_at<PHASE>(P, tiles, p, p1);
-      const int e = s_exp[S.slot], row0 = S.tile * 128;
-      for (int kb = S.kb0; kb < S.kb1; ++kb) {
-        if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
-        if (lane == 0) {
-          const uint32_t fb = smem_u32(&full[stage]);
-          const uint32_t st = smem0 + stage * P.stage_bytes;
-          const int natom = a.red >> 7;  // MX: scale atoms of a 128-row block along K
-          if (PHASE == 1) {
-            const int at0 = kb * C::kSub, nat = C::kSub ? min(C::kSub, natom - at0) : 0;
-            mbar_arrive_expect_tx(fb, 2 * kTileBytes + 2 * 512 * nat);
-            const int x = kb * (FMT == 0 ? 64 : 128);
-            tma_load_4d(st, &tmW, fb, x, row0, 0, e);
-            tma_load_4d(st + kTileBytes, &tmW, fb, x, row0, 1, e);
-            if (C::kSub) {
-              const int64_t rg = ((int64_t)e * 2 * a.I + row0) >> 7, ru = ((int64_t)e * 2 * a.I + a.I + row0) >> 7;
-              bulk_load(st + P.sf_off, a.sa + (rg * natom + at0) * 512, 512 * nat, fb);
-              bulk_load(st + P.sf_off + C::kSub * 512, a.sa + (ru * natom + at0) * 512, 512 * nat, fb);
+    auto produce = [&](auto ph, const Plan& P) {
+      constexpr int PHASE = decltype(ph)::value;
+      const DecodePhase& F = a.ph[PHASE - 1];
+      const int natom = F.red >> 7;  // MX: scale atoms of a 128-row block along K
+      for (int p = P.p0; p < P.p1 && !aborted;) {
+        const Seg S = seg_at<PHASE>(P, p);
+        const int e = s_exp[S.slot], row0 = S.tile * 128;
+        for (int kb = S.kb0; kb < S.kb1; ++kb) {
+          if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
+          if (lane == 0) {
+            const uint32_t fb = smem_u32(&full[stage]);
+            const uint32_t st = smem0 + stage * H.stage_bytes;
+            if (PHASE == 1) {
+              const int at0 = kb * C::kSub, nat = C::kSub ? min(C::kSub, natom - at0) : 0;
+              mbar_arrive_expect_tx(fb, 2 * kTileBytes + 2 * 512 * nat);
+              const int x = kb * (FMT == 0 ? 64 : 128);
+              tma_load_4d(st, &tmW1, fb, x, row0, 0, e);
+              tma_load_4d(st + kTileBytes, &tmW1, fb, x, row0, 1, e);
+              if (C::kSub) {
+                const int64_t rg = ((int64_t)e * 2 * a.I + row0) >> 7, ru = ((int64_t)e * 2 * a.I + a.I + row0) >> 7;
+                bulk_load(st + P.sf_off, F.sa + (rg * natom + at0) * 512, 512 * nat, fb);
+                bulk_load(st + P.sf_off + C::kSub * 512, F.sa + (ru * natom + at0) * 512, 512 * nat, fb);
+              }
+            } else {
+              const int kk0 = kb * H.ns, at0 = kk0 * C::kSub, nat = C::kSub ? min(H.ns * C::kSub, natom - at0) : 0;
+              const bool second = H.ns == 2 && (kk0 + 1) * C::kBK < F.red;
+              mbar_arrive_expect_tx(fb, (second ? 2 : 1) * kTileBytes + 512 * nat);
+              const int x = kk0 * (FMT == 0 ? 64 : 128);
+              tma_load_3d(st, &tmW2, fb, x, row0, e);
+              if (second) tma_load_3d(st + kTileBytes, &tmW2, fb, x + (FMT == 0 ? 64 : 128), row0, e);
+              if (C::kSub)
+                bulk_load(st + P.sf_off, F.sa + ((((int64_t)e * F.rows + row0) >> 7) * natom + at0) * 512, 512 * nat,
+                          fb);
             }
-          } else {
-            const int at0 = kb * P.ns * C::kSub, nat = C::kSub ? min(P.ns * C::kSub, natom - at0) : 0;
-            const int kk0 = kb * P.ns, nsub = min(P.ns, (a.red - kk0 * C::kBK + C::kBK - 1) / C::kBK);
-            mbar_arrive_expect_tx(fb, nsub * kTileBytes + 512 * nat);
-            for (int s = 0; s < nsub; ++s)
-              tma_load_3d(st + s * kTileBytes, &tmW, fb, (kk0 + s) * (FMT == 0 ? 64 : 128), row0, e);
-            if (C::kSub)
-              bulk_load(st + P.sf_off, a.sa + ((((int64_t)e * a.rows + row0) >> 7) * natom + at0) * 512, 512 * nat, fb);
           }
+          __syncwarp();
+          ++issued;
+          advance();
         }
-        __syncwarp();
-        ++issued;
-        advance();
+        p += S.kb1 - S.kb0;
       }
-      p += S.kb1 - S.kb0;
-    }
+    };
+    produce(Phase1(), plan1);
+    produce(Phase2(), plan2);
     if (aborted && lane == 0) {
       // drain: the copies in flight land before the CTA's shared memory goes away.  Their full
       // barriers may lack the token loaders' arrivals, so this may run to its own limit.
-      long long n = issued < P.stages ? issued : P.stages;
+      const long long n = issued < H.stages ? issued : H.stages;
       for (long long i = 0; i < n; ++i) {
-        if (--stage < 0) { stage = P.stages - 1; phase ^= 1u; }
+        if (--stage < 0) { stage = H.stages - 1; phase ^= 1u; }
         mbar_wait_drain(smem_u32(&full[stage]), phase);
       }
     }
@@ -390,194 +429,264 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     int acc = 0;
     uint32_t acc_phase = 0;
-    // descriptors of stage 0's tiles; an address d bytes further on adds d / 16
-    const uint64_t desc_a = smem_desc(smem0, 16, 1024, kSwizzle128B);
-    const uint64_t desc_b = smem_desc(smem0 + P.b_off, 16, 1024, kSwizzle128B);
-    for (int p = p0; p < p1 && !aborted;) {
-      const Seg S = seg_at<PHASE>(P, tiles, p, p1);
-      const uint32_t n16 = (uint32_t)((s_off[S.slot + 1] - s_off[S.slot] + 15) & ~15);
-      const uint32_t N = PHASE == 2 && FMT == 0 ? 2 * n16 : n16;
-      const uint32_t idesc = FMT == 0 ? idesc_bf16(128, N, false, false) : idesc_mx(FMT == kE4M3 ? 0 : 1, 128, N);
-      if (!warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
-      tc_fence_after();
-      const uint32_t d = tmem_base + acc * P.acc_cols;
-      for (int kb = S.kb0; kb < S.kb1; ++kb) {
-        if (!warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) { aborted = true; break; }
+    auto multiply = [&](auto ph, const Plan& P) {
+      constexpr int PHASE = decltype(ph)::value;
+      const int red = a.ph[PHASE - 1].red;
+      // descriptors of stage 0's tiles; an address d bytes further on adds d / 16
+      const uint64_t desc_a = smem_desc(smem0, 16, 1024, kSwizzle128B);
+      const uint64_t desc_b = smem_desc(smem0 + P.b_off, 16, 1024, kSwizzle128B);
+      for (int p = P.p0; p < P.p1 && !aborted;) {
+        const Seg S = seg_at<PHASE>(P, p);
+        const int n = s_off[S.slot + 1] - s_off[S.slot];
+        const uint32_t N = PHASE == 1 ? (n + 15) & ~15 : cols2<FMT>(n);
+        const uint32_t idesc = FMT == 0 ? idesc_bf16(128, N, false, false) : idesc_mx(FMT == kE4M3 ? 0 : 1, 128, N);
+        if (!warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
         tc_fence_after();
-        if (lane == 0) {
-          if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
-          const uint64_t so = (uint64_t)(stage * P.stage_bytes) >> 4;
-          const uint32_t sf = tmem_base + P.sf_col0 + stage * P.sf_per;
+        const uint32_t d = tmem_base + acc * H.acc_cols;
+        for (int kb = S.kb0; kb < S.kb1; ++kb) {
+          if (!warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) { aborted = true; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
+            const uint64_t so = (uint64_t)(stage * H.stage_bytes) >> 4;
+            const uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {  // phase 1: gate and up; phase 2: K pieces
-            if (PHASE == 2 && s == P.ns) break;
-            const int kk = PHASE == 1 ? kb : kb * P.ns + s;
-            // MMAs of this piece that hold data (an e2m1 K may end inside it; the zero-filled end
-            // of a bf16 K adds nothing)
-            const int left = a.red - kk * C::kBK;
-            const uint64_t ad = desc_a + so + s * (kTileBytes >> 4);
-            const uint64_t bd = desc_b + so + (PHASE == 1 ? 0 : s * (P.b_piece >> 4));
-            const uint32_t dd = PHASE == 1 ? d + s * P.ncols : d;
-            const uint32_t sfa = sf + s * C::kSub * 4;
-            const uint32_t sfb = sf + (PHASE == 1 ? C::kSub * 8 : (P.ns + s) * C::kSub * 4);
-            const bool fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
+            for (int s = 0; s < 2; ++s) {  // phase 1: gate and up; phase 2: K pieces
+              if (PHASE == 2 && s == H.ns) break;
+              const int kk = PHASE == 1 ? kb : kb * H.ns + s;
+              // MMAs of this piece that hold data (an e2m1 K may end inside it; the zero-filled end
+              // of a bf16 K adds nothing)
+              const int left = red - kk * C::kBK;
+              const uint64_t ad = desc_a + so + s * (kTileBytes >> 4);
+              const uint64_t bd = desc_b + so + (PHASE == 1 ? 0 : s * (P.b_piece >> 4));
+              const uint32_t dd = PHASE == 1 ? d + s * H.ncols : d;
+              const uint32_t sfa = sf + s * C::kSub * 4;
+              const uint32_t sfb = sf + (PHASE == 1 ? C::kSub * 8 : (H.ns + s) * C::kSub * 4);
+              const bool fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j * C::kPerMma >= left) break;
-              const uint32_t accum = !(fresh && j == 0);
-              if (FMT == 0) {
-                mma_f16(dd, ad + 2 * j, bd + 2 * j, idesc, accum);
-              } else if (FMT == kE4M3) {
-                mma_mxf8(dd, ad + 2 * j, bd + 2 * j, idesc | idesc_sf_ids(j, j), sfa, sfb, accum);
-              } else {
-                const uint32_t id = 2 * (j & 1);
-                mma_mxf4(dd, ad + 2 * j, bd + 2 * j, idesc | idesc_sf_ids(id, id), sfa + 4 * (j >> 1),
-                         sfb + 4 * (j >> 1), accum);
+              for (int j = 0; j < 4; ++j) {
+                if (j * C::kPerMma >= left) break;
+                const uint32_t accum = !(fresh && j == 0);
+                if (FMT == 0) {
+                  mma_f16(dd, ad + 2 * j, bd + 2 * j, idesc, accum);
+                } else if (FMT == kE4M3) {
+                  mma_mxf8(dd, ad + 2 * j, bd + 2 * j, idesc | idesc_sf_ids(j, j), sfa, sfb, accum);
+                } else {
+                  const uint32_t id = 2 * (j & 1);
+                  mma_mxf4(dd, ad + 2 * j, bd + 2 * j, idesc | idesc_sf_ids(id, id), sfa + 4 * (j >> 1),
+                           sfb + 4 * (j >> 1), accum);
+                }
               }
             }
+            mma_commit(smem_u32(&empty[stage]));
           }
-          mma_commit(smem_u32(&empty[stage]));
+          __syncwarp();
+          advance();
         }
+        if (aborted) break;
+        if (lane == 0) mma_commit(smem_u32(&tfull[acc]));
         __syncwarp();
-        advance();
+        if (++acc == H.nacc) { acc = 0; acc_phase ^= 1u; }
+        p += S.kb1 - S.kb0;
       }
-      if (aborted) break;
-      if (lane == 0) mma_commit(smem_u32(&tfull[acc]));
-      __syncwarp();
-      if (++acc == P.nacc) { acc = 0; acc_phase ^= 1u; }
-      p += S.kb1 - S.kb0;
-    }
+    };
+    multiply(Phase1(), plan1);
+    multiply(Phase2(), plan2);
     if (aborted && lane == 0) {
       mma_commit(smem_u32(drain));
       mbar_wait_drain(smem_u32(drain), 0);
     }
   } else if (C::kCopier && warp == 6) {
     // ------------------------------------------------------------ scale copier: a stage's atoms -> tensor memory
-    for (int p = p0; p < p1 && !aborted;) {
-      const Seg S = seg_at<PHASE>(P, tiles, p, p1);
-      for (int kb = S.kb0; kb < S.kb1; ++kb) {
-        if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
-        tc_fence_after();
-        if (lane == 0) {
-          fence_proxy_async_smem();  // the token operand's and its scales' cp.async writes
-          const uint64_t ds = smem_desc(smem0 + stage * P.stage_bytes + P.sf_off, 0, 128, kSwizzleNone);
-          const uint32_t sf = tmem_base + P.sf_col0 + stage * P.sf_per;
-          // groups of atoms: phase 1 gate, up, tokens; phase 2 weights, tokens
-          const int per = PHASE == 1 ? C::kSub : P.ns * C::kSub;
-          const int nat = min(per, (a.red >> 7) - kb * per);
-          for (int g = 0; g < (PHASE == 1 ? 3 : 2); ++g)
-            for (int i = 0; i < nat; ++i) tmem_cp_32x128b_x4(sf + 4 * (g * per + i), ds + (((g * per + i) * 512) >> 4));
-          mma_commit(smem_u32(&sfull[stage]));
+    auto copy = [&](auto ph, const Plan& P) {
+      constexpr int PHASE = decltype(ph)::value;
+      const int natom = a.ph[PHASE - 1].red >> 7;
+      // groups of atoms: phase 1 gate, up, tokens; phase 2 weights, tokens
+      const int per = PHASE == 1 ? C::kSub : H.ns * C::kSub;
+      const uint64_t ds0 = smem_desc(smem0 + P.sf_off, 0, 128, kSwizzleNone);
+      for (int p = P.p0; p < P.p1 && !aborted;) {
+        const Seg S = seg_at<PHASE>(P, p);
+        for (int kb = S.kb0; kb < S.kb1; ++kb) {
+          if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the token operand's and its scales' cp.async writes
+            const uint64_t ds = ds0 + ((uint64_t)(stage * H.stage_bytes) >> 4);
+            const uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
+            const int nat = min(per, natom - kb * per);
+            for (int g = 0; g < (PHASE == 1 ? 3 : 2); ++g)
+              for (int i = 0; i < nat; ++i) tmem_cp_32x128b_x4(sf + 4 * (g * per + i), ds + (((g * per + i) * 512) >> 4));
+            mma_commit(smem_u32(&sfull[stage]));
+          }
+          __syncwarp();
+          advance();
         }
-        __syncwarp();
-        advance();
+        p += S.kb1 - S.kb0;
       }
-      p += S.kb1 - S.kb0;
-    }
+    };
+    copy(Phase1(), plan1);
+    copy(Phase2(), plan2);
     if (aborted && lane == 0) {
       mma_commit(smem_u32(cdrain));
       mbar_wait_drain(smem_u32(cdrain), 0);
     }
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------------------ the token operand
-    if (PHASE == 2) grid_wait();  // A is phase 1's
     // Thread (r0, j) fetches 16-byte chunk j of rows r0, r0 + 8, ...: chunk j of row r goes to chunk
     // j ^ (r % 8) of its 128 bytes (the 128-byte swizzle), so its places are 1024 bytes apart.
     // Rows past n hold leftovers, which only reach accumulator columns that nobody reads.
     const int tid = threadIdx.x - kLoadWarp0 * 32;
     const int j = tid & 7, r0 = tid >> 3;
     const uint32_t place = r0 * 128 + ((j ^ r0) << 4);
-    const int natom = a.red >> 7;
-    const int64_t lo_off = PHASE == 2 && FMT == 0 ? a.b_lo - a.b : 0;
-    for (int p = p0; p < p1 && !aborted;) {
-      const Seg S = seg_at<PHASE>(P, tiles, p, p1);
-      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
-      const uint32_t lo_place = (uint32_t)((n + 15) & ~15) * 128;
-      auto row_of = [&](int r) -> int64_t { return PHASE == 1 ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
-      // the first rows' sources stay in registers over the segment
-      const uint8_t* src0 = a.b + (r0 < n ? row_of(r0) : 0) * a.b_ld + j * 16;
-      const uint8_t* src1 = a.b + (r0 + 8 < n ? row_of(r0 + 8) : 0) * a.b_ld + j * 16;
-      const uint8_t* ssrc = C::kSub ? a.sb + (tid < n ? row_of(tid) : 0) * a.sb_ld : nullptr;
-      for (int kb = S.kb0; kb < S.kb1; ++kb) {
-        if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
-        const uint32_t st = smem0 + stage * P.stage_bytes;
+    const int64_t lo_off = FMT == 0 ? a.act_lo - a.act : 0;
+    auto load = [&](auto ph, const Plan& P) {
+      constexpr int PHASE = decltype(ph)::value;
+      const DecodePhase& F = a.ph[PHASE - 1];
+      const int natom = F.red >> 7;
+      const int64_t sb_ld = F.red >> 5;
+      for (int p = P.p0; p < P.p1 && !aborted;) {
+        const Seg S = seg_at<PHASE>(P, p);
+        const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
+        const uint32_t lo_place = (uint32_t)((n + 7) & ~7) * 128;
+        auto row_of = [&](int r) -> int64_t { return PHASE == 1 ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
+        // the first rows' sources stay in registers over the segment
+        const uint8_t* src0 = F.b + (r0 < n ? row_of(r0) : 0) * F.b_ld + j * 16;
+        const uint8_t* src1 = F.b + (r0 + 8 < n ? row_of(r0 + 8) : 0) * F.b_ld + j * 16;
+        const uint8_t* ssrc = C::kSub ? F.sb + (tid < n ? row_of(tid) : 0) * sb_ld : nullptr;
+        for (int kb = S.kb0; kb < S.kb1; ++kb) {
+          if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
+          const uint32_t st = smem0 + stage * H.stage_bytes;
 #pragma unroll
-        for (int s = 0; s < PHASE; ++s) {
-          const int kk = kb * P.ns + s;
-          if (PHASE == 2 && (s == P.ns || kk * C::kBK >= a.red)) break;
-          const int kbyte = kk * 128;
-          const uint32_t size = kbyte + j * 16 < a.b_ld ? 16u : 0u;  // past the end of K: zeros
-          const int go = size ? kbyte : -j * 16;
-          const uint32_t dst = st + P.b_off + s * P.b_piece + place;
-          auto fetch = [&](const uint8_t* from, uint32_t to) {
-            cp_async_16(to, from + go, size);
-            if (PHASE == 2 && FMT == 0) cp_async_16(to + lo_place, from + lo_off + go, size);
-          };
-          if (r0 < n) fetch(src0, dst);
-          if (r0 + 8 < n) fetch(src1, dst + 1024);
-          for (int r = r0 + 16; r < n; r += 8) fetch(a.b + row_of(r) * a.b_ld + j * 16, dst + (r - r0) * 128);
-          if (C::kSub) {
-            // row r's 4 scales of a 128-element atom: word 4 (r % 32) + r / 32
-            const uint32_t ssf = st + P.sf_off + (PHASE == 1 ? 2 * C::kSub : (P.ns + s) * C::kSub) * 512;
+          for (int s = 0; s < PHASE; ++s) {
+            const int kk = PHASE == 1 ? kb : kb * H.ns + s;
+            if (PHASE == 2 && (s == H.ns || kk * C::kBK >= F.red)) break;
+            const int kbyte = kk * 128;
+            const uint32_t size = kbyte + j * 16 < F.b_ld ? 16u : 0u;  // past the end of K: zeros
+            const int go = size ? kbyte : -j * 16;
+            const uint32_t dst = st + P.b_off + s * P.b_piece + place;
+            auto fetch = [&](const uint8_t* from, uint32_t to) {
+              cp_async_16(to, from + go, size);
+              if (PHASE == 2 && FMT == 0) cp_async_16(to + lo_place, from + lo_off + go, size);
+            };
+            if (r0 < n) fetch(src0, dst);
+            if (r0 + 8 < n) fetch(src1, dst + 1024);
+            for (int r = r0 + 16; r < n; r += 8) fetch(F.b + row_of(r) * F.b_ld + j * 16, dst + (r - r0) * 128);
+            if (C::kSub) {
+              // row r's 4 scales of a 128-element atom: word 4 (r % 32) + r / 32
+              const uint32_t ssf = st + P.sf_off + (PHASE == 1 ? 2 * C::kSub : (H.ns + s) * C::kSub) * 512;
 #pragma unroll
-            for (int sub = 0; sub < C::kSub; ++sub) {
-              const int at = kk * C::kSub + sub;
-              if (at >= natom) break;
-              if (tid < n) cp_async_4(ssf + sub * 512 + (tid & 31) * 16 + (tid >> 5) * 4, ssrc + at * 4, 4u);
-              for (int r = tid + 32 * kLoadWarps; r < n; r += 32 * kLoadWarps)
-                cp_async_4(ssf + sub * 512 + (r & 31) * 16 + (r >> 5) * 4, a.sb + row_of(r) * a.sb_ld + at * 4, 4u);
+              for (int sub = 0; sub < C::kSub; ++sub) {
+                const int at = kk * C::kSub + sub;
+                if (at >= natom) break;
+                if (tid < n) cp_async_4(ssf + sub * 512 + (tid & 31) * 16 + (tid >> 5) * 4, ssrc + at * 4, 4u);
+                for (int r = tid + 32 * kLoadWarps; r < n; r += 32 * kLoadWarps)
+                  cp_async_4(ssf + sub * 512 + (r & 31) * 16 + (r >> 5) * 4, F.sb + row_of(r) * sb_ld + at * 4, 4u);
+              }
             }
           }
+          cp_async_arrive_noinc(smem_u32(&full[stage]));
+          __syncwarp();
+          advance();
         }
-        cp_async_arrive_noinc(smem_u32(&full[stage]));
-        __syncwarp();
-        advance();
+        p += S.kb1 - S.kb0;
       }
-      p += S.kb1 - S.kb0;
+    };
+    load(Phase1(), plan1);
+    // A is complete when every CTA has finished phase 1 (all are resident: a cooperative launch)
+    if (!aborted && plan2.p0 < plan2.p1) {
+      const uint64_t t0 = globaltimer();
+      while (load_acquire(a.done) != gridDim.x && !aborted) {
+        if (s_ctl->abort) aborted = true;
+        else if (globaltimer() - t0 > s_ctl->limit_ns) s_ctl->abort = 1;
+      }
+      aborted = __any_sync(0xffffffffu, aborted);
     }
+    load(Phase2(), plan2);
     cp_async_wait_all();  // nothing of this warp's lands after the block exits
-  } else if (warp >= 2 && warp < 6) {
-    // ------------------------------------------------------------ epilogue
+  } else {
+    // ------------------------------------------------------------ epilogue (warps 2 .. 5)
     const int q = warp & 3, row = q * 32 + lane;  // accumulator row of this thread
     int acc = 0;
     uint32_t acc_phase = 0;
-    if (PHASE == 2) grid_wait();  // the partial sums' space and the counters are phase 1's too
 
     // Arrive at a divided item after writing this CTA's partial sums; true in the last CTA.
-    auto join = [&](int item, int c_first, int c_last) {
+    auto join = [&](unsigned* cnt, int c_first, int c_last) {
       __threadfence();
       epi_sync();
       if (threadIdx.x == 64) {
         const unsigned last = (unsigned)(c_last - c_first);
-        *s_last = atomicInc(a.cnt + c_first, last) == last;  // wraps to 0: ready for the next launch
-        __threadfence();
+        *s_last = atomicInc(cnt + c_first, last) == last;  // wraps to 0: ready for the next launch
       }
       epi_sync();
       const bool mine = *s_last != 0;
-      epi_sync();
       if (mine) __threadfence();
       return mine;
     };
     // Partial sums of an item: CTA c keeps those of an item that begins in its run (`begins`: it is the
     // first of the CTAs) apart from those of the item that its run enters in the middle.
-    const int part_sz = (PHASE == 1 ? 256 : 128) * ((a.T + 15) & ~15);
-    auto part_of = [&](int c, bool begins) { return a.part + (int64_t)(c * 2 + begins) * part_sz; };
-
-    for (int p = p0; p < p1 && !aborted;) {
-      const Seg S = seg_at<PHASE>(P, tiles, p, p1);
-      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
-      const int p_end = p + S.kb1 - S.kb0;
-      const int item0 = S.item * P.L, item1 = item0 + P.L;
-      const int out_row = S.tile * 128 + row;
-      if (PHASE == 2 && (p == p0 || p == item0))
-        for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.0f;
-      if (!epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
+    const int t16 = (a.T + 15) & ~15;
+    auto part_of = [&](int c, bool begins, int rows) { return a.part + (int64_t)(c * 2 + begins) * rows * t16; };
+    auto release = [&]() {  // the accumulator has been read
+      tc_fence_before();
+      mbar_arrive(smem_u32(&tempty[acc]));
+      if (++acc == H.nacc) { acc = 0; acc_phase ^= 1u; }
+    };
+    // The accumulator of the next segment, or false when the pipeline has given up.
+    auto next = [&]() {
+      if (!epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) {
+        aborted = true;
+        return false;
+      }
       tc_fence_after();
-      const uint32_t tb = tmem_base + acc * P.acc_cols + ((uint32_t)(q * 32) << 16);
+      return true;
+    };
 
-      if (PHASE == 1) {
-        // 16 entries' activations of this thread's row from its gate and up sums
-        auto finish = [&](int c0, const float (&g)[16], const float (&u)[16]) {
+    for (int p = plan1.p0; p < plan1.p1;) {
+      const Seg S = seg_at<1>(plan1, p);
+      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
+      const int out_row = S.tile * 128 + row;
+      if (!next()) break;
+      const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
+      const bool whole = S.kb0 == 0 && S.kb1 == plan1.nk;
+      bool write = whole;
+      int c_first = cta, c_last = cta;
+      if (!whole) {
+        float* mine = part_of(cta, S.kb0 == 0, 256);
+        for (int c0 = 0; c0 < n; c0 += 16) {
+          float g[16], u[16];
+          tmem_ld16(tb + c0, g);
+          tmem_ld16(tb + H.ncols + c0, u);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (c0 + c >= n) break;
+            mine[(c0 + c) * 256 + row] = g[c];
+            mine[(c0 + c) * 256 + 128 + row] = u[c];
+          }
+        }
+        release();
+        c_first = plan1.owner(S.item * plan1.L);
+        c_last = plan1.owner(S.item * plan1.L + plan1.L - 1);
+        write = join(a.cnt, c_first, c_last);
+      }
+      if (write) {
+        for (int c0 = 0; c0 < n; c0 += 16) {
+          float g[16], u[16];
+          if (whole) {
+            tmem_ld16(tb + c0, g);
+            tmem_ld16(tb + H.ncols + c0, u);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) g[c] = u[c] = 0.0f;
+            for (int x = c_first; x <= c_last; ++x) {
+              const float* o = part_of(x, x == c_first, 256) + c0 * 256 + row;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                if (c0 + c >= n) break;
+                g[c] += __ldcg(o + c * 256);
+                u[c] += __ldcg(o + c * 256 + 128);
+              }
+            }
+          }
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             if (c0 + c >= n) break;
@@ -613,107 +722,83 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
               if (lane == 0) a.act_scales[(r * a.I + out_row) >> 5] = (uint8_t)sc;
             }
           }
-        };
-        const bool whole = S.kb0 == 0 && S.kb1 == P.nk;
-        float* mine = part_of(cta, S.kb0 == 0);
-        for (int c0 = 0; c0 < n; c0 += 16) {
-          float g[16], u[16];
-          tmem_ld16(tb + c0, g);
-          tmem_ld16(tb + P.ncols + c0, u);
-          if (whole) {
-            finish(c0, g, u);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              if (c0 + c >= n) break;
-              mine[(c0 + c) * 256 + row] = g[c];
-              mine[(c0 + c) * 256 + 128 + row] = u[c];
-            }
-          }
         }
-        tc_fence_before();
-        mbar_arrive(smem_u32(&tempty[acc]));
-        if (!whole) {
-          const int c_first = P.owner(item0), c_last = P.owner(item1 - 1);
-          if (join(S.item, c_first, c_last)) {
-            for (int c0 = 0; c0 < n; c0 += 16) {
-              float g[16], u[16];
+      }
+      if (whole) release();
+      p += S.kb1 - S.kb0;
+    }
+    // this CTA's part of A is written (or it has given up, which the others must not wait for)
+    __threadfence();
+    epi_sync();
+    if (threadIdx.x == 64) atomicAdd(a.done, 1u);
+
+    for (int p = plan2.p0; p < plan2.p1 && !aborted;) {
+      const Seg S = seg_at<2>(plan2, p);
+      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
+      const int p_end = p + S.kb1 - S.kb0;
+      const int item0 = S.item * plan2.L, item1 = item0 + plan2.L;
+      if (p == plan2.p0 || p == item0)
+        for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.0f;
+      if (!next()) break;
+      const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
+      const int lo = (n + 7) & ~7;  // bf16: the column of the first low part
+      for (int c0 = 0; c0 < n; c0 += 16) {
+        float v[16];
+        tmem_ld16(tb + c0, v);
+        if (FMT == 0) {
+          float left[16];
+          tmem_ld16(tb + lo + c0, left);
 #pragma unroll
-              for (int c = 0; c < 16; ++c) g[c] = u[c] = 0.0f;
-              for (int x = c_first; x <= c_last; ++x) {
-                const float* o = part_of(x, x == c_first) + c0 * 256 + row;
+          for (int c = 0; c < 16; ++c) v[c] += left[c];
+        }
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  if (c0 + c >= n) break;
-                  g[c] += __ldcg(o + c * 256);
-                  u[c] += __ldcg(o + c * 256 + 128);
+        for (int c = 0; c < 16; ++c) {
+          if (c0 + c >= n) break;
+          s_acc[s_tok[off + c0 + c] * 128 + row] += s_w[off + c0 + c] * v[c];
+        }
+      }
+      release();
+      if (p_end == plan2.p1 || p_end == item1) {  // this CTA's part of the output tile is complete
+        const int out_row = S.tile * 128 + row, rows = a.ph[1].rows;
+        if (plan2.p0 <= item0 && p_end == item1) {
+          if (out_row < rows)
+            for (int t = 0; t < a.T; ++t)
+              a.out[(int64_t)t * rows + out_row] = __float2bfloat16_rn(s_acc[t * 128 + row]);
+        } else {
+          const int c_first = plan2.owner(item0), c_last = plan2.owner(item1 - 1);
+          float* mine = part_of(cta, plan2.p0 <= item0, 128);
+          for (int t = 0; t < a.T; ++t) mine[t * 128 + row] = s_acc[t * 128 + row];
+          if (join(a.cnt + kMaxCtas, c_first, c_last)) {
+            // a warp takes four tokens at a time, a lane four rows of each; eight loads in flight
+            const float4* first = reinterpret_cast<const float4*>(part_of(c_first, true, 128)) + lane;
+            const float4* rest = reinterpret_cast<const float4*>(part_of(0, false, 128)) + lane;
+            const int step = 2 * 128 / 4 * t16;  // float4s from a CTA's partial sums to the next CTA's
+            for (int t0 = (warp - 2) * 4; t0 < a.T; t0 += 16) {
+              float4 v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[i] = t0 + i < a.T ? __ldcg(first + (t0 + i) * 32) : make_float4(0, 0, 0, 0);
+#pragma unroll 2
+              for (int x = c_first + 1; x <= c_last; ++x) {
+                const float4* o = rest + (int64_t)x * step;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (t0 + i >= a.T) break;
+                  const float4 w4 = __ldcg(o + (t0 + i) * 32);
+                  v[i].x += w4.x; v[i].y += w4.y; v[i].z += w4.z; v[i].w += w4.w;
                 }
               }
-              finish(c0, g, u);
-            }
-          }
-        }
-      } else {
-        const int n16 = (n + 15) & ~15;
-        for (int c0 = 0; c0 < n; c0 += 16) {
-          float v[16];
-          tmem_ld16(tb + c0, v);
-          if (FMT == 0) {
-            float lo[16];
-            tmem_ld16(tb + n16 + c0, lo);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] += lo[c];
-          }
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= n) break;
-            s_acc[s_tok[off + c0 + c] * 128 + row] += s_w[off + c0 + c] * v[c];
-          }
-        }
-        tc_fence_before();
-        mbar_arrive(smem_u32(&tempty[acc]));
-        if (p_end == p1 || p_end == item1) {  // this CTA's part of the output tile is complete
-          if (p0 <= item0 && p_end == item1) {
-            if (out_row < a.rows)
-              for (int t = 0; t < a.T; ++t)
-                a.out[(int64_t)t * a.rows + out_row] = __float2bfloat16_rn(s_acc[t * 128 + row]);
-          } else {
-            const int c_first = P.owner(item0), c_last = P.owner(item1 - 1);
-            float* mine = part_of(cta, p0 <= item0);
-            for (int t = 0; t < a.T; ++t) mine[t * 128 + row] = s_acc[t * 128 + row];
-            if (join(S.item, c_first, c_last)) {
-              // a warp takes four tokens at a time, a lane four rows of each; eight loads in flight
-              const float4* first = reinterpret_cast<const float4*>(part_of(c_first, true)) + lane;
-              const float4* rest = reinterpret_cast<const float4*>(part_of(0, false)) + lane;
-              const int step = part_sz / 2;  // float4s from a CTA's partial sums to the next CTA's
-              for (int t0 = (warp - 2) * 4; t0 < a.T; t0 += 16) {
-                float4 v[4];
+              const int r4 = S.tile * 128 + 4 * lane;
+              if (r4 < rows)  // rows is a multiple of 8
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  v[i] = t0 + i < a.T ? __ldcg(first + (t0 + i) * 32) : make_float4(0, 0, 0, 0);
-#pragma unroll 2
-                for (int x = c_first + 1; x <= c_last; ++x) {
-                  const float4* o = rest + (int64_t)x * step;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    if (t0 + i >= a.T) break;
-                    const float4 w4 = __ldcg(o + (t0 + i) * 32);
-                    v[i].x += w4.x; v[i].y += w4.y; v[i].z += w4.z; v[i].w += w4.w;
-                  }
-                }
-                const int r4 = S.tile * 128 + 4 * lane;
-                if (r4 < a.rows)  // rows is a multiple of 8
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    if (t0 + i < a.T)
-                      *reinterpret_cast<uint2*>(a.out + (int64_t)(t0 + i) * a.rows + r4) =
-                          make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
-              }
+                  if (t0 + i < a.T)
+                    *reinterpret_cast<uint2*>(a.out + (int64_t)(t0 + i) * rows + r4) =
+                        make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
             }
           }
         }
       }
-      if (++acc == P.nacc) { acc = 0; acc_phase ^= 1u; }
       p = p_end;
     }
   }
@@ -725,20 +810,21 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
+  // the last CTA to leave clears the count that the others have waited on
+  if (threadIdx.x == 0 && atomicInc(a.done + 1, gridDim.x - 1) == gridDim.x - 1) atomicExch(a.done, 0u);
 }
 
 // ---------------------------------------------------------------- workspace
-// [counters of both phases][partial sums][A: bf16 high and low parts, or codes and scales]
+// [counters of both phases, CTAs done and left][partial sums][A: bf16 high and low parts, or codes and scales]
 struct DecodeWs {
-  size_t cnt, part, act, act_lo, act_scales, bytes;
+  size_t part, act, act_lo, act_scales, bytes;
 };
 DecodeWs decode_ws(int fmt, int64_t T, int k, int64_t I) {
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
   const size_t rows = (size_t)T * k;
   const size_t row = fmt == 0 ? (size_t)I * 2 : fmt == PGG_FMT_E4M3 ? (size_t)I : (size_t)I / 2;
   DecodeWs w;
-  w.cnt = 0;
-  w.part = up(2 * kMaxCtas * sizeof(unsigned));
+  w.part = up((2 * kMaxCtas + 2) * sizeof(unsigned));
   w.act = w.part + up((size_t)kMaxCtas * 2 * 256 * ((T + 15) / 16 * 16) * sizeof(float));
   w.act_lo = w.act + up(rows * row);
   w.act_scales = w.act_lo;
@@ -754,21 +840,6 @@ int check_decode_dims(int fmt, int64_t T, int k, int64_t H, int64_t I, int E) {
   if (H % mult || I % mult) return PGG_ERR_ALIGNMENT;
   if (T > kMaxT) return PGG_ERR_TOO_LARGE;
   return PGG_OK;
-}
-
-template <int FMT, int PHASE>
-int run_phase(const CUtensorMap& tm, DecodeArgs a, const DeviceInfo& dev, cudaStream_t s) {
-  a.slots_cap = std::min(a.E, a.T * a.k);
-  const size_t lists = 512 + (PHASE == 2 ? (size_t)a.T * 512 + (size_t)a.T * a.k * 4 : 0) +
-                       2 * (2 * (size_t)a.slots_cap + 1) + (size_t)a.T * a.k;
-  // the whole of an SM's shared memory, so that a CTA has its SM and the tensor memory to itself
-  const size_t smem = dev.smem_optin;
-  a.ring_bytes = (int)((smem - 1024 - lists) / 1024 * 1024);
-  auto kern = moe_decode_kernel<FMT, PHASE>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_status(e);
-  kern<<<std::min(dev.sms, kMaxCtas), DecCfg<FMT>::kThreads, smem, s>>>(tm, a);
-  return cuda_status(cudaGetLastError());
 }
 
 template <int FMT>
@@ -804,33 +875,37 @@ int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const fl
   a.E = E;
   a.I = (int)I;
   a.limit = limit;
-  a.err = err;
+  a.ph[0] = {(int)I, (int)H, X, (int64_t)bytes(H), xs, w1s};
+  a.ph[1] = {(int)H, (int)I, ws + L.act, (int64_t)bytes(I), ws + L.act_scales, w2s};
+  a.act = ws + L.act;
+  a.act_lo = ws + L.act_lo;
+  a.act_scales = ws + L.act_scales;
+  a.out = static_cast<__nv_bfloat16*>(out);
   a.part = reinterpret_cast<float*>(ws + L.part);
-  a.cnt = reinterpret_cast<unsigned*>(ws + L.cnt);
-  DecodeArgs a1 = a;
-  a1.rows = (int)I;
-  a1.red = (int)H;
-  a1.b = X;
-  a1.b_ld = (int64_t)bytes(H);
-  a1.sb = xs;
-  a1.sb_ld = H / 32;
-  a1.sa = w1s;
-  a1.act = ws + L.act;
-  a1.act_lo = ws + L.act_lo;
-  a1.act_scales = ws + L.act_scales;
-  if ((st = run_phase<FMT, 1>(t1, a1, dev, s))) return st;
-  DecodeArgs a2 = a;
-  a2.rows = (int)H;
-  a2.red = (int)I;
-  a2.b = ws + L.act;
-  a2.b_lo = ws + L.act_lo;
-  a2.b_ld = (int64_t)bytes(I);
-  a2.sb = ws + L.act_scales;
-  a2.sb_ld = I / 32;
-  a2.sa = w2s;
-  a2.out = static_cast<__nv_bfloat16*>(out);
-  a2.cnt += kMaxCtas;
-  return run_phase<FMT, 2>(t2, a2, dev, s);
+  a.cnt = reinterpret_cast<unsigned*>(ws);
+  a.done = a.cnt + 2 * kMaxCtas;
+  a.err = err;
+  a.slots_cap = std::min(E, a.T * k);
+  const size_t lists = 512 + (size_t)a.T * 512 + (size_t)a.T * k * 4 + 2 * (2 * (size_t)a.slots_cap + 1) +
+                       (size_t)a.T * k;
+  // the whole of an SM's shared memory, so that a CTA has its SM and the tensor memory to itself
+  const size_t smem = dev.smem_optin;
+  a.ring_bytes = (int)((smem - 1024 - lists) / 1024 * 1024);
+  auto kern = moe_decode_kernel<FMT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min(dev.sms, kMaxCtas));
+  cfg.blockDim = dim3(DecCfg<FMT>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeCooperative;  // CTAs wait for one another between the phases
+  at.val.cooperative = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, t1, t2, a);
+  return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 int check_decode(int fmt, const void* X, const int32_t* ids, const float* w, const void* W1, const void* W2, void* out,
