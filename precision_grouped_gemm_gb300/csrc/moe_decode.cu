@@ -33,7 +33,8 @@ namespace {
 constexpr int kMaxT = PGG_MOE_DECODE_MAX_T;
 constexpr int kMaxCtas = 192;   // CTAs of a launch (one per SM); sizes the workspace without a device
 constexpr int kMaxStages = 8;
-constexpr int kLoadWarps = 2;   // warps that fetch the token operand
+constexpr int kLoadWarps = 4;   // warps that fetch the token operand
+constexpr int kBatch = 4;      // tokens that the epilogue works on at a time
 constexpr int kTileBytes = 128 * 128;  // 128 rows x one 128-byte swizzle atom of K
 
 template <int FMT>
@@ -87,6 +88,36 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&f)[16]) {
 }
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// The MMAs of one lane (`go`), issued by a whole converged warp: with the branch on the lane inside
+// the instruction's own predicate, descriptors stay warp-uniform values.
+template <int FMT>
+__device__ __forceinline__ void mma_if(uint32_t go, uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                       uint32_t sfb, uint32_t accum) {
+  if (FMT == 0)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accum), "r"(go)
+        : "memory");
+  else if (FMT == kE4M3)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(go)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(go)
+        : "memory");
 }
 // Barrier of the four epilogue warps that tells each whether `ok` held in all of them: they give
 // up together, so that none is left at a later barrier.
@@ -252,14 +283,32 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   int16_t* s_id = reinterpret_cast<int16_t*>(s_wid + a.T * a.k);      // [T k]: the ids, -1 out of range
   uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_id + a.T * a.k);   // [E]: first entry
   const int n_ids = a.T * a.k;
-  for (int i = threadIdx.x; i < n_ids; i += kNT) {
-    const int e = __ldg(a.ids + i);
-    const bool ok = e >= 0 && e < a.E;
-    if (!ok && blockIdx.x == 0) set_error(a.err, kErrBadExpert);
-    s_id[i] = (int16_t)(ok ? e : -1);
-    s_wid[i] = a.w ? __ldg(a.w + i) : 1.0f;
+  // Up to 32 ids: every warp works the list out in registers (lane i has id i) and all of them write
+  // the same; the slots are in the order of first mention.  Saves three block barriers and the scan
+  // over the experts (a third of the time before the first load, which a one-token call feels).
+  const bool few = n_ids <= 32;
+  int id = -1, tok = 0;
+  float wid = 0.0f;
+  if (few) {
+    if (lane < n_ids) {
+      id = __ldg(a.ids + lane);
+      wid = a.w ? __ldg(a.w + lane) : 1.0f;
+      tok = lane / a.k;
+      if (id < 0 || id >= a.E) {
+        if (blockIdx.x == 0) set_error(a.err, kErrBadExpert);
+        id = -1;
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < n_ids; i += kNT) {
+      const int e = __ldg(a.ids + i);
+      const bool ok = e >= 0 && e < a.E;
+      if (!ok && blockIdx.x == 0) set_error(a.err, kErrBadExpert);
+      s_id[i] = (int16_t)(ok ? e : -1);
+      s_wid[i] = a.w ? __ldg(a.w + i) : 1.0f;
+    }
+    for (int i = threadIdx.x; i < a.E * W; i += kNT) s_mask[i] = 0;
   }
-  for (int i = threadIdx.x; i < a.E * W; i += kNT) s_mask[i] = 0;
   if (warp == 0) {
     if (lane < kMaxStages) {
       mbar_init(smem_u32(&full[lane]), 1 + 32 * kLoadWarps);
@@ -282,69 +331,105 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n_ids; i += kNT) {
-    const int t = i / a.k;
-    if (s_id[i] >= 0) atomicOr(&s_mask[s_id[i] * W + (t >> 5)], 1u << (t & 31));
-  }
-  __syncthreads();
   int n_act, max_n;
-  {
-    const int per = (a.E + kNT - 1) / kNT;
-    const int lo = min((int)threadIdx.x * per, a.E), hi = min(lo + per, a.E);
-    int v = 0, mx = 0;  // experts << 16 | tokens
-    for (int e = lo; e < hi; ++e) {
-      int n = 0;
-      for (int q = 0; q < W; ++q) n += __popc(s_mask[e * W + q]);
-      if (n) v += (1 << 16) + n;
-      mx = max(mx, n);
-    }
-    int inc = v;
+  if (few) {
+    const unsigned all = 0xffffffffu, below = (1u << lane) - 1u;
+    const unsigned same = __match_any_sync(all, id), pair = __match_any_sync(all, id * kMaxT + tok);
+    const bool entry = id >= 0 && (pair & below) == 0;  // the token's first choice of this expert
+    const unsigned entries = __ballot_sync(all, entry), slots = __ballot_sync(all, id >= 0 && (same & below) == 0);
+    n_act = __popc(slots);
+    const int head = __ffs(same) - 1;  // the lane that mentions the expert first
+    const int n = id >= 0 ? __popc(same & entries) : 0;
+    max_n = __reduce_max_sync(all, n);
+    const int mine = id >= 0 && lane == head ? n : 0;  // counted once, at the first mention
+    int inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, d);
+      const int o = __shfl_up_sync(all, inc, d);
       if (lane >= d) inc += o;
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 31) {
-      s_scan[warp] = inc;
-      s_scan[16 + warp] = mx;
+    if (mine) {
+      const int slot = __popc(slots & below);
+      s_exp[slot] = (uint16_t)id;
+      s_off[slot + 1] = (uint16_t)inc;
+    }
+    if (lane == 0) s_off[0] = 0;
+    const int first = __shfl_sync(all, inc - mine, head);
+    float wt = 0.0f;  // the weights of all of the token's choices of this expert
+    for (int i = 0; i < n_ids; ++i) {
+      const float o = __shfl_sync(all, wid, i);
+      if (pair >> i & 1) wt += o;
+    }
+    if (entry) {
+      const int r = first + __popc(same & entries & below);
+      s_tok[r] = (uint8_t)tok;
+      s_w[r] = wt;
+    }
+  } else {
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_ids; i += kNT) {
+      const int t = i / a.k;
+      if (s_id[i] >= 0) atomicOr(&s_mask[s_id[i] * W + (t >> 5)], 1u << (t & 31));
     }
     __syncthreads();
-    int run = inc - v, all = 0;
-    max_n = 0;
-    for (int q = 0; q < kNT / 32; ++q) {
-      if (q < warp) run += s_scan[q];
-      all += s_scan[q];
-      max_n = max(max_n, s_scan[16 + q]);
+    {
+      const int per = (a.E + kNT - 1) / kNT;
+      const int lo = min((int)threadIdx.x * per, a.E), hi = min(lo + per, a.E);
+      int v = 0, mx = 0;  // experts << 16 | tokens
+      for (int e = lo; e < hi; ++e) {
+        int n = 0;
+        for (int q = 0; q < W; ++q) n += __popc(s_mask[e * W + q]);
+        if (n) v += (1 << 16) + n;
+        mx = max(mx, n);
+      }
+      int inc = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 31) {
+        s_scan[warp] = inc;
+        s_scan[16 + warp] = mx;
+      }
+      __syncthreads();
+      int run = inc - v, all = 0;
+      max_n = 0;
+#pragma unroll 1
+      for (int q = 0; q < kNT / 32; ++q) {
+        if (q < warp) run += s_scan[q];
+        all += s_scan[q];
+        max_n = max(max_n, s_scan[16 + q]);
+      }
+      n_act = all >> 16;
+      if (threadIdx.x == 0) s_off[n_act] = (uint16_t)(all & 0xFFFF);
+      for (int e = lo; e < hi; ++e) {
+        int n = 0;
+        for (int q = 0; q < W; ++q) n += __popc(s_mask[e * W + q]);
+        if (!n) continue;
+        s_exp[run >> 16] = (uint16_t)e;
+        s_off[run >> 16] = s_eoff[e] = (uint16_t)(run & 0xFFFF);
+        run += (1 << 16) + n;
+      }
     }
-    n_act = all >> 16;
-    if (threadIdx.x == 0) s_off[n_act] = (uint16_t)(all & 0xFFFF);
-    for (int e = lo; e < hi; ++e) {
-      int n = 0;
-      for (int q = 0; q < W; ++q) n += __popc(s_mask[e * W + q]);
-      if (!n) continue;
-      s_exp[run >> 16] = (uint16_t)e;
-      s_off[run >> 16] = s_eoff[e] = (uint16_t)(run & 0xFFFF);
-      run += (1 << 16) + n;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_ids; i += kNT) {
+      const int e = s_id[i];
+      if (e < 0) continue;
+      const int t = i / a.k, i0 = t * a.k;
+      bool first = true;  // the token's first choice of this expert writes the entry
+      for (int j = i0; j < i; ++j) first &= s_id[j] != e;
+      if (!first) continue;
+      int r = s_eoff[e];
+      for (int q = 0; q < (t >> 5); ++q) r += __popc(s_mask[e * W + q]);
+      r += __popc(s_mask[e * W + (t >> 5)] & ((1u << (t & 31)) - 1u));
+      s_tok[r] = (uint8_t)t;
+      float wt = 0.0f;
+      for (int j = i; j < i0 + a.k; ++j)
+        if (s_id[j] == e) wt += s_wid[j];
+      s_w[r] = wt;
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n_ids; i += kNT) {
-    const int e = s_id[i];
-    if (e < 0) continue;
-    const int t = i / a.k, i0 = t * a.k;
-    bool first = true;  // the token's first choice of this expert writes the entry
-    for (int j = i0; j < i; ++j) first &= s_id[j] != e;
-    if (!first) continue;
-    int r = s_eoff[e];
-    for (int q = 0; q < (t >> 5); ++q) r += __popc(s_mask[e * W + q]);
-    r += __popc(s_mask[e * W + (t >> 5)] & ((1u << (t & 31)) - 1u));
-    s_tok[r] = (uint8_t)t;
-    float wt = 0.0f;
-    for (int j = i; j < i0 + a.k; ++j)
-      if (s_id[j] == e) wt += s_wid[j];
-    s_w[r] = wt;
   }
   fence_proxy_async_smem();  // the ring's scratch use, before its first bulk copies
   tc_fence_before();
@@ -432,6 +517,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     auto multiply = [&](auto ph, const Plan& P) {
       constexpr int PHASE = decltype(ph)::value;
       const int red = a.ph[PHASE - 1].red;
+      const uint32_t one = lane == 0;
       // descriptors of stage 0's tiles; an address d bytes further on adds d / 16
       const uint64_t desc_a = smem_desc(smem0, 16, 1024, kSwizzle128B);
       const uint64_t desc_b = smem_desc(smem0 + P.b_off, 16, 1024, kSwizzle128B);
@@ -446,40 +532,32 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         for (int kb = S.kb0; kb < S.kb1; ++kb) {
           if (!warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) { aborted = true; break; }
           tc_fence_after();
-          if (lane == 0) {
-            if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
-            const uint64_t so = (uint64_t)(stage * H.stage_bytes) >> 4;
-            const uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
+          if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
+          const uint64_t so = (uint64_t)(stage * H.stage_bytes) >> 4;
+          const uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {  // phase 1: gate and up; phase 2: K pieces
-              if (PHASE == 2 && s == H.ns) break;
-              const int kk = PHASE == 1 ? kb : kb * H.ns + s;
-              // MMAs of this piece that hold data (an e2m1 K may end inside it; the zero-filled end
-              // of a bf16 K adds nothing)
-              const int left = red - kk * C::kBK;
-              const uint64_t ad = desc_a + so + s * (kTileBytes >> 4);
-              const uint64_t bd = desc_b + so + (PHASE == 1 ? 0 : s * (P.b_piece >> 4));
-              const uint32_t dd = PHASE == 1 ? d + s * H.ncols : d;
-              const uint32_t sfa = sf + s * C::kSub * 4;
-              const uint32_t sfb = sf + (PHASE == 1 ? C::kSub * 8 : (H.ns + s) * C::kSub * 4);
-              const bool fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
+          for (int s = 0; s < 2; ++s) {  // phase 1: gate and up; phase 2: K pieces
+            if (PHASE == 2 && s == H.ns) break;
+            const int kk = PHASE == 1 ? kb : kb * H.ns + s;
+            // MMAs of this piece that hold data (an e2m1 K may end inside it; the zero-filled end
+            // of a bf16 K adds nothing)
+            const int left = red - kk * C::kBK;
+            const uint64_t ad = desc_a + so + s * (kTileBytes >> 4);
+            const uint64_t bd = desc_b + so + (PHASE == 1 ? 0 : s * (P.b_piece >> 4));
+            const uint32_t dd = PHASE == 1 ? d + s * H.ncols : d;
+            const uint32_t sfa = sf + s * C::kSub * 4;
+            const uint32_t sfb = sf + (PHASE == 1 ? C::kSub * 8 : (H.ns + s) * C::kSub * 4);
+            const bool fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (j * C::kPerMma >= left) break;
-                const uint32_t accum = !(fresh && j == 0);
-                if (FMT == 0) {
-                  mma_f16(dd, ad + 2 * j, bd + 2 * j, idesc, accum);
-                } else if (FMT == kE4M3) {
-                  mma_mxf8(dd, ad + 2 * j, bd + 2 * j, idesc | idesc_sf_ids(j, j), sfa, sfb, accum);
-                } else {
-                  const uint32_t id = 2 * (j & 1);
-                  mma_mxf4(dd, ad + 2 * j, bd + 2 * j, idesc | idesc_sf_ids(id, id), sfa + 4 * (j >> 1),
-                           sfb + 4 * (j >> 1), accum);
-                }
-              }
+            for (int j = 0; j < 4; ++j) {
+              if (j * C::kPerMma >= left) break;
+              // the scale bytes of an MMA's K range: e4m3 block j of its atom, e2m1 a pair of blocks
+              const uint32_t id = FMT == kE4M3 ? j : 2 * (j & 1), at = FMT == kE2M1 ? 4 * (j >> 1) : 0;
+              mma_if<FMT>(one, dd, ad + 2 * j, bd + 2 * j, FMT == 0 ? idesc : idesc | idesc_sf_ids(id, id), sfa + at,
+                          sfb + at, !(fresh && j == 0));
             }
-            mma_commit(smem_u32(&empty[stage]));
           }
+          if (one) mma_commit(smem_u32(&empty[stage]));
           __syncwarp();
           advance();
         }
@@ -532,12 +610,15 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     }
   } else if (warp >= kLoadWarp0) {
     // ------------------------------------------------------------ the token operand
-    // Thread (r0, j) fetches 16-byte chunk j of rows r0, r0 + 8, ...: chunk j of row r goes to chunk
-    // j ^ (r % 8) of its 128 bytes (the 128-byte swizzle), so its places are 1024 bytes apart.
+    // Thread (r0, j) fetches 16-byte chunk j of rows r0, r0 + 16, ...: chunk j of row r goes to chunk
+    // j ^ (r % 8) of its 128 bytes (the 128-byte swizzle), so its places are kStep bytes apart.
     // Rows past n hold leftovers, which only reach accumulator columns that nobody reads.
-    const int tid = threadIdx.x - kLoadWarp0 * 32;
+    // Scales are fetched by the threads counted from the other end: with few tokens a warp has
+    // either kind.
+    constexpr int kRows = 4 * kLoadWarps, kStep = kRows * 128, kHeld = 4;
+    const int tid = threadIdx.x - kLoadWarp0 * 32, sid = 32 * kLoadWarps - 1 - tid;
     const int j = tid & 7, r0 = tid >> 3;
-    const uint32_t place = r0 * 128 + ((j ^ r0) << 4);
+    const uint32_t place = r0 * 128 + ((j ^ (r0 & 7)) << 4);
     const int64_t lo_off = FMT == 0 ? a.act_lo - a.act : 0;
     auto load = [&](auto ph, const Plan& P) {
       constexpr int PHASE = decltype(ph)::value;
@@ -550,9 +631,12 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         const uint32_t lo_place = (uint32_t)((n + 7) & ~7) * 128;
         auto row_of = [&](int r) -> int64_t { return PHASE == 1 ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
         // the first rows' sources stay in registers over the segment
-        const uint8_t* src0 = F.b + (r0 < n ? row_of(r0) : 0) * F.b_ld + j * 16;
-        const uint8_t* src1 = F.b + (r0 + 8 < n ? row_of(r0 + 8) : 0) * F.b_ld + j * 16;
-        const uint8_t* ssrc = C::kSub ? F.sb + (tid < n ? row_of(tid) : 0) * sb_ld : nullptr;
+        const uint8_t* src[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+          src[i] = F.b + (r0 + i * kRows < n ? row_of(r0 + i * kRows) : 0) * F.b_ld + j * 16;
+        const uint8_t* ssrc = C::kSub ? F.sb + (sid < n ? row_of(sid) : 0) * sb_ld : nullptr;
+        const uint32_t splace = (sid & 31) * 16 + (sid >> 5) * 4;  // row r's scales: word 4 (r % 32) + r / 32
         for (int kb = S.kb0; kb < S.kb1; ++kb) {
           if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           const uint32_t st = smem0 + stage * H.stage_bytes;
@@ -568,19 +652,19 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
               cp_async_16(to, from + go, size);
               if (PHASE == 2 && FMT == 0) cp_async_16(to + lo_place, from + lo_off + go, size);
             };
-            if (r0 < n) fetch(src0, dst);
-            if (r0 + 8 < n) fetch(src1, dst + 1024);
-            for (int r = r0 + 16; r < n; r += 8) fetch(F.b + row_of(r) * F.b_ld + j * 16, dst + (r - r0) * 128);
-            if (C::kSub) {
-              // row r's 4 scales of a 128-element atom: word 4 (r % 32) + r / 32
-              const uint32_t ssf = st + P.sf_off + (PHASE == 1 ? 2 * C::kSub : (H.ns + s) * C::kSub) * 512;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+              if (r0 + i * kRows >= n) break;
+              fetch(src[i], dst + i * kStep);
+            }
+            for (int i = kHeld; r0 + i * kRows < n; ++i)
+              fetch(F.b + row_of(r0 + i * kRows) * F.b_ld + j * 16, dst + i * kStep);
+            if (C::kSub && sid < n) {
+              const uint32_t ssf = st + P.sf_off + (PHASE == 1 ? 2 * C::kSub : (H.ns + s) * C::kSub) * 512 + splace;
 #pragma unroll
               for (int sub = 0; sub < C::kSub; ++sub) {
                 const int at = kk * C::kSub + sub;
-                if (at >= natom) break;
-                if (tid < n) cp_async_4(ssf + sub * 512 + (tid & 31) * 16 + (tid >> 5) * 4, ssrc + at * 4, 4u);
-                for (int r = tid + 32 * kLoadWarps; r < n; r += 32 * kLoadWarps)
-                  cp_async_4(ssf + sub * 512 + (r & 31) * 16 + (r >> 5) * 4, F.sb + row_of(r) * sb_ld + at * 4, 4u);
+                if (at < natom) cp_async_4(ssf + sub * 512, ssrc + at * 4, 4u);
               }
             }
           }
@@ -610,17 +694,17 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     uint32_t acc_phase = 0;
 
     // Arrive at a divided item after writing this CTA's partial sums; true in the last CTA.
+    // (The barriers order the warps' writes and reads around one thread's fences.)
     auto join = [&](unsigned* cnt, int c_first, int c_last) {
-      __threadfence();
       epi_sync();
       if (threadIdx.x == 64) {
         const unsigned last = (unsigned)(c_last - c_first);
+        __threadfence();
         *s_last = atomicInc(cnt + c_first, last) == last;  // wraps to 0: ready for the next launch
+        __threadfence();
       }
       epi_sync();
-      const bool mine = *s_last != 0;
-      if (mine) __threadfence();
-      return mine;
+      return *s_last != 0;
     };
     // Partial sums of an item: CTA c keeps those of an item that begins in its run (`begins`: it is the
     // first of the CTAs) apart from those of the item that its run enters in the middle.
@@ -641,6 +725,58 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       return true;
     };
 
+    // The activations of this thread's row for kBatch entries from r on, of which m exist: a batch is
+    // computed whole, so that its exponentials, maxima and conversions overlap.
+    auto finish = [&](int r, int m, int out_row, const float* g, const float* u) {
+      float v[kBatch];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        float gate = g[c], up = u[c];
+        if (a.limit > 0.0f) {  // NaN stays NaN
+          gate = gate > a.limit ? a.limit : gate;
+          up = up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up);
+        }
+        v[c] = silu_f(gate) * up;
+      }
+      const int64_t at = (int64_t)r * a.I + out_row;
+      if (FMT == 0) {
+        if (out_row >= a.I) return;
+        __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(a.act) + at;
+        __nv_bfloat16* act_lo = reinterpret_cast<__nv_bfloat16*>(a.act_lo) + at;
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
+          const __nv_bfloat16 hi = __float2bfloat16_rn(v[c]);
+          const float left = v[c] - __bfloat162float(hi);
+          if (c < m) {
+            act[(int64_t)c * a.I] = hi;
+            act_lo[(int64_t)c * a.I] = __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.0f);
+          }
+        }
+      } else {
+        // the warp's 32 rows are one MX block of each entry
+        uint32_t sc[kBatch];
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+          float mult;
+          const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(am, sc[c], mult);
+          v[c] = fin ? v[c] * mult : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const int64_t e = at + (int64_t)c * a.I;
+          if (FMT == kE4M3) {
+            if (c < m) a.act[e] = (uint8_t)cvt_e4m3x2(v[c], 0.0f);
+          } else {
+            const float y = __shfl_down_sync(0xffffffffu, v[c], 1);
+            if (c < m && (lane & 1) == 0) a.act[e >> 1] = (uint8_t)cvt_e2m1x2(v[c], y);
+          }
+          if (c < m && lane == 0) a.act_scales[e >> 5] = (uint8_t)sc[c];
+        }
+      }
+    };
+
     for (int p = plan1.p0; p < plan1.p1;) {
       const Seg S = seg_at<1>(plan1, p);
       const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
@@ -658,9 +794,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
           tmem_ld16(tb + H.ncols + c0, u);
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= n) break;
-            mine[(c0 + c) * 256 + row] = g[c];
-            mine[(c0 + c) * 256 + 128 + row] = u[c];
+            if (c0 + c < n) {
+              mine[(c0 + c) * 256 + row] = g[c];
+              mine[(c0 + c) * 256 + 128 + row] = u[c];
+            }
           }
         }
         release();
@@ -681,46 +818,17 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
               const float* o = part_of(x, x == c_first, 256) + c0 * 256 + row;
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                if (c0 + c >= n) break;
-                g[c] += __ldcg(o + c * 256);
-                u[c] += __ldcg(o + c * 256 + 128);
+                if (c0 + c < n) {
+                  g[c] += __ldcg(o + c * 256);
+                  u[c] += __ldcg(o + c * 256 + 128);
+                }
               }
             }
           }
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= n) break;
-            float gate = g[c], up = u[c];
-            if (a.limit > 0.0f) {  // NaN stays NaN
-              gate = gate > a.limit ? a.limit : gate;
-              up = up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up);
-            }
-            const float v = silu_f(gate) * up;
-            const int64_t r = off + c0 + c;
-            if (FMT == 0) {
-              if (out_row < a.I) {
-                // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
-                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                const float left = v - __bfloat162float(hi);
-                reinterpret_cast<__nv_bfloat16*>(a.act)[r * a.I + out_row] = hi;
-                reinterpret_cast<__nv_bfloat16*>(a.act_lo)[r * a.I + out_row] =
-                    __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.0f);
-              }
-            } else {
-              // the warp's 32 rows are one MX block of this entry
-              const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
-              uint32_t sc;
-              float mult;
-              const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(am, sc, mult);
-              const float x = fin ? v * mult : 0.0f;
-              if (FMT == kE4M3) {
-                a.act[r * a.I + out_row] = (uint8_t)cvt_e4m3x2(x, 0.0f);
-              } else {
-                const float y = __shfl_down_sync(0xffffffffu, x, 1);
-                if ((lane & 1) == 0) a.act[(r * a.I + out_row) >> 1] = (uint8_t)cvt_e2m1x2(x, y);
-              }
-              if (lane == 0) a.act_scales[(r * a.I + out_row) >> 5] = (uint8_t)sc;
-            }
+          for (int b = 0; b < 16; b += kBatch) {
+            if (c0 + b >= n) break;
+            finish(off + c0 + b, min(kBatch, n - c0 - b), out_row, &g[b], &u[b]);
           }
         }
       }
@@ -728,9 +836,11 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       p += S.kb1 - S.kb0;
     }
     // this CTA's part of A is written (or it has given up, which the others must not wait for)
-    __threadfence();
     epi_sync();
-    if (threadIdx.x == 64) atomicAdd(a.done, 1u);
+    if (threadIdx.x == 64) {
+      __threadfence();
+      atomicAdd(a.done, 1u);
+    }
 
     for (int p = plan2.p0; p < plan2.p1 && !aborted;) {
       const Seg S = seg_at<2>(plan2, p);
@@ -752,9 +862,19 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
           for (int c = 0; c < 16; ++c) v[c] += left[c];
         }
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (c0 + c >= n) break;
-          s_acc[s_tok[off + c0 + c] * 128 + row] += s_w[off + c0 + c] * v[c];
+        for (int b = 0; b < 16; b += kBatch) {
+          if (c0 + b >= n) break;
+          float* at[kBatch];  // an expert's tokens differ, so a batch's sums are apart
+          float sum[kBatch];
+#pragma unroll
+          for (int c = 0; c < kBatch; ++c) {
+            const int r = off + min(c0 + b + c, n - 1);
+            at[c] = s_acc + s_tok[r] * 128 + row;
+            sum[c] = *at[c] + s_w[r] * v[b + c];
+          }
+#pragma unroll
+          for (int c = 0; c < kBatch; ++c)
+            if (c0 + b + c < n) *at[c] = sum[c];
         }
       }
       release();
