@@ -12,11 +12,11 @@
 // up to 16), so a tile is multiplied as it lands in shared memory and no weight passes through a
 // register.  The stages of all tiles of a phase form one sequence that is cut into equal runs,
 // one per CTA, so every SM reads the same number of bytes whatever the routing; a tile that a cut
-// divides is put together from fp32 partial sums by the last of its CTAs to arrive, in CTA order
-// (the result does not depend on which one that is).
+// divides is put together from fp32 partial sums by the CTA that begins it, in CTA order (a
+// cooperative launch: every CTA is resident, and none waits before its own sums are out).
 //
-// Between the phases only the warps that fetch A wait for the other CTAs (a cooperative launch
-// makes all of them resident); the weight loads run on into phase 2 and keep the ring full.
+// Between the phases only the warps that fetch A wait for the other CTAs; the weight loads run on
+// into phase 2 and keep the ring full.
 //
 // Every CTA builds the batch's expert list by itself from the ids: a bit per (expert, token), so
 // an expert named twice by a token is computed once and its weights are added up.
@@ -31,10 +31,11 @@ namespace pgg {
 namespace {
 
 constexpr int kMaxT = PGG_MOE_DECODE_MAX_T;
-constexpr int kMaxCtas = 192;   // CTAs of a launch (one per SM); sizes the workspace without a device
+constexpr int kMaxCtas = 160;   // CTAs of a launch (one per SM); sizes the workspace without a device
 constexpr int kMaxStages = 8;
 constexpr int kLoadWarps = 4;   // warps that fetch the token operand
 constexpr int kBatch = 4;      // tokens that the epilogue works on at a time
+constexpr int kFixedBytes = 768;  // barriers, plans
 constexpr int kTileBytes = 128 * 128;  // 128 rows x one 128-byte swizzle atom of K
 
 template <int FMT>
@@ -46,10 +47,13 @@ struct DecCfg {
   static constexpr int kThreads = 32 * (6 + kCopier + kLoadWarps);
 };
 
-// One matrix of a layer and what the MMAs of its phase read and write.
+// One matrix of a layer and what its phase reads.  Both matrices are seen as [E][halves][rows][red]
+// (W1: gate and up halves; W2: one), so that the two phases run the same code.
 struct DecodePhase {
-  int rows;            // output rows per expert: I (phase 1), H (phase 2)
+  int rows;            // output rows of a half: I (phase 1), H (phase 2)
+  int halves;          // 2 (phase 1), 1 (phase 2)
   int red;             // reduction length: H (phase 1), I (phase 2)
+  int tiles, pieces;   // 128-row tiles of `rows`, 128-byte pieces of `red`
   const uint8_t* b;    // token operand, row-major: X (phase 1) or A (phase 2)
   int64_t b_ld;        // bytes of a row
   const uint8_t* sb;   // its scales, row-major, red / 32 bytes a row
@@ -66,28 +70,48 @@ struct DecodeArgs {
   uint8_t* act_lo;      // bf16: what the rounding to the high part left over
   uint8_t* act_scales;  // MX: row-major scales
   __nv_bfloat16* out;   // [T, H]
-  float* part;          // partial sums: 2 tiles per CTA
-  unsigned* cnt;        // arrivals at a divided tile by its first CTA, for each phase
-  unsigned* done;       // CTAs that have finished phase 1; [1]: that have left.  All zero between launches
+  float* part[2];       // per phase and CTA: a tile of partial sums, zero between launches
+  unsigned* done;       // CTAs that have finished phase 1; [1]: that have left.  Zero between launches
   int ring_bytes;       // shared memory for the stages
   int slots_cap;        // most experts that the batch can name
   int32_t* err;
 };
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&f)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&f)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
   tmem_ld_wait();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Adds v to four columns.
+__device__ __forceinline__ void tmem_add4(uint32_t taddr, const float4& v) {
+  float f[4];
+  tmem_ld4(taddr, f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "r"(__float_as_uint(f[0] + v.x)), "r"(__float_as_uint(f[1] + v.y)), "r"(__float_as_uint(f[2] + v.z)),
+               "r"(__float_as_uint(f[3] + v.w))
+               : "memory");
+}
+// 16- and 4-byte asynchronous copies to shared memory, executed where `go` is set (src_bytes 0: zeros).
+__device__ __forceinline__ void cp_async_16_if(uint32_t go, uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "@q cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+      "l"(src), "r"(src_bytes), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async_4_if(uint32_t go, uint32_t dst, const void* src) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst),
+      "l"(src), "r"(go)
+      : "memory");
 }
 // The MMAs of one lane (`go`), issued by a whole converged warp: with the branch on the lane inside
 // the instruction's own predicate, descriptors stay warp-uniform values.
@@ -119,17 +143,51 @@ __device__ __forceinline__ void mma_if(uint32_t go, uint32_t d, uint64_t ad, uin
         "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(go)
         : "memory");
 }
-// Barrier of the four epilogue warps that tells each whether `ok` held in all of them: they give
-// up together, so that none is left at a later barrier.
+template <int FMT>
+__device__ __forceinline__ void copy_atom_if(uint32_t go, uint32_t taddr, uint64_t sdesc) {
+  if (FMT != 0)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(sdesc), "r"(go)
+        : "memory");
+}
+// Warp 0 has laid out the work (`start_arrive`); the other roles wait for that before their first
+// stage (`start_wait`).  N: the block's threads.
+template <int N>
+__device__ __forceinline__ void start_arrive() { asm volatile("barrier.cta.arrive 3, %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void start_wait() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(N) : "memory"); }
+
+// Partial sums travel without flags or fences: a word that is not zero is a sum.  (A release under a
+// full load of weight reads took 2 to 5 us on this path.)  A zero sum is sent as -0, which adds the
+// same; the reader puts the zero back.
+__device__ __forceinline__ float sent(float v) { return __float_as_uint(v) == 0u ? __uint_as_float(0x80000000u) : v; }
+__device__ __forceinline__ float4 load_relaxed4(const float4* p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_relaxed4(float4* p, float4 v) {
+  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+// Barrier `ID` of 128 threads (the epilogue warps, the token-loading warps) that tells each whether
+// `ok` held in all of them: they give up together, so that none is left at a later barrier.
+template <int ID = 1>
 __device__ __forceinline__ bool epi_all(bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok)
+      : "r"((uint32_t)ok), "n"(ID)
       : "memory");
   return r != 0;
 }
@@ -140,28 +198,43 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
   return v;
 }
 
-// What both phases share of a launch's cut: the shape of a ring stage and of tensor memory.
-struct Shape {
+__device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// How a launch cuts up its work: computed by one warp of each CTA (the same in all of them).
+struct Shape {  // what both phases share: the ring's stages and tensor memory
   int n_act;    // experts that the batch names
   int ncols;    // most tokens of one of them, rounded up to 16
-  int ns;       // phase 2: 128-byte K pieces per stage
+  int ns;       // phase 2: K pieces per stage
   int stages, stage_bytes;
-  int acc_cols, nacc, sf_col0, sf_per;  // tensor memory
+  int acc_cols, nacc, sf_col0, sf_per;
 };
-// One phase's stages, cut into equal runs; every CTA computes the same.
-struct Plan {
-  int tiles;      // 128-row output tiles per expert
-  int nk;         // stages of one (expert, tile)
-  int L;          // stages of one item: an (expert, tile) in phase 1, an output tile in phase 2
-  int total;      // stages of the phase
-  int quot, rem;  // total = ctas quot + rem: the first rem CTAs get a stage more
+struct Plan {  // one phase
+  int np;       // weight pieces of a stage: gate and up (phase 1), ns K pieces (phase 2)
+  int nb;       // token pieces of a stage
+  int nk;       // stages of one (expert, tile)
+  int L;        // stages of one item: an (expert, tile) in phase 1, an output tile in phase 2
+  int quot, rem;  // total stages = ctas quot + rem: the first rem CTAs get a stage more
   int b_off, b_piece, sf_off;  // layout of a stage: weights, token pieces, scale atoms
-  int p0, p1;     // this CTA's run
-  __device__ __forceinline__ int start(int c) const { return c * quot + min(c, rem); }
+  int p, p1;    // this CTA's run of stages, and where it starts:
+  int slot, tile, kb;
   // the CTA that stage p belongs to
   __device__ __forceinline__ int owner(int p) const {
     const int big = rem * (quot + 1);
     return p < big ? p / (quot + 1) : rem + (p - big) / quot;
+  }
+  // The stages of the run's next segment: those of one (expert, tile).
+  __device__ __forceinline__ int length() const { return min(nk - kb, p1 - p); }
+  __device__ __forceinline__ void step(int phase, int tiles, int n_act) {
+    p += length();
+    kb = 0;
+    if (phase == 0) {
+      if (++tile == tiles) { tile = 0; ++slot; }
+    } else if (++slot == n_act) {
+      slot = 0;
+      ++tile;
+    }
   }
 };
 
@@ -173,9 +246,8 @@ __device__ __forceinline__ int cols2(int n) {
 }
 
 template <int FMT>
-__device__ __forceinline__ Shape make_shape(const DecodeArgs& a, int n_act, int max_n) {
+__device__ __forceinline__ void make_plan(const DecodeArgs& a, int n_act, int max_n, int ph, Shape& S, Plan& P) {
   using C = DecCfg<FMT>;
-  Shape S;
   S.n_act = n_act;
   S.ncols = (max_n + 15) & ~15;
   const int b1 = S.ncols * 128, b2 = cols2<FMT>(max_n) * 128;
@@ -190,61 +262,26 @@ __device__ __forceinline__ Shape make_shape(const DecodeArgs& a, int n_act, int 
   S.sf_per = C::kSub * max(12, S.ns * 8);
   S.nacc = 2 * S.acc_cols + S.stages * S.sf_per <= 512 ? 2 : 1;
   S.sf_col0 = S.nacc * S.acc_cols;
-  return S;
+
+  const int pieces = a.ph[ph].pieces, tiles = a.ph[ph].tiles;
+  P.np = ph == 0 ? 2 : S.ns;
+  P.nb = ph == 0 ? 1 : S.ns;
+  P.nk = P.nb == 2 ? (pieces + 1) >> 1 : pieces;
+  P.b_off = P.np * kTileBytes;
+  P.b_piece = ph == 0 ? b1 : b2;
+  P.sf_off = P.b_off + P.nb * P.b_piece;
+  P.L = ph == 0 ? P.nk : n_act * P.nk;
+  const int total = n_act * tiles * P.nk, ctas = max(1, min((int)gridDim.x, total)), cta = blockIdx.x;
+  P.quot = total / ctas;
+  P.rem = total - ctas * P.quot;
+  P.p = cta < ctas ? cta * P.quot + min(cta, P.rem) : 0;
+  P.p1 = cta < ctas ? P.p + P.quot + (cta < P.rem) : 0;
+  if (total == 0) return;
+  const int item = P.p / P.L, q = P.p - item * P.L;
+  P.slot = (ph == 0 ? item : q) / (ph == 0 ? tiles : P.nk);
+  P.tile = ph == 0 ? item - P.slot * tiles : item;
+  P.kb = ph == 0 ? q : q - P.slot * P.nk;
 }
-
-template <int FMT, int PHASE>
-__device__ __forceinline__ Plan make_plan(const DecodeArgs& a, const Shape& S, int max_n) {
-  using C = DecCfg<FMT>;
-  Plan P;
-  const int kb = (a.ph[PHASE - 1].red + C::kBK - 1) / C::kBK;
-  P.tiles = (a.ph[PHASE - 1].rows + 127) / 128;
-  if (PHASE == 1) {
-    P.nk = kb;
-    P.b_off = 2 * kTileBytes;
-    P.b_piece = S.ncols * 128;
-    P.sf_off = P.b_off + P.b_piece;
-  } else {
-    P.nk = S.ns == 2 ? (kb + 1) >> 1 : kb;
-    P.b_off = S.ns * kTileBytes;
-    P.b_piece = cols2<FMT>(max_n) * 128;
-    P.sf_off = P.b_off + S.ns * P.b_piece;
-  }
-  P.L = PHASE == 1 ? P.nk : S.n_act * P.nk;
-  P.total = S.n_act * P.tiles * P.nk;
-  const int ctas = max(1, min((int)gridDim.x, P.total)), cta = blockIdx.x;
-  P.quot = P.total / ctas;
-  P.rem = P.total - ctas * P.quot;
-  P.p0 = cta < ctas ? P.start(cta) : 0;
-  P.p1 = cta < ctas ? P.start(cta + 1) : 0;
-  return P;
-}
-
-// A run of stages [kb0, kb1) of one (expert slot, tile); `item` is what partial sums are joined by.
-struct Seg {
-  int slot, tile, item, kb0, kb1;
-};
-
-template <int PHASE>
-__device__ __forceinline__ Seg seg_at(const Plan& P, int p) {
-  Seg s;
-  s.item = p / P.L;
-  const int q = p - s.item * P.L;
-  if (PHASE == 1) {
-    s.slot = s.item / P.tiles;
-    s.tile = s.item - s.slot * P.tiles;
-    s.kb0 = q;
-  } else {
-    s.tile = s.item;
-    s.slot = q / P.nk;
-    s.kb0 = q - s.slot * P.nk;
-  }
-  s.kb1 = min(P.nk, s.kb0 + (P.p1 - p));
-  return s;
-}
-
-using Phase1 = std::integral_constant<int, 1>;
-using Phase2 = std::integral_constant<int, 2>;
 
 template <int FMT>
 __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
@@ -266,9 +303,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   uint64_t* cdrain = drain + 1;
   volatile WaitCtl* s_ctl = reinterpret_cast<volatile WaitCtl*>(cdrain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<WaitCtl*>(s_ctl) + 1);
-  int* s_last = reinterpret_cast<int*>(s_tmem + 1);
-  int* s_scan = s_last + 1;  // [2 * 16]
-  float* s_acc = reinterpret_cast<float*>(smem + a.ring_bytes + 512);  // phase 2: [T][128]
+  int* s_scan = reinterpret_cast<int*>(s_tmem + 1);  // [2 * 16]
+  Shape* s_shape = reinterpret_cast<Shape*>(s_scan + 32);
+  Plan* s_plan = reinterpret_cast<Plan*>(s_shape + 1);  // [2]
+  float* s_acc = reinterpret_cast<float*>(smem + a.ring_bytes + kFixedBytes);  // phase 2: [T][128]
   float* s_w = s_acc + a.T * 128;                                       // [T k]
   uint16_t* s_off = reinterpret_cast<uint16_t*>(s_w + a.T * a.k);       // [slots + 1]: an expert's first entry
   uint16_t* s_exp = s_off + a.slots_cap + 1;                            // [slots]
@@ -283,23 +321,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   int16_t* s_id = reinterpret_cast<int16_t*>(s_wid + a.T * a.k);      // [T k]: the ids, -1 out of range
   uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_id + a.T * a.k);   // [E]: first entry
   const int n_ids = a.T * a.k;
-  // Up to 32 ids: every warp works the list out in registers (lane i has id i) and all of them write
-  // the same; the slots are in the order of first mention.  Saves three block barriers and the scan
-  // over the experts (a third of the time before the first load, which a one-token call feels).
+  // Up to 32 ids: warp 0 works the list out in registers (lane i has id i), with the slots in the order
+  // of first mention, and starts loading weights while the other warps are still coming up.
   const bool few = n_ids <= 32;
-  int id = -1, tok = 0;
-  float wid = 0.0f;
-  if (few) {
-    if (lane < n_ids) {
-      id = __ldg(a.ids + lane);
-      wid = a.w ? __ldg(a.w + lane) : 1.0f;
-      tok = lane / a.k;
-      if (id < 0 || id >= a.E) {
-        if (blockIdx.x == 0) set_error(a.err, kErrBadExpert);
-        id = -1;
-      }
-    }
-  } else {
+  if (!few) {
     for (int i = threadIdx.x; i < n_ids; i += kNT) {
       const int e = __ldg(a.ids + i);
       const bool ok = e >= 0 && e < a.E;
@@ -331,8 +356,19 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
-  int n_act, max_n;
-  if (few) {
+  int n_act = 0, max_n = 0;
+  if (few && warp == 0) {
+    int id = -1, tok = 0;
+    float wid = 0.0f;
+    if (lane < n_ids) {
+      id = __ldg(a.ids + lane);
+      wid = a.w ? __ldg(a.w + lane) : 1.0f;
+      tok = lane / a.k;
+      if (id < 0 || id >= a.E) {
+        if (blockIdx.x == 0) set_error(a.err, kErrBadExpert);
+        id = -1;
+      }
+    }
     const unsigned all = 0xffffffffu, below = (1u << lane) - 1u;
     const unsigned same = __match_any_sync(all, id), pair = __match_any_sync(all, id * kMaxT + tok);
     const bool entry = id >= 0 && (pair & below) == 0;  // the token's first choice of this expert
@@ -365,7 +401,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       s_tok[r] = (uint8_t)tok;
       s_w[r] = wt;
     }
-  } else {
+  } else if (!few) {
     __syncthreads();
     for (int i = threadIdx.x; i < n_ids; i += kNT) {
       const int t = i / a.k;
@@ -431,76 +467,98 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       s_w[r] = wt;
     }
   }
-  fence_proxy_async_smem();  // the ring's scratch use, before its first bulk copies
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  if (!few) {
+    fence_proxy_async_smem();  // the ring's scratch use, before its first bulk copies
+    __syncthreads();
+  }
+  if (warp == 0) {
+    if (lane < 2) {
+      Shape S;
+      Plan P{};
+      make_plan<FMT>(a, n_act, max_n, lane, S, P);
+      s_plan[lane] = P;
+      if (lane == 0) *s_shape = S;
+    }
+    __syncwarp();
+  }
 
-  const Shape H = make_shape<FMT>(a, n_act, max_n);
-  const Plan plan1 = make_plan<FMT, 1>(a, H, max_n), plan2 = make_plan<FMT, 2>(a, H, max_n);
   const int cta = blockIdx.x;
-  const uint32_t tmem_base = *s_tmem;
   const uint32_t smem0 = smem_u32(smem);
   bool aborted = false;
   int stage = 0;
   uint32_t phase = 0;
+
+  // The other roles first pass once over their loops without effect (`dry`), with a plan of one
+  // stage: that brings their code into the instruction cache while the memory is idle.  Fetched
+  // through a memory system that is full of weight loads, the MMA warp's first stage alone took
+  // 5600 cycles, and the epilogue's first tile about as many.
+  Shape H{};
+  H.n_act = H.stages = H.ns = H.nacc = 1;
+  uint32_t tmem_base = 0;
   auto advance = [&]() {
     if (++stage == H.stages) { stage = 0; phase ^= 1u; }
   };
+  Plan one_stage{};
+  one_stage.np = 2;
+  one_stage.nb = one_stage.nk = one_stage.L = one_stage.quot = one_stage.p1 = 1;
+  auto plan_of = [&](int ph, bool dry) { return dry ? one_stage : s_plan[ph]; };
 
-  if (n_act == 0) {  // no expert is named: the layer's output is zero
-    for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.ph[1].rows; i += (int64_t)gridDim.x * kNT)
-      a.out[i] = __float2bfloat16_rn(0.0f);
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+  const bool dry = pass == 0;
+  if (!dry) {
+    tc_fence_before();
+    if (warp == 0) start_arrive<kNT>();
+    else start_wait<kNT>();
+    tc_fence_after();
+    H = *s_shape;
+    tmem_base = *s_tmem;
+    if (H.n_act == 0)  // no expert is named: the layer's output is zero
+      for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.ph[1].rows;
+           i += (int64_t)gridDim.x * kNT)
+        a.out[i] = __float2bfloat16_rn(0.0f);
+  } else if (warp == 0) {
+    continue;
   }
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights: TMA tiles, bulk scale atoms
     // The producer runs into phase 2 without waiting: its weights do not depend on phase 1.
     long long issued = 0;
-    auto produce = [&](auto ph, const Plan& P) {
-      constexpr int PHASE = decltype(ph)::value;
-      const DecodePhase& F = a.ph[PHASE - 1];
+#pragma unroll 1
+    for (int ph = 0; ph < 2; ++ph) {
+      const DecodePhase& F = a.ph[ph];
+      const CUtensorMap* map = ph == 0 ? &tmW1 : &tmW2;
       const int natom = F.red >> 7;  // MX: scale atoms of a 128-row block along K
-      for (int p = P.p0; p < P.p1 && !aborted;) {
-        const Seg S = seg_at<PHASE>(P, p);
-        const int e = s_exp[S.slot], row0 = S.tile * 128;
-        for (int kb = S.kb0; kb < S.kb1; ++kb) {
+      for (Plan P = s_plan[ph]; P.p < P.p1 && !aborted; P.step(ph, F.tiles, H.n_act)) {
+        const int e = s_exp[P.slot], row0 = P.tile * 128;
+        for (int kb = P.kb, end = P.kb + P.length(); kb < end; ++kb) {
           if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           if (lane == 0) {
             const uint32_t fb = smem_u32(&full[stage]);
             const uint32_t st = smem0 + stage * H.stage_bytes;
-            if (PHASE == 1) {
-              const int at0 = kb * C::kSub, nat = C::kSub ? min(C::kSub, natom - at0) : 0;
-              mbar_arrive_expect_tx(fb, 2 * kTileBytes + 2 * 512 * nat);
-              const int x = kb * (FMT == 0 ? 64 : 128);
-              tma_load_4d(st, &tmW1, fb, x, row0, 0, e);
-              tma_load_4d(st + kTileBytes, &tmW1, fb, x, row0, 1, e);
+            const int kk0 = kb * P.nb;
+            // K pieces that exist, and (MX) their scale atoms
+            const int n = P.nb == 2 && kk0 + 1 < F.pieces ? 2 : 1, nt = ph == 0 ? 2 : n;
+            const int nat = C::kSub ? min(C::kSub * n, natom - kk0 * C::kSub) * F.halves : 0;
+            mbar_arrive_expect_tx(fb, nt * kTileBytes + 512 * nat);
+#pragma unroll 1
+            for (int s = 0; s < nt; ++s) {
+              const int half = ph == 0 ? s : 0, kk = ph == 0 ? kk0 : kk0 + s;
+              tma_load_4d(st + s * kTileBytes, map, fb, kk * (FMT == 0 ? 64 : 128), row0, half, e);
               if (C::kSub) {
-                const int64_t rg = ((int64_t)e * 2 * a.I + row0) >> 7, ru = ((int64_t)e * 2 * a.I + a.I + row0) >> 7;
-                bulk_load(st + P.sf_off, F.sa + (rg * natom + at0) * 512, 512 * nat, fb);
-                bulk_load(st + P.sf_off + C::kSub * 512, F.sa + (ru * natom + at0) * 512, 512 * nat, fb);
+                const int64_t rb = (((int64_t)e * F.halves + half) * F.rows + row0) >> 7;
+                bulk_load(st + P.sf_off + s * C::kSub * 512, F.sa + (rb * natom + kk * C::kSub) * 512,
+                          512 * min(C::kSub, natom - kk * C::kSub), fb);
               }
-            } else {
-              const int kk0 = kb * H.ns, at0 = kk0 * C::kSub, nat = C::kSub ? min(H.ns * C::kSub, natom - at0) : 0;
-              const bool second = H.ns == 2 && (kk0 + 1) * C::kBK < F.red;
-              mbar_arrive_expect_tx(fb, (second ? 2 : 1) * kTileBytes + 512 * nat);
-              const int x = kk0 * (FMT == 0 ? 64 : 128);
-              tma_load_3d(st, &tmW2, fb, x, row0, e);
-              if (second) tma_load_3d(st + kTileBytes, &tmW2, fb, x + (FMT == 0 ? 64 : 128), row0, e);
-              if (C::kSub)
-                bulk_load(st + P.sf_off, F.sa + ((((int64_t)e * F.rows + row0) >> 7) * natom + at0) * 512, 512 * nat,
-                          fb);
             }
           }
           __syncwarp();
           ++issued;
           advance();
         }
-        p += S.kb1 - S.kb0;
       }
-    };
-    produce(Phase1(), plan1);
-    produce(Phase2(), plan2);
+    }
     if (aborted && lane == 0) {
       // drain: the copies in flight land before the CTA's shared memory goes away.  Their full
       // barriers may lack the token loaders' arrivals, so this may run to its own limit.
@@ -514,96 +572,112 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     int acc = 0;
     uint32_t acc_phase = 0;
-    auto multiply = [&](auto ph, const Plan& P) {
-      constexpr int PHASE = decltype(ph)::value;
-      const int red = a.ph[PHASE - 1].red;
-      const uint32_t one = lane == 0;
+#pragma unroll 1
+    for (int ph = 0; ph < (dry ? 1 : 2); ++ph) {
+      const int red = a.ph[ph].red;
+      Plan P = plan_of(ph, dry);
       // descriptors of stage 0's tiles; an address d bytes further on adds d / 16
       const uint64_t desc_a = smem_desc(smem0, 16, 1024, kSwizzle128B);
       const uint64_t desc_b = smem_desc(smem0 + P.b_off, 16, 1024, kSwizzle128B);
-      for (int p = P.p0; p < P.p1 && !aborted;) {
-        const Seg S = seg_at<PHASE>(P, p);
-        const int n = s_off[S.slot + 1] - s_off[S.slot];
-        const uint32_t N = PHASE == 1 ? (n + 15) & ~15 : cols2<FMT>(n);
+      // from a stage's first piece to its second: phase 1 has the up half's accumulator and the same
+      // tokens, phase 2 the same accumulator and the next K piece's tokens
+      const uint32_t d_step = ph == 0 ? H.ncols : 0, b_step = ph == 0 ? 0 : P.b_piece >> 4;
+      const uint32_t sfb0 = P.np * C::kSub * 4, sfb_step = ph == 0 ? 0 : C::kSub * 4;
+      while (P.p < P.p1 && !aborted) {
+        const int n = dry ? 1 : s_off[P.slot + 1] - s_off[P.slot];
+        const uint32_t N = ph == 0 ? (n + 15) & ~15 : cols2<FMT>(n);
         const uint32_t idesc = FMT == 0 ? idesc_bf16(128, N, false, false) : idesc_mx(FMT == kE4M3 ? 0 : 1, 128, N);
-        if (!warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
+        if (!dry && !warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * H.acc_cols;
-        for (int kb = S.kb0; kb < S.kb1; ++kb) {
-          if (!warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) { aborted = true; break; }
+        const int end = P.kb + P.length();
+        for (int kb = P.kb; kb < end; ++kb) {
+          if (!dry && !warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) {
+            aborted = true;
+            break;
+          }
           tc_fence_after();
           if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
+          const uint32_t one = lane == 0 && !dry;
           const uint64_t so = (uint64_t)(stage * H.stage_bytes) >> 4;
-          const uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {  // phase 1: gate and up; phase 2: K pieces
-            if (PHASE == 2 && s == H.ns) break;
-            const int kk = PHASE == 1 ? kb : kb * H.ns + s;
-            // MMAs of this piece that hold data (an e2m1 K may end inside it; the zero-filled end
-            // of a bf16 K adds nothing)
-            const int left = red - kk * C::kBK;
-            const uint64_t ad = desc_a + so + s * (kTileBytes >> 4);
-            const uint64_t bd = desc_b + so + (PHASE == 1 ? 0 : s * (P.b_piece >> 4));
-            const uint32_t dd = PHASE == 1 ? d + s * H.ncols : d;
-            const uint32_t sfa = sf + s * C::kSub * 4;
-            const uint32_t sfb = sf + (PHASE == 1 ? C::kSub * 8 : (H.ns + s) * C::kSub * 4);
-            const bool fresh = kb == S.kb0 && (PHASE == 1 || s == 0);
+          uint64_t ad = desc_a + so, bd = desc_b + so;
+          uint32_t dd = d, sfa = tmem_base + H.sf_col0 + stage * H.sf_per, sfb = sfa + sfb0;
+          // reduction elements left from this piece on: MMAs past them (an e2m1 K may end inside a
+          // piece) and pieces past them are skipped; the zero-filled end of a bf16 K adds nothing
+          int left = red - kb * P.nb * C::kBK;
+          uint32_t accum = kb > P.kb;
+#pragma unroll 1
+          for (int s = 0; s < P.np; ++s) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               if (j * C::kPerMma >= left) break;
               // the scale bytes of an MMA's K range: e4m3 block j of its atom, e2m1 a pair of blocks
               const uint32_t id = FMT == kE4M3 ? j : 2 * (j & 1), at = FMT == kE2M1 ? 4 * (j >> 1) : 0;
               mma_if<FMT>(one, dd, ad + 2 * j, bd + 2 * j, FMT == 0 ? idesc : idesc | idesc_sf_ids(id, id), sfa + at,
-                          sfb + at, !(fresh && j == 0));
+                          sfb + at, j == 0 ? accum : 1u);
+            }
+            ad += kTileBytes >> 4;
+            bd += b_step;
+            dd += d_step;
+            sfa += C::kSub * 4;
+            sfb += sfb_step;
+            if (ph != 0) {
+              left -= C::kBK;
+              accum = 1;
             }
           }
+          if (dry) break;
           if (one) mma_commit(smem_u32(&empty[stage]));
           __syncwarp();
           advance();
         }
-        if (aborted) break;
+        if (aborted || dry) break;
         if (lane == 0) mma_commit(smem_u32(&tfull[acc]));
         __syncwarp();
         if (++acc == H.nacc) { acc = 0; acc_phase ^= 1u; }
-        p += S.kb1 - S.kb0;
+        P.step(ph, a.ph[ph].tiles, H.n_act);
       }
-    };
-    multiply(Phase1(), plan1);
-    multiply(Phase2(), plan2);
+    }
     if (aborted && lane == 0) {
       mma_commit(smem_u32(drain));
       mbar_wait_drain(smem_u32(drain), 0);
     }
   } else if (C::kCopier && warp == 6) {
     // ------------------------------------------------------------ scale copier: a stage's atoms -> tensor memory
-    auto copy = [&](auto ph, const Plan& P) {
-      constexpr int PHASE = decltype(ph)::value;
-      const int natom = a.ph[PHASE - 1].red >> 7;
-      // groups of atoms: phase 1 gate, up, tokens; phase 2 weights, tokens
-      const int per = PHASE == 1 ? C::kSub : H.ns * C::kSub;
+#pragma unroll 1
+    for (int ph = 0; ph < (dry ? 1 : 2); ++ph) {
+      const int natom = a.ph[ph].red >> 7;
+      Plan P = plan_of(ph, dry);
       const uint64_t ds0 = smem_desc(smem0 + P.sf_off, 0, 128, kSwizzleNone);
-      for (int p = P.p0; p < P.p1 && !aborted;) {
-        const Seg S = seg_at<PHASE>(P, p);
-        for (int kb = S.kb0; kb < S.kb1; ++kb) {
-          if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+      while (P.p < P.p1 && !aborted) {
+        const int end = P.kb + P.length();
+        for (int kb = P.kb; kb < end; ++kb) {
+          if (!dry && !warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
           tc_fence_after();
-          if (lane == 0) {
-            fence_proxy_async_smem();  // the token operand's and its scales' cp.async writes
-            const uint64_t ds = ds0 + ((uint64_t)(stage * H.stage_bytes) >> 4);
-            const uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
-            const int nat = min(per, natom - kb * per);
-            for (int g = 0; g < (PHASE == 1 ? 3 : 2); ++g)
-              for (int i = 0; i < nat; ++i) tmem_cp_32x128b_x4(sf + 4 * (g * per + i), ds + (((g * per + i) * 512) >> 4));
-            mma_commit(smem_u32(&sfull[stage]));
+          fence_proxy_async_smem();  // the token operand's and its scales' cp.async writes
+          const uint32_t one = lane == 0 && !dry;
+          uint64_t ds = ds0 + ((uint64_t)(stage * H.stage_bytes) >> 4);
+          uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
+          // the weight pieces' atoms, then the token pieces'; those past the end of K are skipped
+          const int at0 = kb * P.nb * C::kSub;
+#pragma unroll 1
+          for (int s = 0; s < P.np + P.nb; ++s) {
+            const int at = at0 + (ph == 0 ? 0 : (s & (P.nb - 1)) * C::kSub);
+#pragma unroll
+            for (int i = 0; i < C::kSub; ++i)
+              copy_atom_if<FMT>(one && at + i < natom, sf + 4 * i, ds + (i * 512 >> 4));
+            ds += C::kSub * 512 >> 4;
+            sf += C::kSub * 4;
           }
+          if (dry) break;
+          if (one) mma_commit(smem_u32(&sfull[stage]));
           __syncwarp();
           advance();
         }
-        p += S.kb1 - S.kb0;
+        if (aborted || dry) break;
+        P.step(ph, a.ph[ph].tiles, H.n_act);
       }
-    };
-    copy(Phase1(), plan1);
-    copy(Phase2(), plan2);
+    }
     if (aborted && lane == 0) {
       mma_commit(smem_u32(cdrain));
       mbar_wait_drain(smem_u32(cdrain), 0);
@@ -619,38 +693,50 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     const int tid = threadIdx.x - kLoadWarp0 * 32, sid = 32 * kLoadWarps - 1 - tid;
     const int j = tid & 7, r0 = tid >> 3;
     const uint32_t place = r0 * 128 + ((j ^ (r0 & 7)) << 4);
+    const uint32_t splace = (sid & 31) * 16 + (sid >> 5) * 4;  // row r's scales: word 4 (r % 32) + r / 32
     const int64_t lo_off = FMT == 0 ? a.act_lo - a.act : 0;
-    auto load = [&](auto ph, const Plan& P) {
-      constexpr int PHASE = decltype(ph)::value;
-      const DecodePhase& F = a.ph[PHASE - 1];
+#pragma unroll 1
+    for (int ph = 0; ph < (dry ? 1 : 2); ++ph) {
+      const DecodePhase& F = a.ph[ph];
       const int natom = F.red >> 7;
       const int64_t sb_ld = F.red >> 5;
-      for (int p = P.p0; p < P.p1 && !aborted;) {
-        const Seg S = seg_at<PHASE>(P, p);
-        const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
+      Plan P = plan_of(ph, dry);
+      if (ph == 1) {
+        // A is complete when every CTA has finished phase 1 (all are resident: a cooperative launch)
+        static_assert(kLoadWarps == 4, "epi_all's 128 threads");
+        if (warp == kLoadWarp0 && !aborted && P.p < P.p1) {
+          const uint64_t t0 = globaltimer();
+          while (!aborted && load_acquire(a.done) != gridDim.x) {
+            aborted = s_ctl->abort || globaltimer() - t0 > s_ctl->limit_ns;
+            if (aborted) s_ctl->abort = 1;
+          }
+        }
+        aborted = !epi_all<2>(!aborted);
+      }
+      for (; P.p < P.p1 && !aborted; P.step(ph, F.tiles, H.n_act)) {
+        const int off = dry ? 0 : s_off[P.slot], n = dry ? 1 : s_off[P.slot + 1] - off;
         const uint32_t lo_place = (uint32_t)((n + 7) & ~7) * 128;
-        auto row_of = [&](int r) -> int64_t { return PHASE == 1 ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
+        auto row_of = [&](int r) -> int64_t { return ph == 0 && !dry ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
         // the first rows' sources stay in registers over the segment
         const uint8_t* src[kHeld];
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
           src[i] = F.b + (r0 + i * kRows < n ? row_of(r0 + i * kRows) : 0) * F.b_ld + j * 16;
         const uint8_t* ssrc = C::kSub ? F.sb + (sid < n ? row_of(sid) : 0) * sb_ld : nullptr;
-        const uint32_t splace = (sid & 31) * 16 + (sid >> 5) * 4;  // row r's scales: word 4 (r % 32) + r / 32
-        for (int kb = S.kb0; kb < S.kb1; ++kb) {
-          if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
+        for (int kb = P.kb, end = P.kb + P.length(); kb < end; ++kb) {
+          if (!dry && !warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           const uint32_t st = smem0 + stage * H.stage_bytes;
-#pragma unroll
-          for (int s = 0; s < PHASE; ++s) {
-            const int kk = PHASE == 1 ? kb : kb * H.ns + s;
-            if (PHASE == 2 && (s == H.ns || kk * C::kBK >= F.red)) break;
+#pragma unroll 1
+          for (int s = 0; s < P.nb; ++s) {
+            const int kk = kb * P.nb + s;
+            if (kk >= F.pieces) break;
             const int kbyte = kk * 128;
             const uint32_t size = kbyte + j * 16 < F.b_ld ? 16u : 0u;  // past the end of K: zeros
             const int go = size ? kbyte : -j * 16;
             const uint32_t dst = st + P.b_off + s * P.b_piece + place;
             auto fetch = [&](const uint8_t* from, uint32_t to) {
-              cp_async_16(to, from + go, size);
-              if (PHASE == 2 && FMT == 0) cp_async_16(to + lo_place, from + lo_off + go, size);
+              cp_async_16_if(!dry, to, from + go, size);
+              if (FMT == 0 && ph == 1) cp_async_16_if(!dry, to + lo_place, from + lo_off + go, size);
             };
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
@@ -660,74 +746,57 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
             for (int i = kHeld; r0 + i * kRows < n; ++i)
               fetch(F.b + row_of(r0 + i * kRows) * F.b_ld + j * 16, dst + i * kStep);
             if (C::kSub && sid < n) {
-              const uint32_t ssf = st + P.sf_off + (PHASE == 1 ? 2 * C::kSub : (H.ns + s) * C::kSub) * 512 + splace;
+              const uint32_t ssf = st + P.sf_off + (P.np + s) * C::kSub * 512 + splace;
 #pragma unroll
               for (int sub = 0; sub < C::kSub; ++sub) {
                 const int at = kk * C::kSub + sub;
-                if (at < natom) cp_async_4(ssf + sub * 512, ssrc + at * 4, 4u);
+                cp_async_4_if(!dry && at < natom, ssf + sub * 512, ssrc + at * 4);
               }
             }
           }
+          if (dry) break;
           cp_async_arrive_noinc(smem_u32(&full[stage]));
           __syncwarp();
           advance();
         }
-        p += S.kb1 - S.kb0;
       }
-    };
-    load(Phase1(), plan1);
-    // A is complete when every CTA has finished phase 1 (all are resident: a cooperative launch)
-    if (!aborted && plan2.p0 < plan2.p1) {
-      const uint64_t t0 = globaltimer();
-      while (load_acquire(a.done) != gridDim.x && !aborted) {
-        if (s_ctl->abort) aborted = true;
-        else if (globaltimer() - t0 > s_ctl->limit_ns) s_ctl->abort = 1;
-      }
-      aborted = __any_sync(0xffffffffu, aborted);
     }
-    load(Phase2(), plan2);
     cp_async_wait_all();  // nothing of this warp's lands after the block exits
   } else {
     // ------------------------------------------------------------ epilogue (warps 2 .. 5)
+    // An item that a cut divides begins at the end of one CTA's run.  That CTA finishes it; the others
+    // send it their fp32 sums, which all but a whole-run CTA do at the start of their run.
     const int q = warp & 3, row = q * 32 + lane;  // accumulator row of this thread
     int acc = 0;
     uint32_t acc_phase = 0;
-
-    // Arrive at a divided item after writing this CTA's partial sums; true in the last CTA.
-    // (The barriers order the warps' writes and reads around one thread's fences.)
-    auto join = [&](unsigned* cnt, int c_first, int c_last) {
-      epi_sync();
-      if (threadIdx.x == 64) {
-        const unsigned last = (unsigned)(c_last - c_first);
-        __threadfence();
-        *s_last = atomicInc(cnt + c_first, last) == last;  // wraps to 0: ready for the next launch
-        __threadfence();
+    // Wait for another CTA's sums: repeats `load`, which says whether all of its words are there, and
+    // raises the abort flag when that takes too long.
+    auto until = [&](auto load) {
+      uint64_t t0 = 0;
+      for (uint32_t i = 1; !load(); ++i) {
+        if (i & 63u) continue;
+        const uint64_t t = globaltimer();
+        if (t0 == 0) t0 = t;
+        if (s_ctl->abort || t - t0 > s_ctl->limit_ns) {
+          s_ctl->abort = 1;
+          break;
+        }
       }
-      epi_sync();
-      return *s_last != 0;
+      __syncwarp();
     };
-    // Partial sums of an item: CTA c keeps those of an item that begins in its run (`begins`: it is the
-    // first of the CTAs) apart from those of the item that its run enters in the middle.
-    const int t16 = (a.T + 15) & ~15;
-    auto part_of = [&](int c, bool begins, int rows) { return a.part + (int64_t)(c * 2 + begins) * rows * t16; };
+    auto there = [](const float4& v) {
+      return __float_as_uint(v.x) != 0u && __float_as_uint(v.y) != 0u && __float_as_uint(v.z) != 0u &&
+             __float_as_uint(v.w) != 0u;
+    };
+    const float4 zero4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto release = [&]() {  // the accumulator has been read
       tc_fence_before();
       mbar_arrive(smem_u32(&tempty[acc]));
       if (++acc == H.nacc) { acc = 0; acc_phase ^= 1u; }
     };
-    // The accumulator of the next segment, or false when the pipeline has given up.
-    auto next = [&]() {
-      if (!epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) {
-        aborted = true;
-        return false;
-      }
-      tc_fence_after();
-      return true;
-    };
-
     // The activations of this thread's row for kBatch entries from r on, of which m exist: a batch is
     // computed whole, so that its exponentials, maxima and conversions overlap.
-    auto finish = [&](int r, int m, int out_row, const float* g, const float* u) {
+    auto finish = [&](int r, int m, int out_row, const float (&g)[kBatch], const float (&u)[kBatch]) {
       float v[kBatch];
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) {
@@ -777,150 +846,158 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       }
     };
 
-    for (int p = plan1.p0; p < plan1.p1;) {
-      const Seg S = seg_at<1>(plan1, p);
-      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
-      const int out_row = S.tile * 128 + row;
-      if (!next()) break;
+    // (dry: no entry exists, nothing is read or written)
+    for (Plan P = plan_of(0, dry); P.p < P.p1; P.step(0, a.ph[0].tiles, H.n_act)) {
+      const int off = dry ? 0 : s_off[P.slot], n = dry ? 1 : s_off[P.slot + 1] - off;
+      const int out_row = P.tile * 128 + row;
+      const bool head = P.kb != 0, divided = !head && P.length() != P.nk;
+      const int c_last = divided ? P.owner(P.p + P.L - 1) : cta;
+      if (!dry && !epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
+      tc_fence_after();
       const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
-      const bool whole = S.kb0 == 0 && S.kb1 == plan1.nk;
-      bool write = whole;
-      int c_first = cta, c_last = cta;
-      if (!whole) {
-        float* mine = part_of(cta, S.kb0 == 0, 256);
+      // Partial sums lie in float4s of four tokens: [token / 4][gate, up][row].
+      for (int x = cta + 1; x <= c_last || (dry && x == cta + 1); ++x) {
         for (int c0 = 0; c0 < n; c0 += 16) {
-          float g[16], u[16];
-          tmem_ld16(tb + c0, g);
-          tmem_ld16(tb + H.ncols + c0, u);
+          const int m = dry ? 0 : n - c0;
+          float4* o = reinterpret_cast<float4*>(a.part[0]) + (dry ? 0 : ((int64_t)x * (kMaxT / 4) + c0 / 4) * 256 + row);
+          float4 v[8];
+          until([&]() {  // eight loads in flight
+            bool all = true;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c0 + c < n) {
-              mine[(c0 + c) * 256 + row] = g[c];
-              mine[(c0 + c) * 256 + 128 + row] = u[c];
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = 4 * i < m ? load_relaxed4(o + i * 256) : zero4;
+              v[2 * i + 1] = 4 * i < m ? load_relaxed4(o + i * 256 + 128) : zero4;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all &= 4 * i >= m || (there(v[2 * i]) && there(v[2 * i + 1]));
+            return all;
+          });
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (4 * i < m) {
+              store_relaxed4(o + i * 256, zero4);  // ready for the next launch
+              store_relaxed4(o + i * 256 + 128, zero4);
+              tmem_add4(tb + c0 + 4 * i, v[2 * i]);
+              tmem_add4(tb + H.ncols + c0 + 4 * i, v[2 * i + 1]);
             }
           }
         }
-        release();
-        c_first = plan1.owner(S.item * plan1.L);
-        c_last = plan1.owner(S.item * plan1.L + plan1.L - 1);
-        write = join(a.cnt, c_first, c_last);
       }
-      if (write) {
-        for (int c0 = 0; c0 < n; c0 += 16) {
-          float g[16], u[16];
-          if (whole) {
-            tmem_ld16(tb + c0, g);
-            tmem_ld16(tb + H.ncols + c0, u);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) g[c] = u[c] = 0.0f;
-            for (int x = c_first; x <= c_last; ++x) {
-              const float* o = part_of(x, x == c_first, 256) + c0 * 256 + row;
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                if (c0 + c < n) {
-                  g[c] += __ldcg(o + c * 256);
-                  u[c] += __ldcg(o + c * 256 + 128);
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int b = 0; b < 16; b += kBatch) {
-            if (c0 + b >= n) break;
-            finish(off + c0 + b, min(kBatch, n - c0 - b), out_row, &g[b], &u[b]);
+      tmem_st_wait();
+      for (int c0 = 0; c0 < n; c0 += kBatch) {
+        const int m = dry ? 0 : n - c0;
+        float g[kBatch], u[kBatch];
+        if (!dry) {  // (tensor memory may not be there yet)
+          tmem_ld4(tb + c0, g);
+          tmem_ld4(tb + H.ncols + c0, u);
+        }
+        if (head || dry) {  // columns past n hold something as well, and the reader skips them
+          float4* o = reinterpret_cast<float4*>(a.part[0]) + ((int64_t)cta * (kMaxT / 4) + c0 / 4) * 256 + row;
+          if (m > 0) {
+            store_relaxed4(o, make_float4(sent(g[0]), sent(g[1]), sent(g[2]), sent(g[3])));
+            store_relaxed4(o + 128, make_float4(sent(u[0]), sent(u[1]), sent(u[2]), sent(u[3])));
           }
         }
+        if (!head || dry) finish(off + c0, m, out_row, g, u);
       }
-      if (whole) release();
-      p += S.kb1 - S.kb0;
+      if (dry) break;
+      release();
     }
     // this CTA's part of A is written (or it has given up, which the others must not wait for)
     epi_sync();
-    if (threadIdx.x == 64) {
-      __threadfence();
-      atomicAdd(a.done, 1u);
-    }
+    if (threadIdx.x == 64 && !dry) add_release(a.done, 1u);
 
-    for (int p = plan2.p0; p < plan2.p1 && !aborted;) {
-      const Seg S = seg_at<2>(plan2, p);
-      const int off = s_off[S.slot], n = s_off[S.slot + 1] - off;
-      const int p_end = p + S.kb1 - S.kb0;
-      const int item0 = S.item * plan2.L, item1 = item0 + plan2.L;
-      if (p == plan2.p0 || p == item0)
+    Plan P = plan_of(1, dry);
+    for (const int p0 = P.p; P.p < P.p1 && !aborted; P.step(1, a.ph[1].tiles, H.n_act)) {
+      const int off = dry ? 0 : s_off[P.slot], n = dry ? 1 : s_off[P.slot + 1] - off;
+      const int p_end = P.p + P.length();
+      const int item0 = P.tile * P.L, item1 = item0 + P.L;
+      if (P.p == p0 || P.p == item0)
         for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.0f;
-      if (!next()) break;
+      if (!dry && !epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
+      tc_fence_after();
       const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
       const int lo = (n + 7) & ~7;  // bf16: the column of the first low part
-      for (int c0 = 0; c0 < n; c0 += 16) {
-        float v[16];
-        tmem_ld16(tb + c0, v);
-        if (FMT == 0) {
-          float left[16];
-          tmem_ld16(tb + lo + c0, left);
+      for (int c0 = 0; c0 < n; c0 += kBatch) {
+        float v[kBatch];
+        if (!dry) tmem_ld4(tb + c0, v);
+        if (FMT == 0 && !dry) {
+          float left[kBatch];
+          tmem_ld4(tb + lo + c0, left);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] += left[c];
+          for (int c = 0; c < kBatch; ++c) v[c] += left[c];
+        }
+        float* at[kBatch];  // an expert's tokens differ, so a batch's sums are apart
+        float sum[kBatch];
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const int r = off + min(c0 + c, n - 1);
+          at[c] = s_acc + (dry ? 0 : s_tok[r]) * 128 + row;
+          sum[c] = *at[c] + s_w[r] * v[c];
         }
 #pragma unroll
-        for (int b = 0; b < 16; b += kBatch) {
-          if (c0 + b >= n) break;
-          float* at[kBatch];  // an expert's tokens differ, so a batch's sums are apart
-          float sum[kBatch];
-#pragma unroll
-          for (int c = 0; c < kBatch; ++c) {
-            const int r = off + min(c0 + b + c, n - 1);
-            at[c] = s_acc + s_tok[r] * 128 + row;
-            sum[c] = *at[c] + s_w[r] * v[b + c];
-          }
-#pragma unroll
-          for (int c = 0; c < kBatch; ++c)
-            if (c0 + b + c < n) *at[c] = sum[c];
-        }
+        for (int c = 0; c < kBatch; ++c)
+          if (c0 + c < n && !dry) *at[c] = sum[c];
       }
-      release();
-      if (p_end == plan2.p1 || p_end == item1) {  // this CTA's part of the output tile is complete
-        const int out_row = S.tile * 128 + row, rows = a.ph[1].rows;
-        if (plan2.p0 <= item0 && p_end == item1) {
-          if (out_row < rows)
-            for (int t = 0; t < a.T; ++t)
-              a.out[(int64_t)t * rows + out_row] = __float2bfloat16_rn(s_acc[t * 128 + row]);
-        } else {
-          const int c_first = plan2.owner(item0), c_last = plan2.owner(item1 - 1);
-          float* mine = part_of(cta, plan2.p0 <= item0, 128);
-          for (int t = 0; t < a.T; ++t) mine[t * 128 + row] = s_acc[t * 128 + row];
-          if (join(a.cnt + kMaxCtas, c_first, c_last)) {
-            // a warp takes four tokens at a time, a lane four rows of each; eight loads in flight
-            const float4* first = reinterpret_cast<const float4*>(part_of(c_first, true, 128)) + lane;
-            const float4* rest = reinterpret_cast<const float4*>(part_of(0, false, 128)) + lane;
-            const int step = 2 * 128 / 4 * t16;  // float4s from a CTA's partial sums to the next CTA's
-            for (int t0 = (warp - 2) * 4; t0 < a.T; t0 += 16) {
-              float4 v[4];
+      const bool ends = p_end == P.p1 || p_end == item1;  // this CTA's part of the output tile is complete
+      if (!dry) release();
+      if (ends || dry) {
+        const bool head = p0 > item0;
+        const int c_last = head ? cta : P.owner(item1 - 1);
+        if (!dry) epi_sync();
+        // A warp takes four tokens at a time, a lane four rows of each, from four CTAs at a time.
+        const int r4 = P.tile * 128 + 4 * lane, rows = a.ph[1].rows;
+        for (int t0 = (warp - 2) * 4; t0 < a.T; t0 += 16) {
+          const int m = dry ? 0 : a.T - t0;
+          float4 v[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                v[i] = t0 + i < a.T ? __ldcg(first + (t0 + i) * 32) : make_float4(0, 0, 0, 0);
-#pragma unroll 2
-              for (int x = c_first + 1; x <= c_last; ++x) {
-                const float4* o = rest + (int64_t)x * step;
+          for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<float4*>(s_acc)[min(t0 + i, a.T - 1) * 32 + lane];
+          float4* part = reinterpret_cast<float4*>(a.part[1]) + (int64_t)t0 * 32 + lane;
+          if (head || dry) {
+            float4* o = part + (int64_t)cta * kMaxT * 32;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (t0 + i >= a.T) break;
-                  const float4 w4 = __ldcg(o + (t0 + i) * 32);
-                  v[i].x += w4.x; v[i].y += w4.y; v[i].z += w4.z; v[i].w += w4.w;
-                }
-              }
-              const int r4 = S.tile * 128 + 4 * lane;
-              if (r4 < rows)  // rows is a multiple of 8
+            for (int i = 0; i < 4; ++i)
+              if (i < m) store_relaxed4(o + i * 32, make_float4(sent(v[i].x), sent(v[i].y), sent(v[i].z), sent(v[i].w)));
+          }
+          for (int x = cta + 1; x <= c_last || (dry && x == cta + 1); x += 4) {
+            float4* o = part + (dry ? 0 : (int64_t)x * kMaxT * 32);
+            const int mx = c_last - x;
+            float4 w4[4][4];
+            until([&]() {
+              bool all = true;
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (t0 + i < a.T)
-                    *reinterpret_cast<uint2*>(a.out + (int64_t)(t0 + i) * rows + r4) =
-                        make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
-            }
+                  w4[y][i] = i < m && y <= mx ? load_relaxed4(o + y * kMaxT * 32 + i * 32) : zero4;
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) all &= !(i < m && y <= mx) || there(w4[y][i]);
+              return all;
+            });
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i < m && y <= mx) store_relaxed4(o + y * kMaxT * 32 + i * 32, zero4);
+                v[i].x += w4[y][i].x; v[i].y += w4[y][i].y; v[i].z += w4[y][i].z; v[i].w += w4[y][i].w;
+              }
+          }
+          if (!head && r4 < rows) {  // rows is a multiple of 8
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < m)
+                *reinterpret_cast<uint2*>(a.out + (int64_t)(t0 + i) * rows + r4) =
+                    make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
           }
         }
+        if (!dry) epi_sync();  // s_acc has been read by other threads than its writers
       }
-      p = p_end;
+      if (dry) break;
     }
+    if (!dry && s_ctl->abort) aborted = true;  // sums that never came
+  }
   }
 
   if (aborted && lane == 0) set_error(a.err, kErrTimeout);
@@ -935,7 +1012,9 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- workspace
-// [counters of both phases, CTAs done and left][partial sums][A: bf16 high and low parts, or codes and scales]
+// [CTAs done and left][partial sums of both phases][A: bf16 high and low parts, or codes and scales].
+// The first two are zero between calls, so they have the same place whatever the sizes.
+constexpr size_t kPartBytes = (size_t)kMaxCtas * kMaxT * (256 + 128) * sizeof(float);
 struct DecodeWs {
   size_t part, act, act_lo, act_scales, bytes;
 };
@@ -944,8 +1023,8 @@ DecodeWs decode_ws(int fmt, int64_t T, int k, int64_t I) {
   const size_t rows = (size_t)T * k;
   const size_t row = fmt == 0 ? (size_t)I * 2 : fmt == PGG_FMT_E4M3 ? (size_t)I : (size_t)I / 2;
   DecodeWs w;
-  w.part = up((2 * kMaxCtas + 2) * sizeof(unsigned));
-  w.act = w.part + up((size_t)kMaxCtas * 2 * 256 * ((T + 15) / 16 * 16) * sizeof(float));
+  w.part = 1024;
+  w.act = w.part + kPartBytes;
   w.act_lo = w.act + up(rows * row);
   w.act_scales = w.act_lo;
   w.bytes = w.act_lo + (fmt == 0 ? up(rows * row) : up(rows * (size_t)I / 32));
@@ -982,10 +1061,10 @@ int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const fl
     if ((st = encode_tmap(&t1, dt, 4, W1, d, sb, b, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
   }
   {
-    uint64_t d[3] = {elems(I), (uint64_t)H, (uint64_t)E};
-    uint64_t sb[2] = {bytes(I), bytes(I) * (uint64_t)H};
-    uint32_t b[3] = {bx, 128, 1};
-    if ((st = encode_tmap(&t2, dt, 3, W2, d, sb, b, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
+    uint64_t d[4] = {elems(I), (uint64_t)H, 1, (uint64_t)E};
+    uint64_t sb[3] = {bytes(I), bytes(I) * (uint64_t)H, bytes(I) * (uint64_t)H};
+    uint32_t b[4] = {bx, 128, 1, 1};
+    if ((st = encode_tmap(&t2, dt, 4, W2, d, sb, b, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
   }
   DecodeArgs a{};
   a.ids = ids;
@@ -995,18 +1074,20 @@ int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const fl
   a.E = E;
   a.I = (int)I;
   a.limit = limit;
-  a.ph[0] = {(int)I, (int)H, X, (int64_t)bytes(H), xs, w1s};
-  a.ph[1] = {(int)H, (int)I, ws + L.act, (int64_t)bytes(I), ws + L.act_scales, w2s};
+  auto cdiv = [](int64_t x, int64_t y) { return (int)((x + y - 1) / y); };
+  constexpr int kBK = DecCfg<FMT>::kBK;
+  a.ph[0] = {(int)I, 2, (int)H, cdiv(I, 128), cdiv(H, kBK), X, (int64_t)bytes(H), xs, w1s};
+  a.ph[1] = {(int)H, 1, (int)I, cdiv(H, 128), cdiv(I, kBK), ws + L.act, (int64_t)bytes(I), ws + L.act_scales, w2s};
   a.act = ws + L.act;
   a.act_lo = ws + L.act_lo;
   a.act_scales = ws + L.act_scales;
   a.out = static_cast<__nv_bfloat16*>(out);
-  a.part = reinterpret_cast<float*>(ws + L.part);
-  a.cnt = reinterpret_cast<unsigned*>(ws);
-  a.done = a.cnt + 2 * kMaxCtas;
+  a.part[0] = reinterpret_cast<float*>(ws + L.part);
+  a.part[1] = a.part[0] + (size_t)kMaxCtas * kMaxT * 256;
+  a.done = reinterpret_cast<unsigned*>(ws);
   a.err = err;
   a.slots_cap = std::min(E, a.T * k);
-  const size_t lists = 512 + (size_t)a.T * 512 + (size_t)a.T * k * 4 + 2 * (2 * (size_t)a.slots_cap + 1) +
+  const size_t lists = kFixedBytes + (size_t)a.T * 512 + (size_t)a.T * k * 4 + 2 * (2 * (size_t)a.slots_cap + 1) +
                        (size_t)a.T * k;
   // the whole of an SM's shared memory, so that a CTA has its SM and the tensor memory to itself
   const size_t smem = dev.smem_optin;
