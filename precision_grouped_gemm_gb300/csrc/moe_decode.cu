@@ -54,6 +54,8 @@ struct DecodePhase {
   int halves;          // 2 (phase 1), 1 (phase 2)
   int red;             // reduction length: H (phase 1), I (phase 2)
   int tiles, pieces;   // 128-row tiles of `rows`, 128-byte pieces of `red`
+  FastDiv by_tiles;
+  FastDiv by_nk[2];    // by a tile's stages, with one and with two K pieces a stage
   const uint8_t* b;    // token operand, row-major: X (phase 1) or A (phase 2)
   int64_t b_ld;        // bytes of a row
   const uint8_t* sb;   // its scales, row-major, red / 32 bytes a row
@@ -74,6 +76,7 @@ struct DecodeArgs {
   unsigned* done;       // CTAs that have finished phase 1; [1]: that have left.  Zero between launches
   int ring_bytes;       // shared memory for the stages
   int slots_cap;        // most experts that the batch can name
+  FastDiv by_grid;
   int32_t* err;
 };
 
@@ -154,11 +157,12 @@ __device__ __forceinline__ void copy_atom_if(uint32_t go, uint32_t taddr, uint64
         : "memory");
 }
 // Warp 0 has laid out the work (`start_arrive`); the other roles wait for that before their first
-// stage (`start_wait`).  N: the block's threads.
-template <int N>
-__device__ __forceinline__ void start_arrive() { asm volatile("barrier.cta.arrive 3, %0;" ::"n"(N) : "memory"); }
-template <int N>
-__device__ __forceinline__ void start_wait() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(N) : "memory"); }
+// stage (`start_wait`): those that move data at barrier 3, the epilogue, whose first pass takes
+// longer, at barrier 4.  N: the threads of both sides.
+template <int ID, int N>
+__device__ __forceinline__ void start_arrive() { asm volatile("barrier.cta.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+template <int ID, int N>
+__device__ __forceinline__ void start_wait() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
 
 // Partial sums travel without flags or fences: a word that is not zero is a sum.  (A release under a
 // full load of weight reads took 2 to 5 us on this path.)  A zero sum is sent as -0, which adds the
@@ -245,6 +249,10 @@ __device__ __forceinline__ int cols2(int n) {
   return FMT == 0 ? (2 * ((n + 7) & ~7) + 15) & ~15 : (n + 15) & ~15;
 }
 
+// a / b for 0 <= a < 2^20, b > 0: (a + 1/2) / b is at least 2^-21 of itself away from a whole number,
+// the fast division within 2^-22 of the quotient.
+__device__ __forceinline__ int div_small(int a, int b) { return (int)__fdividef((float)a + 0.5f, (float)b); }
+
 template <int FMT>
 __device__ __forceinline__ void make_plan(const DecodeArgs& a, int n_act, int max_n, int ph, Shape& S, Plan& P) {
   using C = DecCfg<FMT>;
@@ -254,10 +262,11 @@ __device__ __forceinline__ void make_plan(const DecodeArgs& a, int n_act, int ma
   const int s1 = 2 * kTileBytes + b1 + C::kSub * 3 * 512;
   const int two = 2 * (kTileBytes + b2 + C::kSub * 1024), one = kTileBytes + b2 + C::kSub * 1024;
   // phase 2: two K pieces a stage, or one where many tokens would leave fewer than three stages
-  const int st1 = (max(s1, one) + 1023) & ~1023, st2 = (max(s1, two) + 1023) & ~1023;
-  S.ns = a.ring_bytes / st2 >= min(3, a.ring_bytes / st1) ? 2 : 1;
-  S.stage_bytes = S.ns == 2 ? st2 : st1;
-  S.stages = min(kMaxStages, a.ring_bytes / S.stage_bytes);
+  const int st1 = (max(s1, one) + 1023) >> 10, st2 = (max(s1, two) + 1023) >> 10;
+  const int n1 = div_small(a.ring_bytes >> 10, st1), n2 = div_small(a.ring_bytes >> 10, st2);
+  S.ns = n2 >= min(3, n1) ? 2 : 1;
+  S.stage_bytes = (S.ns == 2 ? st2 : st1) << 10;
+  S.stages = min(kMaxStages, S.ns == 2 ? n2 : n1);
   S.acc_cols = max(2 * S.ncols, b2 / 128);
   S.sf_per = C::kSub * max(12, S.ns * 8);
   S.nacc = 2 * S.acc_cols + S.stages * S.sf_per <= 512 ? 2 : 1;
@@ -271,16 +280,21 @@ __device__ __forceinline__ void make_plan(const DecodeArgs& a, int n_act, int ma
   P.b_piece = ph == 0 ? b1 : b2;
   P.sf_off = P.b_off + P.nb * P.b_piece;
   P.L = ph == 0 ? P.nk : n_act * P.nk;
-  const int total = n_act * tiles * P.nk, ctas = max(1, min((int)gridDim.x, total)), cta = blockIdx.x;
-  P.quot = total / ctas;
-  P.rem = total - ctas * P.quot;
+  const int total = n_act * tiles * P.nk, grid = gridDim.x, cta = blockIdx.x;
+  const int ctas = min(grid, total);  // CTAs that get any
+  P.quot = total < grid ? 1 : (int)a.by_grid.div(total);
+  P.rem = total < grid ? 0 : total - grid * P.quot;
   P.p = cta < ctas ? cta * P.quot + min(cta, P.rem) : 0;
   P.p1 = cta < ctas ? P.p + P.quot + (cta < P.rem) : 0;
-  if (total == 0) return;
-  const int item = P.p / P.L, q = P.p - item * P.L;
-  P.slot = (ph == 0 ? item : q) / (ph == 0 ? tiles : P.nk);
-  P.tile = ph == 0 ? item - P.slot * tiles : item;
-  P.kb = ph == 0 ? q : q - P.slot * P.nk;
+  const int unit = (int)a.ph[ph].by_nk[P.nb - 1].div(P.p);  // (expert, tile) number
+  P.kb = P.p - unit * P.nk;
+  if (ph == 0) {
+    P.slot = (int)a.ph[0].by_tiles.div(unit);
+    P.tile = unit - P.slot * tiles;
+  } else {
+    P.tile = div_small(unit, max(n_act, 1));
+    P.slot = unit - P.tile * n_act;
+  }
 }
 
 template <int FMT>
@@ -324,6 +338,12 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   // Up to 32 ids: warp 0 works the list out in registers (lane i has id i), with the slots in the order
   // of first mention, and starts loading weights while the other warps are still coming up.
   const bool few = n_ids <= 32;
+  int id = -1;
+  float wid = 0.0f;
+  if (few && warp == 0 && lane < n_ids) {  // (their latency passes while the barriers are set up)
+    id = __ldg(a.ids + lane);
+    wid = a.w ? __ldg(a.w + lane) : 1.0f;
+  }
   if (!few) {
     for (int i = threadIdx.x; i < n_ids; i += kNT) {
       const int e = __ldg(a.ids + i);
@@ -358,16 +378,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   }
   int n_act = 0, max_n = 0;
   if (few && warp == 0) {
-    int id = -1, tok = 0;
-    float wid = 0.0f;
-    if (lane < n_ids) {
-      id = __ldg(a.ids + lane);
-      wid = a.w ? __ldg(a.w + lane) : 1.0f;
-      tok = lane / a.k;
-      if (id < 0 || id >= a.E) {
-        if (blockIdx.x == 0) set_error(a.err, kErrBadExpert);
-        id = -1;
-      }
+    const int tok = lane < n_ids ? div_small(lane, a.k) : 0;
+    if (lane < n_ids && (id < 0 || id >= a.E)) {
+      if (blockIdx.x == 0) set_error(a.err, kErrBadExpert);
+      id = -1;
     }
     const unsigned all = 0xffffffffu, below = (1u << lane) - 1u;
     const unsigned same = __match_any_sync(all, id), pair = __match_any_sync(all, id * kMaxT + tok);
@@ -508,8 +522,14 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   const bool dry = pass == 0;
   if (!dry) {
     tc_fence_before();
-    if (warp == 0) start_arrive<kNT>();
-    else start_wait<kNT>();
+    if (warp == 0) {
+      start_arrive<3, kNT - 128>();
+      start_arrive<4, 32 + 128>();
+    } else if (warp >= 2 && warp < 6) {
+      start_wait<4, 32 + 128>();
+    } else {
+      start_wait<3, kNT - 128>();
+    }
     tc_fence_after();
     H = *s_shape;
     tmem_base = *s_tmem;
@@ -1076,8 +1096,15 @@ int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const fl
   a.limit = limit;
   auto cdiv = [](int64_t x, int64_t y) { return (int)((x + y - 1) / y); };
   constexpr int kBK = DecCfg<FMT>::kBK;
-  a.ph[0] = {(int)I, 2, (int)H, cdiv(I, 128), cdiv(H, kBK), X, (int64_t)bytes(H), xs, w1s};
-  a.ph[1] = {(int)H, 1, (int)I, cdiv(H, 128), cdiv(I, kBK), ws + L.act, (int64_t)bytes(I), ws + L.act_scales, w2s};
+  auto phase = [&](int64_t rows, int halves, int64_t red, const uint8_t* b, const uint8_t* sb, const uint8_t* sa) {
+    const int tiles = cdiv(rows, 128), pieces = cdiv(red, kBK);
+    return DecodePhase{(int)rows, halves, (int)red, tiles, pieces, FastDiv((uint32_t)tiles),
+                       {FastDiv((uint32_t)pieces), FastDiv((uint32_t)(pieces + 1) / 2)}, b, (int64_t)bytes(red), sb, sa};
+  };
+  a.ph[0] = phase(I, 2, H, X, xs, w1s);
+  a.ph[1] = phase(H, 1, I, ws + L.act, ws + L.act_scales, w2s);
+  const int grid = std::min(dev.sms, kMaxCtas);
+  a.by_grid = FastDiv((uint32_t)grid);
   a.act = ws + L.act;
   a.act_lo = ws + L.act_lo;
   a.act_scales = ws + L.act_scales;
@@ -1096,7 +1123,7 @@ int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const fl
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::min(dev.sms, kMaxCtas));
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(DecCfg<FMT>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
