@@ -14,6 +14,7 @@
 // ordered as an unsigned integer, so that one warp reduction finds the largest and a second one
 // the lowest expert that has it.  Everything is fp32; sums run in a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "block.cuh"
 #include "sched.cuh"
@@ -90,7 +91,12 @@ __device__ __forceinline__ bool load_row(const RouteArgs<T>& a, const T* row, in
   return __any_sync(kAll, bad);
 }
 
-template <typename T, int N>
+// The logit of a key that has no bias in it.
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+// PACK (bf16 logits without a bias): a key is the 16 ordered bits with the expert, counted down,
+// below them, so that one reduction gives both the largest key and the lowest expert that has it.
+template <typename T, int N, bool PACK>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs<T> a) {
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
@@ -113,28 +119,52 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
       Z = warp_sum(Z);
     }
   }
-  // k rounds: the largest key left in the warp, then the lowest expert that holds it
-  int mine = -1;  // lane j: the expert of choice j
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    uint32_t e = 0xffffffffu;
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i)
-      if (key[i] == top) e = lane + 32 * i;
-    e = __reduce_min_sync(kAll, e);
+  if (PACK) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (e == (uint32_t)(lane + 32 * i)) key[i] = 0;
-    if (lane == j) mine = (int)e;
+      if (key[i]) key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - (lane + 32 * i));
+  }
+  // k rounds: the largest key left in the warp, then the lowest expert that holds it
+  int mine = 0;          // lane j: the expert of choice j
+  uint32_t my_key = 0;   // and its key
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) best = max(best, key[i]);
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    uint32_t e;
+    if (PACK) {
+      e = 0xFFFFu - (top & 0xFFFFu);
+    } else {
+      e = 0xffffffffu;
+      if (best == top) {
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+          if (key[i] == top) e = lane + 32 * i;
+      }
+      e = __reduce_min_sync(kAll, e);
+    }
+    if (lane == j) {
+      mine = (int)e;
+      my_key = top;
+    }
+    if ((e & 31) == lane) {  // the expert's lane takes it out
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if ((int)(e >> 5) == i) key[i] = 0;
+        best = max(best, key[i]);
+      }
+    }
   }
   float s = 0.0f;
   if (lane < a.k) {
-    const float v = load_logit(row + mine);
-    const float kf = a.bias ? v + __ldg(a.bias + mine) : v;
-    if (!(kf == -INFINITY)) s = a.softmax ? expf(v - m) : sigmoid(v);
+    // (a negative bf16 number's ordered form ends in ones)
+    if (PACK) my_key = my_key & 0x80000000u ? my_key & 0xFFFF0000u : my_key | 0xFFFFu;
+    // a masked expert's key is -inf; with a bias the logit itself is not in the key
+    const bool masked = my_key == kOrderedNegInf;
+    const float v = a.bias ? load_logit(row + mine) : unordered(my_key);
+    if (!masked) s = a.softmax ? expf(v - m) : sigmoid(v);
   }
   if (a.renorm) Z = warp_sum(s);
   if (lane < a.k) {
@@ -226,7 +256,9 @@ void launch_route(const RouteArgs<T>& a, cudaStream_t s) {
   const int n = (a.E + 31) / 32;
   auto go = [&](auto N) {
     if constexpr (BWD) moe_route_bwd_kernel<T, decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
-    else moe_route_kernel<T, decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
+    else if (std::is_same_v<T, __nv_bfloat16> && !a.bias)
+      moe_route_kernel<T, decltype(N)::value, std::is_same_v<T, __nv_bfloat16>><<<grid, kRouteWarps * 32, 0, s>>>(a);
+    else moe_route_kernel<T, decltype(N)::value, false><<<grid, kRouteWarps * 32, 0, s>>>(a);
   };
   if (n <= 1) go(std::integral_constant<int, 1>());
   else if (n <= 2) go(std::integral_constant<int, 2>());

@@ -142,47 +142,58 @@ struct NormBwdArgs {
 };
 
 // The same ownership: a thread's columns stay its own over all rows of the block, so dgamma's
-// partial sums are registers, written once per block.
+// partial sums are registers, written once per block.  A row's chunks stay packed across the block's
+// sum, and the next row's are already in flight: the loads wait for no barrier.
 template <int V>
-__global__ void __launch_bounds__(V == 1 ? 256 : 512) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
   __shared__ float s_sum[2][32];
   const int nwarps = blockDim.x >> 5;
-  float dg[V][8], g[V][8];
+  float dg[V][8];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int v = threadIdx.x + j * blockDim.x;
+  for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[j][e] = g[j][e] = 0.0f;
-    if (v < a.nvec) unpack8(__ldg(a.gamma + v), g[j]);
-  }
-  int par = 0;
-  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, par ^= 1) {
+    for (int e = 0; e < 8; ++e) dg[j][e] = 0.0f;
+  uint4 hn[V], yn[V], dn[V];
+  float rstd_n = 0.0f;
+  auto fetch = [&](int64_t row) {
     const int64_t base = row * a.nvec;
-    const float rstd = __ldg(a.rstd + row);
-    float xh[V][8], u[V][8];
-    float dot = 0.0f;
-    uint4 hv[V], yv[V], dv[V];
+    rstd_n = __ldg(a.rstd + row);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v < a.nvec) {
-        hv[j] = a.h[base + v];
-        yv[j] = a.dy[base + v];
-        if (a.dh) dv[j] = a.dh[base + v];
+        hn[j] = a.h[base + v];
+        yn[j] = a.dy[base + v];
+        if (a.dh) dn[j] = a.dh[base + v];
       }
     }
+  };
+  fetch(blockIdx.x);
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, par ^= 1) {
+    uint4 h[V], y[V], d[V];
+    const float rstd = rstd_n;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      h[j] = hn[j];
+      y[j] = yn[j];
+      d[j] = dn[j];
+    }
+    if (row + gridDim.x < a.R) fetch(row + gridDim.x);
+    float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v < a.nvec) {
-        unpack8(hv[j], xh[j]);
-        unpack8(yv[j], u[j]);
+        float xh[8], u[8], g[8];
+        unpack8(h[j], xh);
+        unpack8(y[j], u);
+        unpack8(__ldg(a.gamma + v), g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          xh[j][e] *= rstd;
-          dg[j][e] += u[j][e] * xh[j][e];
-          u[j][e] *= g[j][e];
-          dot += u[j][e] * xh[j][e];
+          const float t = u[e] * (xh[e] * rstd);
+          dg[j][e] += t;
+          dot += t * g[e];
         }
       }
     }
@@ -191,14 +202,17 @@ __global__ void __launch_bounds__(V == 1 ? 256 : 512) add_rmsnorm_bwd_kernel(con
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v < a.nvec) {
-        float d[8];
-        if (a.dh) unpack8(dv[j], d);
+        float xh[8], u[8], g[8], o[8];
+        unpack8(h[j], xh);
+        unpack8(y[j], u);
+        unpack8(__ldg(a.gamma + v), g);
+        if (a.dh) unpack8(d[j], o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float n = rstd * (u[j][e] - xh[j][e] * mean);
-          d[e] = a.dh ? d[e] + n : n;
+          const float n = rstd * (u[e] * g[e] - xh[e] * rstd * mean);
+          o[e] = a.dh ? o[e] + n : n;
         }
-        a.dx[base + v] = pack8(d);
+        a.dx[row * a.nvec + v] = pack8(o);
       }
     }
   }
@@ -213,22 +227,27 @@ __global__ void __launch_bounds__(V == 1 ? 256 : 512) add_rmsnorm_bwd_kernel(con
   }
 }
 
-// dgamma[c] = sum over the n partial rows, in a fixed order: 8 warps of a block take every
-// eighth row of 32 columns, and warp 0 adds the eight sums up.
+// dgamma[c] = sum over the n partial rows, in a fixed order: a block has eight columns (a 32-byte
+// sector of each row), thread (i, c) sums rows i, i + 32, ..., and 32 sums a column are joined by
+// shuffles and one exchange.  Launched as the dependent of the kernel above (it waits for its rows).
 __global__ void __launch_bounds__(256) dgamma_reduce_kernel(const float* __restrict__ part, int n, int C,
                                                             float* __restrict__ dgamma) {
-  __shared__ float s[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  __shared__ float s[8][8];
+  const int c = threadIdx.x & 7, i0 = threadIdx.x >> 3, w = threadIdx.x >> 5;
+  const float* p = part + blockIdx.x * 8 + c;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float t = 0.0f;
-  if (c < C)
-    for (int i = w; i < n; i += 8) t += part[(int64_t)i * C + c];
-  s[w][lane] = t;
+#pragma unroll 8
+  for (int i = i0; i < n; i += 32) t += p[(int64_t)i * C];
+  t += __shfl_xor_sync(0xffffffffu, t, 8);
+  t += __shfl_xor_sync(0xffffffffu, t, 16);
+  if ((threadIdx.x & 31) < 8) s[w][c] = t;
   __syncthreads();
-  if (w == 0 && c < C) {
+  if (threadIdx.x < 8) {
+    t = s[0][c];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += s[i][lane];
-    dgamma[c] = t;
+    for (int k = 1; k < 8; ++k) t += s[k][c];
+    dgamma[blockIdx.x * 8 + c] = t;
   }
 }
 
@@ -237,7 +256,13 @@ int norm_threads(int nvec, int V) { return std::max(32, ((nvec + V - 1) / V + 31
 int norm_v(int nvec) { return nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4; }
 
 // Blocks of the backward pass: a thread block's partial dgamma is one row of the workspace.
-constexpr int kNormBwdBlocks = 456;  // 3 a SM
+// At most as many as are resident at once (each walks its rows; a block of a second wave would start
+// when the first ones end), which this bounds for the workspace.
+int norm_bwd_v(int nvec) { return nvec <= 384 ? 1 : nvec <= 1024 ? 2 : 4; }
+int norm_bwd_blocks(int64_t R, int64_t C) {
+  const int V = norm_bwd_v((int)(C / 8)), threads = norm_threads((int)(C / 8), V);
+  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, (V == 4 ? 512 : 1024) / threads)));
+}
 
 template <int V>
 void launch_norm(const NormArgs& a, int fmt, int grid, int threads, cudaStream_t s) {
@@ -249,7 +274,7 @@ void launch_norm(const NormArgs& a, int fmt, int grid, int threads, cudaStream_t
 }  // namespace
 
 size_t add_rmsnorm_bwd_ws_bytes(int64_t R, int64_t C) {
-  return (size_t)std::min<int64_t>(R, kNormBwdBlocks) * (size_t)C * sizeof(float);
+  return (size_t)norm_bwd_blocks(R, C) * (size_t)C * sizeof(float);
 }
 
 int check_norm_dims(int64_t R, int64_t C, int mult) {
@@ -313,16 +338,27 @@ int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const voi
   DeviceInfo dev;
   if ((st = current_device(&dev)) != PGG_OK) return st;
   float* part = static_cast<float*>(ws);
-  const int grid = (int)std::min<int64_t>(R, kNormBwdBlocks);
   NormBwdArgs a{static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(h),
                 static_cast<const uint4*>(gamma), rstd, R, (int)(C / 8), 1.0f / (float)C, static_cast<uint4*>(dx),
                 part};
-  const int V = norm_v(a.nvec), threads = norm_threads(a.nvec, V);
-  if (V == 1) add_rmsnorm_bwd_kernel<1><<<grid, threads, 0, s>>>(a);
-  else if (V == 2) add_rmsnorm_bwd_kernel<2><<<grid, threads, 0, s>>>(a);
-  else add_rmsnorm_bwd_kernel<4><<<grid, threads, 0, s>>>(a);
-  dgamma_reduce_kernel<<<(unsigned)((C + 31) / 32), 256, 0, s>>>(part, grid, (int)C, dgamma);
-  return cuda_status(cudaGetLastError());
+  const int V = norm_bwd_v(a.nvec), threads = norm_threads(a.nvec, V);
+  auto kern = V == 1 ? add_rmsnorm_bwd_kernel<1> : V == 2 ? add_rmsnorm_bwd_kernel<2> : add_rmsnorm_bwd_kernel<4>;
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  if (e != cudaSuccess) return cuda_status(e);
+  const int grid = std::min(norm_bwd_blocks(R, C), dev.sms * std::max(1, per_sm));
+  kern<<<grid, threads, 0, s>>>(a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(C / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, dgamma_reduce_kernel, (const float*)part, grid, (int)C, dgamma);
+  return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 }  // extern "C"
