@@ -142,10 +142,17 @@ struct NormBwdArgs {
 };
 
 // The same ownership: a thread's columns stay its own over all rows of the block, so dgamma's
-// partial sums are registers, written once per block.  A row's chunks stay packed across the block's
-// sum, and the next row's are already in flight: the loads wait for no barrier.
+// partial sums are registers, written once per block.  A thread copies its chunks of the next
+// kDepth - 1 rows into its own places of shared memory (no thread reads another's, so a wait for its
+// own copies is enough).  With the next row alone in flight, in registers, the kernel was bound by
+// the memory's latency: 8192 x 2880 took 40 us.  With
+// t = dy h: dgamma += rstd t, mean(u xh) = rstd mean(t gamma), dx = dh + rstd dy gamma - c h,
+// c = rstd^2 mean(u xh): six operations an element besides the conversions.
+__host__ __device__ constexpr int norm_bwd_depth(int V) { return V > 0 ? 2 : 0; }
 template <int V>
 __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int kDepth = norm_bwd_depth(V);
+  extern __shared__ uint4 s_row[];  // [kDepth][3][V][blockDim]
   __shared__ float s_sum[2][32];
   const int nwarps = blockDim.x >> 5;
   float dg[V][8];
@@ -153,65 +160,75 @@ __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(con
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[j][e] = 0.0f;
-  uint4 hn[V], yn[V], dn[V];
-  float rstd_n = 0.0f;
-  auto fetch = [&](int64_t row) {
-    const int64_t base = row * a.nvec;
-    rstd_n = __ldg(a.rstd + row);
+  auto place = [&](int slot, int which, int j) {
+    return s_row + ((slot * 3 + which) * V + j) * blockDim.x + threadIdx.x;
+  };
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < a.R) {
+      const int64_t base = row * a.nvec;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int v = threadIdx.x + j * blockDim.x;
-      if (v < a.nvec) {
-        hn[j] = a.h[base + v];
-        yn[j] = a.dy[base + v];
-        if (a.dh) dn[j] = a.dh[base + v];
+      for (int j = 0; j < V; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < a.nvec) {
+          cp_async_16(smem_u32(place(slot, 0, j)), a.h + base + v);
+          cp_async_16(smem_u32(place(slot, 1, j)), a.dy + base + v);
+          if (a.dh) cp_async_16(smem_u32(place(slot, 2, j)), a.dh + base + v);
+        }
       }
     }
+    cp_async_commit();
   };
-  fetch(blockIdx.x);
-  int par = 0;
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+  int par = 0, slot = 0;
+  float rstd_next = __ldg(a.rstd + blockIdx.x);
   for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, par ^= 1) {
+    const float rstd = rstd_next;
+    if (row + gridDim.x < a.R) rstd_next = __ldg(a.rstd + row + gridDim.x);
+    fetch(row + (int64_t)(kDepth - 1) * gridDim.x, slot == 0 ? kDepth - 1 : slot - 1);
+    cp_async_wait<kDepth - 1>();
     uint4 h[V], y[V], d[V];
-    const float rstd = rstd_n;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      h[j] = hn[j];
-      y[j] = yn[j];
-      d[j] = dn[j];
+      h[j] = *place(slot, 0, j);
+      y[j] = *place(slot, 1, j);
+      d[j] = *place(slot, 2, j);
     }
-    if (row + gridDim.x < a.R) fetch(row + gridDim.x);
+    if (++slot == kDepth) slot = 0;
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v < a.nvec) {
-        float xh[8], u[8], g[8];
-        unpack8(h[j], xh);
+        float x[8], u[8], g[8];
+        unpack8(h[j], x);
         unpack8(y[j], u);
         unpack8(__ldg(a.gamma + v), g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float t = u[e] * (xh[e] * rstd);
-          dg[j][e] += t;
-          dot += t * g[e];
+          const float t = u[e] * x[e];
+          dg[j][e] = fmaf(t, rstd, dg[j][e]);
+          dot = fmaf(t, g[e], dot);
         }
       }
     }
-    const float mean = block_sum(dot, s_sum[par], nwarps) * a.inv_c;
+    const float c = -rstd * rstd * (block_sum(dot, s_sum[par], nwarps) * rstd * a.inv_c);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v < a.nvec) {
-        float xh[8], u[8], g[8], o[8];
-        unpack8(h[j], xh);
+        float x[8], u[8], g[8], o[8];
+        unpack8(h[j], x);
         unpack8(y[j], u);
         unpack8(__ldg(a.gamma + v), g);
-        if (a.dh) unpack8(d[j], o);
+        if (a.dh) {
+          unpack8(d[j], o);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = rstd * (u[e] * g[e] - xh[e] * rstd * mean);
-          o[e] = a.dh ? o[e] + n : n;
+          for (int e = 0; e < 8; ++e) o[e] = 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(c, x[e], fmaf(u[e] * g[e], rstd, o[e]));
         a.dx[row * a.nvec + v] = pack8(o);
       }
     }
@@ -228,26 +245,30 @@ __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(con
 }
 
 // dgamma[c] = sum over the n partial rows, in a fixed order: a block has eight columns (a 32-byte
-// sector of each row), thread (i, c) sums rows i, i + 32, ..., and 32 sums a column are joined by
-// shuffles and one exchange.  Launched as the dependent of the kernel above (it waits for its rows).
-__global__ void __launch_bounds__(256) dgamma_reduce_kernel(const float* __restrict__ part, int n, int C,
-                                                            float* __restrict__ dgamma) {
-  __shared__ float s[8][8];
+// sector of each row), thread (i, c) sums rows i, i + 128, ..., and the 128 sums of a column are
+// joined by shuffles and one exchange.  Launched as the dependent of the kernel above (it waits for
+// its rows).
+constexpr int kReduceThreads = 1024;
+__global__ void __launch_bounds__(kReduceThreads) dgamma_reduce_kernel(const float* __restrict__ part, int n, int C,
+                                                                       float* __restrict__ dgamma) {
+  constexpr int kWarps = kReduceThreads / 32, kGroups = kReduceThreads / 8;
+  __shared__ float s[kWarps][8];
   const int c = threadIdx.x & 7, i0 = threadIdx.x >> 3, w = threadIdx.x >> 5;
   const float* p = part + blockIdx.x * 8 + c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float t = 0.0f;
-#pragma unroll 8
-  for (int i = i0; i < n; i += 32) t += p[(int64_t)i * C];
+#pragma unroll 4
+  for (int i = i0; i < n; i += kGroups) t += p[(int64_t)i * C];
   t += __shfl_xor_sync(0xffffffffu, t, 8);
   t += __shfl_xor_sync(0xffffffffu, t, 16);
   if ((threadIdx.x & 31) < 8) s[w][c] = t;
   __syncthreads();
-  if (threadIdx.x < 8) {
-    t = s[0][c];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) t += s[k][c];
-    dgamma[blockIdx.x * 8 + c] = t;
+  if (w == 0) {
+    t = 0.0f;
+    for (int k = threadIdx.x >> 3; k < kWarps; k += 4) t += s[k][c];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if (threadIdx.x < 8) dgamma[blockIdx.x * 8 + c] = t;
   }
 }
 
@@ -261,7 +282,7 @@ int norm_v(int nvec) { return nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4; }
 int norm_bwd_v(int nvec) { return nvec <= 384 ? 1 : nvec <= 1024 ? 2 : 4; }
 int norm_bwd_blocks(int64_t R, int64_t C) {
   const int V = norm_bwd_v((int)(C / 8)), threads = norm_threads((int)(C / 8), V);
-  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, (V == 4 ? 512 : 1024) / threads)));
+  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, 1536 / threads) >> (V >> 1)));
 }
 
 template <int V>
@@ -343,14 +364,16 @@ int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const voi
                 part};
   const int V = norm_bwd_v(a.nvec), threads = norm_threads(a.nvec, V);
   auto kern = V == 1 ? add_rmsnorm_bwd_kernel<1> : V == 2 ? add_rmsnorm_bwd_kernel<2> : add_rmsnorm_bwd_kernel<4>;
+  const size_t smem = (size_t)norm_bwd_depth(V) * 3 * V * threads * sizeof(uint4);
   int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
   if (e != cudaSuccess) return cuda_status(e);
   const int grid = std::min(norm_bwd_blocks(R, C), dev.sms * std::max(1, per_sm));
-  kern<<<grid, threads, 0, s>>>(a);
+  kern<<<grid, threads, smem, s>>>(a);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(C / 8));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kReduceThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
