@@ -94,9 +94,24 @@ __device__ __forceinline__ bool load_row(const RouteArgs<T>& a, const T* row, in
 // The logit of a key that has no bias in it.
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-// PACK (bf16 logits without a bias): a key is the 16 ordered bits with the expert, counted down,
-// below them, so that one reduction gives both the largest key and the lowest expert that has it.
-template <typename T, int N, bool PACK>
+// Weights of one token's choices from lane j's expert, its score's argument and whether it counts.
+template <typename T>
+__device__ __forceinline__ void write_choice(const RouteArgs<T>& a, int64_t t, int lane, int mine, bool masked, float v,
+                                             float m, float Z, bool bad) {
+  float s = 0.0f;
+  if (lane < a.k && !masked) s = a.softmax ? expf(v - m) : sigmoid(v);
+  if (a.renorm) Z = warp_sum(s);
+  if (lane < a.k) {
+    float w = s == 0.0f ? 0.0f : a.scale * s / Z;
+    if (bad) w = __uint_as_float(0x7FC00000u);
+    a.ids[t * a.k + lane] = mine;
+    a.w[t * a.k + lane] = w;
+  }
+}
+
+// Any logits and a bias: k rounds of the largest key left in the warp, then the lowest expert that
+// holds it.
+template <typename T, int N>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs<T> a) {
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
@@ -119,60 +134,101 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
       Z = warp_sum(Z);
     }
   }
-  if (PACK) {
+  int mine = 0;         // lane j: the expert of choice j
+  uint32_t my_key = 0;  // and its key
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    uint32_t e = 0xffffffffu;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i)
+      if (key[i] == top) e = lane + 32 * i;
+    e = __reduce_min_sync(kAll, e);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (key[i]) key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - (lane + 32 * i));
-  }
-  // k rounds: the largest key left in the warp, then the lowest expert that holds it
-  int mine = 0;          // lane j: the expert of choice j
-  uint32_t my_key = 0;   // and its key
-  uint32_t best = key[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) best = max(best, key[i]);
-  for (int j = 0; j < a.k; ++j) {
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    uint32_t e;
-    if (PACK) {
-      e = 0xFFFFu - (top & 0xFFFFu);
-    } else {
-      e = 0xffffffffu;
-      if (best == top) {
-#pragma unroll
-        for (int i = N - 1; i >= 0; --i)
-          if (key[i] == top) e = lane + 32 * i;
-      }
-      e = __reduce_min_sync(kAll, e);
-    }
+      if (e == (uint32_t)(lane + 32 * i)) key[i] = 0;
     if (lane == j) {
       mine = (int)e;
       my_key = top;
     }
-    if ((e & 31) == lane) {  // the expert's lane takes it out
-      best = 0;
+  }
+  // (with a bias the logit itself is not in the key)
+  const float v = a.bias && lane < a.k ? load_logit(row + mine) : unordered(my_key);
+  write_choice(a, t, lane, mine, my_key == kOrderedNegInf, v, m, Z, bad);
+}
+
+// Sorts a lane's N keys, largest first: the odd-even merge network, 19 exchanges for 8 keys.
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if ((int)(e >> 5) == i) key[i] = 0;
-        best = max(best, key[i]);
-      }
-    }
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t hi = max(k[i + j], k[i + j + q]);
+            k[i + j + q] = min(k[i + j], k[i + j + q]);
+            k[i + j] = hi;
+          }
+}
+
+// bf16 logits without a bias, the gate of a bf16 model: a key is the 16 ordered bits with the expert,
+// counted down, below them.  All keys differ, so one reduction gives both the largest key and the
+// lowest expert that has it, and with every lane's keys sorted a round costs the winner's lane a
+// shift.  Bound by instructions: the kernel above took 17.1 us for 16384 x 256 logits with k = 8.
+template <int N>
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_bf16_kernel(const RouteArgs<__nv_bfloat16> a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= a.T_) return;
+  const unsigned short* row = reinterpret_cast<const unsigned short*>(a.logits) + t * a.E;
+  uint32_t u[N], key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    u[i] = e < a.E ? (uint32_t)__ldg(row + e) << 16 : 0xFF800000u;  // -inf past the last expert
   }
-  float s = 0.0f;
-  if (lane < a.k) {
-    // (a negative bf16 number's ordered form ends in ones)
-    if (PACK) my_key = my_key & 0x80000000u ? my_key & 0xFFFF0000u : my_key | 0xFFFFu;
-    // a masked expert's key is -inf; with a bias the logit itself is not in the key
-    const bool masked = my_key == kOrderedNegInf;
-    const float v = a.bias ? load_logit(row + mine) : unordered(my_key);
-    if (!masked) s = a.softmax ? expf(v - m) : sigmoid(v);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    const bool nan = (u[i] & 0x7FFFFFFFu) > 0x7F800000u;
+    bad |= nan;
+    // the ordered form: -0 as +0, a NaN as -inf
+    const uint32_t z = nan ? 0xFF800000u : u[i] == 0x80000000u ? 0u : u[i];
+    const uint32_t o = z ^ ((uint32_t)((int32_t)z >> 31) | 0x80000000u);
+    key[i] = e < a.E ? (o & 0xFFFF0000u) | (0xFFFFu - e) : 0u;
   }
-  if (a.renorm) Z = warp_sum(s);
-  if (lane < a.k) {
-    float w = s == 0.0f ? 0.0f : a.scale * s / Z;
-    if (bad) w = __uint_as_float(0x7FC00000u);
-    a.ids[t * a.k + lane] = mine;
-    a.w[t * a.k + lane] = w;
+  bad = __any_sync(kAll, bad);
+  sort_keys<N>(key);
+  uint32_t my_key = 0;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t top = __reduce_max_sync(kAll, key[0]);
+    if (lane == j) my_key = top;
+    const bool won = key[0] == top;
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) key[i] = won ? key[i + 1] : key[i];
+    key[N - 1] = won ? 0u : key[N - 1];
   }
+  const int mine = (int)(0xFFFFu - (my_key & 0xFFFFu));
+  // the logit back from its ordered form (a negative number's ends in ones)
+  const uint32_t o = my_key & 0x80000000u ? my_key & 0xFFFF0000u : my_key | 0xFFFFu;
+  const float v = unordered(o);
+  const bool masked = o == kOrderedNegInf;
+  float m = __shfl_sync(kAll, v, 0), Z = 1.0f;  // the first choice is the largest
+  if (m == -INFINITY) m = 0.0f;                 // every expert is masked: all weights are 0
+  if (a.softmax && !a.renorm) {
+    Z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) Z += expf(__uint_as_float(u[i]) - m);
+    Z = warp_sum(Z);
+  }
+  write_choice(a, t, lane, mine, masked, v, m, Z, bad);
 }
 
 template <typename T, int N>
@@ -256,9 +312,15 @@ void launch_route(const RouteArgs<T>& a, cudaStream_t s) {
   const int n = (a.E + 31) / 32;
   auto go = [&](auto N) {
     if constexpr (BWD) moe_route_bwd_kernel<T, decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
-    else if (std::is_same_v<T, __nv_bfloat16> && !a.bias)
-      moe_route_kernel<T, decltype(N)::value, std::is_same_v<T, __nv_bfloat16>><<<grid, kRouteWarps * 32, 0, s>>>(a);
-    else moe_route_kernel<T, decltype(N)::value, false><<<grid, kRouteWarps * 32, 0, s>>>(a);
+    else {
+      if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        if (!a.bias) {
+          moe_route_bf16_kernel<decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
+          return;
+        }
+      }
+      moe_route_kernel<T, decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
+    }
   };
   if (n <= 1) go(std::integral_constant<int, 1>());
   else if (n <= 2) go(std::integral_constant<int, 2>());
