@@ -99,70 +99,22 @@ __device__ __forceinline__ void tmem_add4(uint32_t taddr, const float4& v) {
                "r"(__float_as_uint(f[3] + v.w))
                : "memory");
 }
-// 16- and 4-byte asynchronous copies to shared memory, executed where `go` is set (src_bytes 0: zeros).
-__device__ __forceinline__ void cp_async_16_if(uint32_t go, uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %3, 0;\n\t"
-      "@q cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
-      "l"(src), "r"(src_bytes), "r"(go)
-      : "memory");
-}
-__device__ __forceinline__ void cp_async_4_if(uint32_t go, uint32_t dst, const void* src) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst),
-      "l"(src), "r"(go)
-      : "memory");
-}
-// The MMAs of one lane (`go`), issued by a whole converged warp: with the branch on the lane inside
-// the instruction's own predicate, descriptors stay warp-uniform values.
-template <int FMT>
-__device__ __forceinline__ void mma_if(uint32_t go, uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                       uint32_t sfb, uint32_t accum) {
-  if (FMT == 0)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(accum), "r"(go)
-        : "memory");
-  else if (FMT == kE4M3)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(go)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(go)
-        : "memory");
+__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, uint32_t src_bytes) {  // 0 bytes: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 template <int FMT>
-__device__ __forceinline__ void copy_atom_if(uint32_t go, uint32_t taddr, uint64_t sdesc) {
-  if (FMT != 0)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-        "l"(sdesc), "r"(go)
-        : "memory");
+__device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                    uint32_t accum) {
+  if (FMT == 0) mma_f16(d, ad, bd, idesc, accum);
+  else if (FMT == kE4M3) mma_mxf8(d, ad, bd, idesc, sfa, sfb, accum);
+  else mma_mxf4(d, ad, bd, idesc, sfa, sfb, accum);
 }
-// Warp 0 has laid out the work (`start_arrive`); the other roles wait for that before their first
-// stage (`start_wait`): those that move data at barrier 3, the epilogue, whose first pass takes
-// longer, at barrier 4.  N: the threads of both sides.
-template <int ID, int N>
-__device__ __forceinline__ void start_arrive() { asm volatile("barrier.cta.arrive %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
-template <int ID, int N>
-__device__ __forceinline__ void start_wait() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
+// Warp 0 has laid out the work (`start_arrive`) and goes on to the first loads; the other roles wait
+// for that (`start_wait`).  N: the block's threads.
+template <int N>
+__device__ __forceinline__ void start_arrive() { asm volatile("barrier.cta.arrive 3, %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void start_wait() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(N) : "memory"); }
 
 // Partial sums travel without flags or fences: a word that is not zero is a sum.  (A release under a
 // full load of weight reads took 2 to 5 us on this path.)  A zero sum is sent as -0, which adds the
@@ -502,44 +454,18 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   int stage = 0;
   uint32_t phase = 0;
 
-  // The other roles first pass once over their loops without effect (`dry`), with a plan of one
-  // stage: that brings their code into the instruction cache while the memory is idle.  Fetched
-  // through a memory system that is full of weight loads, the MMA warp's first stage alone took
-  // 5600 cycles, and the epilogue's first tile about as many.
-  Shape H{};
-  H.n_act = H.stages = H.ns = H.nacc = 1;
-  uint32_t tmem_base = 0;
+  tc_fence_before();
+  if (warp == 0) start_arrive<kNT>();
+  else start_wait<kNT>();
+  tc_fence_after();
+  const Shape H = *s_shape;
+  const uint32_t tmem_base = *s_tmem;
   auto advance = [&]() {
     if (++stage == H.stages) { stage = 0; phase ^= 1u; }
   };
-  Plan one_stage{};
-  one_stage.np = 2;
-  one_stage.nb = one_stage.nk = one_stage.L = one_stage.quot = one_stage.p1 = 1;
-  auto plan_of = [&](int ph, bool dry) { return dry ? one_stage : s_plan[ph]; };
-
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-  const bool dry = pass == 0;
-  if (!dry) {
-    tc_fence_before();
-    if (warp == 0) {
-      start_arrive<3, kNT - 128>();
-      start_arrive<4, 32 + 128>();
-    } else if (warp >= 2 && warp < 6) {
-      start_wait<4, 32 + 128>();
-    } else {
-      start_wait<3, kNT - 128>();
-    }
-    tc_fence_after();
-    H = *s_shape;
-    tmem_base = *s_tmem;
-    if (H.n_act == 0)  // no expert is named: the layer's output is zero
-      for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.ph[1].rows;
-           i += (int64_t)gridDim.x * kNT)
-        a.out[i] = __float2bfloat16_rn(0.0f);
-  } else if (warp == 0) {
-    continue;
-  }
+  if (H.n_act == 0)  // no expert is named: the layer's output is zero
+    for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.ph[1].rows; i += (int64_t)gridDim.x * kNT)
+      a.out[i] = __float2bfloat16_rn(0.0f);
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights: TMA tiles, bulk scale atoms
@@ -593,9 +519,9 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
 #pragma unroll 1
-    for (int ph = 0; ph < (dry ? 1 : 2); ++ph) {
+    for (int ph = 0; ph < 2; ++ph) {
       const int red = a.ph[ph].red;
-      Plan P = plan_of(ph, dry);
+      Plan P = s_plan[ph];
       // descriptors of stage 0's tiles; an address d bytes further on adds d / 16
       const uint64_t desc_a = smem_desc(smem0, 16, 1024, kSwizzle128B);
       const uint64_t desc_b = smem_desc(smem0 + P.b_off, 16, 1024, kSwizzle128B);
@@ -604,54 +530,51 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       const uint32_t d_step = ph == 0 ? H.ncols : 0, b_step = ph == 0 ? 0 : P.b_piece >> 4;
       const uint32_t sfb0 = P.np * C::kSub * 4, sfb_step = ph == 0 ? 0 : C::kSub * 4;
       while (P.p < P.p1 && !aborted) {
-        const int n = dry ? 1 : s_off[P.slot + 1] - s_off[P.slot];
+        const int n = s_off[P.slot + 1] - s_off[P.slot];
         const uint32_t N = ph == 0 ? (n + 15) & ~15 : cols2<FMT>(n);
         const uint32_t idesc = FMT == 0 ? idesc_bf16(128, N, false, false) : idesc_mx(FMT == kE4M3 ? 0 : 1, 128, N);
-        if (!dry && !warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
+        if (!warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * H.acc_cols;
         const int end = P.kb + P.length();
         for (int kb = P.kb; kb < end; ++kb) {
-          if (!dry && !warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) {
-            aborted = true;
-            break;
-          }
+          if (!warp_wait(smem_u32(C::kCopier ? &sfull[stage] : &full[stage]), phase, s_ctl)) { aborted = true; break; }
           tc_fence_after();
           if (!C::kCopier) fence_proxy_async_smem();  // the token operand's cp.async writes
-          const uint32_t one = lane == 0 && !dry;
-          const uint64_t so = (uint64_t)(stage * H.stage_bytes) >> 4;
-          uint64_t ad = desc_a + so, bd = desc_b + so;
-          uint32_t dd = d, sfa = tmem_base + H.sf_col0 + stage * H.sf_per, sfb = sfa + sfb0;
-          // reduction elements left from this piece on: MMAs past them (an e2m1 K may end inside a
-          // piece) and pieces past them are skipped; the zero-filled end of a bf16 K adds nothing
-          int left = red - kb * P.nb * C::kBK;
-          uint32_t accum = kb > P.kb;
+          if (lane == 0) {
+            const uint64_t so = (uint64_t)(stage * H.stage_bytes) >> 4;
+            uint64_t ad = desc_a + so, bd = desc_b + so;
+            uint32_t dd = d, sfa = tmem_base + H.sf_col0 + stage * H.sf_per, sfb = sfa + sfb0;
+            // reduction elements left from this piece on: MMAs past them (an e2m1 K may end inside a
+            // piece) and pieces past them are skipped; the zero-filled end of a bf16 K adds nothing
+            int left = red - kb * P.nb * C::kBK;
+            uint32_t accum = kb > P.kb;
 #pragma unroll 1
-          for (int s = 0; s < P.np; ++s) {
+            for (int s = 0; s < P.np; ++s) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j * C::kPerMma >= left) break;
-              // the scale bytes of an MMA's K range: e4m3 block j of its atom, e2m1 a pair of blocks
-              const uint32_t id = FMT == kE4M3 ? j : 2 * (j & 1), at = FMT == kE2M1 ? 4 * (j >> 1) : 0;
-              mma_if<FMT>(one, dd, ad + 2 * j, bd + 2 * j, FMT == 0 ? idesc : idesc | idesc_sf_ids(id, id), sfa + at,
-                          sfb + at, j == 0 ? accum : 1u);
+              for (int j = 0; j < 4; ++j) {
+                if (j * C::kPerMma >= left) break;
+                // the scale bytes of an MMA's K range: e4m3 block j of its atom, e2m1 a pair of blocks
+                const uint32_t id = FMT == kE4M3 ? j : 2 * (j & 1), at = FMT == kE2M1 ? 4 * (j >> 1) : 0;
+                mma<FMT>(dd, ad + 2 * j, bd + 2 * j, FMT == 0 ? idesc : idesc | idesc_sf_ids(id, id), sfa + at,
+                         sfb + at, j == 0 ? accum : 1u);
+              }
+              ad += kTileBytes >> 4;
+              bd += b_step;
+              dd += d_step;
+              sfa += C::kSub * 4;
+              sfb += sfb_step;
+              if (ph != 0) {
+                left -= C::kBK;
+                accum = 1;
+              }
             }
-            ad += kTileBytes >> 4;
-            bd += b_step;
-            dd += d_step;
-            sfa += C::kSub * 4;
-            sfb += sfb_step;
-            if (ph != 0) {
-              left -= C::kBK;
-              accum = 1;
-            }
+            mma_commit(smem_u32(&empty[stage]));
           }
-          if (dry) break;
-          if (one) mma_commit(smem_u32(&empty[stage]));
           __syncwarp();
           advance();
         }
-        if (aborted || dry) break;
+        if (aborted) break;
         if (lane == 0) mma_commit(smem_u32(&tfull[acc]));
         __syncwarp();
         if (++acc == H.nacc) { acc = 0; acc_phase ^= 1u; }
@@ -665,36 +588,36 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   } else if (C::kCopier && warp == 6) {
     // ------------------------------------------------------------ scale copier: a stage's atoms -> tensor memory
 #pragma unroll 1
-    for (int ph = 0; ph < (dry ? 1 : 2); ++ph) {
+    for (int ph = 0; ph < 2; ++ph) {
       const int natom = a.ph[ph].red >> 7;
-      Plan P = plan_of(ph, dry);
+      Plan P = s_plan[ph];
       const uint64_t ds0 = smem_desc(smem0 + P.sf_off, 0, 128, kSwizzleNone);
       while (P.p < P.p1 && !aborted) {
         const int end = P.kb + P.length();
         for (int kb = P.kb; kb < end; ++kb) {
-          if (!dry && !warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+          if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
           tc_fence_after();
           fence_proxy_async_smem();  // the token operand's and its scales' cp.async writes
-          const uint32_t one = lane == 0 && !dry;
-          uint64_t ds = ds0 + ((uint64_t)(stage * H.stage_bytes) >> 4);
-          uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
-          // the weight pieces' atoms, then the token pieces'; those past the end of K are skipped
-          const int at0 = kb * P.nb * C::kSub;
+          if (lane == 0) {
+            uint64_t ds = ds0 + ((uint64_t)(stage * H.stage_bytes) >> 4);
+            uint32_t sf = tmem_base + H.sf_col0 + stage * H.sf_per;
+            // the weight pieces' atoms, then the token pieces'; those past the end of K are skipped
+            const int at0 = kb * P.nb * C::kSub;
 #pragma unroll 1
-          for (int s = 0; s < P.np + P.nb; ++s) {
-            const int at = at0 + (ph == 0 ? 0 : (s & (P.nb - 1)) * C::kSub);
+            for (int s = 0; s < P.np + P.nb; ++s) {
+              const int at = at0 + (ph == 0 ? 0 : (s & (P.nb - 1)) * C::kSub);
 #pragma unroll
-            for (int i = 0; i < C::kSub; ++i)
-              copy_atom_if<FMT>(one && at + i < natom, sf + 4 * i, ds + (i * 512 >> 4));
-            ds += C::kSub * 512 >> 4;
-            sf += C::kSub * 4;
+              for (int i = 0; i < C::kSub; ++i)
+                if (at + i < natom) tmem_cp_32x128b_x4(sf + 4 * i, ds + (i * 512 >> 4));
+              ds += C::kSub * 512 >> 4;
+              sf += C::kSub * 4;
+            }
+            mma_commit(smem_u32(&sfull[stage]));
           }
-          if (dry) break;
-          if (one) mma_commit(smem_u32(&sfull[stage]));
           __syncwarp();
           advance();
         }
-        if (aborted || dry) break;
+        if (aborted) break;
         P.step(ph, a.ph[ph].tiles, H.n_act);
       }
     }
@@ -716,11 +639,11 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     const uint32_t splace = (sid & 31) * 16 + (sid >> 5) * 4;  // row r's scales: word 4 (r % 32) + r / 32
     const int64_t lo_off = FMT == 0 ? a.act_lo - a.act : 0;
 #pragma unroll 1
-    for (int ph = 0; ph < (dry ? 1 : 2); ++ph) {
+    for (int ph = 0; ph < 2; ++ph) {
       const DecodePhase& F = a.ph[ph];
       const int natom = F.red >> 7;
       const int64_t sb_ld = F.red >> 5;
-      Plan P = plan_of(ph, dry);
+      Plan P = s_plan[ph];
       if (ph == 1) {
         // A is complete when every CTA has finished phase 1 (all are resident: a cooperative launch)
         static_assert(kLoadWarps == 4, "epi_all's 128 threads");
@@ -734,9 +657,9 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         aborted = !epi_all<2>(!aborted);
       }
       for (; P.p < P.p1 && !aborted; P.step(ph, F.tiles, H.n_act)) {
-        const int off = dry ? 0 : s_off[P.slot], n = dry ? 1 : s_off[P.slot + 1] - off;
+        const int off = s_off[P.slot], n = s_off[P.slot + 1] - off;
         const uint32_t lo_place = (uint32_t)((n + 7) & ~7) * 128;
-        auto row_of = [&](int r) -> int64_t { return ph == 0 && !dry ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
+        auto row_of = [&](int r) -> int64_t { return ph == 0 ? (int64_t)s_tok[off + r] : (int64_t)(off + r); };
         // the first rows' sources stay in registers over the segment
         const uint8_t* src[kHeld];
 #pragma unroll
@@ -744,7 +667,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
           src[i] = F.b + (r0 + i * kRows < n ? row_of(r0 + i * kRows) : 0) * F.b_ld + j * 16;
         const uint8_t* ssrc = C::kSub ? F.sb + (sid < n ? row_of(sid) : 0) * sb_ld : nullptr;
         for (int kb = P.kb, end = P.kb + P.length(); kb < end; ++kb) {
-          if (!dry && !warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
+          if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           const uint32_t st = smem0 + stage * H.stage_bytes;
 #pragma unroll 1
           for (int s = 0; s < P.nb; ++s) {
@@ -755,8 +678,8 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
             const int go = size ? kbyte : -j * 16;
             const uint32_t dst = st + P.b_off + s * P.b_piece + place;
             auto fetch = [&](const uint8_t* from, uint32_t to) {
-              cp_async_16_if(!dry, to, from + go, size);
-              if (FMT == 0 && ph == 1) cp_async_16_if(!dry, to + lo_place, from + lo_off + go, size);
+              cp_async_16z(to, from + go, size);
+              if (FMT == 0 && ph == 1) cp_async_16z(to + lo_place, from + lo_off + go, size);
             };
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
@@ -770,11 +693,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
 #pragma unroll
               for (int sub = 0; sub < C::kSub; ++sub) {
                 const int at = kk * C::kSub + sub;
-                cp_async_4_if(!dry && at < natom, ssf + sub * 512, ssrc + at * 4);
+                if (at < natom) cp_async_4(ssf + sub * 512, ssrc + at * 4, 4u);
               }
             }
           }
-          if (dry) break;
           cp_async_arrive_noinc(smem_u32(&full[stage]));
           __syncwarp();
           advance();
@@ -866,20 +788,19 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       }
     };
 
-    // (dry: no entry exists, nothing is read or written)
-    for (Plan P = plan_of(0, dry); P.p < P.p1; P.step(0, a.ph[0].tiles, H.n_act)) {
-      const int off = dry ? 0 : s_off[P.slot], n = dry ? 1 : s_off[P.slot + 1] - off;
+    for (Plan P = s_plan[0]; P.p < P.p1; P.step(0, a.ph[0].tiles, H.n_act)) {
+      const int off = s_off[P.slot], n = s_off[P.slot + 1] - off;
       const int out_row = P.tile * 128 + row;
       const bool head = P.kb != 0, divided = !head && P.length() != P.nk;
       const int c_last = divided ? P.owner(P.p + P.L - 1) : cta;
-      if (!dry && !epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
+      if (!epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
       // Partial sums lie in float4s of four tokens: [token / 4][gate, up][row].
-      for (int x = cta + 1; x <= c_last || (dry && x == cta + 1); ++x) {
+      for (int x = cta + 1; x <= c_last; ++x) {
         for (int c0 = 0; c0 < n; c0 += 16) {
-          const int m = dry ? 0 : n - c0;
-          float4* o = reinterpret_cast<float4*>(a.part[0]) + (dry ? 0 : ((int64_t)x * (kMaxT / 4) + c0 / 4) * 256 + row);
+          const int m = n - c0;
+          float4* o = reinterpret_cast<float4*>(a.part[0]) + ((int64_t)x * (kMaxT / 4) + c0 / 4) * 256 + row;
           float4 v[8];
           until([&]() {  // eight loads in flight
             bool all = true;
@@ -905,43 +826,38 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       }
       tmem_st_wait();
       for (int c0 = 0; c0 < n; c0 += kBatch) {
-        const int m = dry ? 0 : n - c0;
         float g[kBatch], u[kBatch];
-        if (!dry) {  // (tensor memory may not be there yet)
-          tmem_ld4(tb + c0, g);
-          tmem_ld4(tb + H.ncols + c0, u);
-        }
-        if (head || dry) {  // columns past n hold something as well, and the reader skips them
+        tmem_ld4(tb + c0, g);
+        tmem_ld4(tb + H.ncols + c0, u);
+        if (head) {  // columns past n hold something as well, and the reader skips them
           float4* o = reinterpret_cast<float4*>(a.part[0]) + ((int64_t)cta * (kMaxT / 4) + c0 / 4) * 256 + row;
-          if (m > 0) {
-            store_relaxed4(o, make_float4(sent(g[0]), sent(g[1]), sent(g[2]), sent(g[3])));
-            store_relaxed4(o + 128, make_float4(sent(u[0]), sent(u[1]), sent(u[2]), sent(u[3])));
-          }
+          store_relaxed4(o, make_float4(sent(g[0]), sent(g[1]), sent(g[2]), sent(g[3])));
+          store_relaxed4(o + 128, make_float4(sent(u[0]), sent(u[1]), sent(u[2]), sent(u[3])));
+        } else {
+          finish(off + c0, n - c0, out_row, g, u);
         }
-        if (!head || dry) finish(off + c0, m, out_row, g, u);
       }
-      if (dry) break;
       release();
     }
     // this CTA's part of A is written (or it has given up, which the others must not wait for)
     epi_sync();
-    if (threadIdx.x == 64 && !dry) add_release(a.done, 1u);
+    if (threadIdx.x == 64) add_release(a.done, 1u);
 
-    Plan P = plan_of(1, dry);
+    Plan P = s_plan[1];
     for (const int p0 = P.p; P.p < P.p1 && !aborted; P.step(1, a.ph[1].tiles, H.n_act)) {
-      const int off = dry ? 0 : s_off[P.slot], n = dry ? 1 : s_off[P.slot + 1] - off;
+      const int off = s_off[P.slot], n = s_off[P.slot + 1] - off;
       const int p_end = P.p + P.length();
       const int item0 = P.tile * P.L, item1 = item0 + P.L;
       if (P.p == p0 || P.p == item0)
         for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.0f;
-      if (!dry && !epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
+      if (!epi_all(warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl))) { aborted = true; break; }
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
       const int lo = (n + 7) & ~7;  // bf16: the column of the first low part
       for (int c0 = 0; c0 < n; c0 += kBatch) {
         float v[kBatch];
-        if (!dry) tmem_ld4(tb + c0, v);
-        if (FMT == 0 && !dry) {
+        tmem_ld4(tb + c0, v);
+        if (FMT == 0) {
           float left[kBatch];
           tmem_ld4(tb + lo + c0, left);
 #pragma unroll
@@ -952,35 +868,35 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kBatch; ++c) {
           const int r = off + min(c0 + c, n - 1);
-          at[c] = s_acc + (dry ? 0 : s_tok[r]) * 128 + row;
+          at[c] = s_acc + s_tok[r] * 128 + row;
           sum[c] = *at[c] + s_w[r] * v[c];
         }
 #pragma unroll
         for (int c = 0; c < kBatch; ++c)
-          if (c0 + c < n && !dry) *at[c] = sum[c];
+          if (c0 + c < n) *at[c] = sum[c];
       }
       const bool ends = p_end == P.p1 || p_end == item1;  // this CTA's part of the output tile is complete
-      if (!dry) release();
-      if (ends || dry) {
+      release();
+      if (ends) {
         const bool head = p0 > item0;
         const int c_last = head ? cta : P.owner(item1 - 1);
-        if (!dry) epi_sync();
+        epi_sync();
         // A warp takes four tokens at a time, a lane four rows of each, from four CTAs at a time.
         const int r4 = P.tile * 128 + 4 * lane, rows = a.ph[1].rows;
         for (int t0 = (warp - 2) * 4; t0 < a.T; t0 += 16) {
-          const int m = dry ? 0 : a.T - t0;
+          const int m = a.T - t0;
           float4 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<float4*>(s_acc)[min(t0 + i, a.T - 1) * 32 + lane];
           float4* part = reinterpret_cast<float4*>(a.part[1]) + (int64_t)t0 * 32 + lane;
-          if (head || dry) {
+          if (head) {
             float4* o = part + (int64_t)cta * kMaxT * 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (i < m) store_relaxed4(o + i * 32, make_float4(sent(v[i].x), sent(v[i].y), sent(v[i].z), sent(v[i].w)));
           }
-          for (int x = cta + 1; x <= c_last || (dry && x == cta + 1); x += 4) {
-            float4* o = part + (dry ? 0 : (int64_t)x * kMaxT * 32);
+          for (int x = cta + 1; x <= c_last; x += 4) {
+            float4* o = part + (int64_t)x * kMaxT * 32;
             const int mx = c_last - x;
             float4 w4[4][4];
             until([&]() {
@@ -1012,12 +928,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
                     make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
           }
         }
-        if (!dry) epi_sync();  // s_acc has been read by other threads than its writers
+        epi_sync();  // s_acc has been read by other threads than its writers
       }
-      if (dry) break;
     }
-    if (!dry && s_ctl->abort) aborted = true;  // sums that never came
-  }
+    if (s_ctl->abort) aborted = true;  // sums that never came
   }
 
   if (aborted && lane == 0) set_error(a.err, kErrTimeout);
