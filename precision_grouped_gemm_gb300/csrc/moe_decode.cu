@@ -80,25 +80,19 @@ struct DecodeArgs {
   int32_t* err;
 };
 
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&f)[4]) {
-  uint32_t r[4];
+// Four accumulator columns of this thread's row; the values are there after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Adds v to four columns.
-__device__ __forceinline__ void tmem_add4(uint32_t taddr, const float4& v) {
-  float f[4];
-  tmem_ld4(taddr, f);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
-               "r"(__float_as_uint(f[0] + v.x)), "r"(__float_as_uint(f[1] + v.y)), "r"(__float_as_uint(f[2] + v.z)),
-               "r"(__float_as_uint(f[3] + v.w))
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, float4 v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(__float_as_uint(v.x)),
+               "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w))
                : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float as_float(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, uint32_t src_bytes) {  // 0 bytes: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
@@ -813,22 +807,33 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
             for (int i = 0; i < 4; ++i) all &= 4 * i >= m || (there(v[2 * i]) && there(v[2 * i + 1]));
             return all;
           });
+          uint32_t own[8][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (4 * i < m) {
               store_relaxed4(o + i * 256, zero4);  // ready for the next launch
               store_relaxed4(o + i * 256 + 128, zero4);
-              tmem_add4(tb + c0 + 4 * i, v[2 * i]);
-              tmem_add4(tb + H.ncols + c0 + 4 * i, v[2 * i + 1]);
+              tmem_ld4(tb + c0 + 4 * i, own[2 * i]);
+              tmem_ld4(tb + H.ncols + c0 + 4 * i, own[2 * i + 1]);
             }
           }
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (4 * (i >> 1) < m)
+              tmem_st4(tb + (i & 1) * H.ncols + c0 + 4 * (i >> 1),
+                       make_float4(as_float(own[i][0]) + v[i].x, as_float(own[i][1]) + v[i].y,
+                                   as_float(own[i][2]) + v[i].z, as_float(own[i][3]) + v[i].w));
         }
       }
       tmem_st_wait();
       for (int c0 = 0; c0 < n; c0 += kBatch) {
-        float g[kBatch], u[kBatch];
-        tmem_ld4(tb + c0, g);
-        tmem_ld4(tb + H.ncols + c0, u);
+        uint32_t gr[kBatch], ur[kBatch];
+        tmem_ld4(tb + c0, gr);
+        tmem_ld4(tb + H.ncols + c0, ur);
+        tmem_ld_wait();
+        const float g[kBatch] = {as_float(gr[0]), as_float(gr[1]), as_float(gr[2]), as_float(gr[3])};
+        const float u[kBatch] = {as_float(ur[0]), as_float(ur[1]), as_float(ur[2]), as_float(ur[3])};
         if (head) {  // columns past n hold something as well, and the reader skips them
           float4* o = reinterpret_cast<float4*>(a.part[0]) + ((int64_t)cta * (kMaxT / 4) + c0 / 4) * 256 + row;
           store_relaxed4(o, make_float4(sent(g[0]), sent(g[1]), sent(g[2]), sent(g[3])));
@@ -855,14 +860,13 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       const uint32_t tb = tmem_base + acc * H.acc_cols + ((uint32_t)(q * 32) << 16);
       const int lo = (n + 7) & ~7;  // bf16: the column of the first low part
       for (int c0 = 0; c0 < n; c0 += kBatch) {
+        uint32_t vr[kBatch], left[kBatch];
+        tmem_ld4(tb + c0, vr);
+        if (FMT == 0) tmem_ld4(tb + lo + c0, left);
+        tmem_ld_wait();
         float v[kBatch];
-        tmem_ld4(tb + c0, v);
-        if (FMT == 0) {
-          float left[kBatch];
-          tmem_ld4(tb + lo + c0, left);
 #pragma unroll
-          for (int c = 0; c < kBatch; ++c) v[c] += left[c];
-        }
+        for (int c = 0; c < kBatch; ++c) v[c] = FMT == 0 ? as_float(vr[c]) + as_float(left[c]) : as_float(vr[c]);
         float* at[kBatch];  // an expert's tokens differ, so a batch's sums are apart
         float sum[kBatch];
 #pragma unroll
