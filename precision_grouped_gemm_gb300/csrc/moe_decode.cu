@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     wid = a.w ? __ldg(a.w + lane) : 1.0f;
   }
   if (!few) {
+#pragma unroll 1
     for (int i = threadIdx.x; i < n_ids; i += kNT) {
       const int e = __ldg(a.ids + i);
       const bool ok = e >= 0 && e < a.E;
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       s_id[i] = (int16_t)(ok ? e : -1);
       s_wid[i] = a.w ? __ldg(a.w + i) : 1.0f;
     }
+#pragma unroll 1
     for (int i = threadIdx.x; i < a.E * W; i += kNT) s_mask[i] = 0;
   }
   if (warp == 0) {
@@ -353,6 +355,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     if (lane == 0) s_off[0] = 0;
     const int first = __shfl_sync(all, inc - mine, head);
     float wt = 0.0f;  // the weights of all of the token's choices of this expert
+#pragma unroll 1
     for (int i = 0; i < n_ids; ++i) {
       const float o = __shfl_sync(all, wid, i);
       if (pair >> i & 1) wt += o;
@@ -364,6 +367,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     }
   } else if (!few) {
     __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < n_ids; i += kNT) {
       const int t = i / a.k;
       if (s_id[i] >= 0) atomicOr(&s_mask[s_id[i] * W + (t >> 5)], 1u << (t & 31));
@@ -373,8 +377,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       const int per = (a.E + kNT - 1) / kNT;
       const int lo = min((int)threadIdx.x * per, a.E), hi = min(lo + per, a.E);
       int v = 0, mx = 0;  // experts << 16 | tokens
+#pragma unroll 1
       for (int e = lo; e < hi; ++e) {
         int n = 0;
+#pragma unroll 1
         for (int q = 0; q < W; ++q) n += __popc(s_mask[e * W + q]);
         if (n) v += (1 << 16) + n;
         mx = max(mx, n);
@@ -401,8 +407,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       }
       n_act = all >> 16;
       if (threadIdx.x == 0) s_off[n_act] = (uint16_t)(all & 0xFFFF);
+#pragma unroll 1
       for (int e = lo; e < hi; ++e) {
         int n = 0;
+#pragma unroll 1
         for (int q = 0; q < W; ++q) n += __popc(s_mask[e * W + q]);
         if (!n) continue;
         s_exp[run >> 16] = (uint16_t)e;
@@ -411,18 +419,22 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       }
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < n_ids; i += kNT) {
       const int e = s_id[i];
       if (e < 0) continue;
       const int t = i / a.k, i0 = t * a.k;
       bool first = true;  // the token's first choice of this expert writes the entry
+#pragma unroll 1
       for (int j = i0; j < i; ++j) first &= s_id[j] != e;
       if (!first) continue;
       int r = s_eoff[e];
+#pragma unroll 1
       for (int q = 0; q < (t >> 5); ++q) r += __popc(s_mask[e * W + q]);
       r += __popc(s_mask[e * W + (t >> 5)] & ((1u << (t & 31)) - 1u));
       s_tok[r] = (uint8_t)t;
       float wt = 0.0f;
+#pragma unroll 1
       for (int j = i; j < i0 + a.k; ++j)
         if (s_id[j] == e) wt += s_wid[j];
       s_w[r] = wt;
@@ -915,18 +927,18 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
           float4* part = reinterpret_cast<float4*>(a.part[1]) + ((int64_t)c_first * 2 * kMaxT + t) * 32 + lane;
           auto from = [&](int i) { return part + (int64_t)(2 * i + (i == 0)) * kMaxT * 32; };
           float4 sum = zero4;
-          for (int i0 = 0; i0 < m; i0 += 8) {
-            float4 v[8];
-            until([&]() {  // eight loads in flight
+          for (int i0 = 0; i0 < m; i0 += 4) {
+            float4 v[4];
+            until([&]() {  // four loads in flight (eight or sixteen were slower: more code to fetch)
               bool all = true;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = i0 + i < m ? load_relaxed4(from(i0 + i)) : zero4;
+              for (int i = 0; i < 4; ++i) v[i] = i0 + i < m ? load_relaxed4(from(i0 + i)) : zero4;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) all &= i0 + i >= m || there(v[i]);
+              for (int i = 0; i < 4; ++i) all &= i0 + i >= m || there(v[i]);
               return all;
             });
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               if (i0 + i < m) store_relaxed4(from(i0 + i), zero4);  // ready for the next launch
               sum.x += v[i].x; sum.y += v[i].y; sum.z += v[i].z; sum.w += v[i].w;
             }
