@@ -460,10 +460,12 @@ int pgg_moe_decode_workspace_size(int fmt, int64_t T, int k, int64_t H, int64_t 
  *   0 <= T <= PGG_MOE_DECODE_MAX_T (else PGG_ERR_TOO_LARGE: permute and use the grouped GEMMs),
  *   1 <= k <= 32, H and I multiples of 8 up to 65536.  A token may name an expert twice.
  * An id outside [0, E) sets *err = PGG_ERR_BAD_EXPERT and has no part.
- * ws: device scratch of pgg_moe_decode_workspace_size bytes, 16-byte aligned.  Its first 4096
- * bytes have to be zero at the first call; every call leaves them zero, so one buffer serves any
- * number of calls (of any sizes that it is large enough for) on one stream.  Zero them again after
- * a call that set PGG_ERR_TIMEOUT.  Calls that may overlap need a workspace each. */
+ * ws: device scratch of pgg_moe_decode_workspace_size bytes, 16-byte aligned, zeroed before the first
+ * call.  Every call leaves it ready for the next, so one buffer serves any number of calls, of any
+ * sizes and formats that it is large enough for, in the order of one stream.  Zero it again after a
+ * call that set PGG_ERR_TIMEOUT.  Calls that may overlap need a workspace each.
+ * One cooperative launch: the CTAs wait for one another, so the call needs the whole GPU for its
+ * time and starts when the kernels of other streams leave it. */
 int pgg_moe_decode(const void* X, const int32_t* topk_ids, const float* w, const void* W1, const void* W2, void* out,
                    int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
                    int32_t* err, void* stream);
@@ -477,6 +479,15 @@ int pgg_mx_moe_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_
                       const uint8_t* W1, const uint8_t* SW1, const uint8_t* W2, const uint8_t* SW2, void* out,
                       int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
                       int32_t* err, void* stream);
+
+/* Test hook, as pgg_test_stalled_fwd below for the few-token layer (fmt 0: bf16, SX / SW1 / SW2
+ * unused; weights 1): every CTA's load producer stops before the stall_at-th stage of its run, and
+ * every wait is limited to wait_ns.  The kernel must give up, free its tensor memory, exit and write
+ * PGG_ERR_TIMEOUT to *err.  The workspace has to be zeroed before its next use. */
+int pgg_test_stalled_moe_decode(int fmt, const void* X, const uint8_t* SX, const int32_t* topk_ids, const void* W1,
+                                const uint8_t* SW1, const void* W2, const uint8_t* SW2, void* out, int64_t T, int k,
+                                int64_t H, int64_t I, int E, int64_t stall_at, uint64_t wait_ns, void* ws,
+                                size_t ws_bytes, int32_t* err, void* stream);
 
 /* Test hook; the pages have no counterpart.  Runs the forward grouped GEMM --
  * BF16 when fmt == 0 (A = X, B = W, SA and SB unused), else the block-scaled

@@ -55,6 +55,8 @@ SIGNATURES = {
     "pgg_moe_decode": [_P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _F32, _P, ctypes.c_size_t, _P, _P],
     "pgg_mx_moe_decode": [_I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _F32, _P,
                           ctypes.c_size_t, _P, _P],
+    "pgg_test_stalled_moe_decode": [_I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _I64,
+                                    ctypes.c_uint64, _P, ctypes.c_size_t, _P, _P],
     "pgg_test_stalled_fwd": [_I32, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I64, ctypes.c_uint64, _P, _P],
 }
 

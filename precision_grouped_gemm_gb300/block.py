@@ -1,0 +1,89 @@
+"""A MoE block around the expert layer: norm, gate, routing, experts, in its two uses.
+
+Training (`MoeBlock.forward` / `backward`) goes the long way, over the permuted batch and the grouped
+GEMMs; decoding (`MoeBlock.decode`, up to 128 tokens) hands the norm's output straight to the
+few-token layer: three small kernels and one weight stream.  With `fmt` the decode weights are MX
+operands, quantized once, and the norm emits the MX operand of its tokens itself.
+
+    s = x + residual, y = rmsnorm(s) gamma     add_rmsnorm
+    logits = y gate^T                          grouped_gemm_fwd with one group
+    ids, w = top-k of the logits               moe_route
+    out = sum_j w_j expert_{ids_j}(y)          moe_permute ... moe_combine, or moe_decode
+"""
+from __future__ import annotations
+
+import dataclasses
+
+import torch
+
+from . import _binding as B
+
+
+@dataclasses.dataclass
+class MoeBlock:
+    gamma: torch.Tensor        # [H] bf16
+    gate: torch.Tensor         # [E, H] bf16, E % 8 == 0
+    W1: torch.Tensor           # [E, 2I, H] bf16 (gate | up)
+    W2: torch.Tensor           # [E, H, I] bf16
+    k: int
+    bias: torch.Tensor = None  # [E] fp32: added to the logits for the choice only
+    score: str = "softmax"
+    renormalize: bool = True
+    scale: float = 1.0
+    swiglu_limit: float = 0.0
+    eps: float = 1e-6
+    fmt: str = None            # decode weights: None (bf16), "e4m3" or "e2m1"
+
+    def __post_init__(self):
+        E, I2, H = self.W1.shape
+        self.sizes = E, H, I2 // 2
+        self._mx = None
+        self._ws = None
+        if self.fmt is not None:
+            self._mx = (*B.mx_quantize_rowwise_blocked(self.W1.view(E * I2, H), self.fmt),
+                        *B.mx_quantize_rowwise_blocked(self.W2.view(E * H, I2 // 2), self.fmt))
+
+    def _one_group(self, rows, device):
+        return torch.full((1,), rows, dtype=torch.int32, device=device)
+
+    def _route(self, y):
+        logits = B.grouped_gemm_fwd(y, self.gate[None], self._one_group(y.shape[0], y.device))
+        ids, w = B.moe_route(logits, self.k, self.bias, self.score, self.renormalize, self.scale)
+        return logits, ids, w
+
+    def forward(self, x, residual=None):
+        """-> (out [T,H], h [T,H]: the new residual stream, saved tensors for `backward`)."""
+        E, _, _ = self.sizes
+        h, y, _, _, rstd = B.add_rmsnorm(x, residual, self.gamma, self.eps)
+        logits, ids, w = self._route(y)
+        Xs, lens, pos = B.moe_permute(ids, y, E)
+        A, Hs = B.grouped_fc1_swiglu(Xs, self.W1, lens, swiglu_limit=self.swiglu_limit)
+        Ys = B.grouped_gemm_fwd(A, self.W2, lens)
+        return B.moe_combine(Ys, pos, w), h, (h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys)
+
+    def backward(self, dout, dh, saved):
+        """Gradients of `forward` -> dict: dx (of x and of residual), dgamma, dgate, dW1, dW2."""
+        h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys = saved
+        one = self._one_group(y.shape[0], y.device)
+        dYs, dw = B.moe_combine_bwd(dout, Ys, pos, w)
+        dH = B.grouped_fc2_dgrad_swiglu_bwd(dYs, self.W2, Hs, lens, swiglu_limit=self.swiglu_limit)
+        dW2 = B.grouped_gemm_wgrad(A, dYs, lens)
+        dW1 = B.grouped_gemm_wgrad(Xs, dH, lens)
+        dy = B.moe_combine(B.grouped_gemm_dgrad(dH, self.W1, lens), pos)
+        dlogits = B.moe_route_bwd(logits, ids, dw, self.bias, self.score, self.renormalize, self.scale)
+        dgate = B.grouped_gemm_wgrad(y, dlogits, one)[0]
+        dy += B.grouped_gemm_dgrad(dlogits, self.gate[None], one)
+        dx, dgamma = B.add_rmsnorm_bwd(dy, dh, h, self.gamma, rstd)
+        return {"dx": dx, "dgamma": dgamma, "dgate": dgate, "dW1": dW1, "dW2": dW2}
+
+    def decode(self, x, residual=None, err=None):
+        """`forward` for up to 128 tokens, inference only -> (out, h)."""
+        E, H, I = self.sizes
+        if self._ws is None:  # kept for the block's life: every call leaves it ready for the next
+            self._ws = B.moe_decode_workspace(128, self.k, H, I, E, self.fmt, x.device)
+        h, y, codes, scales, _ = B.add_rmsnorm(x, residual, self.gamma, self.eps, fmt=self.fmt, save_rstd=False)
+        _, ids, w = self._route(y)
+        if self.fmt is None:
+            return B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=self._ws, err=err), h
+        return B.mx_moe_decode(self.fmt, codes, scales, ids, w, *self._mx, swiglu_limit=self.swiglu_limit, ws=self._ws,
+                               err=err), h

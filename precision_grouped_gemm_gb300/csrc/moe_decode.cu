@@ -78,6 +78,8 @@ struct DecodeArgs {
   int ring_bytes;       // shared memory for the stages
   int slots_cap;        // most experts that the batch can name
   FastDiv by_grid;
+  unsigned long long wait_ns;  // limit of every wait
+  long long stall_at;          // test hook: the producer stops before this stage of its run (-1: never)
   int32_t* err;
 };
 
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       mbar_init(smem_u32(drain), 1);
       mbar_init(smem_u32(cdrain), 1);
       s_ctl->abort = 0;
-      s_ctl->limit_ns = kWaitTimeoutNs;
+      s_ctl->limit_ns = a.wait_ns;
       prefetch_tmap(&tmW1);
       prefetch_tmap(&tmW2);
     }
@@ -478,14 +480,16 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     // ------------------------------------------------------------ weights: TMA tiles, bulk scale atoms
     // The producer runs into phase 2 without waiting: its weights do not depend on phase 1.
     long long issued = 0;
+    bool stalled = false;
 #pragma unroll 1
-    for (int ph = 0; ph < 2; ++ph) {
+    for (int ph = 0; ph < 2 && !stalled; ++ph) {
       const DecodePhase& F = a.ph[ph];
       const CUtensorMap* map = ph == 0 ? &tmW1 : &tmW2;
       const int natom = F.red >> 7;  // MX: scale atoms of a 128-row block along K
-      for (Plan P = s_plan[ph]; P.p < P.p1 && !aborted; P.step(ph, F.tiles, H.n_act)) {
+      for (Plan P = s_plan[ph]; P.p < P.p1 && !aborted && !stalled; P.step(ph, F.tiles, H.n_act)) {
         const int e = s_exp[P.slot], row0 = P.tile * 128;
         for (int kb = P.kb, end = P.kb + P.length(); kb < end; ++kb) {
+          if (issued == a.stall_at) { stalled = true; break; }
           if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           if (lane == 0) {
             const uint32_t fb = smem_u32(&full[stage]);
@@ -994,10 +998,12 @@ int check_decode_dims(int fmt, int64_t T, int k, int64_t H, int64_t I, int E) {
   return PGG_OK;
 }
 
+constexpr unsigned long long kWaitLimit = kWaitTimeoutNs;
 template <int FMT>
 int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const float* w, const void* W1,
                const uint8_t* w1s, const void* W2, const uint8_t* w2s, void* out, int64_t T, int k, int64_t H,
-               int64_t I, int E, float limit, uint8_t* ws, int32_t* err, cudaStream_t s) {
+               int64_t I, int E, float limit, uint8_t* ws, int32_t* err, cudaStream_t s,
+               unsigned long long wait_ns = kWaitLimit, long long stall_at = -1) {
   DeviceInfo dev;
   int st = current_device(&dev);
   if (st != PGG_OK) return st;
@@ -1046,6 +1052,8 @@ int run_decode(const uint8_t* X, const uint8_t* xs, const int32_t* ids, const fl
   a.part[1] = a.part[0] + (size_t)kMaxCtas * kMaxT * 256;
   a.done = reinterpret_cast<unsigned*>(ws);
   a.err = err;
+  a.wait_ns = wait_ns;
+  a.stall_at = stall_at;
   a.slots_cap = std::min(E, a.T * k);
   const size_t lists = kFixedBytes + (size_t)a.T * 512 + (size_t)a.T * k * 4 + 2 * (2 * (size_t)a.slots_cap + 1) +
                        (size_t)a.T * k;
@@ -1108,10 +1116,10 @@ int pgg_moe_decode(const void* X, const int32_t* topk_ids, const float* w, const
                        E, swiglu_limit, static_cast<uint8_t*>(ws), err, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int pgg_mx_moe_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_t* topk_ids, const float* w,
-                      const uint8_t* W1, const uint8_t* SW1, const uint8_t* W2, const uint8_t* SW2, void* out,
-                      int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
-                      int32_t* err, void* stream) {
+static int mx_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_t* topk_ids, const float* w,
+                     const uint8_t* W1, const uint8_t* SW1, const uint8_t* W2, const uint8_t* SW2, void* out, int64_t T,
+                     int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes, int32_t* err,
+                     void* stream, unsigned long long wait_ns, long long stall_at) {
   if (fmt != PGG_FMT_E4M3 && fmt != PGG_FMT_E2M1) return PGG_ERR_INVALID_ARG;
   const int st = check_decode(fmt, X, topk_ids, w, W1, W2, out, T, k, H, I, E, swiglu_limit, ws, ws_bytes, err);
   if (st || T == 0) return st;
@@ -1119,7 +1127,31 @@ int pgg_mx_moe_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_
   if (!aligned_to(SX, 4) || !aligned_to(SW1, 16) || !aligned_to(SW2, 16)) return PGG_ERR_ALIGNMENT;
   auto go = fmt == PGG_FMT_E4M3 ? run_decode<kE4M3> : run_decode<kE2M1>;
   return go(X, SX, topk_ids, w, W1, SW1, W2, SW2, out, T, k, H, I, E, swiglu_limit, static_cast<uint8_t*>(ws), err,
-            reinterpret_cast<cudaStream_t>(stream));
+            reinterpret_cast<cudaStream_t>(stream), wait_ns, stall_at);
+}
+
+int pgg_mx_moe_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_t* topk_ids, const float* w,
+                      const uint8_t* W1, const uint8_t* SW1, const uint8_t* W2, const uint8_t* SW2, void* out,
+                      int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
+                      int32_t* err, void* stream) {
+  return mx_decode(fmt, X, SX, topk_ids, w, W1, SW1, W2, SW2, out, T, k, H, I, E, swiglu_limit, ws, ws_bytes, err,
+                   stream, kWaitLimit, -1);
+}
+
+int pgg_test_stalled_moe_decode(int fmt, const void* X, const uint8_t* SX, const int32_t* topk_ids, const void* W1,
+                                const uint8_t* SW1, const void* W2, const uint8_t* SW2, void* out, int64_t T, int k,
+                                int64_t H, int64_t I, int E, int64_t stall_at, uint64_t wait_ns, void* ws,
+                                size_t ws_bytes, int32_t* err, void* stream) {
+  if (stall_at < 0 || wait_ns < 100000ull || wait_ns > 1000000000ull) return PGG_ERR_INVALID_ARG;
+  if (fmt != 0)
+    return mx_decode(fmt, static_cast<const uint8_t*>(X), SX, topk_ids, nullptr, static_cast<const uint8_t*>(W1), SW1,
+                     static_cast<const uint8_t*>(W2), SW2, out, T, k, H, I, E, 0.0f, ws, ws_bytes, err, stream, wait_ns,
+                     stall_at);
+  const int st = check_decode(0, X, topk_ids, nullptr, W1, W2, out, T, k, H, I, E, 0.0f, ws, ws_bytes, err);
+  if (st || T == 0) return st;
+  return run_decode<0>(static_cast<const uint8_t*>(X), nullptr, topk_ids, nullptr, W1, nullptr, W2, nullptr, out, T, k,
+                       H, I, E, 0.0f, static_cast<uint8_t*>(ws), err, reinterpret_cast<cudaStream_t>(stream), wait_ns,
+                       stall_at);
 }
 
 }  // extern "C"

@@ -176,6 +176,13 @@ def test_decode_refusals(lib):
     assert mx(sx=None) == 1 and mx(s1=None) == 1 and mx(sx=G + 2) == 3 and mx(s2=G + 8) == 3
 
 
+def test_stall_hook_refusals(lib):
+    def run(stall=0, wait=2_000_000):
+        return lib.pgg_test_stalled_moe_decode(0, G, None, G, G, None, G, None, G, 4, 2, 256, 128, 8, stall, wait, G, 1 << 30,
+                                               None, None)
+    assert run(stall=-1) == 1 and run(wait=50_000) == 1 and run(wait=2_000_000_000) == 1
+
+
 def test_binding_refuses_wrong_tensors():
     import precision_grouped_gemm_gb300 as pgg
     bf = torch.bfloat16

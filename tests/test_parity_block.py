@@ -9,6 +9,8 @@ differ, by one step of the grid.  After an MX rounding in the middle (the activa
 few-token layer) one activation of each output may be such a step off: 1/8 of its term in e4m3, 1/2
 in e2m1."""
 
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -17,6 +19,7 @@ from oracle import block as ob
 from oracle import grouped_gemm as og
 from oracle import moe_glue as mg
 from oracle import mx as omx
+from precision_grouped_gemm_gb300 import _binding
 import util
 
 pgg = pytest.importorskip("precision_grouped_gemm_gb300")
@@ -381,6 +384,44 @@ def test_decode_workspace_is_left_ready_and_results_repeat():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, first[0])
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+@pytest.mark.parametrize("stall_at", [0, 2, 9])
+def test_decode_whose_loads_stop_gives_up(fmt, stall_at):
+    # no weights arrive after a CTA's stall_at-th stage (of 15 or more): every wait behind them runs out,
+    # the call ends with the timeout code, and the next call, on a zeroed workspace, is right
+    T, k, E, H, I = 24, 4, 24, 2048, 1024
+    g = torch.Generator(device=DEV).manual_seed(17)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV).to(BF)  # noqa: E731
+    gid = torch.from_numpy(np.random.default_rng(17).permuted(np.tile(np.arange(E, dtype=np.int32), (T, 1)), axis=1)
+                           [:, :k].copy()).to(DEV)
+    x, w1, w2 = rnd(T, H), 0.02 * rnd(E * 2 * I, H), 0.02 * rnd(E * H, I)
+    sx = s1 = s2 = None
+    if fmt is not None:
+        (x, sx), (w1, s1), (w2, s2) = (pgg.mx_quantize_rowwise(x, fmt), pgg.mx_quantize_rowwise_blocked(w1, fmt),
+                                       pgg.mx_quantize_rowwise_blocked(w2, fmt))
+    ws = pgg.moe_decode_workspace(T, k, H, I, E, fmt)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call():
+        if fmt is None:
+            return pgg.moe_decode(x, gid, None, w1.view(E, 2 * I, H), w2.view(E, H, I), ws=ws, err=err)
+        return pgg.mx_moe_decode(fmt, x, sx, gid, None, w1, s1, w2, s2, ws=ws, err=err)
+
+    good = call()
+    out = torch.zeros(T, H, dtype=BF, device=DEV)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    st = _binding.lib().pgg_test_stalled_moe_decode(
+        {None: 0, "e4m3": 1, "e2m1": 2}[fmt], p(x), p(sx), p(gid), p(w1), p(s1), p(w2), p(s2), p(out), T, k, H, I, E,
+        stall_at, 2_000_000, p(ws), ws.numel(), p(err), torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and pgg.read_error(err) == 17
+    assert time.monotonic() - t0 < 5.0
+    ws.zero_()
+    err.zero_()
+    assert torch.equal(call(), good) and pgg.read_error(err) == 0
 
 
 def test_route_decode_equals_the_long_path():
