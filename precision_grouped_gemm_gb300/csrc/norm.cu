@@ -142,20 +142,27 @@ struct NormBwdArgs {
 };
 
 // The same ownership: a thread's columns stay its own over all rows of the block, so dgamma's
-// partial sums are registers, written once per block.  A thread copies its chunks of the next
-// kDepth - 1 rows into its own places of shared memory (no thread reads another's, so a wait for its
-// own copies is enough).  With the next row alone in flight, in registers, the kernel was bound by
-// the memory's latency: 8192 x 2880 took 40 us.  With
+// partial sums are registers, written once per block.  A thread copies its chunks of the next row
+// into its own places of shared memory (no thread reads another's, so a wait for its own copies is
+// enough): with the loads in registers instead, 8192 x 2880 took 40 us; with three rows ahead, and so
+// fewer blocks, 36.5 us; as it is, 33.9 us with the reduction below (189 MB: 27.9 us at the copy
+// rate).  Instructions come next: 68% of the issue slots.  With
 // t = dy h: dgamma += rstd t, mean(u xh) = rstd mean(t gamma), dx = dh + rstd dy gamma - c h,
 // c = rstd^2 mean(u xh): six operations an element besides the conversions.
-__host__ __device__ constexpr int norm_bwd_depth(int V) { return V > 0 ? 2 : 0; }
+constexpr int kNormBwdDepth = 2;
 template <int V>
 __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  constexpr int kDepth = norm_bwd_depth(V);
+  constexpr int kDepth = kNormBwdDepth;
   extern __shared__ uint4 s_row[];  // [kDepth][3][V][blockDim]
   __shared__ float s_sum[2][32];
   const int nwarps = blockDim.x >> 5;
   float dg[V][8];
+  uint4 gam[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    gam[j] = v < a.nvec ? __ldg(a.gamma + v) : make_uint4(0, 0, 0, 0);
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(con
         float x[8], u[8], g[8];
         unpack8(h[j], x);
         unpack8(y[j], u);
-        unpack8(__ldg(a.gamma + v), g);
+        unpack8(gam[j], g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float t = u[e] * x[e];
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(con
         float x[8], u[8], g[8], o[8];
         unpack8(h[j], x);
         unpack8(y[j], u);
-        unpack8(__ldg(a.gamma + v), g);
+        unpack8(gam[j], g);
         if (a.dh) {
           unpack8(d[j], o);
         } else {
@@ -245,10 +252,10 @@ __global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(con
 }
 
 // dgamma[c] = sum over the n partial rows, in a fixed order: a block has eight columns (a 32-byte
-// sector of each row), thread (i, c) sums rows i, i + 128, ..., and the 128 sums of a column are
+// sector of each row), thread (i, c) sums rows i, i + 64, ..., and the 64 sums of a column are
 // joined by shuffles and one exchange.  Launched as the dependent of the kernel above (it waits for
 // its rows).
-constexpr int kReduceThreads = 1024;
+constexpr int kReduceThreads = 512;
 __global__ void __launch_bounds__(kReduceThreads) dgamma_reduce_kernel(const float* __restrict__ part, int n, int C,
                                                                        float* __restrict__ dgamma) {
   constexpr int kWarps = kReduceThreads / 32, kGroups = kReduceThreads / 8;
@@ -364,7 +371,7 @@ int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const voi
                 part};
   const int V = norm_bwd_v(a.nvec), threads = norm_threads(a.nvec, V);
   auto kern = V == 1 ? add_rmsnorm_bwd_kernel<1> : V == 2 ? add_rmsnorm_bwd_kernel<2> : add_rmsnorm_bwd_kernel<4>;
-  const size_t smem = (size_t)norm_bwd_depth(V) * 3 * V * threads * sizeof(uint4);
+  const size_t smem = (size_t)kNormBwdDepth * 3 * V * threads * sizeof(uint4);
   int per_sm = 0;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
