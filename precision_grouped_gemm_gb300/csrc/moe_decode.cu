@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   uint64_t* cdrain = drain + 1;
   volatile WaitCtl* s_ctl = reinterpret_cast<volatile WaitCtl*>(cdrain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<WaitCtl*>(s_ctl) + 1);
-  int* s_scan = reinterpret_cast<int*>(s_tmem + 1);  // [2 * 16]
+  int* s_last_tile = reinterpret_cast<int*>(s_tmem + 1);  // the last output tile of this CTA's run
+  int* s_scan = s_last_tile + 1;  // [2 * 16]
   Shape* s_shape = reinterpret_cast<Shape*>(s_scan + 32);
   Plan* s_plan = reinterpret_cast<Plan*>(s_shape + 1);  // [2]
   float* s_acc = reinterpret_cast<float*>(smem + a.ring_bytes + kFixedBytes);  // phase 2: [T][128]
@@ -475,6 +476,27 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   if (H.n_act == 0)  // no expert is named: the layer's output is zero
     for (int64_t i = (int64_t)cta * kNT + threadIdx.x; i < (int64_t)a.T * a.ph[1].rows; i += (int64_t)gridDim.x * kNT)
       a.out[i] = __float2bfloat16_rn(0.0f);
+
+  // Wait for another CTA's sums: repeats `load`, which says whether all of its words are there, and
+  // raises the abort flag when that takes too long.
+  auto until = [&](auto load) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !load(); ++i) {
+      if (i & 63u) continue;
+      const uint64_t t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (s_ctl->abort || t - t0 > s_ctl->limit_ns) {
+        s_ctl->abort = 1;
+        break;
+      }
+    }
+    __syncwarp();
+  };
+  auto there = [](const float4& v) {
+    return __float_as_uint(v.x) != 0u && __float_as_uint(v.y) != 0u && __float_as_uint(v.z) != 0u &&
+           __float_as_uint(v.w) != 0u;
+  };
+  const float4 zero4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights: TMA tiles, bulk scale atoms
@@ -722,26 +744,6 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     const int q = warp & 3, row = q * 32 + lane;  // accumulator row of this thread
     int acc = 0;
     uint32_t acc_phase = 0;
-    // Wait for another CTA's sums: repeats `load`, which says whether all of its words are there, and
-    // raises the abort flag when that takes too long.
-    auto until = [&](auto load) {
-      uint64_t t0 = 0;
-      for (uint32_t i = 1; !load(); ++i) {
-        if (i & 63u) continue;
-        const uint64_t t = globaltimer();
-        if (t0 == 0) t0 = t;
-        if (s_ctl->abort || t - t0 > s_ctl->limit_ns) {
-          s_ctl->abort = 1;
-          break;
-        }
-      }
-      __syncwarp();
-    };
-    auto there = [](const float4& v) {
-      return __float_as_uint(v.x) != 0u && __float_as_uint(v.y) != 0u && __float_as_uint(v.z) != 0u &&
-             __float_as_uint(v.w) != 0u;
-    };
-    const float4 zero4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto release = [&]() {  // the accumulator has been read
       tc_fence_before();
       mbar_arrive(smem_u32(&tempty[acc]));
@@ -917,44 +919,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         epi_sync();  // s_acc has been read by other threads than its writers
       }
     }
-    // The divided tiles of this CTA's run, its first and its last: each of a tile's CTAs adds up an
-    // equal share of the tokens, in CTA order.  All have sent everything before they wait here.
-    // (Left to one CTA, the sums of 42 tokens from 50 CTAs took 60 us.)
-    const Plan Q = s_plan[1];
-    for (int tile = Q.tile; Q.p < Q.p1 && !aborted; tile = last_tile) {
-      const int item0 = tile * Q.L, item1 = item0 + Q.L;
-      if (Q.p > item0 || Q.p1 < item1) {
-        const int c_first = Q.owner(item0), m = Q.owner(item1 - 1) - c_first + 1;
-        const int r4 = tile * 128 + 4 * lane, rows = a.ph[1].rows;
-        for (int t = cta - c_first + (warp - 2) * m; t < a.T; t += 4 * m) {
-          // the first CTA's sums are those of an item that begins in its run, the others' are not
-          float4* part = reinterpret_cast<float4*>(a.part[1]) + ((int64_t)c_first * 2 * kMaxT + t) * 32 + lane;
-          auto from = [&](int i) { return part + (int64_t)(2 * i + (i == 0)) * kMaxT * 32; };
-          float4 sum = zero4;
-          for (int i0 = 0; i0 < m; i0 += 4) {
-            float4 v[4];
-            until([&]() {  // four loads in flight (eight or sixteen were slower: more code to fetch)
-              bool all = true;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = i0 + i < m ? load_relaxed4(from(i0 + i)) : zero4;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) all &= i0 + i >= m || there(v[i]);
-              return all;
-            });
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i0 + i < m) store_relaxed4(from(i0 + i), zero4);  // ready for the next launch
-              sum.x += v[i].x; sum.y += v[i].y; sum.z += v[i].z; sum.w += v[i].w;
-            }
-          }
-          if (r4 < rows)
-            *reinterpret_cast<uint2*>(a.out + (int64_t)t * rows + r4) =
-                make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-        }
-      }
-      if (tile == last_tile) break;
-    }
-    if (s_ctl->abort) aborted = true;  // sums that never came
+    if (threadIdx.x == 64) *s_last_tile = last_tile;
   }
 
   if (aborted && lane == 0) set_error(a.err, kErrTimeout);
@@ -964,6 +929,46 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
+  // The divided tiles of this CTA's run, its first and its last: each of a tile's CTAs adds up an
+  // equal share of the tokens, by all of its warps and in CTA order.  All have sent everything before
+  // they wait here.  (Left to one CTA, the sums of 42 tokens from 50 CTAs took 60 us.)
+  const Plan Q = s_plan[1];
+  const int last_tile = *s_last_tile;
+  // (the whole warp goes by one reading of the flag)
+  for (int tile = Q.tile; Q.p < Q.p1 && !__any_sync(0xffffffffu, s_ctl->abort); tile = last_tile) {
+    const int item0 = tile * Q.L, item1 = item0 + Q.L;
+    if (Q.p > item0 || Q.p1 < item1) {
+      const int c_first = Q.owner(item0), m = Q.owner(item1 - 1) - c_first + 1;
+      const int r4 = tile * 128 + 4 * lane, rows = a.ph[1].rows;
+      for (int t = cta - c_first + warp * m; t < a.T; t += kNT / 32 * m) {
+        // the first CTA's sums are those of an item that begins in its run, the others' are not
+        float4* part = reinterpret_cast<float4*>(a.part[1]) + ((int64_t)c_first * 2 * kMaxT + t) * 32 + lane;
+        auto from = [&](int i) { return part + (int64_t)(2 * i + (i == 0)) * kMaxT * 32; };
+        float4 sum = zero4;
+        for (int i0 = 0; i0 < m; i0 += 4) {
+          float4 v[4];
+          until([&]() {  // four loads in flight (eight or sixteen were slower: more code to fetch)
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = i0 + i < m ? load_relaxed4(from(i0 + i)) : zero4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all &= i0 + i >= m || there(v[i]);
+            return all;
+          });
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i0 + i < m) store_relaxed4(from(i0 + i), zero4);  // ready for the next launch
+            sum.x += v[i].x; sum.y += v[i].y; sum.z += v[i].z; sum.w += v[i].w;
+          }
+        }
+        if (r4 < rows)
+          *reinterpret_cast<uint2*>(a.out + (int64_t)t * rows + r4) =
+              make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+      }
+    }
+    if (tile == last_tile) break;
+  }
+  if (s_ctl->abort && lane == 0) set_error(a.err, kErrTimeout);  // sums that never came
   // the last CTA to leave clears the count that the others have waited on
   if (threadIdx.x == 0 && atomicInc(a.done + 1, gridDim.x - 1) == gridDim.x - 1) atomicExch(a.done, 0u);
 }
