@@ -498,6 +498,23 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   };
   const float4 zero4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
+  // This CTA's sums of output tile `tile`, of which its run has reached the end or its own: stored, or
+  // sent.  Warp w of n takes a token at a time, a lane four rows of it.
+  auto flush = [&](int tile, int w, int n) {
+    const Plan& Q = s_plan[1];
+    const int item0 = tile * Q.L, r4 = tile * 128 + 4 * lane, rows = a.ph[1].rows;
+    const bool begins = Q.p <= item0, whole = begins && Q.p1 >= item0 + Q.L;
+    float4* part = reinterpret_cast<float4*>(a.part[1]) + (int64_t)(cta * 2 + begins) * kMaxT * 32 + lane;
+    for (int t = w; t < a.T; t += n) {
+      const float4 v = reinterpret_cast<float4*>(s_acc)[t * 32 + lane];
+      if (!whole)
+        store_relaxed4(part + t * 32, make_float4(sent(v.x), sent(v.y), sent(v.z), sent(v.w)));
+      else if (r4 < rows)  // rows is a multiple of 8
+        *reinterpret_cast<uint2*>(a.out + (int64_t)t * rows + r4) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ weights: TMA tiles, bulk scale atoms
     // The producer runs into phase 2 without waiting: its weights do not depend on phase 1.
@@ -900,22 +917,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         for (int c = 0; c < kBatch; ++c)
           if (c0 + c < n) *at[c] = sum[c];
       }
-      const bool ends = p_end == P.p1 || p_end == item1;  // this CTA's part of the output tile is complete
       release();
-      if (ends) {
-        const int r4 = P.tile * 128 + 4 * lane, rows = a.ph[1].rows;
-        const bool begins = p0 <= item0, whole = begins && p_end == item1;
+      if (p_end == item1 && p_end != P.p1) {  // an output tile ends inside the run (the last one: below)
         epi_sync();
-        // a warp takes a token at a time, a lane four rows of it
-        float4* part = reinterpret_cast<float4*>(a.part[1]) + (int64_t)(cta * 2 + begins) * kMaxT * 32 + lane;
-        for (int t = warp - 2; t < a.T; t += 4) {
-          const float4 v = reinterpret_cast<float4*>(s_acc)[t * 32 + lane];
-          if (!whole)
-            store_relaxed4(part + t * 32, make_float4(sent(v.x), sent(v.y), sent(v.z), sent(v.w)));
-          else if (r4 < rows)  // rows is a multiple of 8
-            *reinterpret_cast<uint2*>(a.out + (int64_t)t * rows + r4) =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        }
+        flush(P.tile, warp - 2, 4);
         epi_sync();  // s_acc has been read by other threads than its writers
       }
     }
@@ -934,6 +939,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
   // they wait here.  (Left to one CTA, the sums of 42 tokens from 50 CTAs took 60 us.)
   const Plan Q = s_plan[1];
   const int last_tile = *s_last_tile;
+  if (Q.p < Q.p1 && !__any_sync(0xffffffffu, s_ctl->abort)) flush(last_tile, warp, kNT / 32);
   // (the whole warp goes by one reading of the flag)
   for (int tile = Q.tile; Q.p < Q.p1 && !__any_sync(0xffffffffu, s_ctl->abort); tile = last_tile) {
     const int item0 = tile * Q.L, item1 = item0 + Q.L;
