@@ -3,16 +3,18 @@
 //
 //   key_e = logit_e + bias_e in fp32 (bias 0 without one); masked: key_e = -inf
 //   S     = the k largest keys, ties to the lowest expert
-//   a_e   = exp(logit_e - max) or sigmoid(logit_e); 0 for a masked expert
+//   a_e   = exp(logit_e - m) or sigmoid(logit_e); 0 for a masked expert (m: the largest logit of
+//           those that Z sums)
 //   w_j   = scale a_j / Z, Z = sum of a over all experts (softmax), over S (renormalised), or 1
 //
 //   softmax over all   dlogit_e = p_e (D_e - sum_j D_j p_j), D_j = scale dw_j, 0 outside S
 //   otherwise          dlogit_j = a_j / Z r_j (D_j - [renormalised] sum_i D_i a_i / Z), r_j = 1
 //                      (softmax) or sigmoid(-logit_j), and 0 outside S
 //
-// One warp per token, the row's keys in registers: lane l holds experts l, l + 32, ...  A key is
-// ordered as an unsigned integer, so that one warp reduction finds the largest and a second one
-// the lowest expert that has it.  Everything is fp32; sums run in a fixed order.
+// One warp per token (four tokens for a large batch of bf16 logits), the row's keys in registers: lane l
+// holds experts l, l + 32, ...  A key is ordered as an unsigned integer, so that one warp reduction finds
+// the largest and a second one the lowest expert that has it.  Everything is fp32; sums run in a fixed
+// order.
 #include <algorithm>
 #include <type_traits>
 
@@ -72,21 +74,20 @@ struct RouteArgs {
 template <typename T, int N>
 __device__ __forceinline__ bool load_row(const RouteArgs<T>& a, const T* row, int lane, float (&x)[N],
                                          uint32_t (&key)[N]) {
+  // every load before the first use: 33 x 256 logits with a bias took 3.5 us with the loads one by one
+  float bias[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = load_logit(row + min(lane + 32 * i, a.E - 1));
+#pragma unroll
+  for (int i = 0; i < N; ++i) bias[i] = a.bias ? __ldg(a.bias + min(lane + 32 * i, a.E - 1)) : 0.0f;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int e = lane + 32 * i;
-    x[i] = -INFINITY;
-    key[i] = 0;
-    if (e < a.E) {
-      const float v = load_logit(row + e);
-      // + 0 turns -0 into +0, which compares equal to it
-      const float kf = a.bias ? v + __ldg(a.bias + e) : v + 0.0f;
-      const bool nan = kf != kf;
-      bad |= nan;
-      key[i] = nan ? kOrderedNegInf : ordered(kf == 0.0f ? 0.0f : kf);
-      x[i] = key[i] == kOrderedNegInf ? -INFINITY : v;
-    }
+    const float kf = x[i] + bias[i];  // (+ 0 turns -0 into +0, which compares equal to it)
+    const bool nan = kf != kf, in = lane + 32 * i < a.E;
+    bad |= nan && in;
+    key[i] = !in ? 0u : nan ? kOrderedNegInf : ordered(kf == 0.0f ? 0.0f : kf);
+    if (key[i] <= kOrderedNegInf) x[i] = -INFINITY;
   }
   return __any_sync(kAll, bad);
 }
@@ -94,12 +95,22 @@ __device__ __forceinline__ bool load_row(const RouteArgs<T>& a, const T* row, in
 // The logit of a key that has no bias in it.
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-// Weights of one token's choices from lane j's expert, its score's argument and whether it counts.
+// The score of logit v: exp(v - m) or sigmoid(v), which is 0 below fp32's range.
+__device__ __forceinline__ float score_of(int softmax, float v, float m) { return softmax ? expf(v - m) : sigmoid(v); }
+// The softmax's m from the largest logit: over the choices for renormalised weights, which a bias may
+// have chosen far below the others, over all experts otherwise.
+__device__ __forceinline__ float shift_of(float top) {
+  return top == -INFINITY ? 0.0f : top;  // -inf: every one is masked, all weights are 0
+}
+
+// Weights of one token's choices from lane j's expert, its score's argument and whether it counts; m and
+// Z: the shift and the sum of weights that are not renormalised.
 template <typename T>
 __device__ __forceinline__ void write_choice(const RouteArgs<T>& a, int64_t t, int lane, int mine, bool masked, float v,
                                              float m, float Z, bool bad) {
-  float s = 0.0f;
-  if (lane < a.k && !masked) s = a.softmax ? expf(v - m) : sigmoid(v);
+  const bool on = lane < a.k && !masked;
+  if (a.softmax && a.renorm) m = shift_of(warp_max(on ? v : -INFINITY));
+  const float s = on ? score_of(a.softmax, v, m) : 0.0f;
   if (a.renorm) Z = warp_sum(s);
   if (lane < a.k) {
     float w = s == 0.0f ? 0.0f : a.scale * s / Z;
@@ -121,18 +132,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
   uint32_t key[N];
   const bool bad = load_row<T, N>(a, row, lane, x, key);
   float m = 0.0f, Z = 1.0f;
-  if (a.softmax) {
+  if (a.softmax && !a.renorm) {
     m = x[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
     m = warp_max(m);
     if (m == -INFINITY) m = 0.0f;  // every expert is masked: all weights are 0
-    if (!a.renorm) {
-      Z = 0.0f;
+    Z = 0.0f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) Z += expf(x[i] - m);
-      Z = warp_sum(Z);
-    }
+    for (int i = 0; i < N; ++i) Z += expf(x[i] - m);
+    Z = warp_sum(Z);
   }
   int mine = 0;         // lane j: the expert of choice j
   uint32_t my_key = 0;  // and its key
@@ -177,6 +186,11 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
           }
 }
 
+// The ordered form of a bf16 logit from its key (a negative number's ends in ones).
+__device__ __forceinline__ uint32_t ordered_bf16(uint32_t key) {
+  return key & 0x80000000u ? key & 0xFFFF0000u : key | 0xFFFFu;
+}
+
 // bf16 logits without a bias, the gate of a bf16 model: a key is the 16 ordered bits with the expert,
 // counted down, below them.  All keys differ, so one reduction gives both the largest key and the
 // lowest expert that has it, and with every lane's keys sorted a round costs the winner's lane a
@@ -216,19 +230,125 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_bf16_kernel(const 
     key[N - 1] = won ? 0u : key[N - 1];
   }
   const int mine = (int)(0xFFFFu - (my_key & 0xFFFFu));
-  // the logit back from its ordered form (a negative number's ends in ones)
-  const uint32_t o = my_key & 0x80000000u ? my_key & 0xFFFF0000u : my_key | 0xFFFFu;
+  const uint32_t o = ordered_bf16(my_key);
   const float v = unordered(o);
   const bool masked = o == kOrderedNegInf;
-  float m = __shfl_sync(kAll, v, 0), Z = 1.0f;  // the first choice is the largest
-  if (m == -INFINITY) m = 0.0f;                 // every expert is masked: all weights are 0
+  float m = 0.0f, Z = 1.0f;
   if (a.softmax && !a.renorm) {
+    m = __shfl_sync(kAll, v, 0);    // the first choice is the largest
+    if (m == -INFINITY) m = 0.0f;  // every expert is masked: all weights are 0
     Z = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) Z += expf(__uint_as_float(u[i]) - m);
     Z = warp_sum(Z);
   }
   write_choice(a, t, lane, mine, masked, v, m, Z, bad);
+}
+
+// The same for many tokens, where k <= 8 and rows are whole 16-byte chunks: eight lanes a token, so that a
+// warp's work on the choices serves four tokens.  A lane takes eight experts at a time, in pairs of
+// 16-bit halves up to their keys, sorts them, and merges them into the eight largest that it has seen:
+// the larger of best[i] and key[7 - i] are the eight largest of both, in bitonic order.  Three such
+// merges between lanes leave the token's choices in all of them.  Still bound by instructions: 16384 x
+// 256, k = 8: 5.5 us (the kernel above: 9.5; the logits at the copy rate: 1.2); 2048 x 256: 2.4 (2.8).
+// Up to kManyTokens its longer chain of steps loses: 256 x 256: 2.4 (2.15).  With 64-bit keys, for fp32
+// logits or a bias, it gained nothing over the first kernel (17 us).
+constexpr int kManyTokens = 1024;
+__device__ __forceinline__ void merge_keys(uint32_t (&best)[8], const uint32_t (&key)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) best[i] = max(best[i], key[7 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const uint32_t hi = max(best[i], best[i + d]);
+        best[i + d] = min(best[i], best[i + d]);
+        best[i] = hi;
+      }
+}
+
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_bf16_many_kernel(const RouteArgs<__nv_bfloat16> a) {
+  constexpr int kAhead = 3;  // chunks in flight
+  const int lane = threadIdx.x & 31, l = lane & 7;
+  const int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5)) * 4 + (lane >> 3);
+  const int64_t t = t0 < a.T_ ? t0 : a.T_ - 1;  // (lanes past the last token do its work and store nothing)
+  const uint4* row = reinterpret_cast<const uint4*>(a.logits + t * a.E);
+  const int nvec = a.E >> 3;
+  auto load = [&](int v) { return __ldg(row + min(v, nvec - 1)); };  // past the end: keys that are dropped
+  uint4 next[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) next[i] = load(l + 8 * i);
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f), low = __float2bfloat162_rn(-INFINITY);
+  __nv_bfloat162 any = low;  // the maximum of the logits, NaN if there is one
+  uint32_t best[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+  for (int v = l; v - l < nvec; v += 8) {
+    const uint32_t pair[4] = {next[0].x, next[0].y, next[0].z, next[0].w};
+#pragma unroll
+    for (int j = 0; j + 1 < kAhead; ++j) next[j] = next[j + 1];
+    next[kAhead - 1] = load(v + 8 * kAhead);
+    const uint32_t b = 0xFFFFu - 8 * v;
+    uint32_t key[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&pair[i]);
+      any = __hmax2_nan(any, x);
+      x = __hmax2(__hadd2_rn(x, zero), low);  // -0 as +0, a NaN as -inf
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&x);
+      uint32_t neg;  // the halves' signs, spread
+      asm("prmt.b32 %0, %1, %1, 0xBB99;" : "=r"(neg) : "r"(u));
+      const uint32_t o = u ^ (neg | 0x80008000u);
+      key[2 * i] = (o << 16) | (b - 2 * i);
+      key[2 * i + 1] = (o & 0xFFFF0000u) | (b - 2 * i - 1);
+    }
+    if (v >= nvec)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = 0;
+    sort_keys<8>(key);
+    merge_keys(best, key);
+  }
+#pragma unroll 1
+  for (int d = 1; d < 8; d <<= 1) {
+    uint32_t other[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, best[i], d);
+    merge_keys(best, other);
+  }
+  const float2 top = __bfloat1622float2(any);
+  const bool bad = (__ballot_sync(kAll, top.x != top.x || top.y != top.y) >> (lane & 24) & 0xFFu) != 0;
+  uint32_t my_key = best[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) my_key = l == i ? best[i] : my_key;
+  const uint32_t o = ordered_bf16(my_key);
+  const bool on = l < a.k && o != kOrderedNegInf;
+  const float v = unordered(o), m = shift_of(unordered(ordered_bf16(best[0])));  // the first choice is the largest
+  auto sum8 = [](float x) {
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+    return x;
+  };
+  float Z = 1.0f;
+  const float s = on ? score_of(a.softmax, v, m) : 0.0f;
+  if (a.renorm) {
+    Z = sum8(s);
+  } else if (a.softmax) {
+    Z = 0.0f;
+#pragma unroll 1
+    for (int i = l; i < nvec; i += 8) {
+      float x[8];
+      unpack8(__ldg(row + i), x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) Z += expf(x[j] - m);
+    }
+    Z = sum8(Z);
+  }
+  if (l < a.k && t0 < a.T_) {
+    float w = s == 0.0f ? 0.0f : a.scale * s / Z;
+    if (bad) w = __uint_as_float(0x7FC00000u);
+    a.ids[t * a.k + l] = (int)(0xFFFFu - (my_key & 0xFFFFu));
+    a.w[t * a.k + l] = w;
+  }
 }
 
 template <typename T, int N>
@@ -276,13 +396,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_bwd_kernel(const R
     dot = warp_sum(D * p);
     c = D;
   } else {
-    if (a.softmax) {
-      float m = warp_max(v);
-      if (m == -INFINITY) m = 0.0f;
-      p = expf(v - m);
-    } else {
-      p = lane < a.k && id >= 0 ? sigmoid(v) : 0.0f;
-    }
+    const bool on = lane < a.k && id >= 0 && v != -INFINITY;
+    const float m = a.softmax ? shift_of(warp_max(on ? v : -INFINITY)) : 0.0f;
+    p = on ? score_of(a.softmax, v, m) : 0.0f;
     if (a.renorm) {
       const float Z = warp_sum(p);
       p = p == 0.0f ? 0.0f : p / Z;
@@ -315,7 +431,10 @@ void launch_route(const RouteArgs<T>& a, cudaStream_t s) {
     else {
       if constexpr (std::is_same_v<T, __nv_bfloat16>) {
         if (!a.bias) {
-          moe_route_bf16_kernel<decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
+          if (a.k <= 8 && a.E % 8 == 0 && a.T_ > kManyTokens)
+            moe_route_bf16_many_kernel<<<(grid + 3) / 4, kRouteWarps * 32, 0, s>>>(a);
+          else
+            moe_route_bf16_kernel<decltype(N)::value><<<grid, kRouteWarps * 32, 0, s>>>(a);
           return;
         }
       }

@@ -236,6 +236,61 @@ def test_moe_route_masked_rows_nan_inf_and_ties():
     assert pgg.moe_route(torch.empty(0, 8, device=DEV), 2)[0].shape == (0, 2)
 
 
+@pytest.mark.parametrize("T,E,k", [(1025, 8, 8), (1026, 8, 1), (1027, 16, 3), (1100, 72, 7), (1031, 256, 8),
+                                   (1028, 512, 6), (1029, 1024, 8)])
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("dtype,bias", [("bf16", False), ("bf16", True), ("f32", False), ("f32", True)])
+def test_moe_route_many_tokens(T, E, k, score, renormalize, dtype, bias):
+    rng = np.random.default_rng(T + E)
+    # few different values, so that most choices are ties; masked places, a NaN row, a row masked whole
+    x = torch.from_numpy(rng.integers(-4, 5, (64, E)).astype(np.float32) / 2)
+    x[torch.from_numpy(rng.random((64, E)) < 0.2)] = -float("inf")
+    x[11, E // 3] = float("nan")
+    x[20] = -float("inf")
+    rows = rng.integers(0, 64, T)
+    rows[-3:] = (11, 20, 5)
+    x = x.to(BF if dtype == "bf16" else torch.float32)
+    b = torch.from_numpy(rng.integers(-4, 5, E).astype(np.float32) / 2) if bias else None
+    ids, w = pgg.moe_route(x[rows].to(DEV), k, None if b is None else b.to(DEV), score, renormalize, 2.5)
+    rid, rw = ob.moe_route(_np(x), None if b is None else b.numpy(), k, score, renormalize, 2.5)
+    np.testing.assert_array_equal(ids.cpu().numpy(), rid[rows])
+    _close(w, rw[rows], np.abs(rw[rows]), F32_REL, "w")
+
+
+def test_moe_route_bf16_every_value():
+    # every bf16 value but the NaNs, in rows of 256 in random order: signs, zeros, subnormals, infinities
+    v = np.arange(65536, dtype=np.uint16)
+    v = np.random.default_rng(3).permutation(v[(v & 0x7FFF) <= 0x7F80])
+    v = v[:len(v) // 256 * 256].reshape(-1, 256)
+    x = torch.from_numpy(v.astype(np.int32) << 16).view(torch.float32).to(BF)
+    for E, times in ((256, 1), (256, 5), (255, 5)):  # few tokens and many; in whole chunks, and not
+        y = x[:, :E].contiguous()
+        ids, w = pgg.moe_route(y.repeat(times, 1).to(DEV), 8, None, "sigmoid", True)
+        rid, rw = ob.moe_route(_np(y), None, 8, "sigmoid", True, 1.0)
+        np.testing.assert_array_equal(ids.cpu().numpy(), np.tile(rid, (times, 1)))
+        _close(w, np.tile(rw, (times, 1)), np.abs(np.tile(rw, (times, 1))), F32_REL, "w")
+
+
+@pytest.mark.parametrize("T", [3, 1027])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_moe_route_chosen_far_below(T, dtype):
+    # the bias chooses experts whose scores are below fp32's range next to the largest logit's:
+    # the renormalised weights do not depend on that
+    x = torch.full((T, 8), 3.0)
+    x[:, 2], x[:, 5], x[:, 7] = -200.0, -201.0, -199.0
+    b = torch.full((8,), -1000.0)
+    b[2], b[5], b[7] = 0.0, 1.0, 0.5
+    x = x.to(BF if dtype == "bf16" else torch.float32)
+    ids, w = pgg.moe_route(x.to(DEV), 3, b.to(DEV), "softmax", True)
+    rid, rw = ob.moe_route(_np(x), b.numpy(), 3, "softmax", True, 1.0)
+    np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+    _close(w, rw, np.abs(rw), F32_REL, "w")
+    dw = torch.tensor([[1.0, -2.0, 0.5]]).repeat(T, 1)
+    d = pgg.moe_route_bwd(x.to(DEV), ids, dw.to(DEV), b.to(DEV), "softmax", True)
+    ref = ob.moe_route_bwd(_np(x), b.numpy(), rid, dw.double().numpy(), "softmax", True, 1.0)
+    _close(d, ref, 3.5 * np.ones_like(ref), BF16_REL if dtype == "bf16" else F32_REL, "dlogits")
+
+
 def test_moe_route_bwd_ids_of_other_kinds():
     # an id out of range has no part; an expert named twice gets both terms
     x = torch.tensor([[0.5, -1.0, 2.0, 0.0]], device=DEV)
