@@ -291,6 +291,19 @@ def test_moe_route_chosen_far_below(T, dtype):
     _close(d, ref, 3.5 * np.ones_like(ref), BF16_REL if dtype == "bf16" else F32_REL, "dlogits")
 
 
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", False)])
+def test_moe_route_bwd_masked_choice_has_no_part(score, renormalize):
+    # two experts left of eight: the third choice is masked, and its dw (here not a number) is not used
+    x = torch.full((5, 8), -float("inf"))
+    x[:, 3], x[:, 6] = 0.5, -0.25
+    ids, _ = pgg.moe_route(x.to(DEV), 3, None, score, renormalize)
+    dw = torch.tensor([[1.0, 2.0, 0.0]]).repeat(5, 1)
+    ref = ob.moe_route_bwd(_np(x), None, ids.cpu().numpy(), dw.double().numpy(), score, renormalize, 1.0)
+    dw[:, 2] = float("nan")
+    d = pgg.moe_route_bwd(x.to(DEV), ids, dw.to(DEV), None, score, renormalize)
+    _close(d, ref, 3.0 * np.ones_like(ref), F32_REL, "dlogits")
+
+
 def test_moe_route_bwd_ids_of_other_kinds():
     # an id out of range has no part; an expert named twice gets both terms
     x = torch.tensor([[0.5, -1.0, 2.0, 0.0]], device=DEV)
