@@ -35,6 +35,7 @@ constexpr int kMaxT = PGG_MOE_DECODE_MAX_T;
 constexpr int kMaxCtas = 160;   // CTAs of a launch (one per SM); sizes the workspace without a device
 constexpr int kMaxStages = 8;
 constexpr int kLoadWarps = 4;   // warps that fetch the token operand
+constexpr int kFin = 2;
 constexpr int kBatch = 4;      // tokens that the epilogue works on at a time
 constexpr int kFixedBytes = 768;  // barriers, plans
 constexpr int kTileBytes = 128 * 128;  // 128 rows x one 128-byte swizzle atom of K
@@ -88,6 +89,12 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[2]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[1]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, float4 v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(__float_as_uint(v.x)),
@@ -768,10 +775,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     };
     // The activations of this thread's row for kBatch entries from r on, of which m exist: a batch is
     // computed whole, so that its exponentials, maxima and conversions overlap.
-    auto finish = [&](int r, int m, int out_row, const float (&g)[kBatch], const float (&u)[kBatch]) {
-      float v[kBatch];
+    auto finish = [&](int r, int m, int out_row, const float (&g)[kFin], const float (&u)[kFin]) {
+      float v[kFin];
 #pragma unroll
-      for (int c = 0; c < kBatch; ++c) {
+      for (int c = 0; c < kFin; ++c) {
         float gate = g[c], up = u[c];
         if (a.limit > 0.0f) {  // NaN stays NaN
           gate = gate > a.limit ? a.limit : gate;
@@ -785,7 +792,7 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(a.act) + at;
         __nv_bfloat16* act_lo = reinterpret_cast<__nv_bfloat16*>(a.act_lo) + at;
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < kFin; ++c) {
           // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
           const __nv_bfloat16 hi = __float2bfloat16_rn(v[c]);
           const float left = v[c] - __bfloat162float(hi);
@@ -796,16 +803,16 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         }
       } else {
         // the warp's 32 rows are one MX block of each entry
-        uint32_t sc[kBatch];
+        uint32_t sc[kFin];
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < kFin; ++c) {
           const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(v[c]) & 0x7FFFFFFFu);
           float mult;
           const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(am, sc[c], mult);
           v[c] = fin ? v[c] * mult : 0.0f;
         }
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < kFin; ++c) {
           const int64_t e = at + (int64_t)c * a.I;
           if (FMT == kE4M3) {
             if (c < m) a.act[e] = (uint8_t)cvt_e4m3x2(v[c], 0.0f);
@@ -863,18 +870,30 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         }
       }
       tmem_st_wait();
-      for (int c0 = 0; c0 < n; c0 += kBatch) {
-        uint32_t gr[kBatch], ur[kBatch];
-        tmem_ld4(tb + c0, gr);
-        tmem_ld4(tb + H.ncols + c0, ur);
-        tmem_ld_wait();
-        const float g[kBatch] = {as_float(gr[0]), as_float(gr[1]), as_float(gr[2]), as_float(gr[3])};
-        const float u[kBatch] = {as_float(ur[0]), as_float(ur[1]), as_float(ur[2]), as_float(ur[3])};
-        if (head) {  // columns past n hold something as well, and the reader skips them
+      if (head) {  // columns past n hold something as well, and the reader skips them
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += 4) {
+          uint32_t g[4], u[4];
+          tmem_ld4(tb + c0, g);
+          tmem_ld4(tb + H.ncols + c0, u);
+          tmem_ld_wait();
           float4* o = reinterpret_cast<float4*>(a.part[0]) + ((int64_t)cta * (kMaxT / 4) + c0 / 4) * 256 + row;
-          store_relaxed4(o, make_float4(sent(g[0]), sent(g[1]), sent(g[2]), sent(g[3])));
-          store_relaxed4(o + 128, make_float4(sent(u[0]), sent(u[1]), sent(u[2]), sent(u[3])));
-        } else {
+          store_relaxed4(o, make_float4(sent(as_float(g[0])), sent(as_float(g[1])), sent(as_float(g[2])), sent(as_float(g[3]))));
+          store_relaxed4(o + 128, make_float4(sent(as_float(u[0])), sent(as_float(u[1])), sent(as_float(u[2])), sent(as_float(u[3]))));
+        }
+      } else {
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += kFin) {
+          uint32_t gr[kFin], ur[kFin];
+          tmem_ldn(tb + c0, gr);
+          tmem_ldn(tb + H.ncols + c0, ur);
+          tmem_ld_wait();
+          float g[kFin], u[kFin];
+#pragma unroll
+          for (int c = 0; c < kFin; ++c) {
+            g[c] = as_float(gr[c]);
+            u[c] = as_float(ur[c]);
+          }
           finish(off + c0, n - c0, out_row, g, u);
         }
       }
