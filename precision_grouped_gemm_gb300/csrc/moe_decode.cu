@@ -35,7 +35,6 @@ constexpr int kMaxT = PGG_MOE_DECODE_MAX_T;
 constexpr int kMaxCtas = 160;   // CTAs of a launch (one per SM); sizes the workspace without a device
 constexpr int kMaxStages = 8;
 constexpr int kLoadWarps = 4;   // warps that fetch the token operand
-constexpr int kFin = 2;
 constexpr int kBatch = 4;      // tokens that the epilogue works on at a time
 constexpr int kFixedBytes = 768;  // barriers, plans
 constexpr int kTileBytes = 128 * 128;  // 128 rows x one 128-byte swizzle atom of K
@@ -90,11 +89,8 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[2]) {
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t (&r)[2]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[1]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, float4 v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(__float_as_uint(v.x)),
@@ -773,56 +769,12 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       mbar_arrive(smem_u32(&tempty[acc]));
       if (++acc == H.nacc) { acc = 0; acc_phase ^= 1u; }
     };
-    // The activations of this thread's row for kBatch entries from r on, of which m exist: a batch is
-    // computed whole, so that its exponentials, maxima and conversions overlap.
-    auto finish = [&](int r, int m, int out_row, const float (&g)[kFin], const float (&u)[kFin]) {
-      float v[kFin];
-#pragma unroll
-      for (int c = 0; c < kFin; ++c) {
-        float gate = g[c], up = u[c];
-        if (a.limit > 0.0f) {  // NaN stays NaN
-          gate = gate > a.limit ? a.limit : gate;
-          up = up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up);
-        }
-        v[c] = silu_f(gate) * up;
+    auto activation = [&](float gate, float up) {
+      if (a.limit > 0.0f) {  // NaN stays NaN
+        gate = gate > a.limit ? a.limit : gate;
+        up = up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up);
       }
-      const int64_t at = (int64_t)r * a.I + out_row;
-      if (FMT == 0) {
-        if (out_row >= a.I) return;
-        __nv_bfloat16* act = reinterpret_cast<__nv_bfloat16*>(a.act) + at;
-        __nv_bfloat16* act_lo = reinterpret_cast<__nv_bfloat16*>(a.act_lo) + at;
-#pragma unroll
-        for (int c = 0; c < kFin; ++c) {
-          // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
-          const __nv_bfloat16 hi = __float2bfloat16_rn(v[c]);
-          const float left = v[c] - __bfloat162float(hi);
-          if (c < m) {
-            act[(int64_t)c * a.I] = hi;
-            act_lo[(int64_t)c * a.I] = __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.0f);
-          }
-        }
-      } else {
-        // the warp's 32 rows are one MX block of each entry
-        uint32_t sc[kFin];
-#pragma unroll
-        for (int c = 0; c < kFin; ++c) {
-          const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(v[c]) & 0x7FFFFFFFu);
-          float mult;
-          const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(am, sc[c], mult);
-          v[c] = fin ? v[c] * mult : 0.0f;
-        }
-#pragma unroll
-        for (int c = 0; c < kFin; ++c) {
-          const int64_t e = at + (int64_t)c * a.I;
-          if (FMT == kE4M3) {
-            if (c < m) a.act[e] = (uint8_t)cvt_e4m3x2(v[c], 0.0f);
-          } else {
-            const float y = __shfl_down_sync(0xffffffffu, v[c], 1);
-            if (c < m && (lane & 1) == 0) a.act[e >> 1] = (uint8_t)cvt_e2m1x2(v[c], y);
-          }
-          if (c < m && lane == 0) a.act_scales[e >> 5] = (uint8_t)sc[c];
-        }
-      }
+      return silu_f(gate) * up;
     };
 
     for (Plan P = s_plan[0]; P.p < P.p1; P.step(0, a.ph[0].tiles, H.n_act)) {
@@ -882,19 +834,45 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
           store_relaxed4(o + 128, make_float4(sent(as_float(u[0])), sent(as_float(u[1])), sent(as_float(u[2])), sent(as_float(u[3]))));
         }
       } else {
+        // Two tokens at a time: the even lanes store the first one's, the odd lanes the second one's, two
+        // rows each, so that both take one conversion and one store.
+        const int odd = lane & 1;
+        int64_t at = (int64_t)(off + odd) * a.I + (out_row & ~1);
 #pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += kFin) {
-          uint32_t gr[kFin], ur[kFin];
-          tmem_ldn(tb + c0, gr);
-          tmem_ldn(tb + H.ncols + c0, ur);
+        for (int c0 = 0; c0 < n; c0 += 2, at += 2 * (int64_t)a.I) {
+          uint32_t g[2], u[2];
+          tmem_ld2(tb + c0, g);
+          tmem_ld2(tb + H.ncols + c0, u);
           tmem_ld_wait();
-          float g[kFin], u[kFin];
-#pragma unroll
-          for (int c = 0; c < kFin; ++c) {
-            g[c] = as_float(gr[c]);
-            u[c] = as_float(ur[c]);
+          const float v0 = activation(as_float(g[0]), as_float(u[0])), v1 = activation(as_float(g[1]), as_float(u[1]));
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+          float x = odd ? other : v0, y = odd ? v1 : other;
+          const bool on = c0 + odd < n;
+          if (FMT == 0) {
+            // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
+            x -= __low2float(hi);
+            y -= __high2float(hi);
+            if (on && out_row < a.I) {
+              *reinterpret_cast<__nv_bfloat162*>(a.act + 2 * at) = hi;
+              *reinterpret_cast<uint32_t*>(a.act_lo + 2 * at) =
+                  pack_bf16x2(fabsf(x) < INFINITY ? x : 0.0f, fabsf(y) < INFINITY ? y : 0.0f);
+            }
+          } else {
+            // the warp's 32 rows are one MX block of each token
+            const uint32_t am0 = __reduce_max_sync(0xffffffffu, __float_as_uint(v0) & 0x7FFFFFFFu);
+            const uint32_t am1 = __reduce_max_sync(0xffffffffu, __float_as_uint(v1) & 0x7FFFFFFFu);
+            uint32_t sc;
+            float mult;
+            const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(odd ? am1 : am0, sc, mult);
+            x = fin ? x * mult : 0.0f;
+            y = fin ? y * mult : 0.0f;
+            if (on) {
+              if (FMT == kE4M3) *reinterpret_cast<uint16_t*>(a.act + at) = (uint16_t)cvt_e4m3x2(x, y);
+              else a.act[at >> 1] = (uint8_t)cvt_e2m1x2(x, y);
+              if (lane < 2) a.act_scales[at >> 5] = (uint8_t)sc;
+            }
           }
-          finish(off + c0, n - c0, out_row, g, u);
         }
       }
       release();
