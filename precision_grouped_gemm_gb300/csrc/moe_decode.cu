@@ -115,6 +115,11 @@ template <int N>
 __device__ __forceinline__ void start_arrive() { asm volatile("barrier.cta.arrive 3, %0;" ::"n"(N) : "memory"); }
 template <int N>
 __device__ __forceinline__ void start_wait() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(N) : "memory"); }
+// The other warps have read the list's scratch in the ring for the last time; warp 0 may load over it.
+template <int N>
+__device__ __forceinline__ void scratch_arrive() { asm volatile("barrier.cta.arrive 4, %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void scratch_wait() { asm volatile("barrier.cta.sync 4, %0;" ::"n"(N) : "memory"); }
 
 // Partial sums travel without flags or fences: a word that is not zero is a sum.  (A release under a
 // full load of weight reads took 2 to 5 us on this path.)  A zero sum is sent as -0, which adds the
@@ -281,9 +286,11 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- the batch's experts and their tokens (scratch: the ring, before the first stage lands)
+  // ---- the batch's experts and their tokens.  Scratch: the place of phase 2's sums; where that is too
+  // small (many experts, few tokens), the ring, before the first stage lands.
   const int W = (a.T + 31) / 32;  // mask words per expert
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem);               // [E][W]
+  const bool in_ring = a.E * (4 * W + 2) + a.T * a.k * 6 > a.T * 512;
+  uint32_t* s_mask = in_ring ? reinterpret_cast<uint32_t*>(smem) : reinterpret_cast<uint32_t*>(s_acc);  // [E][W]
   float* s_wid = reinterpret_cast<float*>(s_mask + a.E * W);          // [T k]: the weights as given
   int16_t* s_id = reinterpret_cast<int16_t*>(s_wid + a.T * a.k);      // [T k]: the ids, -1 out of range
   uint16_t* s_eoff = reinterpret_cast<uint16_t*>(s_id + a.T * a.k);   // [E]: first entry
@@ -425,8 +432,24 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
       }
     }
     __syncthreads();
+  }
+  // Warp 0 knows enough for the first weights; the others write the experts' entries meanwhile.
+  if (warp == 0) {
+    if (lane < 2) {
+      Shape S;
+      Plan P{};
+      make_plan<FMT>(a, n_act, max_n, lane, S, P);
+      s_plan[lane] = P;
+      if (lane == 0) *s_shape = S;
+    }
+    __syncwarp();
+    if (!few && in_ring) {
+      scratch_wait<kNT>();
+      fence_proxy_async_smem();
+    }
+  } else if (!few) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < n_ids; i += kNT) {
+    for (int i = threadIdx.x - 32; i < n_ids; i += kNT - 32) {
       const int e = s_id[i];
       if (e < 0) continue;
       const int t = i / a.k, i0 = t * a.k;
@@ -445,20 +468,10 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         if (s_id[j] == e) wt += s_wid[j];
       s_w[r] = wt;
     }
-  }
-  if (!few) {
-    fence_proxy_async_smem();  // the ring's scratch use, before its first bulk copies
-    __syncthreads();
-  }
-  if (warp == 0) {
-    if (lane < 2) {
-      Shape S;
-      Plan P{};
-      make_plan<FMT>(a, n_act, max_n, lane, S, P);
-      s_plan[lane] = P;
-      if (lane == 0) *s_shape = S;
+    if (in_ring) {
+      fence_proxy_async_smem();
+      scratch_arrive<kNT>();
     }
-    __syncwarp();
   }
 
   const int cta = blockIdx.x;

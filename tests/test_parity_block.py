@@ -383,6 +383,17 @@ def test_mx_moe_decode(T, k, E, H, I, fmt):
 
 
 @pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+@pytest.mark.parametrize("T,k,E", [(9, 4, 1000), (2, 32, 200), (12, 3, 1024)])
+def test_decode_many_experts_few_tokens(T, k, E, fmt):
+    ids, w, dev, ref = _layer(T, k, E, 128, 128, fmt, T + E)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for _ in range(3):
+        out = _call(fmt, dev, err=err)
+        assert pgg.read_error(err) == 0
+        _check_layer(out, ids, w, ref, fmt)
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
 def test_decode_skewed_and_repeated_experts(fmt):
     # most tokens on one expert, and tokens that name an expert several times: the weights add up
     ids, w, dev, ref = _layer(60, 5, 12, 256, 256, fmt, 11, distinct=False, skew=2.0)
