@@ -848,42 +848,52 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
         }
       } else {
         // Two tokens at a time: the even lanes store the first one's, the odd lanes the second one's, two
-        // rows each, so that both take one conversion and one store.
+        // rows each, so that both take one conversion and one store.  Two such pairs overlap.
         const int odd = lane & 1;
         int64_t at = (int64_t)(off + odd) * a.I + (out_row & ~1);
 #pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += 2, at += 2 * (int64_t)a.I) {
-          uint32_t g[2], u[2];
-          tmem_ld2(tb + c0, g);
-          tmem_ld2(tb + H.ncols + c0, u);
+        for (int c0 = 0; c0 < n; c0 += 4) {
+          uint32_t g[4], u[4];
+          tmem_ld4(tb + c0, g);
+          tmem_ld4(tb + H.ncols + c0, u);
           tmem_ld_wait();
-          const float v0 = activation(as_float(g[0]), as_float(u[0])), v1 = activation(as_float(g[1]), as_float(u[1]));
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-          float x = odd ? other : v0, y = odd ? v1 : other;
-          const bool on = c0 + odd < n;
-          if (FMT == 0) {
-            // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
-            x -= __low2float(hi);
-            y -= __high2float(hi);
-            if (on && out_row < a.I) {
-              *reinterpret_cast<__nv_bfloat162*>(a.act + 2 * at) = hi;
-              *reinterpret_cast<uint32_t*>(a.act_lo + 2 * at) =
-                  pack_bf16x2(fabsf(x) < INFINITY ? x : 0.0f, fabsf(y) < INFINITY ? y : 0.0f);
-            }
-          } else {
-            // the warp's 32 rows are one MX block of each token
-            const uint32_t am0 = __reduce_max_sync(0xffffffffu, __float_as_uint(v0) & 0x7FFFFFFFu);
-            const uint32_t am1 = __reduce_max_sync(0xffffffffu, __float_as_uint(v1) & 0x7FFFFFFFu);
-            uint32_t sc;
-            float mult;
-            const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(odd ? am1 : am0, sc, mult);
-            x = fin ? x * mult : 0.0f;
-            y = fin ? y * mult : 0.0f;
-            if (on) {
-              if (FMT == kE4M3) *reinterpret_cast<uint16_t*>(a.act + at) = (uint16_t)cvt_e4m3x2(x, y);
-              else a.act[at >> 1] = (uint8_t)cvt_e2m1x2(x, y);
-              if (lane < 2) a.act_scales[at >> 5] = (uint8_t)sc;
+          float v[4], x[2], y[2];
+          uint32_t am[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = activation(as_float(g[c]), as_float(u[c]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (FMT != 0) am[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+            x[i] = odd ? other : v[2 * i];
+            y[i] = odd ? v[2 * i + 1] : other;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i, at += 2 * (int64_t)a.I) {
+            const bool on = c0 + 2 * i + odd < n;
+            if (FMT == 0) {
+              // A as the sum of two bf16 numbers (16 mantissa bits): both are multiplied
+              const __nv_bfloat162 hi = __floats2bfloat162_rn(x[i], y[i]);
+              const float lx = x[i] - __low2float(hi), ly = y[i] - __high2float(hi);
+              if (on && out_row < a.I) {
+                *reinterpret_cast<__nv_bfloat162*>(a.act + 2 * at) = hi;
+                *reinterpret_cast<uint32_t*>(a.act_lo + 2 * at) =
+                    pack_bf16x2(fabsf(lx) < INFINITY ? lx : 0.0f, fabsf(ly) < INFINITY ? ly : 0.0f);
+              }
+            } else {
+              // the warp's 32 rows are one MX block of each token
+              uint32_t sc;
+              float mult;
+              const bool fin = block_scale_f32<FMT == 0 ? kE4M3 : FMT>(odd ? am[2 * i + 1] : am[2 * i], sc, mult);
+              x[i] = fin ? x[i] * mult : 0.0f;
+              y[i] = fin ? y[i] * mult : 0.0f;
+              if (on) {
+                if (FMT == kE4M3) *reinterpret_cast<uint16_t*>(a.act + at) = (uint16_t)cvt_e4m3x2(x[i], y[i]);
+                else a.act[at >> 1] = (uint8_t)cvt_e2m1x2(x[i], y[i]);
+                if (lane < 2) a.act_scales[at >> 5] = (uint8_t)sc;
+              }
             }
           }
         }
