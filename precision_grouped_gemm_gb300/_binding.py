@@ -448,7 +448,8 @@ def moe_combine_bwd(dOut, Ys, pos, w, dYs=None, dw=None, stream=None):
 
 
 def _in(t, what, dtype, shape):
-    """The address of a caller's tensor of this type and shape (None for None); _dev checks the rest."""
+    """The address of a caller's tensor of this type and shape (None for None); _dev checks the rest
+    of what the caller has given."""
     if t is None:
         return None
     if t.dtype is not dtype:
@@ -458,10 +459,19 @@ def _in(t, what, dtype, shape):
     return t.data_ptr()
 
 
-def _out(t, what, dtype, shape, device):
+def _new(make, shape, dtype, device, stream):
+    """A new tensor in the order of the call's stream (None: the current one)."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _out(t, what, dtype, shape, device, stream):
     """The caller's output tensor or a new one, and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = (torch.empty(shape, dtype=dtype, device=device) if stream is None
+             else _new(torch.empty, shape, dtype, device, stream))
         return t, t.data_ptr()
     return t, _in(t, what, dtype, shape)
 
@@ -486,23 +496,24 @@ def add_rmsnorm(x, residual, gamma, eps=1e-6, fmt=None, h=None, y=None, codes=No
 
     -> (h = bf16(s), y, codes, scales, rstd): y None with save_y=False, codes / scales (the
     row-wise MX operand in `fmt`) None without fmt, rstd None with save_rstd=False."""
+    given = x, residual, gamma, h, y, codes, scales, rstd
     R, C = shape = x.shape
     dev = x.device
     f = 0 if fmt is None else _FMT[fmt]
     px, pr = _in(x, "x", _BF, shape), _in(residual, "residual", _BF, shape)
     pg = _in(gamma, "gamma", _BF, (C,))
-    h, ph = _out(h, "h", _BF, shape, dev)
+    h, ph = _out(h, "h", _BF, shape, dev, stream)
     py = pc = ps = pd = None
     if save_y or y is not None:
-        y, py = _out(y, "y", _BF, shape, dev)
+        y, py = _out(y, "y", _BF, shape, dev, stream)
     if f:
-        codes, pc = _out(codes, "codes", _U8, (R, C if f == FMT_E4M3 else C // 2), dev)
-        scales, ps = _out(scales, "scales", _U8, (R, C // 32), dev)
+        codes, pc = _out(codes, "codes", _U8, (R, C if f == FMT_E4M3 else C // 2), dev, stream)
+        scales, ps = _out(scales, "scales", _U8, (R, C // 32), dev, stream)
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales need fmt")
     if save_rstd or rstd is not None:
-        rstd, pd = _out(rstd, "rstd", _F, (R,), dev)
-    _dev(x, residual, gamma, h, y, codes, scales, rstd)
+        rstd, pd = _out(rstd, "rstd", _F, (R,), dev, stream)
+    _dev(*given)
     _check(lib().pgg_add_rmsnorm(px, pr, pg, R, C, eps, f, ph, py, pc, ps, pd, _stream(stream)), "pgg_add_rmsnorm")
     return h, y, codes, scales, rstd
 
@@ -514,15 +525,16 @@ def add_rmsnorm_bwd_workspace_size(R: int, C: int) -> int:
 def add_rmsnorm_bwd(dy, dh, h, gamma, rstd, dx=None, dgamma=None, ws=None, stream=None):
     """Backward of add_rmsnorm: dy [R,C] bf16, dh the gradient of h (or None), h and rstd as saved
     -> (dx [R,C] bf16, the gradient of x and of residual, dgamma [C] fp32)."""
+    given = dy, dh, h, gamma, rstd, dx, dgamma, ws
     R, C = shape = dy.shape
     dev = dy.device
     py, pd, ph = _in(dy, "dy", _BF, shape), _in(dh, "dh", _BF, shape), _in(h, "h", _BF, shape)
     pg, pr = _in(gamma, "gamma", _BF, (C,)), _in(rstd, "rstd", _F, (R,))
-    dx, px = _out(dx, "dx", _BF, shape, dev)
-    dgamma, pw = _out(dgamma, "dgamma", _F, (C,), dev)
+    dx, px = _out(dx, "dx", _BF, shape, dev, stream)
+    dgamma, pw = _out(dgamma, "dgamma", _F, (C,), dev, stream)
     if ws is None:
-        ws = torch.empty(max(16, add_rmsnorm_bwd_workspace_size(R, C)), dtype=_U8, device=dev)
-    _dev(dy, dh, h, gamma, rstd, dx, dgamma, ws)
+        ws = _new(torch.empty, max(16, add_rmsnorm_bwd_workspace_size(R, C)), _U8, dev, stream)
+    _dev(*given)
     _check(lib().pgg_add_rmsnorm_bwd(py, pd, ph, pg, pr, R, C, px, pw, *_scratch(ws), _stream(stream)),
            "pgg_add_rmsnorm_bwd")
     return dx, dgamma
@@ -544,12 +556,13 @@ def moe_route(logits, k, bias=None, score="softmax", renormalize=True, scale=1.0
     """Top-k routing of gate logits [T,E] (fp32 or bf16) -> (topk_ids [T,k] int32, w [T,k] fp32).
 
     bias [E] fp32 is added for the choice only (-inf masks an expert); see pgg.h."""
+    given = logits, bias, ids, w
     T, E = shape = logits.shape
     dtype, kind = _route_kind(logits, score)
     pl, pb = _in(logits, "logits", logits.dtype, shape), _in(bias, "bias", _F, (E,))
-    ids, pi = _out(ids, "ids", _I, (T, k), logits.device)
-    w, pw = _out(w, "w", _F, (T, k), logits.device)
-    _dev(logits, bias, ids, w)
+    ids, pi = _out(ids, "ids", _I, (T, k), logits.device, stream)
+    w, pw = _out(w, "w", _F, (T, k), logits.device, stream)
+    _dev(*given)
     _check(lib().pgg_moe_route(pl, dtype, pb, T, E, k, kind, int(renormalize), scale, pi, pw, _stream(stream)),
            "pgg_moe_route")
     return ids, w
@@ -558,13 +571,14 @@ def moe_route(logits, k, bias=None, score="softmax", renormalize=True, scale=1.0
 def moe_route_bwd(logits, ids, dw, bias=None, score="softmax", renormalize=True, scale=1.0, dlogits=None,
                   stream=None):
     """dlogits [T,E] (the logits' type) from dw [T,k] at the ids of moe_route."""
+    given = logits, bias, ids, dw, dlogits
     T, E = shape = logits.shape
     k = ids.shape[1]
     dtype, kind = _route_kind(logits, score)
     pl, pb = _in(logits, "logits", logits.dtype, shape), _in(bias, "bias", _F, (E,))
     pi, pw = _in(ids, "ids", _I, (T, k)), _in(dw, "dw", _F, (T, k))
-    dlogits, pd = _out(dlogits, "dlogits", logits.dtype, shape, logits.device)
-    _dev(logits, bias, ids, dw, dlogits)
+    dlogits, pd = _out(dlogits, "dlogits", logits.dtype, shape, logits.device, stream)
+    _dev(*given)
     _check(lib().pgg_moe_route_bwd(pl, dtype, pb, pi, pw, T, E, k, kind, int(renormalize), scale, pd,
                                    _stream(stream)), "pgg_moe_route_bwd")
     return dlogits
@@ -583,16 +597,17 @@ def moe_decode(X, ids, w, W1, W2, out=None, swiglu_limit=0.0, ws=None, err=None,
     """A whole expert layer for T <= 128 tokens: X [T,H] bf16, ids [T,k] int32, w [T,k] fp32 (or None),
     W1 [E,2I,H], W2 [E,H,I] bf16 -> out [T,H] bf16.  ws: a moe_decode_workspace kept between calls
     (None: one is made for this call)."""
+    given = X, ids, w, W1, W2, out, ws, err
     T, H = shape = X.shape
     E, _, I = W2.shape
     k = ids.shape[1]
     px, pi, pw = _in(X, "X", _BF, shape), _in(ids, "ids", _I, (T, k)), _in(w, "w", _F, (T, k))
     p1, p2 = _in(W1, "W1", _BF, (E, 2 * I, H)), _in(W2, "W2", _BF, (E, H, I))
-    out, po = _out(out, "out", _BF, shape, X.device)
+    out, po = _out(out, "out", _BF, shape, X.device, stream)
     if ws is None:
-        ws = moe_decode_workspace(T, k, H, I, E, None, X.device)
+        ws = _new(torch.zeros, moe_decode_workspace_size(T, k, H, I, E), _U8, X.device, stream)
     pe = None if err is None else _in(err, "err", _I, err.shape)
-    _dev(X, ids, w, W1, W2, out, ws, err)
+    _dev(*given)
     _check(lib().pgg_moe_decode(px, pi, pw, p1, p2, po, T, k, H, I, E, swiglu_limit, *_scratch(ws), pe,
                                 _stream(stream)), "pgg_moe_decode")
     return out
@@ -602,6 +617,7 @@ def mx_moe_decode(fmt, X, SX, ids, w, W1, SW1, W2, SW2, out=None, swiglu_limit=0
     """moe_decode on MX operands: X / SX row-wise codes and scales [T, .] (add_rmsnorm or
     mx_quantize_rowwise), W1 [E*2I, .] and W2 [E*H, .] codes with blocked scales
     (mx_quantize_rowwise_blocked)."""
+    given = X, SX, ids, w, W1, SW1, W2, SW2, out, ws, err
     f = _FMT[fmt]
     per = 1 if f == FMT_E4M3 else 2  # elements of a byte
     T, H = X.shape[0], X.shape[1] * per
@@ -614,11 +630,11 @@ def mx_moe_decode(fmt, X, SX, ids, w, W1, SW1, W2, SW2, out=None, swiglu_limit=0
     q1, q2 = _in(SW1, "SW1", _U8, SW1.shape), _in(SW2, "SW2", _U8, SW2.shape)
     if SW1.numel() < E * 2 * I * (H // 32) or SW2.numel() < E * H * (I // 32):
         raise ValueError("SW1 / SW2 are too small for W1 / W2")
-    out, po = _out(out, "out", _BF, (T, H), X.device)
+    out, po = _out(out, "out", _BF, (T, H), X.device, stream)
     if ws is None:
-        ws = moe_decode_workspace(T, k, H, I, E, f, X.device)
+        ws = _new(torch.zeros, moe_decode_workspace_size(T, k, H, I, E, f), _U8, X.device, stream)
     pe = None if err is None else _in(err, "err", _I, err.shape)
-    _dev(X, SX, ids, w, W1, SW1, W2, SW2, out, ws, err)
+    _dev(*given)
     _check(lib().pgg_mx_moe_decode(f, px, ps, pi, pw, p1, q1, p2, q2, po, T, k, H, I, E, swiglu_limit,
                                    *_scratch(ws), pe, _stream(stream)), "pgg_mx_moe_decode")
     return out

@@ -77,7 +77,8 @@ class MoeBlock:
         return {"dx": dx, "dgamma": dgamma, "dgate": dgate, "dW1": dW1, "dW2": dW2}
 
     def decode(self, x, residual=None, err=None):
-        """`forward` for up to 128 tokens, inference only -> (out, h)."""
+        """`forward` for up to 128 tokens, inference only -> (out, h).  A block has one workspace, so its
+        decode calls run in the order of one stream."""
         E, H, I = self.sizes
         if self._ws is None:  # kept for the block's life: every call leaves it ready for the next
             self._ws = B.moe_decode_workspace(128, self.k, H, I, E, self.fmt, x.device)

@@ -393,6 +393,31 @@ def test_decode_many_experts_few_tokens(T, k, E, fmt):
         _check_layer(out, ids, w, ref, fmt)
 
 
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_calls_on_another_stream_than_the_current_one(fmt):
+    # what a call makes for itself (outputs, workspaces and their zeros) is in the order of its stream,
+    # not behind or ahead of the current stream's work
+    ids, w, dev, ref = _layer(6, 3, 8, 256, 128, fmt, 5)
+    x, g = _bf(np.random.default_rng(2), 40, 256).to(DEV), torch.ones(256, dtype=BF, device=DEV)
+    logits = torch.randn(50, 16, device=DEV)
+    here = pgg.add_rmsnorm(x, x, g), pgg.moe_route(logits, 4)
+    back = pgg.add_rmsnorm_bwd(x, None, here[0][0], g, here[0][4])
+    big = torch.randn(8192, 8192, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    filler = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    del filler  # the current stream's next small blocks are not zero
+    for _ in range(20):
+        big = big @ big * 1e-4  # the current stream is busy
+    out = _call(fmt, dev, stream=side)
+    there = pgg.add_rmsnorm(x, x, g, stream=side), pgg.moe_route(logits, 4, stream=side)
+    bside = pgg.add_rmsnorm_bwd(x, None, there[0][0], g, there[0][4], stream=side)
+    side.synchronize()
+    _check_layer(out, ids, w, ref, fmt)
+    for a, b in zip([*here[0], *here[1], *back], [*there[0], *there[1], *bside]):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+
+
 @pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
 def test_decode_skewed_and_repeated_experts(fmt):
     # most tokens on one expert, and tokens that name an expert several times: the weights add up
