@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -518,6 +519,7 @@ def add_rmsnorm(x, residual, gamma, eps=1e-6, fmt=None, h=None, y=None, codes=No
     return h, y, codes, scales, rstd
 
 
+@functools.lru_cache(maxsize=1024)
 def add_rmsnorm_bwd_workspace_size(R: int, C: int) -> int:
     return _size_of("pgg_add_rmsnorm_bwd_workspace_size", R, C)
 
@@ -584,6 +586,7 @@ def moe_route_bwd(logits, ids, dw, bias=None, score="softmax", renormalize=True,
     return dlogits
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_decode_workspace_size(T: int, k: int, H: int, I: int, E: int, fmt=None) -> int:
     return _size_of("pgg_moe_decode_workspace_size", 0 if fmt is None else _FMT[fmt], T, k, H, I, E)
 

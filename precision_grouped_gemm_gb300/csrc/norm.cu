@@ -10,6 +10,7 @@
 //
 //   xh = h rstd, u = dy gamma   dx = dh + rstd (u - xh mean(u xh)),  dgamma = sum_rows dy xh
 #include <algorithm>
+#include <atomic>
 
 #include "block.cuh"
 
@@ -375,11 +376,21 @@ int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const voi
   const int V = norm_bwd_v(a.nvec), threads = norm_threads(a.nvec, V);
   auto kern = V == 1 ? add_rmsnorm_bwd_kernel<1> : V == 2 ? add_rmsnorm_bwd_kernel<2> : add_rmsnorm_bwd_kernel<4>;
   const size_t smem = (size_t)kNormBwdDepth * 3 * V * threads * sizeof(uint4);
-  int per_sm = 0;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024)  // (48 KB, the static part included, need no leave)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // Resident blocks of a configuration: the same on every device that the library runs on, and asked
+  // for once (the query takes about a microsecond).
+  static std::atomic<int> resident[5][17];
+  std::atomic<int>& known = resident[V][threads / 32];
+  int per_sm = known.load(std::memory_order_relaxed);
+  if (e == cudaSuccess && per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+    per_sm = std::max(1, per_sm);
+    if (e == cudaSuccess) known.store(per_sm, std::memory_order_relaxed);
+  }
   if (e != cudaSuccess) return cuda_status(e);
-  const int grid = std::min(norm_bwd_blocks(R, C), dev.sms * std::max(1, per_sm));
+  const int grid = std::min(norm_bwd_blocks(R, C), dev.sms * per_sm);
   kern<<<grid, threads, smem, s>>>(a);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(C / 8));
