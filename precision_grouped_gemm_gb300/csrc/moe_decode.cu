@@ -841,11 +841,11 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
                          make_float4(as_float(own[i][0]) + v[i].x, as_float(own[i][1]) + v[i].y,
                                      as_float(own[i][2]) + v[i].z, as_float(own[i][3]) + v[i].w));
           }
+          tmem_st_wait();  // the next CTA's sums are added to what has been stored here
         }
       };
       if (n <= 8) join(std::integral_constant<int, 8>());
       else join(std::integral_constant<int, 16>());
-      tmem_st_wait();
       if (head) {  // columns past n hold something as well, and the reader skips them
 #pragma unroll 1
         for (int c0 = 0; c0 < n; c0 += 4) {
