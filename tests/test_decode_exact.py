@@ -127,3 +127,67 @@ CHAINS = [(1, 1, 1, 2048, 384), (1, 1, 1, 4096, 128), (2, 2, 2, 1024, 256), (5, 
 def test_tile_divided_over_many_ctas(T, k, E, H, I, fmt):
     ids, w, x, W1, W2, ref, mag = _layer(T, k, E, H, I, 1)
     _check(_run(fmt, ids, w, x, W1, W2, times=20), ref, mag)
+
+
+# Every token names one common expert, so its MMAs have up to 128 columns (256 for the two bf16 parts of
+# the activation): one accumulator instead of two, all four words of a scale atom's rows, and with k = 32
+# the least shared memory for the ring (two stages in bf16).
+FULL = [(128, 1, 1, 512, 384), (128, 1, 2, 384, 128), (128, 2, 2, 640, 256), (128, 8, 16, 384, 384),
+        (128, 32, 40, 256, 256), (113, 8, 12, 512, 128), (100, 4, 8, 384, 640), (97, 3, 3, 1152, 384)]
+
+
+def _common(T, k, E, H, I):
+    return _layer(T, k, E, H, I, 2, common=E - 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+@pytest.mark.parametrize("T,k,E,H,I", FULL)
+def test_an_expert_that_every_token_names(T, k, E, H, I, fmt):
+    ids, w, x, W1, W2, ref, mag = _common(T, k, E, H, I)
+    assert (ids == E - 1).any(1).all()
+    _check(_run(fmt, ids, w, x, W1, W2, times=3), ref, mag)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,E,H,I", [(128, 1, 1, 520, 200), (128, 8, 16, 72, 264), (128, 32, 40, 328, 136),
+                                       (120, 2, 5, 1032, 72), (128, 3, 3, 8, 1000)])
+def test_an_expert_that_every_token_names_off_the_tiles(T, k, E, H, I):
+    ids, w, x, W1, W2, ref, mag = _common(T, k, E, H, I)
+    _check(_run(None, ids, w, x, W1, W2, times=3), ref, mag)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+def test_weights_past_32_bit_offsets(fmt):
+    # 1024 experts of 2048 x 1152: 4.8 G elements of W1 and 2.4 G of W2.  The tokens name the experts
+    # at both ends, just below and above an element offset of 2^31 and 2^32, and around byte offsets of those.
+    import precision_grouped_gemm_gb300 as pgg
+    E, H, I = 1024, 2048, 1152
+    per1, per2 = 2 * I * H, H * I
+    at = {0, E - 1}
+    for n in (2 ** 31, 2 ** 32):
+        for size in {None: 2, "e4m3": 1, "e2m1": 0.5}[fmt], 1:  # in bytes, in elements
+            for per in (per1, per2):
+                e = int(n / size / per)
+                at |= {e - 1, e, e + 1}
+    named = np.array(sorted(e for e in at if e < E), dtype=np.int32)
+    T = len(named)
+    some, w, x, W1, W2, ref, mag = _layer(T, 2, T, H, I, 3, ids=np.stack([np.arange(T), np.arange(T)[::-1]], 1).astype(np.int32))
+    ids, d = torch.from_numpy(named[some]).to(DEV), lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    X, where = d(x).to(BF), d(named).long()
+    if fmt is None:
+        U = torch.full((E, 2 * I, H), float("nan"), dtype=BF, device=DEV)  # no other expert has a part
+        V = torch.full((E, H, I), float("nan"), dtype=BF, device=DEV)
+        U[where], V[where] = d(W1).to(BF), d(W2).to(BF)
+        out = pgg.moe_decode(X, ids, d(w), U, V)
+    else:
+        def spread(m, rows, cols):  # codes and blocked scales (whole atoms of 128 rows) of the named experts
+            c, s = pgg.mx_quantize_rowwise_blocked(d(m).to(BF).view(-1, cols), fmt)
+            c, s = c.view(T, -1), s.view(T, -1)
+            C = torch.empty((E, c.shape[1]), dtype=torch.uint8, device=DEV)
+            S = torch.full((E, s.shape[1]), 255, dtype=torch.uint8, device=DEV)  # NaN scales elsewhere
+            C[where], S[where] = c, s
+            return C.view(E * rows, -1), S.view(E * rows, -1)
+        out = pgg.mx_moe_decode(fmt, *pgg.mx_quantize_rowwise(X, fmt), ids, d(w), *spread(W1, 2 * I, H), *spread(W2, H, I))
+    _check([out], ref, mag)
