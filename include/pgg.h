@@ -463,7 +463,8 @@ int pgg_moe_decode_workspace_size(int fmt, int64_t T, int k, int64_t H, int64_t 
  * ws: device scratch of pgg_moe_decode_workspace_size bytes, 16-byte aligned, zeroed before the first
  * call.  Every call leaves it ready for the next, so one buffer serves any number of calls, of any
  * sizes and formats that it is large enough for, in the order of one stream.  Zero it again after a
- * call that set PGG_ERR_TIMEOUT.  Calls that may overlap need a workspace each.
+ * call that set PGG_ERR_TIMEOUT: until then every call on it sets PGG_ERR_TIMEOUT, whatever it writes.
+ * Calls that may overlap need a workspace each.
  * One cooperative launch: the CTAs wait for one another, so the call needs the whole GPU for its
  * time and starts when the kernels of other streams leave it. */
 int pgg_moe_decode(const void* X, const int32_t* topk_ids, const float* w, const void* W1, const void* W2, void* out,

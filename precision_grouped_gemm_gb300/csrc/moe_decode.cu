@@ -82,7 +82,8 @@ struct DecodeArgs {
   uint8_t* act_scales;  // MX: row-major scales
   __nv_bfloat16* out;   // [T, H]
   float* part[2];       // per phase and CTA: a tile of partial sums, zero between launches
-  unsigned* done;       // CTAs that have finished phase 1; [1]: that have left.  Zero between launches
+  unsigned* done;       // CTAs that have finished phase 1; [1]: that have left.  Zero between launches.
+                        // [2]: a launch gave up, so the sums in `part` are not to be trusted
   int ring_bytes;       // shared memory for the stages
   int slots_cap;        // most experts that the batch can name
   FastDiv by_grid;
@@ -779,6 +780,8 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     // An item that a cut divides begins at the end of one CTA's run.  That CTA finishes it; the others
     // send it their fp32 sums, which all but a whole-run CTA do at the start of their run.
     const int q = warp & 3, row = q * 32 + lane;  // accumulator row of this thread
+    // (read while this warp would wait for the first product, so it costs no time)
+    if (cta == 0 && threadIdx.x == 64 && load_acquire(a.done + 2) != 0u) set_error(a.err, kErrTimeout);
     int acc = 0;
     uint32_t acc_phase = 0;
     auto release = [&]() {  // the accumulator has been read
@@ -958,7 +961,6 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     if (threadIdx.x == 64) *s_last_tile = last_tile;
   }
 
-  if (aborted && lane == 0) set_error(a.err, kErrTimeout);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1005,14 +1007,17 @@ __global__ void __launch_bounds__(DecCfg<FMT>::kThreads, 1)
     }
     if (tile == last_tile) break;
   }
-  if (s_ctl->abort && lane == 0) set_error(a.err, kErrTimeout);  // sums that never came
+  if (s_ctl->abort && lane == 0) {  // a role gave up (whichever did has raised the flag), or sums never came
+    set_error(a.err, kErrTimeout);
+    atomicExch(a.done + 2, 1u);  // what other CTAs have sent to this one is left behind
+  }
   // the last CTA to leave clears the count that the others have waited on
   if (threadIdx.x == 0 && atomicInc(a.done + 1, gridDim.x - 1) == gridDim.x - 1) atomicExch(a.done, 0u);
 }
 
 // ---------------------------------------------------------------- workspace
-// [CTAs done and left][partial sums of both phases][A: bf16 high and low parts, or codes and scales].
-// The first two are zero between calls, so they have the same place whatever the sizes.
+// [CTAs done and left, given up][partial sums of both phases][A: bf16 high and low parts, or codes and
+// scales].  The first two are zero between calls, so they have the same place whatever the sizes.
 constexpr size_t kPartBytes = (size_t)kMaxCtas * kMaxT * (256 + 2 * 128) * sizeof(float);
 struct DecodeWs {
   size_t part, act, act_lo, act_scales, bytes;

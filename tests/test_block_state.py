@@ -1,0 +1,62 @@
+"""What the few-token layer and the MoE block keep between calls: the workspace after a timeout, and
+the quantized weights after an update."""
+import numpy as np
+import pytest
+import torch
+
+import util
+
+pgg = pytest.importorskip("precision_grouped_gemm_gb300")
+from precision_grouped_gemm_gb300 import _binding  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+FMT = {None: 0, "e4m3": 1, "e2m1": 2}
+
+
+def _stall(fmt, x, sx, ids, w1, s1, w2, s2, E, ws, err, stall_at=9):
+    """A call of the layer whose loads stop, on this workspace: it ends with the timeout code."""
+    T, k = ids.shape
+    H, I = w2.shape[-2] if w2.dim() == 3 else w2.shape[0] // E, w1.numel() // E // x.shape[1] // 2
+    out = torch.zeros(T, H, dtype=BF, device=DEV)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = _binding.lib().pgg_test_stalled_moe_decode(
+        FMT[fmt], p(x), p(sx), p(ids), p(w1), p(s1), p(w2), p(s2), p(out), T, k, H, I, E, stall_at, 2_000_000, p(ws),
+        ws.numel(), p(err), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+def test_a_workspace_that_a_timeout_left_is_reported(fmt):
+    # sums of the call that gave up are still in the workspace, and the next call cannot tell them from
+    # its own: every call on it reports the timeout until it is zeroed
+    T, k, E, H, I = 24, 4, 24, 2048, 1024
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV).to(BF)  # noqa: E731
+    ids = torch.from_numpy(np.random.default_rng(3).permuted(np.tile(np.arange(E, dtype=np.int32), (T, 1)), axis=1)
+                           [:, :k].copy()).to(DEV)
+    x, w1, w2 = rnd(T, H), 0.02 * rnd(E * 2 * I, H), 0.02 * rnd(E * H, I)
+    sx = s1 = s2 = None
+    if fmt is not None:
+        (x, sx), (w1, s1), (w2, s2) = (pgg.mx_quantize_rowwise(x, fmt), pgg.mx_quantize_rowwise_blocked(w1, fmt),
+                                       pgg.mx_quantize_rowwise_blocked(w2, fmt))
+    ws = pgg.moe_decode_workspace(T, k, H, I, E, fmt)
+
+    def call():
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        if fmt is None:
+            out = pgg.moe_decode(x, ids, None, w1.view(E, 2 * I, H), w2.view(E, H, I), ws=ws, err=err)
+        else:
+            out = pgg.mx_moe_decode(fmt, x, sx, ids, None, w1, s1, w2, s2, ws=ws, err=err)
+        return out, pgg.read_error(err)
+
+    good, code = call()
+    assert code == 0
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    _stall(fmt, x, sx, ids, w1, s1, w2, s2, E, ws, err)
+    assert pgg.read_error(err) == 17
+    assert call()[1] == 17 and call()[1] == 17
+    ws.zero_()
+    out, code = call()
+    assert code == 0 and torch.equal(out, good)
