@@ -39,6 +39,7 @@ class MoeBlock:
         self.sizes = E, H, I2 // 2
         self._mx = None
         self._ws = None
+        self._err = torch.zeros(1, dtype=torch.int32, device=self.W1.device)
         if self.fmt is not None:
             self._mx = (*B.mx_quantize_rowwise_blocked(self.W1.view(E * I2, H), self.fmt),
                         *B.mx_quantize_rowwise_blocked(self.W2.view(E * H, I2 // 2), self.fmt))
@@ -78,13 +79,36 @@ class MoeBlock:
 
     def decode(self, x, residual=None, err=None):
         """`forward` for up to 128 tokens, inference only -> (out, h).  A block has one workspace, so its
-        decode calls run in the order of one stream."""
-        E, H, I = self.sizes
-        if self._ws is None:  # kept for the block's life: every call leaves it ready for the next
-            self._ws = B.moe_decode_workspace(128, self.k, H, I, E, self.fmt, x.device)
+        decode calls run in the order of one stream.  err: the caller's error word; without one the block's
+        own, which `check_decode` reads."""
+        err = self._err if err is None else err
+        ws = self._ws if self._ws is not None else self.prepare_decode()
         h, y, codes, scales, _ = B.add_rmsnorm(x, residual, self.gamma, self.eps, fmt=self.fmt, save_rstd=False)
         _, ids, w = self._route(y)
         if self.fmt is None:
-            return B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=self._ws, err=err), h
-        return B.mx_moe_decode(self.fmt, codes, scales, ids, w, *self._mx, swiglu_limit=self.swiglu_limit, ws=self._ws,
+            return B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=ws, err=err), h
+        return B.mx_moe_decode(self.fmt, codes, scales, ids, w, *self._mx, swiglu_limit=self.swiglu_limit, ws=ws,
                                err=err), h
+
+    def _workspace(self):
+        E, H, I = self.sizes
+        return B.moe_decode_workspace(128, self.k, H, I, E, self.fmt, self.W1.device)
+
+    def prepare_decode(self):
+        """Makes the decode workspace, which is kept for the block's life: every call leaves it ready for
+        the next.  A workspace that is there is zeroed, which it needs after a timeout."""
+        if self._ws is None:
+            self._ws = self._workspace()
+        else:
+            self._ws.zero_()
+        return self._ws
+
+    def check_decode(self):
+        """Raises PggError if a decode call without an error word of the caller's has failed since the last
+        check, with the block ready again.  Waits for the current stream."""
+        code = B.read_error(self._err)
+        if code:
+            self._err.zero_()
+            if self._ws is not None:
+                self.prepare_decode()
+            raise B.PggError(code, "MoeBlock.decode")

@@ -8,6 +8,7 @@ import util
 
 pgg = pytest.importorskip("precision_grouped_gemm_gb300")
 from precision_grouped_gemm_gb300 import _binding  # noqa: E402
+from precision_grouped_gemm_gb300.block import MoeBlock  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -60,3 +61,38 @@ def test_a_workspace_that_a_timeout_left_is_reported(fmt):
     ws.zero_()
     out, code = call()
     assert code == 0 and torch.equal(out, good)
+
+
+def _block(seed, fmt=None, T=24, H=2048, I=1024, E=24, k=4, **kw):
+    """A block (the same weights for a seed), and inputs x, residual [T, H]."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s, scale=1.0: (scale * torch.randn(s, generator=g, device=DEV)).to(BF)  # noqa: E731
+    b = MoeBlock(1 + rnd(H, scale=0.1), rnd(E, H, scale=0.1), rnd(E, 2 * I, H, scale=H ** -0.5),
+                 rnd(E, H, I, scale=I ** -0.5), k, fmt=fmt, **kw)
+    return b, rnd(T, H), rnd(T, H)
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+@pytest.mark.parametrize("own_word", [True, False])
+def test_block_is_ready_again_after_a_timeout(fmt, own_word):
+    b, x, res = _block(1, fmt)
+    good, _ = b.decode(x, res)
+    b.check_decode()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ids = torch.arange(24 * 4, dtype=torch.int32, device=DEV).view(24, 4) % 24
+    if fmt is None:
+        _stall(fmt, x, None, ids, b.W1, None, b.W2, None, 24, b._ws, b._err if own_word else err)
+    else:
+        w1, s1, w2, s2 = b._mx
+        _stall(fmt, *pgg.mx_quantize_rowwise(x, fmt), ids, w1, s1, w2, s2, 24, b._ws, b._err if own_word else err)
+    if own_word:  # the block finds it out by itself
+        with pytest.raises(pgg.PggError) as e:
+            b.check_decode()
+        assert e.value.status == 17
+    else:         # the caller, from a word that was given; later calls say so too
+        b.decode(x, res, err=err.zero_())
+        assert pgg.read_error(err) == 17
+        b.prepare_decode()
+    for _ in range(2):
+        assert torch.equal(b.decode(x, res)[0], good)
+    b.check_decode()
