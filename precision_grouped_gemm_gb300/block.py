@@ -80,9 +80,13 @@ class MoeBlock:
     def decode(self, x, residual=None, err=None):
         """`forward` for up to 128 tokens, inference only -> (out, h).  A block has one workspace, so its
         decode calls run in the order of one stream.  err: the caller's error word; without one the block's
-        own, which `check_decode` reads."""
+        own, which `check_decode` reads.  A first call inside a graph's capture has a workspace of the
+        graph's, zeroed at every replay: call `prepare_decode` before the capture to avoid that."""
         err = self._err if err is None else err
-        ws = self._ws if self._ws is not None else self.prepare_decode()
+        ws = self._ws
+        if ws is None:
+            # (memory of a graph's pool is the graph's: eager calls and other graphs get their own)
+            ws = self._workspace() if torch.cuda.is_current_stream_capturing() else self.prepare_decode()
         h, y, codes, scales, _ = B.add_rmsnorm(x, residual, self.gamma, self.eps, fmt=self.fmt, save_rstd=False)
         _, ids, w = self._route(y)
         if self.fmt is None:

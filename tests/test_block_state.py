@@ -96,3 +96,29 @@ def test_block_is_ready_again_after_a_timeout(fmt, own_word):
     for _ in range(2):
         assert torch.equal(b.decode(x, res)[0], good)
     b.check_decode()
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_block_first_decode_inside_a_capture(fmt):
+    # what the capture records is not what eager calls use: not before the first replay, nor between replays
+    b, x, res = _block(2, fmt)
+    good, _ = _block(2, fmt)[0].decode(x, res)  # (another block of the same weights)
+    filler = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    del filler  # fresh memory is not zero
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = b.decode(x, res)
+    assert torch.equal(b.decode(x, res)[0], good)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, good)
+        assert torch.equal(b.decode(x, res)[0], good)
+    b.check_decode()
+    graph = torch.cuda.CUDAGraph()  # after `prepare_decode` (here: a decode) the capture has the block's own
+    with torch.cuda.graph(graph):
+        out2, _ = b.decode(x, res)
+    for _ in range(2):
+        graph.replay()
+        assert torch.equal(out2, good) and torch.equal(b.decode(x, res)[0], good)
+    b.check_decode()
