@@ -3,7 +3,8 @@
 Training (`MoeBlock.forward` / `backward`) goes the long way, over the permuted batch and the grouped
 GEMMs; decoding (`MoeBlock.decode`, up to 128 tokens) hands the norm's output straight to the
 few-token layer: three small kernels and one weight stream.  With `fmt` the decode weights are MX
-operands, quantized once, and the norm emits the MX operand of its tokens itself.
+operands, quantized when the block is made and again when W1 or W2 have changed, and the norm emits
+the MX operand of its tokens itself.
 
     s = x + residual, y = rmsnorm(s) gamma     add_rmsnorm
     logits = y gate^T                          grouped_gemm_fwd with one group
@@ -13,10 +14,19 @@ operands, quantized once, and the norm emits the MX operand of its tokens itself
 from __future__ import annotations
 
 import dataclasses
+import weakref
 
 import torch
 
 from . import _binding as B
+
+
+def _gone():
+    return None
+
+
+def _version(t):
+    return None if t.is_inference() else t._version
 
 
 @dataclasses.dataclass
@@ -37,12 +47,9 @@ class MoeBlock:
     def __post_init__(self):
         E, I2, H = self.W1.shape
         self.sizes = E, H, I2 // 2
-        self._mx = None
-        self._ws = None
+        self._mx = self._mx_of = self._ws = None
         self._err = torch.zeros(1, dtype=torch.int32, device=self.W1.device)
-        if self.fmt is not None:
-            self._mx = (*B.mx_quantize_rowwise_blocked(self.W1.view(E * I2, H), self.fmt),
-                        *B.mx_quantize_rowwise_blocked(self.W2.view(E * H, I2 // 2), self.fmt))
+        self.quantize_weights()
 
     def _one_group(self, rows, device):
         return torch.full((1,), rows, dtype=torch.int32, device=device)
@@ -87,16 +94,47 @@ class MoeBlock:
         if ws is None:
             # (memory of a graph's pool is the graph's: eager calls and other graphs get their own)
             ws = self._workspace() if torch.cuda.is_current_stream_capturing() else self.prepare_decode()
+        if self.fmt is not None:
+            mx = self._mx
+            if not self._current():
+                # (a capture quantizes into its own memory, at every replay)
+                mx = self._quantized() if torch.cuda.is_current_stream_capturing() else self.quantize_weights()
         h, y, codes, scales, _ = B.add_rmsnorm(x, residual, self.gamma, self.eps, fmt=self.fmt, save_rstd=False)
         _, ids, w = self._route(y)
         if self.fmt is None:
             return B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=ws, err=err), h
-        return B.mx_moe_decode(self.fmt, codes, scales, ids, w, *self._mx, swiglu_limit=self.swiglu_limit, ws=ws,
+        return B.mx_moe_decode(self.fmt, codes, scales, ids, w, *mx, swiglu_limit=self.swiglu_limit, ws=ws,
                                err=err), h
+
+    def _quantized(self, into=(None,) * 4):
+        E, H, I = self.sizes
+        return (*B.mx_quantize_rowwise_blocked(self.W1.view(E * 2 * I, H), self.fmt, *into[:2]),
+                *B.mx_quantize_rowwise_blocked(self.W2.view(E * H, I), self.fmt, *into[2:]))
+
+    def _current(self):
+        """Whether the MX operands are those of W1 and W2: the same tensors, not written to since.  (A decoding
+        block may give up its bf16 weights: with W1 or W2 None the operands are what there is.)"""
+        if self.W1 is None or self.W2 is None:
+            return True
+        return all(ref() is t and version == _version(t) for (ref, version), t in zip(self._mx_of, (self.W1, self.W2)))
+
+    def __getstate__(self):  # references to tensors by identity do not travel: a copy quantizes anew
+        return {**self.__dict__, "_mx_of": [(_gone, None)] * 2}
+
+    def quantize_weights(self):
+        """The MX operands of W1 and W2 as they are now (fmt), in the memory of the ones before: decode calls
+        this itself after a change that torch counts.  For changes that it does not (`.data`, kernels that write
+        through an address, inference tensors), and before replays of a captured decode, the caller does.
+        Without fmt decode reads W1 and W2 themselves, and this does nothing."""
+        if self.fmt is None:
+            return None
+        self._mx = self._quantized(self._mx or (None,) * 4)
+        self._mx_of = [(weakref.ref(t), _version(t)) for t in (self.W1, self.W2)]
+        return self._mx
 
     def _workspace(self):
         E, H, I = self.sizes
-        return B.moe_decode_workspace(128, self.k, H, I, E, self.fmt, self.W1.device)
+        return B.moe_decode_workspace(128, self.k, H, I, E, self.fmt, self.gamma.device)
 
     def prepare_decode(self):
         """Makes the decode workspace, which is kept for the block's life: every call leaves it ready for

@@ -1,10 +1,11 @@
 """What the few-token layer and the MoE block keep between calls: the workspace after a timeout, and
 the quantized weights after an update."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
-
-import util
 
 pgg = pytest.importorskip("precision_grouped_gemm_gb300")
 from precision_grouped_gemm_gb300 import _binding  # noqa: E402
@@ -122,3 +123,71 @@ def test_block_first_decode_inside_a_capture(fmt):
         graph.replay()
         assert torch.equal(out2, good) and torch.equal(b.decode(x, res)[0], good)
     b.check_decode()
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "e2m1"])
+def test_block_decode_follows_its_weights(fmt):
+    b, x, res = _block(4, fmt, T=9, H=256, I=128, E=8, k=2)
+    first, _ = b.decode(x, res)
+
+    def fresh():  # a block that is made of the weights as they are now
+        return MoeBlock(b.gamma, b.gate, b.W1.clone(), b.W2.clone(), b.k, fmt=fmt).decode(x, res)[0]
+
+    def check(what):
+        out, _ = b.decode(x, res)
+        assert torch.equal(out, fresh()), what
+        return out
+
+    out = check("no change")
+    assert torch.equal(out, first)
+    b.W1.mul_(1.5)
+    out2 = check("W1 in place")
+    assert not torch.equal(out2, out)
+    with torch.no_grad():
+        b.W2[3:].add_(0.1 * torch.randn_like(b.W2[3:]))
+    out3 = check("a part of W2 in place")
+    assert not torch.equal(out3, out2)
+    for _ in range(3):  # a tensor that takes the place, and often the address, of the one before
+        w, b.W1 = b.W1 * 0.5, None
+        b.W1 = w
+        del w
+        check("another W1")
+    b.W2 = -b.W2
+    check("another W2")
+    graph = torch.cuda.CUDAGraph()
+    b.W1.neg_()
+    with torch.cuda.graph(graph):  # an update that no decode has seen, and then a capture
+        out, _ = b.decode(x, res)
+    check("before the replay")
+    graph.replay()
+    assert torch.equal(out, fresh())
+    b.W1.data.mul_(2.0)            # torch does not count this: the caller says so
+    b.quantize_weights()
+    check("told")
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_block_copies_and_blocks_without_bf16_weights(fmt):
+    b, x, res = _block(5, fmt, T=5, H=256, I=128, E=8, k=2)
+    good, _ = b.decode(x, res)
+    for c in (copy.deepcopy(b), pickle.loads(pickle.dumps(b))):
+        assert torch.equal(c.decode(x, res)[0], good)
+        c.W1.mul_(2.0)
+        assert not torch.equal(c.decode(x, res)[0], good)
+    assert torch.equal(b.decode(x, res)[0], good)
+    if fmt is not None:
+        b.W1 = b.W2 = None
+        assert torch.equal(b.decode(x, res)[0], good)
+        b, x, res = _block(5, fmt, T=5, H=256, I=128, E=8, k=2)
+        b.W1 = b.W2 = None  # before the first decode
+        assert torch.equal(b.decode(x, res)[0], good)
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_block_in_inference_mode(fmt):
+    with torch.inference_mode():
+        b, x, res = _block(5, fmt, T=5, H=256, I=128, E=8, k=2)
+        good, _ = b.decode(x, res)
+        assert torch.equal(b.decode(x, res)[0], good)
+    ref, _ = _block(5, fmt, T=5, H=256, I=128, E=8, k=2)[0].decode(x, res)
+    assert torch.equal(good, ref)
