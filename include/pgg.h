@@ -428,7 +428,8 @@ int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const voi
  *   key_e = logit_e + bias_e (fp32; the bias decides the choice only);
  *   topk_ids: the k largest keys, largest first, ties to the lowest expert;
  *   w_j = scale a_j / Z with a = exp(logit - max) or sigmoid(logit); Z = the sum of a over all
- *   experts (softmax), over the k chosen (renormalize = 1), or 1 (sigmoid without it).
+ *   experts (softmax), over the k chosen (renormalize = 1; also where all of these are sigmoids below
+ *   fp32's range), or 1 (sigmoid without it).  A sigmoid score counts as 0 below a logit of -700.
  * An expert whose key is -inf is masked: it counts in no sum, and where fewer than k are left it
  * fills the choice with weight 0 (a row that is masked whole has ids 0 .. k-1, weights 0).  A NaN
  * key ranks as -inf and makes the row's weights NaN; the ids are in range whatever the logits.
