@@ -152,9 +152,9 @@ struct NormBwdArgs {
 // rate).  Instructions come next: 68% of the issue slots.  With
 // t = dy h: dgamma += rstd t, mean(u xh) = rstd mean(t gamma), dx = dh + rstd dy gamma - c h,
 // c = rstd^2 mean(u xh): six operations an element besides the conversions.
-constexpr int kNormBwdDepth = 2;
+constexpr int kNormBwdDepth = 2, kNormBwdThreads = 512;
 template <int V>
-__global__ void __launch_bounds__(V == 1 ? 384 : 512) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 384 : kNormBwdThreads) add_rmsnorm_bwd_kernel(const NormBwdArgs a) {
   constexpr int kDepth = kNormBwdDepth;
   extern __shared__ uint4 s_row[];  // [kDepth][3][V][blockDim]
   __shared__ float s_sum[2][32];
@@ -377,8 +377,11 @@ int pgg_add_rmsnorm_bwd(const void* dy, const void* dh, const void* h, const voi
   auto kern = V == 1 ? add_rmsnorm_bwd_kernel<1> : V == 2 ? add_rmsnorm_bwd_kernel<2> : add_rmsnorm_bwd_kernel<4>;
   const size_t smem = (size_t)kNormBwdDepth * 3 * V * threads * sizeof(uint4);
   cudaError_t e = cudaSuccess;
-  if (smem > 32 * 1024)  // (48 KB, the static part included, need no leave)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The most that the kernel is ever launched with, not this call's share: between this line and the launch
+  // another thread may make a call of another width.  (V == 1 stays below the 48 KB that need no leave.)
+  if (V > 1)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kNormBwdDepth * 3 * V * kNormBwdThreads * sizeof(uint4)));
   // Resident blocks of a configuration: the same on every device that the library runs on, and asked
   // for once (the query takes about a microsecond).
   static std::atomic<int> resident[5][17];
