@@ -407,7 +407,8 @@ typedef enum { PGG_SCORE_SOFTMAX = 0, PGG_SCORE_SIGMOID = 1 } pgg_score;
  *   pgg_mx_quantize_rowwise, applied to the fp32 y, not to its bf16 rounding; a block whose amax
  *   is an fp32 subnormal has scale code 0).  fmt 0: codes and scales are NULL.
  *   8 <= C <= PGG_NORM_MAX_COLS, C % 8 == 0, with codes C % 32 == 0; eps >= 0.  h may be x or
- *   residual (in place).  R == 0 is a no-op. */
+ *   residual (in place).  R == 0 is a no-op.  The sum of squares is fp32: a row whose sum leaves its
+ *   range (elements of about 1.8e19 / sqrt(C)) has rstd 0 and y 0. */
 int pgg_add_rmsnorm(const void* x, const void* residual, const void* gamma, int64_t R, int64_t C, float eps,
                     int fmt, void* h, void* y, uint8_t* codes, uint8_t* scales, float* rstd, void* stream);
 
@@ -458,7 +459,8 @@ int pgg_moe_decode_workspace_size(int fmt, int64_t T, int k, int64_t H, int64_t 
  *   up), W2 [E, H, I] bf16; out [T, H] bf16.  fp32 accumulation; the activation between the two
  *   products is kept as the sum of two bf16 numbers.  swiglu_limit as in
  *   pgg_grouped_fc1_swiglu_clamped (0: none).
- *   0 <= T <= PGG_MOE_DECODE_MAX_T (else PGG_ERR_TOO_LARGE: permute and use the grouped GEMMs),
+ *   0 <= T <= PGG_MOE_DECODE_MAX_T (else PGG_ERR_TOO_LARGE: permute and use the grouped GEMMs, which
+ *   are as fast from about 100 tokens on in bf16),
  *   1 <= k <= 32, H and I multiples of 8 up to 65536.  A token may name an expert twice.
  * An id outside [0, E) sets *err = PGG_ERR_BAD_EXPERT and has no part.
  * ws: device scratch of pgg_moe_decode_workspace_size bytes, 16-byte aligned, zeroed before the first

@@ -599,7 +599,7 @@ def moe_decode_workspace(T: int, k: int, H: int, I: int, E: int, fmt=None, devic
 def moe_decode(X, ids, w, W1, W2, out=None, swiglu_limit=0.0, ws=None, err=None, stream=None):
     """A whole expert layer for T <= 128 tokens: X [T,H] bf16, ids [T,k] int32, w [T,k] fp32 (or None),
     W1 [E,2I,H], W2 [E,H,I] bf16 -> out [T,H] bf16.  ws: a moe_decode_workspace kept between calls
-    (None: one is made for this call)."""
+    (None: one is made and zeroed for this call: 42 MB and more, as long as a small layer takes)."""
     given = X, ids, w, W1, W2, out, ws, err
     T, H = shape = X.shape
     E, _, I = W2.shape
@@ -619,7 +619,7 @@ def moe_decode(X, ids, w, W1, W2, out=None, swiglu_limit=0.0, ws=None, err=None,
 def mx_moe_decode(fmt, X, SX, ids, w, W1, SW1, W2, SW2, out=None, swiglu_limit=0.0, ws=None, err=None, stream=None):
     """moe_decode on MX operands: X / SX row-wise codes and scales [T, .] (add_rmsnorm or
     mx_quantize_rowwise), W1 [E*2I, .] and W2 [E*H, .] codes with blocked scales
-    (mx_quantize_rowwise_blocked)."""
+    (mx_quantize_rowwise_blocked).  ws: as there."""
     given = X, SX, ids, w, W1, SW1, W2, SW2, out, ws, err
     f = _FMT[fmt]
     per = 1 if f == FMT_E4M3 else 2  # elements of a byte

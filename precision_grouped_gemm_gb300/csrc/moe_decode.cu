@@ -23,13 +23,14 @@
 // an expert named twice by a token is computed once and its weights are added up.
 //
 // What bounds it: the weight stream where there is much of it.  The named experts' bytes at the plain
-// copy rate, and the call's time: BF16, 32 tokens, 32 experts of 2880 x 2880: 219 us, 237 (92%);
+// copy rate, and the call's time: BF16, 32 tokens, 32 experts of 2880 x 2880: 219 us, 235 (93%);
 // MXFP8, 8 tokens of 256 experts, 4096 x 2048: 172, 179 (96%; tensor pipe 4% busy); MXFP4, 64 skewed
-// tokens: 255, 281 (91%: the CTAs with the hottest expert's activations are last).  Where there is
+// tokens: 255, 280 (91%: the CTAs with the hottest expert's activations are last).  Where there is
 // little, the steps that are not streams: ~2 us to the first load, ~4 us from the last activation to
 // the first product of phase 2 (partial sums, the count of CTAs, the fetch of A), ~1.5 us for the last
-// sums.  One token, six BF16 experts: 44.6, 56; one token, eight MXFP4 experts: 15.8, 28.8.  At that
-// size instruction fetch shows too: loops are not unrolled and the phases share their code.
+// sums.  One token, six BF16 experts: 44.6, 56; one token, eight MXFP4 experts: 15.8, 28.6.  At that
+// size instruction fetch shows too: loops are not unrolled and the phases share their code.  (Comments on
+// single steps give before and after on one machine each, some of them 2% faster.)
 #include <algorithm>
 #include <type_traits>
 

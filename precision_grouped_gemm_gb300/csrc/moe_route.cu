@@ -126,7 +126,7 @@ __device__ __forceinline__ void write_choice(const RouteArgs<T>& a, int64_t t, i
 }
 
 // Any logits and a bias: k rounds of the largest key left in the warp, then the lowest expert that
-// holds it.  Bound by instructions for many tokens (16384 x 256 fp32, bias, sigmoid, k = 8: 16.1 us; the
+// holds it.  Bound by instructions for many tokens (16384 x 256 fp32, bias, sigmoid, k = 8: 16.2 us; the
 // logits at the copy rate: 2.5), by latency for few (33 x 256: 2.1 us).
 template <typename T, int N>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs<T> a) {
