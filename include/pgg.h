@@ -484,6 +484,94 @@ int pgg_mx_moe_decode(int fmt, const uint8_t* X, const uint8_t* SX, const int32_
                       int64_t T, int k, int64_t H, int64_t I, int E, float swiglu_limit, void* ws, size_t ws_bytes,
                       int32_t* err, void* stream);
 
+/* ---------------------------------------------------------------- products with biases, joints between blocks */
+
+/* Activations of the two calls below. */
+typedef enum { PGG_ACT_NONE = 0, PGG_ACT_SILU = 1, PGG_ACT_GELU = 2, PGG_ACT_SWIGLU = 3 } pgg_act;
+
+/* A matrix product per group with the bias, the activation and a residual in its epilogue:
+ *   Z_g = X_g W_g^T + b_g,   Y = act(Z) + residual
+ *   X [M, K], W [G, N, K] bf16; bias [G, N] bf16 or NULL; Z [M, N] bf16 (out) or NULL: what the
+ *   backward pass reads; dtype: the type of Y and residual (PGG_DTYPE_BF16 or PGG_DTYPE_F32).
+ *   Y and residual are [M, N], with PGG_ACT_SWIGLU [M, N/2]; residual may be NULL, and may be Y.
+ *   group_lens NULL: one group of M rows (G = 1), a dense product.
+ *   act: PGG_ACT_SILU z sigmoid(alpha z); PGG_ACT_GELU z Phi(z), exactly; PGG_ACT_SWIGLU of the halves
+ *   z = [g | u]: g sigmoid(alpha g) (u + offset), with limit > 0 g <- min(g, limit) and u <-
+ *   clamp(u, -limit, limit) first.  alpha, offset and limit are not read where act has no use for them,
+ *   but must be finite, limit >= 0.  alpha = 1, offset = 0 is the SwiGLU of pgg_grouped_fc1_swiglu.
+ *   Z is fp32 up to Y; Z, Y are each rounded once.  N % 8 == 0 (swiglu: % 16), K % 8 == 0.
+ * The result of a row does not depend on its group's other rows beyond the order in which K is summed
+ * up, which follows the sizes of the call; it is deterministic. */
+int pgg_grouped_linear(const void* X, const void* W, const int32_t* group_lens, const void* bias, const void* residual,
+                       void* Y, int dtype, void* Z, int64_t M, int64_t N, int64_t K, int G, int act, float alpha,
+                       float offset, float limit, int32_t* err, void* stream);
+
+/* Bytes of the workspace that pgg_grouped_linear_bwd needs, into *bytes. */
+int pgg_grouped_linear_bwd_workspace_size(int64_t M, int64_t N, int G, int act, size_t* bytes);
+
+/* Its gradient up to the product:  dZ = dY act'(Z),  dbias_g = sum over group g's rows of dZ
+ * (fp32, in a fixed order; 0 for an empty group).  dX and dW are pgg_grouped_gemm_dgrad and
+ * pgg_grouped_gemm_wgrad on dZ; the residual's gradient is dY.
+ *   dY [M, N] bf16 (PGG_ACT_SWIGLU: [M, N/2]), Z [M, N] bf16 as saved; dZ [M, N] bf16 (out; NULL: the
+ *   bias' gradient alone; may be Z, and dY where they have one shape); dbias [G, N] fp32 (out).
+ *   PGG_ACT_NONE: Z and dZ are NULL (dZ is dY).  No gradient passes where a clamp is active.
+ *   ws: device scratch, 16-byte aligned; it holds nothing between calls.  M == 0 writes dbias = 0.
+ *   Bad group_lens set *err and write nothing. */
+int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_lens, void* dZ, float* dbias, int64_t M,
+                           int64_t N, int G, int act, float alpha, float offset, float limit, void* ws,
+                           size_t ws_bytes, int32_t* err, void* stream);
+
+/* Test hook, as pgg_test_stalled_fwd below for pgg_grouped_linear (bf16 Y, alpha 1, no bias). */
+int pgg_test_stalled_linear(const void* X, const void* W, const int32_t* group_lens, void* Y, int64_t M, int64_t N,
+                            int64_t K, int G, int act, int64_t stall_at, uint64_t wait_ns, int32_t* err, void* stream);
+
+/* Forms of a block's gate. */
+typedef enum { PGG_GATE_NONE = 0, PGG_GATE_TOKEN = 1, PGG_GATE_CHANNEL = 2 } pgg_gate;
+
+/* Between two blocks, in one pass: the norm of a block's output, dropout, its gate, the scaled
+ * residual's addition, the next block's norm and the MX operand of its first product.
+ *   t = x rstd_post gamma_post    rstd_post = 1 / sqrt(mean(x^2) + eps)   (gamma_post NULL: t = x)
+ *   b = keep t / (1 - p)
+ *   s = residual_scale residual + branch_scale gate b     h = bf16(s)     (residual NULL: 0)
+ *   y = s rstd gamma              rstd = 1 / sqrt(mean(s^2) + eps)        (gamma NULL: no y, rstd, codes)
+ *   in fp32, every output rounded once.  x, residual [R, C], gamma_post, gamma [C] bf16.
+ *   gate: PGG_GATE_TOKEN [R] fp32, PGG_GATE_CHANNEL [C] bf16; NULL with PGG_GATE_NONE (1).
+ *   Dropout, 0 <= p < 1 (0: none): rng is a device int64[2] {seed, offset}, 8-byte aligned, read when the
+ *   call runs (a replayed graph takes what it holds then).  Element i of the row-major tensor is kept
+ *   where word i % 4 of Philox4x32-10 with the counter (i / 4, offset), low words first, and the key
+ *   seed is at least floor(p 2^32); a dropped element is 0 whatever it held.  Calls with other offsets
+ *   have independent masks.  The mask is not stored: pgg_block_join_bwd computes it again from the same
+ *   rng and p.
+ *   Outputs, each optional (NULL), at least one given: h, y [R, C] bf16, rstd_post, rstd [R] fp32, and
+ *   with fmt codes and scales as in pgg_add_rmsnorm.  8 <= C <= PGG_NORM_MAX_COLS, C % 8 == 0, with codes
+ *   C % 32 == 0; eps >= 0.  h may be x or residual (in place).  R == 0 is a no-op.  Sums of squares are
+ *   fp32, with the range given at pgg_add_rmsnorm. */
+int pgg_block_join(const void* x, const void* residual, const void* gamma_post, const void* gamma, const void* gate,
+                   int gate_kind, const int64_t* rng, int64_t R, int64_t C, double p, float residual_scale,
+                   float branch_scale, float eps, int fmt, void* h, void* y, uint8_t* codes, uint8_t* scales,
+                   float* rstd_post, float* rstd, void* stream);
+
+/* Bytes of the workspace that pgg_block_join_bwd needs, into *bytes. */
+int pgg_block_join_bwd_workspace_size(int64_t R, int64_t C, size_t* bytes);
+
+/* Backward pass, with xh = x rstd_post and hh = h rstd:
+ *   d = dh + rstd (u - hh mean(u hh)), u = dy gamma          dgamma = sum over rows of dy hh
+ *   dresidual = residual_scale d
+ *   dgate = branch_scale sum of d b over the row (token), over the rows (channel)
+ *   dt = branch_scale gate d keep / (1 - p)                  dgamma_post = sum over rows of dt xh
+ *   dx = rstd_post (w - xh mean(w xh)), w = dt gamma_post    (without gamma_post: dx = dt)
+ *   dy [R, C] bf16 (NULL without gamma), dh [R, C] bf16 or NULL, x, h, rstd_post, rstd as in and from the
+ *   forward call (h and rstd NULL without gamma, rstd_post without gamma_post); the other arguments are
+ *   that call's.  dx [R, C] bf16; dresidual [R, C] bf16 or NULL; dgamma_post, dgamma [C], dgate [R] or
+ *   [C] fp32, each given where its operand is, summed up in a fixed order.
+ *   dx and dresidual may be dy, dh, x or h (not the same of them).  ws: device scratch, 16-byte
+ *   aligned; it holds nothing between calls.  R == 0 writes zero sums. */
+int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void* h, const float* rstd_post,
+                       const float* rstd, const void* gamma_post, const void* gamma, const void* gate, int gate_kind,
+                       const int64_t* rng, int64_t R, int64_t C, double p, float residual_scale, float branch_scale,
+                       void* dx, void* dresidual, float* dgamma_post, float* dgamma, float* dgate, void* ws,
+                       size_t ws_bytes, void* stream);
+
 /* Test hook, as pgg_test_stalled_fwd below for the few-token layer (fmt 0: bf16, SX / SW1 / SW2
  * unused; weights 1): every CTA's load producer stops before the stall_at-th stage of its run, and
  * every wait is limited to wait_ns.  The kernel must give up, free its tensor memory, exit and write

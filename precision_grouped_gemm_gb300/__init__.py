@@ -17,7 +17,9 @@ from ._binding import (PggError, PAD, FMT_E4M3, FMT_E2M1, MODE_FWD, MODE_DGRAD, 
                        fp8_grouped_gemm,
                        moe_permute_workspace_size, moe_permute, moe_combine, moe_combine_bwd,
                        add_rmsnorm, add_rmsnorm_bwd, add_rmsnorm_bwd_workspace_size, moe_route, moe_route_bwd,
-                       moe_decode, mx_moe_decode, moe_decode_workspace, moe_decode_workspace_size)
+                       moe_decode, mx_moe_decode, moe_decode_workspace, moe_decode_workspace_size,
+                       grouped_linear, grouped_linear_bwd, grouped_linear_bwd_workspace_size,
+                       block_join, block_join_bwd, block_join_bwd_workspace_size)
 
 __all__ = [
     "PggError", "PAD", "FMT_E4M3", "FMT_E2M1", "MODE_FWD", "MODE_DGRAD", "MODE_WGRAD",
@@ -29,4 +31,6 @@ __all__ = [
     "fp8_workspace_size", "fp8_grouped_gemm", "moe_permute_workspace_size", "moe_permute", "moe_combine",
     "moe_combine_bwd", "add_rmsnorm", "add_rmsnorm_bwd", "add_rmsnorm_bwd_workspace_size", "moe_route",
     "moe_route_bwd", "moe_decode", "mx_moe_decode", "moe_decode_workspace", "moe_decode_workspace_size",
+    "grouped_linear", "grouped_linear_bwd", "grouped_linear_bwd_workspace_size",
+    "block_join", "block_join_bwd", "block_join_bwd_workspace_size",
 ]

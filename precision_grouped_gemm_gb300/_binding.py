@@ -58,6 +58,16 @@ SIGNATURES = {
                           ctypes.c_size_t, _P, _P],
     "pgg_test_stalled_moe_decode": [_I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _I64,
                                     ctypes.c_uint64, _P, ctypes.c_size_t, _P, _P],
+    "pgg_grouped_linear": [_P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _I32, _I32, _F32, _F32, _F32, _P, _P],
+    "pgg_grouped_linear_bwd_workspace_size": [_I64, _I64, _I32, _I32, _P],
+    "pgg_grouped_linear_bwd": [_P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _F32, _F32, _F32, _P, ctypes.c_size_t, _P,
+                               _P],
+    "pgg_test_stalled_linear": [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I64, ctypes.c_uint64, _P, _P],
+    "pgg_block_join": [_P, _P, _P, _P, _P, _I32, _P, _I64, _I64, ctypes.c_double, _F32, _F32, _F32, _I32, _P, _P, _P,
+                       _P, _P, _P, _P],
+    "pgg_block_join_bwd_workspace_size": [_I64, _I64, _P],
+    "pgg_block_join_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, ctypes.c_double, _F32, _F32, _P,
+                           _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "pgg_test_stalled_fwd": [_I32, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I64, ctypes.c_uint64, _P, _P],
 }
 
@@ -641,3 +651,195 @@ def mx_moe_decode(fmt, X, SX, ids, w, W1, SW1, W2, SW2, out=None, swiglu_limit=0
     _check(lib().pgg_mx_moe_decode(f, px, ps, pi, pw, p1, q1, p2, q2, po, T, k, H, I, E, swiglu_limit,
                                    *_scratch(ws), pe, _stream(stream)), "pgg_mx_moe_decode")
     return out
+
+
+_ACT = {None: 0, "silu": 1, "gelu": 2, "swiglu": 3}
+
+
+def _act(act):
+    if act not in _ACT:
+        raise ValueError("act must be None, 'silu', 'gelu' or 'swiglu'")
+    return _ACT[act]
+
+
+def _groups(group_lens, G):
+    """The lengths' address; None: one group of all rows."""
+    if group_lens is None:
+        if G != 1:
+            raise ValueError("several groups need group_lens")
+        return None
+    return _in(group_lens, "group_lens", _I, (G,))
+
+
+def grouped_linear(X, W, group_lens=None, bias=None, residual=None, act=None, alpha=1.0, offset=0.0, limit=0.0, Y=None,
+                   Z=None, save_z=False, out_dtype=torch.bfloat16, err=None, stream=None):
+    """Z_g = X_g W_g^T + bias_g, Y = act(Z) + residual: X [M,K], W [G,N,K] (or [N,K] for one group), bias [G,N]
+    (or [N]) bf16; group_lens [G] int32, or None for one group -> (Y, Z).
+
+    Y [M,N] ([M,N/2] with act "swiglu"), in out_dtype (bf16 or fp32), which residual has too; Z [M,N] bf16
+    with save_z, for the backward pass, else None.  act: None, "silu", "gelu" or "swiglu" (gate | up);
+    alpha, offset and limit are theirs, see pgg.h."""
+    given = X, W, group_lens, bias, residual, Y, Z, err
+    M, K = X.shape
+    G, N = (1, W.shape[0]) if W.dim() == 2 else W.shape[:2]
+    kind = _act(act)
+    width = N // 2 if kind == 3 else N
+    if Y is not None:
+        out_dtype = Y.dtype
+    if out_dtype not in _DTYPE:
+        raise ValueError("Y must be float32 or bfloat16")
+    px, pw = _in(X, "X", _BF, (M, K)), _in(W, "W", _BF, (N, K) if W.dim() == 2 else (G, N, K))
+    pl = _groups(group_lens, G)
+    pb = None if bias is None else _in(bias, "bias", _BF, (N,) if bias.dim() == 1 and G == 1 else (G, N))
+    pr = _in(residual, "residual", out_dtype, (M, width))
+    Y, py = _out(Y, "Y", out_dtype, (M, width), X.device, stream)
+    pz = None
+    if save_z or Z is not None:
+        Z, pz = _out(Z, "Z", _BF, (M, N), X.device, stream)
+    pe = None if err is None else _in(err, "err", _I, err.shape)
+    _dev(*given)
+    _check(lib().pgg_grouped_linear(px, pw, pl, pb, pr, py, _DTYPE[out_dtype], pz, M, N, K, G, kind, alpha, offset, limit,
+                                    pe, _stream(stream)), "pgg_grouped_linear")
+    return Y, Z
+
+
+@functools.lru_cache(maxsize=1024)
+def grouped_linear_bwd_workspace_size(M: int, N: int, G: int, act=None) -> int:
+    return _size_of("pgg_grouped_linear_bwd_workspace_size", M, N, G, _act(act))
+
+
+def grouped_linear_bwd(dY, Z=None, group_lens=None, act=None, alpha=1.0, offset=0.0, limit=0.0, dZ=None, dbias=None,
+                       ws=None, err=None, stream=None):
+    """Backward of grouped_linear up to its product: dY bf16, Z [M,N] as saved (None without act)
+    -> (dZ = dY act'(Z) [M,N] bf16, dbias [G,N] fp32: dZ summed over each group's rows).
+
+    Without act dZ is dY itself.  dX and dW are grouped_gemm_dgrad and grouped_gemm_wgrad on dZ."""
+    given = dY, Z, group_lens, dZ, dbias, ws, err
+    kind = _act(act)
+    M, width = dY.shape
+    N = 2 * width if kind == 3 else width
+    G = 1 if group_lens is None else group_lens.numel()
+    if kind == 0 and (Z is not None or dZ is not None):
+        raise ValueError("Z and dZ need act")
+    if kind and Z is None:
+        raise ValueError("act needs Z")
+    py, pz = _in(dY, "dY", _BF, (M, width)), _in(Z, "Z", _BF, (M, N))
+    pl = _groups(group_lens, G)
+    pd = None
+    if kind:
+        dZ, pd = _out(dZ, "dZ", _BF, (M, N), dY.device, stream)
+    dbias, pb = _out(dbias, "dbias", _F, (G, N), dY.device, stream)
+    if ws is None:
+        ws = _new(torch.empty, max(16, grouped_linear_bwd_workspace_size(M, N, G, act)), _U8, dY.device, stream)
+    pe = None if err is None else _in(err, "err", _I, err.shape)
+    _dev(*given)
+    _check(lib().pgg_grouped_linear_bwd(py, pz, pl, pd, pb, M, N, G, kind, alpha, offset, limit, *_scratch(ws), pe,
+                                        _stream(stream)), "pgg_grouped_linear_bwd")
+    return (dZ if kind else dY), dbias
+
+
+def _gate(gate, R, C):
+    """(kind, address) of a gate: None, fp32 [R] (a row's) or bf16 [C] (a column's)."""
+    if gate is None:
+        return 0, None
+    if gate.dtype is _F:
+        return 1, _in(gate, "gate", _F, (R,))
+    return 2, _in(gate, "gate", _BF, (C,))
+
+
+def _rng(rng, p):
+    if not 0.0 <= p < 1.0:
+        raise ValueError("p must be at least 0 and below 1")
+    if p and rng is None:
+        raise ValueError("dropout needs rng")
+    return _in(rng, "rng", torch.int64, (2,))
+
+
+def block_join(x, residual, gamma_post=None, gamma=None, gate=None, residual_scale=1.0, branch_scale=1.0, p=0.0, rng=None,
+               eps=1e-6, fmt=None, h=None, y=None, codes=None, scales=None, rstd_post=None, rstd=None, save_y=True,
+               save_rstd=True, stream=None):
+    """Between two blocks: s = residual_scale residual + branch_scale gate dropout(rmsnorm(x) gamma_post),
+    y = rmsnorm(s) gamma; x, residual (or None) [R,C] bf16.
+
+    gate: fp32 [R] (per row), bf16 [C] (per column) or None; gamma_post None: no norm of x; gamma None: no y.
+    Dropout with probability p: rng int64 [2] on the device, (seed, offset); see pgg.h.
+    -> (h = bf16(s), y, codes, scales, rstd_post, rstd): y None with save_y=False or without gamma, codes /
+    scales (the row-wise MX operand in `fmt`) None without fmt, the rstd (what block_join_bwd reads) None
+    with save_rstd=False and without their gamma."""
+    given = x, residual, gamma_post, gamma, gate, rng, h, y, codes, scales, rstd_post, rstd
+    R, C = shape = x.shape
+    dev = x.device
+    f = 0 if fmt is None else _FMT[fmt]
+    px, pr = _in(x, "x", _BF, shape), _in(residual, "residual", _BF, shape)
+    p1, p2 = _in(gamma_post, "gamma_post", _BF, (C,)), _in(gamma, "gamma", _BF, (C,))
+    kind, pg = _gate(gate, R, C)
+    pn = _rng(rng, p)
+    if gamma is None and (f or y is not None or rstd is not None):
+        raise ValueError("y, fmt and rstd need gamma")
+    if gamma_post is None and rstd_post is not None:
+        raise ValueError("rstd_post needs gamma_post")
+    h, ph = _out(h, "h", _BF, shape, dev, stream)
+    py = pc = ps = pd1 = pd2 = None
+    if gamma is not None and (save_y or y is not None):
+        y, py = _out(y, "y", _BF, shape, dev, stream)
+    if f:
+        codes, pc = _out(codes, "codes", _U8, (R, C if f == FMT_E4M3 else C // 2), dev, stream)
+        scales, ps = _out(scales, "scales", _U8, (R, C // 32), dev, stream)
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales need fmt")
+    if gamma_post is not None and (save_rstd or rstd_post is not None):
+        rstd_post, pd1 = _out(rstd_post, "rstd_post", _F, (R,), dev, stream)
+    if gamma is not None and (save_rstd or rstd is not None):
+        rstd, pd2 = _out(rstd, "rstd", _F, (R,), dev, stream)
+    _dev(*given)
+    _check(lib().pgg_block_join(px, pr, p1, p2, pg, kind, pn, R, C, p, residual_scale, branch_scale, eps, f, ph, py, pc,
+                                ps, pd1, pd2, _stream(stream)), "pgg_block_join")
+    return h, y, codes, scales, rstd_post, rstd
+
+
+@functools.lru_cache(maxsize=1024)
+def block_join_bwd_workspace_size(R: int, C: int) -> int:
+    return _size_of("pgg_block_join_bwd_workspace_size", R, C)
+
+
+def block_join_bwd(dy, dh, x, h=None, rstd_post=None, rstd=None, gamma_post=None, gamma=None, gate=None,
+                   residual_scale=1.0, branch_scale=1.0, p=0.0, rng=None, dx=None, dresidual=None, dgamma_post=None,
+                   dgamma=None, dgate=None, save_dresidual=True, ws=None, stream=None):
+    """Backward of block_join: dy the gradient of y (None without gamma), dh that of h (or None), x, h and the
+    two rstd as in and from the forward call; rng must hold what it held there
+    -> (dx [R,C] bf16, dresidual [R,C] bf16 (None with save_dresidual=False), dgamma_post [C], dgamma [C], dgate
+    [R] or [C], fp32, each None without its operand)."""
+    given = (dy, dh, x, h, rstd_post, rstd, gamma_post, gamma, gate, rng, dx, dresidual, dgamma_post, dgamma, dgate, ws)
+    R, C = shape = x.shape
+    dev = x.device
+    if gamma is None and dy is not None:
+        raise ValueError("dy needs gamma")
+    if gamma is not None and (dy is None or h is None or rstd is None):
+        raise ValueError("gamma needs dy, h and rstd")
+    if gamma_post is not None and rstd_post is None:
+        raise ValueError("gamma_post needs rstd_post")
+    for name, out, of in (("dgamma_post", dgamma_post, gamma_post), ("dgamma", dgamma, gamma), ("dgate", dgate, gate)):
+        if out is not None and of is None:
+            raise ValueError(f"{name} needs {name[1:]}")
+    py, pd = _in(dy, "dy", _BF, shape), _in(dh, "dh", _BF, shape)
+    px, ph = _in(x, "x", _BF, shape), _in(h, "h", _BF, shape)
+    q1, q2 = _in(rstd_post, "rstd_post", _F, (R,)), _in(rstd, "rstd", _F, (R,))
+    p1, p2 = _in(gamma_post, "gamma_post", _BF, (C,)), _in(gamma, "gamma", _BF, (C,))
+    kind, pg = _gate(gate, R, C)
+    pn = _rng(rng, p)
+    dx, pdx = _out(dx, "dx", _BF, shape, dev, stream)
+    pdr = pd1 = pd2 = pdg = None
+    if save_dresidual or dresidual is not None:
+        dresidual, pdr = _out(dresidual, "dresidual", _BF, shape, dev, stream)
+    if gamma_post is not None:
+        dgamma_post, pd1 = _out(dgamma_post, "dgamma_post", _F, (C,), dev, stream)
+    if gamma is not None:
+        dgamma, pd2 = _out(dgamma, "dgamma", _F, (C,), dev, stream)
+    if gate is not None:
+        dgate, pdg = _out(dgate, "dgate", _F, gate.shape, dev, stream)
+    if ws is None:
+        ws = _new(torch.empty, max(16, block_join_bwd_workspace_size(R, C)), _U8, dev, stream)
+    _dev(*given)
+    _check(lib().pgg_block_join_bwd(py, pd, px, ph, q1, q2, p1, p2, pg, kind, pn, R, C, p, residual_scale, branch_scale,
+                                    pdx, pdr, pd1, pd2, pdg, *_scratch(ws), _stream(stream)), "pgg_block_join_bwd")
+    return dx, dresidual, dgamma_post, dgamma, dgate

@@ -1,0 +1,594 @@
+// Between two blocks: the norm of a block's output, dropout, its gate, the scaled residual's
+// addition, the next block's norm and the MX operand of its first product, in one pass:
+//
+//   t = x rstd1 gamma1 (or x)        rstd1 = 1 / sqrt(mean(x^2) + eps)
+//   b = keep t / (1 - p)
+//   s = ra residual + rb gate b      h = bf16(s)
+//   y = s rstd2 gamma2               rstd2 = 1 / sqrt(mean(s^2) + eps)
+//
+// fp32 throughout, every output rounded once.  gate: a number per row, or per column.
+//
+// Backward, from x, h and the two rstd (xh = x rstd1, hh = h rstd2):
+//
+//   d = dh + rstd2 (u - hh mean(u hh)),  u = dy gamma2       dgamma2 = sum_rows dy hh
+//   dresidual = ra d                                         dgate = rb sum d b (over columns, or rows)
+//   dt = rb gate d keep / (1 - p)                            dgamma1 = sum_rows dt xh
+//   dx = rstd1 (w - xh mean(w xh)),  w = dt gamma1 (or dx = dt)
+//
+// The mask is never stored: element i of the row-major tensor is kept where word i % 4 of block
+// (i / 4, offset) of Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as
+// 1, 2, 3", 2011) under the key `seed` is at least floor(p 2^32); both passes compute it.
+#include <algorithm>
+#include <atomic>
+
+#include "block.cuh"
+
+namespace pgg {
+namespace {
+
+// Sums of N values over the block, in a fixed order, in every thread.  s: one buffer of a pair that
+// successive sums alternate between, so that one barrier a sum is enough.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[32], int nwarps) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if ((threadIdx.x & 31) == 0) s[i][threadIdx.x >> 5] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = (threadIdx.x & 31) < nwarps ? s[i][threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+  }
+}
+
+struct Drop {
+  const int64_t* rng;  // {seed, offset}
+  uint32_t below;      // words below it drop their element
+  float inv;           // 1 / (1 - p); 1 without dropout
+};
+
+struct Key {
+  uint32_t k0, k1, o0, o1;
+};
+__device__ __forceinline__ Key load_key(const Drop& d) {
+  const uint64_t seed = (uint64_t)__ldg(reinterpret_cast<const long long*>(d.rng));
+  const uint64_t off = (uint64_t)__ldg(reinterpret_cast<const long long*>(d.rng) + 1);
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+}
+
+__device__ __forceinline__ uint4 philox(uint64_t block, const Key& key) {
+  uint32_t x0 = (uint32_t)block, x1 = (uint32_t)(block >> 32), x2 = key.o0, x3 = key.o1;
+  uint32_t k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = (uint64_t)0xD2511F53u * x0, p1 = (uint64_t)0xCD9E8D57u * x2;
+    x0 = (uint32_t)(p1 >> 32) ^ x1 ^ k0;
+    x1 = (uint32_t)p1;
+    x2 = (uint32_t)(p0 >> 32) ^ x3 ^ k1;
+    x3 = (uint32_t)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(x0, x1, x2, x3);
+}
+// Bit e: element e of the 8-element piece number `piece` of the tensor is kept.
+__device__ __forceinline__ uint32_t keep8(int64_t piece, const Drop& d, const Key& key) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = philox((uint64_t)piece * 2 + i, key);
+    m |= ((w.x >= d.below ? 1u : 0u) | (w.y >= d.below ? 2u : 0u) | (w.z >= d.below ? 4u : 0u) |
+          (w.w >= d.below ? 8u : 0u)) << (4 * i);
+  }
+  return m;
+}
+
+enum { kGateNone = 0, kGateRow = 1, kGateColumn = 2 };
+
+struct JoinArgs {
+  const uint4* x;
+  const uint4* residual;  // or nullptr
+  const uint4* gamma1;    // or nullptr
+  const uint4* gamma2;    // or nullptr
+  const float* gate_row;  // or nullptr
+  const uint4* gate_col;  // or nullptr
+  Drop drop;              // rng nullptr: none
+  int64_t R;
+  int nvec;
+  float inv_c, eps, ra, rb;
+  uint4* h;  // outputs: each or nullptr
+  uint4* y;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* rstd1;
+  float* rstd2;
+};
+
+// A block walks rows with a grid stride; thread t owns the row's 8-element pieces t, t + blockDim, ...
+// (V of them), which stay in registers from their load to the outputs, so every byte moves once.
+template <int V, int FMT>
+__global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
+  __shared__ float s_sum[2][1][32];
+  const int nwarps = blockDim.x >> 5;
+  Key key{};
+  if (a.drop.rng) key = load_key(a.drop);
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
+    const int64_t base = row * a.nvec;
+    uint4 xv[V], rv[V];  // every load of the row before the first store (h may be x or residual)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      xv[j] = rv[j] = make_uint4(0, 0, 0, 0);
+      if (v < a.nvec) {
+        xv[j] = a.x[base + v];
+        if (a.residual) rv[j] = a.residual[base + v];
+      }
+    }
+    const float gate = a.rb * (a.gate_row ? __ldg(a.gate_row + row) : 1.0f);
+    uint32_t keep[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
+    float rstd1 = 1.0f;
+    if (a.gamma1) {
+      float q[1] = {0.0f};
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float f[8];
+        unpack8(xv[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[0] += f[e] * f[e];
+      }
+      block_sums(q, s_sum[par], nwarps);
+      par ^= 1;
+      rstd1 = rsqrtf(q[0] * a.inv_c + a.eps);
+      if (a.rstd1 && threadIdx.x == 0) a.rstd1[row] = rstd1;
+    }
+    float s[V][8];
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      if (v < a.nvec) {
+        float t[8], r[8], g[8];
+        unpack8(xv[j], t);
+        unpack8(rv[j], r);
+        if (a.gamma1) {
+          unpack8(__ldg(a.gamma1 + v), g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = t[e] * rstd1 * g[e];
+        }
+        if (a.gate_col) unpack8(__ldg(a.gate_col + v), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float b = (keep[j] >> e) & 1u ? t[e] * a.drop.inv : 0.0f;
+          s[j][e] = fmaf(a.ra, r[e], (a.gate_col ? gate * g[e] : gate) * b);
+          q[0] += s[j][e] * s[j][e];
+        }
+        if (a.h) a.h[base + v] = pack8(s[j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[j][e] = 0.0f;
+      }
+    }
+    if (!a.gamma2) continue;
+    block_sums(q, s_sum[par], nwarps);
+    par ^= 1;
+    const float rstd2 = rsqrtf(q[0] * a.inv_c + a.eps);
+    if (a.rstd2 && threadIdx.x == 0) a.rstd2[row] = rstd2;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      // the four lanes of an MX block are in range together: nvec is a multiple of 4 with FMT
+      const bool in = v < a.nvec;
+      float y[8];
+      if (in) {
+        float g[8];
+        unpack8(__ldg(a.gamma2 + v), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = s[j][e] * rstd2 * g[e];
+        if (a.y) a.y[base + v] = pack8(y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+      }
+      if (FMT) {
+        uint32_t am = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        uint32_t sc;
+        float mult;
+        const bool fin = block_scale_f32<FMT>(am, sc, mult);
+        if (in) {
+          float c[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c[e] = fin ? y[e] * mult : 0.0f;
+          if (FMT == kE4M3) {
+            uint2 o;
+            o.x = cvt_e4m3x2(c[0], c[1]) | (cvt_e4m3x2(c[2], c[3]) << 16);
+            o.y = cvt_e4m3x2(c[4], c[5]) | (cvt_e4m3x2(c[6], c[7]) << 16);
+            reinterpret_cast<uint2*>(a.codes)[base + v] = o;
+          } else {
+            reinterpret_cast<uint32_t*>(a.codes)[base + v] =
+                cvt_e2m1x2(c[0], c[1]) | (cvt_e2m1x2(c[2], c[3]) << 8) | (cvt_e2m1x2(c[4], c[5]) << 16) |
+                (cvt_e2m1x2(c[6], c[7]) << 24);
+          }
+          if ((v & 3) == 0) a.scales[(base + v) >> 2] = (uint8_t)sc;
+        }
+      }
+    }
+  }
+}
+
+struct JoinBwdArgs {
+  const uint4* dy;  // or nullptr (no gamma2)
+  const uint4* dh;  // or nullptr
+  const uint4* x;
+  const uint4* h;
+  const float* rstd1;
+  const float* rstd2;
+  const uint4* gamma1;
+  const uint4* gamma2;
+  const float* gate_row;
+  const uint4* gate_col;
+  Drop drop;
+  int64_t R;
+  int nvec;
+  float inv_c, ra, rb;
+  uint4* dx;
+  uint4* dres;       // or nullptr
+  float* dgate_row;  // or nullptr
+  float* part;       // [3][gridDim.x][C]: the blocks' sums for dgamma1, dgamma2, dgate per column
+};
+
+// The same ownership: a thread's columns stay its own over all rows of the block, so the sums over
+// rows are registers, written once per block.  A thread copies its pieces of coming rows into its own
+// places of shared memory, DEPTH - 1 rows ahead (no thread reads another's).
+template <int V, int DEPTH>
+__global__ void __launch_bounds__(512) join_bwd_kernel(const JoinBwdArgs a) {
+  extern __shared__ uint4 s_row[];  // [DEPTH][4][V][blockDim]
+  __shared__ float s_sum[2][2][32];
+  const int nwarps = blockDim.x >> 5;
+  Key key{};
+  if (a.drop.rng) key = load_key(a.drop);
+  float dg1[V][8], dg2[V][8], dgc[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg1[j][e] = dg2[j][e] = dgc[j][e] = 0.0f;
+  auto place = [&](int slot, int which, int j) {
+    return s_row + ((slot * 4 + which) * V + j) * blockDim.x + threadIdx.x;
+  };
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < a.R) {
+      const int64_t base = row * a.nvec;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < a.nvec) {
+          if (a.gamma2) {
+            cp_async_16(smem_u32(place(slot, 0, j)), a.h + base + v);
+            cp_async_16(smem_u32(place(slot, 1, j)), a.dy + base + v);
+          }
+          if (a.dh) cp_async_16(smem_u32(place(slot, 2, j)), a.dh + base + v);
+          cp_async_16(smem_u32(place(slot, 3, j)), a.x + base + v);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+  int par = 0, slot = 0;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
+    const int64_t base = row * a.nvec;
+    fetch(row + (int64_t)(DEPTH - 1) * gridDim.x, slot == 0 ? DEPTH - 1 : slot - 1);
+    uint32_t keep[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
+    const float rstd1 = a.gamma1 ? __ldg(a.rstd1 + row) : 1.0f, rstd2 = a.gamma2 ? __ldg(a.rstd2 + row) : 0.0f;
+    const float gate = a.rb * (a.gate_row ? __ldg(a.gate_row + row) : 1.0f);
+    cp_async_wait<DEPTH - 1>();
+    // d = dh + rstd2 u + c h, with the sum over the row in c
+    float c = 0.0f;
+    if (a.gamma2) {
+      float q[1] = {0.0f};
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < a.nvec) {
+          float hv[8], dy[8], g[8];
+          unpack8(*place(slot, 0, j), hv);
+          unpack8(*place(slot, 1, j), dy);
+          unpack8(__ldg(a.gamma2 + v), g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float t = dy[e] * hv[e];
+            dg2[j][e] = fmaf(t, rstd2, dg2[j][e]);
+            q[0] = fmaf(t, g[e], q[0]);
+          }
+        }
+      }
+      block_sums(q, s_sum[par], nwarps);
+      par ^= 1;
+      c = -rstd2 * rstd2 * (q[0] * rstd2 * a.inv_c);
+    }
+    float w[V][8];  // the gradient of x, before the norm's mean is taken out of it
+    float q[2] = {0.0f, 0.0f};  // sum w x, sum d b
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      if (v < a.nvec) {
+        float d[8], x[8], g1[8], gc[8];
+        if (a.dh) {
+          unpack8(*place(slot, 2, j), d);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+        }
+        if (a.gamma2) {
+          float hv[8], dy[8], g[8];
+          unpack8(*place(slot, 0, j), hv);
+          unpack8(*place(slot, 1, j), dy);
+          unpack8(__ldg(a.gamma2 + v), g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = fmaf(c, hv[e], fmaf(dy[e] * g[e], rstd2, d[e]));
+        }
+        if (a.dres) {
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = a.ra * d[e];
+          a.dres[base + v] = pack8(o);
+        }
+        unpack8(*place(slot, 3, j), x);
+        if (a.gamma1) unpack8(__ldg(a.gamma1 + v), g1);
+        if (a.gate_col) unpack8(__ldg(a.gate_col + v), gc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // d keep / (1 - p): the part of it that reaches t, and with t the gate's gradient
+          const float dk = (keep[j] >> e) & 1u ? d[e] * a.drop.inv : 0.0f;
+          const float xh = x[e] * rstd1;
+          const float t = a.gamma1 ? xh * g1[e] : x[e];
+          const float db = (keep[j] >> e) & 1u ? dk * t : 0.0f;
+          if (a.gate_col) dgc[j][e] = fmaf(a.rb, db, dgc[j][e]);
+          q[1] += db;
+          const float dt = (a.gate_col ? gate * gc[e] : gate) * dk;
+          if (a.gamma1) dg1[j][e] = fmaf(dt, xh, dg1[j][e]);
+          w[j][e] = a.gamma1 ? dt * g1[e] : dt;
+          q[0] = fmaf(w[j][e], x[e], q[0]);
+        }
+      }
+    }
+    float mean = 0.0f;
+    if (a.gamma1 || a.dgate_row) {
+      block_sums(q, s_sum[par], nwarps);
+      par ^= 1;
+      if (a.dgate_row && threadIdx.x == 0) a.dgate_row[row] = a.rb * q[1];
+      mean = q[0] * rstd1 * a.inv_c;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      if (v < a.nvec) {
+        if (a.gamma1) {
+          float x[8];
+          unpack8(*place(slot, 3, j), x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[j][e] = rstd1 * fmaf(-(x[e] * rstd1), mean, w[j][e]);
+        }
+        a.dx[base + v] = pack8(w[j]);
+      }
+    }
+    if (++slot == DEPTH) slot = 0;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v < a.nvec) {
+      const int64_t plane = (int64_t)gridDim.x * a.nvec * 2;
+      float4* p = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.nvec + v) * 2;
+      auto put = [&](float4* dst, const float (&f)[8]) {
+        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+      };
+      if (a.gamma1) put(p, dg1[j]);
+      if (a.gamma2) put(p + plane, dg2[j]);
+      if (a.gate_col) put(p + 2 * plane, dgc[j]);
+    }
+  }
+}
+
+// Columns of the three sums: n partial rows each, added in a fixed order; a block has eight columns
+// (a 32-byte sector of each row) of one of them.
+struct JoinReduce {
+  const float* part;
+  int n, C;
+  float* out[3];  // of dgamma1, dgamma2, dgate; the first `count` of which[] are wanted
+  int which[3];
+};
+constexpr int kReduceThreads = 512;
+__global__ void __launch_bounds__(kReduceThreads) join_reduce_kernel(const JoinReduce a) {
+  constexpr int kWarps = kReduceThreads / 32, kGroups = kReduceThreads / 8;
+  __shared__ float s[kWarps][8];
+  const int c = threadIdx.x & 7, i0 = threadIdx.x >> 3, w = threadIdx.x >> 5;
+  const int which = a.which[blockIdx.y];
+  const float* p = a.part + (int64_t)which * a.n * a.C + blockIdx.x * 8 + c;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float t = 0.0f;
+#pragma unroll 4
+  for (int i = i0; i < a.n; i += kGroups) t += p[(int64_t)i * a.C];
+  t += __shfl_xor_sync(0xffffffffu, t, 8);
+  t += __shfl_xor_sync(0xffffffffu, t, 16);
+  if ((threadIdx.x & 31) < 8) s[w][c] = t;
+  __syncthreads();
+  if (w == 0) {
+    t = 0.0f;
+    for (int k = threadIdx.x >> 3; k < kWarps; k += 4) t += s[k][c];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if (threadIdx.x < 8) a.out[which][blockIdx.x * 8 + c] = t;
+  }
+}
+
+int threads_of(int nvec, int V) { return std::max(32, ((nvec + V - 1) / V + 31) / 32 * 32); }
+int join_v(int nvec) { return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4; }
+
+// Blocks of the backward pass: at most as many as are resident at once, which this bounds for the
+// workspace.
+int bwd_blocks(int64_t R, int nvec) {
+  const int threads = threads_of(nvec, join_v(nvec));
+  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, 1024 / threads)));
+}
+
+template <int V>
+void launch_join(const JoinArgs& a, int fmt, int grid, int threads, cudaStream_t s) {
+  if (fmt == kE4M3) join_kernel<V, kE4M3><<<grid, threads, 0, s>>>(a);
+  else if (fmt == kE2M1) join_kernel<V, kE2M1><<<grid, threads, 0, s>>>(a);
+  else join_kernel<V, 0><<<grid, threads, 0, s>>>(a);
+}
+
+int check(int64_t R, int64_t C, int mult, const void* gate, int gate_kind, const int64_t* rng, double p, float ra,
+          float rb) {
+  if (R < 0 || R >= ((int64_t)1 << 31) || C < mult || C > PGG_NORM_MAX_COLS) return PGG_ERR_INVALID_ARG;
+  if (C % mult) return PGG_ERR_ALIGNMENT;
+  if (gate_kind < PGG_GATE_NONE || gate_kind > PGG_GATE_CHANNEL) return PGG_ERR_INVALID_ARG;
+  if (!(p >= 0.0 && p < 1.0)) return PGG_ERR_INVALID_ARG;
+  const float big = 3.0e38f;
+  if (!(ra >= -big && ra <= big) || !(rb >= -big && rb <= big)) return PGG_ERR_INVALID_ARG;
+  if (R == 0) return PGG_OK;
+  if ((gate_kind != PGG_GATE_NONE) != (gate != nullptr) || (p > 0.0 && !rng)) return PGG_ERR_INVALID_ARG;
+  if (!aligned_to(gate, gate_kind == PGG_GATE_TOKEN ? 4 : 16) || !aligned_to(rng, 8)) return PGG_ERR_ALIGNMENT;
+  return PGG_OK;
+}
+
+Drop make_drop(const int64_t* rng, double p) {
+  const uint32_t below = (uint32_t)(p * 4294967296.0);  // p < 1: below 2^32; toward zero
+  return {p > 0.0 ? rng : nullptr, below, (float)(1.0 / (1.0 - p))};
+}
+
+}  // namespace
+}  // namespace pgg
+
+using namespace pgg;
+
+extern "C" {
+
+int pgg_block_join(const void* x, const void* residual, const void* gamma_post, const void* gamma, const void* gate,
+                   int gate_kind, const int64_t* rng, int64_t R, int64_t C, double p, float residual_scale,
+                   float branch_scale, float eps, int fmt, void* h, void* y, uint8_t* codes, uint8_t* scales,
+                   float* rstd_post, float* rstd, void* stream) {
+  if (fmt != 0 && fmt != PGG_FMT_E4M3 && fmt != PGG_FMT_E2M1) return PGG_ERR_INVALID_ARG;
+  int st = check(R, C, fmt ? 32 : 8, gate, gate_kind, rng, p, residual_scale, branch_scale);
+  if (st) return st;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return PGG_ERR_INVALID_ARG;
+  if (R == 0) return PGG_OK;
+  if ((fmt != 0) != (codes != nullptr) || (fmt != 0) != (scales != nullptr)) return PGG_ERR_INVALID_ARG;
+  if (!x || (!gamma && (y || fmt || rstd)) || (!gamma_post && rstd_post)) return PGG_ERR_INVALID_ARG;
+  if (!h && !y && !fmt && !rstd && !rstd_post) return PGG_ERR_INVALID_ARG;
+  for (const void* q : {x, residual, gamma_post, gamma, (const void*)h, (const void*)y, (const void*)codes})
+    if (!aligned_to(q, 16)) return PGG_ERR_ALIGNMENT;
+  if (!aligned_to(rstd_post, 4) || !aligned_to(rstd, 4)) return PGG_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != PGG_OK) return st;
+  JoinArgs a{static_cast<const uint4*>(x), static_cast<const uint4*>(residual), static_cast<const uint4*>(gamma_post),
+             static_cast<const uint4*>(gamma),
+             gate_kind == PGG_GATE_TOKEN ? static_cast<const float*>(gate) : nullptr,
+             gate_kind == PGG_GATE_CHANNEL ? static_cast<const uint4*>(gate) : nullptr, make_drop(rng, p), R,
+             (int)(C / 8), 1.0f / (float)C, eps, residual_scale, branch_scale, static_cast<uint4*>(h),
+             static_cast<uint4*>(y), codes, scales, rstd_post, rstd};
+  const int V = join_v(a.nvec), threads = threads_of(a.nvec, V);
+  const int grid = (int)std::min<int64_t>(R, (int64_t)dev.sms * std::max(1, 2048 / threads));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (V == 1) launch_join<1>(a, fmt, grid, threads, s);
+  else if (V == 2) launch_join<2>(a, fmt, grid, threads, s);
+  else launch_join<4>(a, fmt, grid, threads, s);
+  return cuda_status(cudaGetLastError());
+}
+
+int pgg_block_join_bwd_workspace_size(int64_t R, int64_t C, size_t* bytes) {
+  const int st = check(R, C, 8, nullptr, 0, nullptr, 0.0, 1.0f, 1.0f);
+  if (st) return st;
+  if (!bytes) return PGG_ERR_INVALID_ARG;
+  *bytes = (size_t)bwd_blocks(R, (int)(C / 8)) * 3 * (size_t)C * sizeof(float);
+  return PGG_OK;
+}
+
+int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void* h, const float* rstd_post,
+                       const float* rstd, const void* gamma_post, const void* gamma, const void* gate, int gate_kind,
+                       const int64_t* rng, int64_t R, int64_t C, double p, float residual_scale, float branch_scale,
+                       void* dx, void* dresidual, float* dgamma_post, float* dgamma, float* dgate, void* ws,
+                       size_t ws_bytes, void* stream) {
+  int st = check(R, C, 8, gate, gate_kind, rng, p, residual_scale, branch_scale);
+  if (st) return st;
+  // R == 0 has no gamma to tell by: the sums that are asked for are zero
+  if (R > 0 && ((gamma_post != nullptr) != (dgamma_post != nullptr) || (gamma != nullptr) != (dgamma != nullptr) ||
+                (gate_kind != PGG_GATE_NONE) != (dgate != nullptr)))
+    return PGG_ERR_INVALID_ARG;
+  const bool col = gate_kind == PGG_GATE_CHANNEL;
+  if (!aligned_to(dgamma_post, 4) || !aligned_to(dgamma, 4) || !aligned_to(dgate, 4)) return PGG_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (R == 0) {
+    for (float* q : {dgamma_post, dgamma, col ? dgate : nullptr})
+      if (q && (st = cuda_status(cudaMemsetAsync(q, 0, (size_t)C * sizeof(float), s)))) return st;
+    return PGG_OK;
+  }
+  if (!x || !dx || !ws || (gamma_post && !rstd_post) || (gamma && (!dy || !h || !rstd))) return PGG_ERR_INVALID_ARG;
+  if (!gamma && dy) return PGG_ERR_INVALID_ARG;
+  size_t need = 0;
+  if ((st = pgg_block_join_bwd_workspace_size(R, C, &need))) return st;
+  if (ws_bytes < need) return PGG_ERR_INVALID_ARG;
+  for (const void* q : {dy, dh, x, h, gamma_post, gamma, (const void*)dx, (const void*)dresidual, (const void*)ws})
+    if (!aligned_to(q, 16)) return PGG_ERR_ALIGNMENT;
+  if (!aligned_to(rstd_post, 4) || !aligned_to(rstd, 4)) return PGG_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != PGG_OK) return st;
+  const int nvec = (int)(C / 8), V = join_v(nvec), threads = threads_of(nvec, V);
+  JoinBwdArgs a{static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(x),
+                static_cast<const uint4*>(h), rstd_post, rstd, static_cast<const uint4*>(gamma_post),
+                static_cast<const uint4*>(gamma),
+                gate_kind == PGG_GATE_TOKEN ? static_cast<const float*>(gate) : nullptr,
+                col ? static_cast<const uint4*>(gate) : nullptr, make_drop(rng, p), R, nvec, 1.0f / (float)C,
+                residual_scale, branch_scale, static_cast<uint4*>(dx), static_cast<uint4*>(dresidual),
+                col ? nullptr : dgate, static_cast<float*>(ws)};
+  auto kern = V == 1 ? join_bwd_kernel<1, 2> : V == 2 ? join_bwd_kernel<2, 2> : join_bwd_kernel<4, 1>;
+  const int depth = V == 4 ? 1 : 2;
+  const size_t row = (size_t)4 * V * threads * sizeof(uint4);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(depth * 4 * V * 512 * sizeof(uint4)));
+  static std::atomic<int> resident[5][17];
+  std::atomic<int>& known = resident[V][threads / 32];
+  int per_sm = known.load(std::memory_order_relaxed);
+  if (e == cudaSuccess && per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, depth * row);
+    per_sm = std::max(1, per_sm);
+    if (e == cudaSuccess) known.store(per_sm, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) return cuda_status(e);
+  const int grid = std::min(bwd_blocks(R, nvec), dev.sms * per_sm);
+  kern<<<grid, threads, depth * row, s>>>(a);
+  if ((st = cuda_status(cudaGetLastError()))) return st;
+  JoinReduce r{a.part, grid, (int)C, {dgamma_post, dgamma, col ? dgate : nullptr}, {0, 0, 0}};
+  int sums = 0;
+  for (int i = 0; i < 3; ++i)
+    if (r.out[i]) r.which[sums++] = i;
+  if (!sums) return PGG_OK;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)nvec, (unsigned)sums);
+  cfg.blockDim = dim3(kReduceThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, join_reduce_kernel, r);
+  return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+}  // extern "C"
