@@ -75,7 +75,18 @@ __device__ __forceinline__ uint4 philox(uint64_t block, const Key& key) {
   }
   return make_uint4(x0, x1, x2, x3);
 }
-// Bit e: element e of the 8-element piece number `piece` of the tensor is kept.
+// Element e of the 8-element piece number `piece` of the tensor becomes 0 where it is dropped.
+__device__ __forceinline__ void drop8(float (&t)[8], int64_t piece, const Drop& d, const Key& key) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = philox((uint64_t)piece * 2 + i, key);
+    t[4 * i] = w.x >= d.below ? t[4 * i] : 0.0f;
+    t[4 * i + 1] = w.y >= d.below ? t[4 * i + 1] : 0.0f;
+    t[4 * i + 2] = w.z >= d.below ? t[4 * i + 2] : 0.0f;
+    t[4 * i + 3] = w.w >= d.below ? t[4 * i + 3] : 0.0f;
+  }
+}
+// Bit e: element e of that piece is kept.
 __device__ __forceinline__ uint32_t keep8(int64_t piece, const Drop& d, const Key& key) {
   uint32_t m = 0;
 #pragma unroll
@@ -87,7 +98,15 @@ __device__ __forceinline__ uint32_t keep8(int64_t piece, const Drop& d, const Ke
   return m;
 }
 
-enum { kGateNone = 0, kGateRow = 1, kGateColumn = 2 };
+// Piece v of a row of bf16 factors in fp32: ones where there are none, zeros past the row's end.
+__device__ __forceinline__ void load_factors(const uint4* p, int v, int nvec, float (&f)[8]) {
+  if (p && v < nvec) {
+    unpack8(__ldg(p + v), f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = v < nvec ? 1.0f : 0.0f;
+  }
+}
 
 struct JoinArgs {
   const uint4* x;
@@ -109,31 +128,51 @@ struct JoinArgs {
 };
 
 // A block walks rows with a grid stride; thread t owns the row's 8-element pieces t, t + blockDim, ...
-// (V of them), which stay in registers from their load to the outputs, so every byte moves once.
+// (V of them) in all of them, so gamma1 gate_col and gamma2 stay in registers, and each row from its
+// load, one row ahead, to its outputs: every byte moves once.
 template <int V, int FMT>
 __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
   __shared__ float s_sum[2][1][32];
   const int nwarps = blockDim.x >> 5;
   Key key{};
   if (a.drop.rng) key = load_key(a.drop);
-  int par = 0;
-  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
-    const int64_t base = row * a.nvec;
-    uint4 xv[V], rv[V];  // every load of the row before the first store (h may be x or residual)
+  float g1[V][8], g2[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    load_factors(a.gamma1, v, a.nvec, g1[j]);
+    load_factors(a.gamma2, v, a.nvec, g2[j]);
+    if (a.gate_col) {
+      float c[8];
+      load_factors(a.gate_col, v, a.nvec, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g1[j][e] *= c[e];
+    }
+  }
+  uint4 xn[V], rn[V];  // the next row's pieces (zeros past the row's end)
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
-      xv[j] = rv[j] = make_uint4(0, 0, 0, 0);
-      if (v < a.nvec) {
-        xv[j] = a.x[base + v];
-        if (a.residual) rv[j] = a.residual[base + v];
+      xn[j] = rn[j] = make_uint4(0, 0, 0, 0);
+      if (v < a.nvec && row < a.R) {
+        xn[j] = a.x[row * a.nvec + v];
+        if (a.residual) rn[j] = a.residual[row * a.nvec + v];
       }
     }
-    const float gate = a.rb * (a.gate_row ? __ldg(a.gate_row + row) : 1.0f);
-    uint32_t keep[V];
+  };
+  fetch(blockIdx.x);
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
+    const int64_t base = row * a.nvec;
+    uint4 xv[V], rv[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
-    float rstd1 = 1.0f;
+    for (int j = 0; j < V; ++j) {
+      xv[j] = xn[j];
+      rv[j] = rn[j];
+    }
+    float k = a.rb * a.drop.inv * (a.gate_row ? __ldg(a.gate_row + row) : 1.0f);
+    fetch(row + gridDim.x);  // (h may be x or residual: other rows than the one that is written)
     if (a.gamma1) {
       float q[1] = {0.0f};
 #pragma unroll
@@ -145,35 +184,25 @@ __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
       }
       block_sums(q, s_sum[par], nwarps);
       par ^= 1;
-      rstd1 = rsqrtf(q[0] * a.inv_c + a.eps);
+      const float rstd1 = rsqrtf(q[0] * a.inv_c + a.eps);
       if (a.rstd1 && threadIdx.x == 0) a.rstd1[row] = rstd1;
+      k *= rstd1;
     }
     float s[V][8];
     float q[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
-      if (v < a.nvec) {
-        float t[8], r[8], g[8];
-        unpack8(xv[j], t);
-        unpack8(rv[j], r);
-        if (a.gamma1) {
-          unpack8(__ldg(a.gamma1 + v), g);
+      float t[8], r[8];
+      unpack8(xv[j], t);
+      unpack8(rv[j], r);
+      if (a.drop.rng) drop8(t, base + v, a.drop, key);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = t[e] * rstd1 * g[e];
-        }
-        if (a.gate_col) unpack8(__ldg(a.gate_col + v), g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float b = (keep[j] >> e) & 1u ? t[e] * a.drop.inv : 0.0f;
-          s[j][e] = fmaf(a.ra, r[e], (a.gate_col ? gate * g[e] : gate) * b);
-          q[0] += s[j][e] * s[j][e];
-        }
-        if (a.h) a.h[base + v] = pack8(s[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[j][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        s[j][e] = fmaf(a.ra, r[e], t[e] * g1[j][e] * k);
+        q[0] = fmaf(s[j][e], s[j][e], q[0]);
       }
+      if (a.h && v < a.nvec) a.h[base + v] = pack8(s[j]);
     }
     if (!a.gamma2) continue;
     block_sums(q, s_sum[par], nwarps);
@@ -186,16 +215,9 @@ __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
       // the four lanes of an MX block are in range together: nvec is a multiple of 4 with FMT
       const bool in = v < a.nvec;
       float y[8];
-      if (in) {
-        float g[8];
-        unpack8(__ldg(a.gamma2 + v), g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = s[j][e] * rstd2 * g[e];
-        if (a.y) a.y[base + v] = pack8(y);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-      }
+      for (int e = 0; e < 8; ++e) y[e] = s[j][e] * rstd2 * g2[j][e];
+      if (a.y && in) a.y[base + v] = pack8(y);
       if (FMT) {
         uint32_t am = 0;
 #pragma unroll
@@ -250,21 +272,45 @@ struct JoinBwdArgs {
 // The same ownership: a thread's columns stay its own over all rows of the block, so the sums over
 // rows are registers, written once per block.  A thread copies its pieces of coming rows into its own
 // places of shared memory, DEPTH - 1 rows ahead (no thread reads another's).
-template <int V, int DEPTH>
-__global__ void __launch_bounds__(512) join_bwd_kernel(const JoinBwdArgs a) {
+//
+// With dk = d where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none), all the
+// gradients of the branch come from two sums of dk x: over the rows S = sum gate_row rstd1 dk x, over the
+// row q = sum gg dk x.  With f = rb / (1 - p):
+//   dgamma1 = f gate_col S    dgate_col = f gamma1 S    dgate_row = f rstd1 q
+//   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C)
+template <int V, int DEPTH, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwdArgs a) {
   extern __shared__ uint4 s_row[];  // [DEPTH][4][V][blockDim]
-  __shared__ float s_sum[2][2][32];
+  __shared__ float s_sum[2][1][32];
   const int nwarps = blockDim.x >> 5;
   Key key{};
   if (a.drop.rng) key = load_key(a.drop);
-  float dg1[V][8], dg2[V][8], dgc[V][8];
+  float sum_b[V][8], sum_2[V][8], gg[V][8], g2[V][8];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
+  for (int j = 0; j < V; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    load_factors(a.gamma1, v, a.nvec, gg[j]);
+    load_factors(a.gamma2, v, a.nvec, g2[j]);
+    if (a.gate_col) {
+      float c[8];
+      load_factors(a.gate_col, v, a.nvec, c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg1[j][e] = dg2[j][e] = dgc[j][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) gg[j][e] *= c[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum_b[j][e] = sum_2[j][e] = 0.0f;
+  }
   auto place = [&](int slot, int which, int j) {
     return s_row + ((slot * 4 + which) * V + j) * blockDim.x + threadIdx.x;
   };
+  // places that no row is copied to read as zeros: those past the row's end, and of operands that are not given
+#pragma unroll
+  for (int i = 0; i < DEPTH * 4; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const bool given = i % 4 == 3 || (i % 4 == 2 ? a.dh != nullptr : a.gamma2 != nullptr);
+      if (!given || threadIdx.x + j * blockDim.x >= a.nvec) *place(0, i, j) = make_uint4(0, 0, 0, 0);
+    }
   auto fetch = [&](int64_t row, int slot) {
     if (row < a.R) {
       const int64_t base = row * a.nvec;
@@ -293,7 +339,7 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinBwdArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
     const float rstd1 = a.gamma1 ? __ldg(a.rstd1 + row) : 1.0f, rstd2 = a.gamma2 ? __ldg(a.rstd2 + row) : 0.0f;
-    const float gate = a.rb * (a.gate_row ? __ldg(a.gate_row + row) : 1.0f);
+    const float gate = a.gate_row ? __ldg(a.gate_row + row) : 1.0f;
     cp_async_wait<DEPTH - 1>();
     // d = dh + rstd2 u + c h, with the sum over the row in c
     float c = 0.0f;
@@ -301,105 +347,103 @@ __global__ void __launch_bounds__(512) join_bwd_kernel(const JoinBwdArgs a) {
       float q[1] = {0.0f};
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
-        if (v < a.nvec) {
-          float hv[8], dy[8], g[8];
-          unpack8(*place(slot, 0, j), hv);
-          unpack8(*place(slot, 1, j), dy);
-          unpack8(__ldg(a.gamma2 + v), g);
+        float hv[8], dy[8];
+        unpack8(*place(slot, 0, j), hv);
+        unpack8(*place(slot, 1, j), dy);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float t = dy[e] * hv[e];
-            dg2[j][e] = fmaf(t, rstd2, dg2[j][e]);
-            q[0] = fmaf(t, g[e], q[0]);
-          }
+        for (int e = 0; e < 8; ++e) {
+          const float t = dy[e] * hv[e];
+          sum_2[j][e] = fmaf(t, rstd2, sum_2[j][e]);
+          q[0] = fmaf(t, g2[j][e], q[0]);
         }
       }
       block_sums(q, s_sum[par], nwarps);
       par ^= 1;
       c = -rstd2 * rstd2 * (q[0] * rstd2 * a.inv_c);
     }
-    float w[V][8];  // the gradient of x, before the norm's mean is taken out of it
-    float q[2] = {0.0f, 0.0f};  // sum w x, sum d b
+    const float scale = gate * rstd1;
+    float dk[V][8];
+    float q[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
-      if (v < a.nvec) {
-        float d[8], x[8], g1[8], gc[8];
-        if (a.dh) {
-          unpack8(*place(slot, 2, j), d);
-        } else {
+      float d[8], x[8];
+      unpack8(*place(slot, 2, j), d);
+      if (a.gamma2) {
+        float hv[8], dy[8];
+        unpack8(*place(slot, 0, j), hv);
+        unpack8(*place(slot, 1, j), dy);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = 0.0f;
-        }
-        if (a.gamma2) {
-          float hv[8], dy[8], g[8];
-          unpack8(*place(slot, 0, j), hv);
-          unpack8(*place(slot, 1, j), dy);
-          unpack8(__ldg(a.gamma2 + v), g);
+        for (int e = 0; e < 8; ++e) d[e] = fmaf(c, hv[e], fmaf(dy[e] * g2[j][e], rstd2, d[e]));
+      }
+      if (a.dres && v < a.nvec) {
+        float o[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = fmaf(c, hv[e], fmaf(dy[e] * g[e], rstd2, d[e]));
-        }
-        if (a.dres) {
-          float o[8];
+        for (int e = 0; e < 8; ++e) o[e] = a.ra * d[e];
+        a.dres[base + v] = pack8(o);
+      }
+      unpack8(*place(slot, 3, j), x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = a.ra * d[e];
-          a.dres[base + v] = pack8(o);
-        }
-        unpack8(*place(slot, 3, j), x);
-        if (a.gamma1) unpack8(__ldg(a.gamma1 + v), g1);
-        if (a.gate_col) unpack8(__ldg(a.gate_col + v), gc);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // d keep / (1 - p): the part of it that reaches t, and with t the gate's gradient
-          const float dk = (keep[j] >> e) & 1u ? d[e] * a.drop.inv : 0.0f;
-          const float xh = x[e] * rstd1;
-          const float t = a.gamma1 ? xh * g1[e] : x[e];
-          const float db = (keep[j] >> e) & 1u ? dk * t : 0.0f;
-          if (a.gate_col) dgc[j][e] = fmaf(a.rb, db, dgc[j][e]);
-          q[1] += db;
-          const float dt = (a.gate_col ? gate * gc[e] : gate) * dk;
-          if (a.gamma1) dg1[j][e] = fmaf(dt, xh, dg1[j][e]);
-          w[j][e] = a.gamma1 ? dt * g1[e] : dt;
-          q[0] = fmaf(w[j][e], x[e], q[0]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const bool kept = (keep[j] >> e) & 1u;
+        const float t = kept ? d[e] * x[e] : 0.0f;
+        dk[j][e] = kept ? gg[j][e] * d[e] : 0.0f;
+        sum_b[j][e] = fmaf(t, scale, sum_b[j][e]);
+        q[0] = fmaf(t, gg[j][e], q[0]);
       }
     }
-    float mean = 0.0f;
+    const float f = a.rb * a.drop.inv;
+    float m = 0.0f;
     if (a.gamma1 || a.dgate_row) {
       block_sums(q, s_sum[par], nwarps);
       par ^= 1;
-      if (a.dgate_row && threadIdx.x == 0) a.dgate_row[row] = a.rb * q[1];
-      mean = q[0] * rstd1 * a.inv_c;
+      if (a.dgate_row && threadIdx.x == 0) a.dgate_row[row] = f * rstd1 * q[0];
+      m = a.gamma1 ? -rstd1 * rstd1 * (q[0] * a.inv_c) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v < a.nvec) {
+        float o[8];
         if (a.gamma1) {
           float x[8];
           unpack8(*place(slot, 3, j), x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[j][e] = rstd1 * fmaf(-(x[e] * rstd1), mean, w[j][e]);
+          for (int e = 0; e < 8; ++e) o[e] = f * scale * fmaf(x[e], m, dk[j][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = f * scale * dk[j][e];
         }
-        a.dx[base + v] = pack8(w[j]);
+        a.dx[base + v] = pack8(o);
       }
     }
     if (++slot == DEPTH) slot = 0;
   }
+  const float f = a.rb * a.drop.inv;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
     if (v < a.nvec) {
       const int64_t plane = (int64_t)gridDim.x * a.nvec * 2;
       float4* p = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.nvec + v) * 2;
-      auto put = [&](float4* dst, const float (&f)[8]) {
-        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+      auto put = [&](float4* dst, const float (&o)[8]) {
+        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
       };
-      if (a.gamma1) put(p, dg1[j]);
-      if (a.gamma2) put(p + plane, dg2[j]);
-      if (a.gate_col) put(p + 2 * plane, dgc[j]);
+      float fac[8];
+      if (a.gamma1) {
+        load_factors(a.gate_col, v, a.nvec, fac);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) fac[e] *= f * sum_b[j][e];
+        put(p, fac);
+      }
+      if (a.gamma2) put(p + plane, sum_2[j]);
+      if (a.gate_col) {
+        load_factors(a.gamma1, v, a.nvec, fac);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) fac[e] *= f * sum_b[j][e];
+        put(p + 2 * plane, fac);
+      }
     }
   }
 }
@@ -438,12 +482,13 @@ __global__ void __launch_bounds__(kReduceThreads) join_reduce_kernel(const JoinR
 
 int threads_of(int nvec, int V) { return std::max(32, ((nvec + V - 1) / V + 31) / 32 * 32); }
 int join_v(int nvec) { return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4; }
+int bwd_v(int nvec) { return nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4; }
 
 // Blocks of the backward pass: at most as many as are resident at once, which this bounds for the
 // workspace.
 int bwd_blocks(int64_t R, int nvec) {
-  const int threads = threads_of(nvec, join_v(nvec));
-  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, 1024 / threads)));
+  const int threads = threads_of(nvec, bwd_v(nvec));
+  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, 768 / threads)));
 }
 
 template <int V>
@@ -548,7 +593,7 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
   if (!aligned_to(rstd_post, 4) || !aligned_to(rstd, 4)) return PGG_ERR_ALIGNMENT;
   DeviceInfo dev;
   if ((st = current_device(&dev)) != PGG_OK) return st;
-  const int nvec = (int)(C / 8), V = join_v(nvec), threads = threads_of(nvec, V);
+  const int nvec = (int)(C / 8), V = bwd_v(nvec), threads = threads_of(nvec, V);
   JoinBwdArgs a{static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(x),
                 static_cast<const uint4*>(h), rstd_post, rstd, static_cast<const uint4*>(gamma_post),
                 static_cast<const uint4*>(gamma),
@@ -556,8 +601,8 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
                 col ? static_cast<const uint4*>(gate) : nullptr, make_drop(rng, p), R, nvec, 1.0f / (float)C,
                 residual_scale, branch_scale, static_cast<uint4*>(dx), static_cast<uint4*>(dresidual),
                 col ? nullptr : dgate, static_cast<float*>(ws)};
-  auto kern = V == 1 ? join_bwd_kernel<1, 2> : V == 2 ? join_bwd_kernel<2, 2> : join_bwd_kernel<4, 1>;
-  const int depth = V == 4 ? 1 : 2;
+  auto kern = V == 1 ? join_bwd_kernel<1, 3, 256, 3> : V == 2 ? join_bwd_kernel<2, 3, 512, 1> : join_bwd_kernel<4, 1, 512, 1>;
+  const int depth = V == 4 ? 1 : 3;
   const size_t row = (size_t)4 * V * threads * sizeof(uint4);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(depth * 4 * V * 512 * sizeof(uint4)));

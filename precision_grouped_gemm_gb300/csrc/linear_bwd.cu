@@ -42,8 +42,8 @@ struct LinBwdArgs {
 };
 
 // HALVES 2: swiglu; 1: silu, gelu; 0: no activation, sums only.
-template <int ACT, int UNROLL>
-__global__ void __launch_bounds__(kThreads) linear_bwd_kernel(const LinBwdArgs a) {
+template <int ACT, int UNROLL, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS) linear_bwd_kernel(const LinBwdArgs a) {
   constexpr bool GATED = ACT == kActSwiglu;
   constexpr int H = GATED ? 2 : 1;
   extern __shared__ int32_t s_off[];  // [G + 1], and as many for the scan's tile counts
@@ -200,13 +200,14 @@ __global__ void __launch_bounds__(32 * kRedWarps) bias_grad_reduce_kernel(const 
 struct Cut {
   int nvec, per, slabs, runs, run_rows;
 };
-constexpr int kBlocks = 152 * 4;
-Cut cut(int64_t M, int64_t width) {
+constexpr int per_sm(int act) { return act == kActSwiglu ? 3 : act == kActNone ? 5 : 3; }
+Cut cut(int64_t M, int64_t N, int act) {
+  const int64_t width = act == kActSwiglu ? N / 2 : N;
   Cut c;
   c.nvec = (int)(width / 8);
   c.slabs = (c.nvec + kChunks - 1) / kChunks;
   c.per = (c.nvec + c.slabs - 1) / c.slabs;
-  const int64_t most = std::max(1, kBlocks / c.slabs);
+  const int64_t most = std::max(1, 152 * per_sm(act) / c.slabs);
   const int64_t rows = std::max<int64_t>(kMinRows, (M + most - 1) / most);
   c.run_rows = (int)((rows + kWarps - 1) / kWarps * kWarps);
   c.runs = (int)((M + c.run_rows - 1) / c.run_rows);
@@ -233,7 +234,7 @@ int pgg_grouped_linear_bwd_workspace_size(int64_t M, int64_t N, int G, int act, 
   const int st = check_dims(M, N, G, act);
   if (st) return st;
   if (!bytes) return PGG_ERR_INVALID_ARG;
-  *bytes = ws_need(cut(M, act == PGG_ACT_SWIGLU ? N / 2 : N), G, N);
+  *bytes = ws_need(cut(M, N, act), G, N);
   return PGG_OK;
 }
 
@@ -251,7 +252,7 @@ int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_l
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (M == 0) return cuda_status(cudaMemsetAsync(dbias, 0, (size_t)G * N * sizeof(float), s));
   if (!dY || !ws || (act != PGG_ACT_NONE) != (Z != nullptr) || (dZ && act == PGG_ACT_NONE)) return PGG_ERR_INVALID_ARG;
-  const Cut c = cut(M, act == PGG_ACT_SWIGLU ? N / 2 : N);
+  const Cut c = cut(M, N, act);
   if (ws_bytes < ws_need(c, G, N)) return PGG_ERR_INVALID_ARG;
   for (const void* p : {dY, Z, (const void*)dZ, (const void*)ws})
     if (!aligned_to(p, 16)) return PGG_ERR_ALIGNMENT;
@@ -265,10 +266,10 @@ int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_l
   const unsigned grid = (unsigned)(c.slabs * c.runs);
   const size_t smem = 2 * ((size_t)G + 1) * sizeof(int32_t);
   switch (act) {
-    case PGG_ACT_NONE: linear_bwd_kernel<kActNone, 4><<<grid, kThreads, smem, s>>>(a); break;
-    case PGG_ACT_SILU: linear_bwd_kernel<kActSilu, 4><<<grid, kThreads, smem, s>>>(a); break;
-    case PGG_ACT_GELU: linear_bwd_kernel<kActGelu, 4><<<grid, kThreads, smem, s>>>(a); break;
-    default: linear_bwd_kernel<kActSwiglu, 2><<<grid, kThreads, smem, s>>>(a);
+    case PGG_ACT_NONE: linear_bwd_kernel<kActNone, 4, per_sm(kActNone)><<<grid, kThreads, smem, s>>>(a); break;
+    case PGG_ACT_SILU: linear_bwd_kernel<kActSilu, 4, per_sm(kActSilu)><<<grid, kThreads, smem, s>>>(a); break;
+    case PGG_ACT_GELU: linear_bwd_kernel<kActGelu, 4, per_sm(kActGelu)><<<grid, kThreads, smem, s>>>(a); break;
+    default: linear_bwd_kernel<kActSwiglu, 2, per_sm(kActSwiglu)><<<grid, kThreads, smem, s>>>(a);
   }
   if ((st = cuda_status(cudaGetLastError()))) return st;
   cudaLaunchConfig_t cfg{};
