@@ -18,22 +18,27 @@ struct ActForm {
   float alpha, offset, limit;  // limit 0: no clamp
 };
 
-// 1 / (1 + e^-x); the quotient's few units of error stay far inside the outputs' roundings.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// 1 / (1 + e^-x).  FAST: the short exponential and quotient, whose error (some 2^-20 at |x| = 10) stays
+// far inside the rounding to bf16; fp32 results take the full ones.
+template <bool FAST = true>
+__device__ __forceinline__ float sigmoid_f(float x) {
+  return FAST ? __fdividef(1.0f, 1.0f + __expf(-x)) : 1.0f / (1.0f + expf(-x));
+}
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
 
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ float act_f(float z, const ActForm& f) {
-  if (ACT == kActSilu) return z * sigmoid_f(f.alpha * z);
+  if (ACT == kActSilu) return z * sigmoid_f<FAST>(f.alpha * z);
   if (ACT == kActGelu) return z * normal_cdf(z);
   return z;
 }
+template <bool FAST>
 __device__ __forceinline__ float swiglu_f(float g, float u, const ActForm& f) {
   if (f.limit > 0.0f) {
     g = g > f.limit ? f.limit : g;
     u = u > f.limit ? f.limit : u < -f.limit ? -f.limit : u;
   }
-  return g * sigmoid_f(f.alpha * g) * (u + f.offset);
+  return g * sigmoid_f<FAST>(f.alpha * g) * (u + f.offset);
 }
 
 // dy act'(z)
