@@ -28,7 +28,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // the epilogue adds them up in registers
   constexpr bool kWide = std::is_same<T, float>::value;
   constexpr int kBufs = kWide ? 4 : 2;              // accumulators in turn
-  constexpr int kBox = TN < 64 ? TN : 64;           // rows of X per load
   constexpr int kAcc = (GATED ? 2 : 1) * TN;        // columns of an accumulator
   constexpr uint32_t kTmemCols = kBufs * kAcc;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
@@ -95,18 +94,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     long long issued = 0;
     bool stalled = false;
     for (int t = blockIdx.x; t < tiles && !aborted && !stalled; t += gridDim.x) {
-      const LinTile T_ = lin_tile<kBN>(t, a, TN, nct, s_off, s_tile, cur);
-      const int boxes = (T_.rows + kBox - 1) / kBox;
+      const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
       for (int kb = 0; kb < nkb; ++kb) {
         if (issued == a.stall_at) { stalled = true; break; }
         if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
         if (lane == 0) {
           const uint32_t fb = smem_u32(&full[stage]);
           const uint32_t sa = smem_a + stage * L::kABytes, sb = smem_b + stage * L::kBBytes;
-          mbar_arrive_expect_tx(fb, L::kABytes + boxes * kBox * 128);
+          mbar_arrive_expect_tx(fb, L::kStageBytes);
           tma_load_3d(sa, &tmW, fb, kb * kBK, T_.col0, T_.g);
           if (GATED) tma_load_3d(sa + kBN * 128, &tmW, fb, kb * kBK, a.width + T_.col0, T_.g);
-          for (int b = 0; b < boxes; ++b) tma_load_2d(sb + b * kBox * 128, &tmX, fb, kb * kBK, T_.row0 + b * kBox);
+          tma_load_2d(sb, &tmX, fb, kb * kBK, T_.row0);
         }
         __syncwarp();
         ++issued;
@@ -130,7 +128,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint64_t desc_a = smem_desc(smem_a, 16, 1024, kSwizzle128B);
     const uint64_t desc_b = smem_desc(smem_b, 16, 1024, kSwizzle128B);
     for (int t = blockIdx.x; t < tiles && !aborted; t += gridDim.x) {
-      const LinTile T_ = lin_tile<kBN>(t, a, TN, nct, s_off, s_tile, cur);
+      const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
       const uint32_t idesc = idesc_bf16(kBN, (T_.rows + 15) & ~15, false, false);
       for (int k0 = 0; k0 < nkb && !aborted; k0 += kWide ? kChunk : nkb) {
         const int k1 = kWide ? min(nkb, k0 + kChunk) : nkb;
@@ -171,7 +169,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = blockIdx.x; t < tiles && !aborted; t += gridDim.x) {
-      const LinTile T_ = lin_tile<kBN>(t, a, TN, nct, s_off, s_tile, cur);
+      const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
       const int col = T_.col0 + q * 32, n = col + lane;
       float bg = 0.0f, bu = 0.0f;
       if (a.bias && n < a.width) {
@@ -248,7 +246,7 @@ int launch(const LinCall& c, const DeviceInfo& dev) {
   using L = LinSmem<GATED, TN, STAGES>;
   auto kern = linear_kernel<GATED, TN, STAGES, T>;
   CUtensorMap tw, tx;
-  const int st = lin_maps(c, TN < 64 ? TN : 64, &tw, &tx);
+  const int st = lin_maps(c, TN, false, &tw, &tx);
   if (st) return st;
   // the most that the kernel is ever launched with: another thread may call with more groups meanwhile
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes(kMaxGroups));
@@ -279,7 +277,7 @@ int dispatch(const LinCall& c, const DeviceInfo& dev) {
   }
   if (rows >= 512) return launch_linear_pair(c, dev);
   if (gated) return rows <= 16 ? launch<true, 32, 5, __nv_bfloat16>(c, dev) : launch<true, 128, 4, __nv_bfloat16>(c, dev);
-  return rows <= 16 ? launch<false, 32, 9, __nv_bfloat16>(c, dev) : launch<false, 256, 4, __nv_bfloat16>(c, dev);
+  return rows <= 16 ? launch<false, 32, 9, __nv_bfloat16>(c, dev) : launch<false, 128, 6, __nv_bfloat16>(c, dev);
 }
 
 int linear_impl(const void* X, const void* W, const int32_t* group_lens, const void* bias, const void* residual,

@@ -24,7 +24,7 @@ namespace pgg {
 constexpr int kBN = 128;     // output columns of a tile (of each half with swiglu): TMEM lanes
 constexpr int kBK = 64;      // one 128-byte swizzle atom of the reduction
 constexpr int kLinThreads = 192;
-constexpr int kBand = 16;    // row tiles that take their turns at one column tile
+constexpr int kBand = 8;     // row tiles that take their turns at one column tile
 
 struct LinArgs {
   const int32_t* group_lens;  // or nullptr: one group of M rows
@@ -47,9 +47,11 @@ struct LinTile {
   int g, row0, rows, col0;
 };
 
-// Tile t: TN rows by CW columns, nct column tiles.  Within a group, up to kBand row tiles take turns at
-// one column tile, so that what runs at one time shares a band of X and a few column tiles of W in L2.
-template <int CW>
+// Tile t: up to TN rows by CW columns, nct column tiles.  Within a group, up to kBand row tiles take turns
+// at one column tile, so that what runs at one time shares a band of X and a few column tiles of W in L2.
+// EVEN: a short group's rows are shared out evenly over its tiles (in steps of 16), so that its last tile
+// is not a small one that costs the weights' loads of a full one.
+template <int CW, bool EVEN>
 __device__ __forceinline__ LinTile lin_tile(int t, const LinArgs& a, int TN, int nct, const int32_t* s_off,
                                             const int32_t* s_tile, GroupCursor& cur) {
   cur.at(s_tile, s_off, nullptr, a.G, t);
@@ -57,7 +59,9 @@ __device__ __forceinline__ LinTile lin_tile(int t, const LinArgs& a, int TN, int
   const int band = local / (kBand * nct), in = local - band * kBand * nct;
   const int bm = min(kBand, nmt - band * kBand);
   const int ct = in / bm, mt = band * kBand + in - ct * bm;
-  return {cur.g, cur.off + mt * TN, min(TN, cur.len - mt * TN), ct * CW};
+  // (with at most 8 tiles the steps of 16 leave none without rows)
+  const int per = EVEN && nmt <= 8 ? ((cur.len + nmt - 1) / nmt + 15) & ~15 : TN;
+  return {cur.g, cur.off + mt * per, min(per, cur.len - mt * per), ct * CW};
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -95,15 +99,17 @@ __device__ __forceinline__ void put_chunk(uint8_t* stg, const float (&v)[32], fl
   }
   __syncwarp();
 }
-// v[j] += the residual's row j at this lane's column.
-__device__ __forceinline__ void add_chunk(uint8_t* stg, float (&v)[32], const __nv_bfloat16* src, size_t ld, int nrows,
-                                          int ncols, int lane) {
-  uint4 w[4];
+// The chunk's residual in the order of its 16-byte pieces, zeros outside; and v[j] += its row j at this
+// lane's column.
+__device__ __forceinline__ void fetch_chunk(uint4 (&w)[4], const __nv_bfloat16* src, size_t ld, int nrows, int ncols,
+                                            int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3);
-    w[i] = r < nrows && c < ncols ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * ld + c)) : make_uint4(0, 0, 0, 0);
+    w[i] = r < nrows && c < ncols ? *reinterpret_cast<const uint4*>(src + (size_t)r * ld + c) : make_uint4(0, 0, 0, 0);
   }
+}
+__device__ __forceinline__ void add_fetched(uint8_t* stg, float (&v)[32], const uint4 (&w)[4], int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(stg)[32 * i + lane] = w[i];
   __syncwarp();
@@ -112,11 +118,17 @@ __device__ __forceinline__ void add_chunk(uint8_t* stg, float (&v)[32], const __
   for (int j = 0; j < 32; ++j) v[j] += __bfloat162float(s[j * 32 + lane]);
   __syncwarp();
 }
+__device__ __forceinline__ void add_chunk(uint8_t* stg, float (&v)[32], const __nv_bfloat16* src, size_t ld, int nrows,
+                                          int ncols, int lane) {
+  uint4 w[4];
+  fetch_chunk(w, src, ld, nrows, ncols, lane);
+  add_fetched(stg, v, w, lane);
+}
 __device__ __forceinline__ void add_chunk(uint8_t* stg, float (&v)[32], const float* src, size_t ld, int nrows,
                                           int ncols, int lane) {
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (j < nrows && lane < ncols) v[j] += __ldg(src + (size_t)j * ld + lane);
+    if (j < nrows && lane < ncols) v[j] += src[(size_t)j * ld + lane];
 }
 
 // 32 accumulator columns of this thread's lane, plus the bias; or added to what is there.
@@ -165,6 +177,16 @@ __device__ __forceinline__ void finish_chunk(const LinArgs& a, float (&z)[32], f
   put_chunk(stg, z, static_cast<T*>(a.y) + row * a.width + col, a.width, nrows, ncols, lane);
 }
 
+// The same for bf16 without halves, the residual's chunk fetched before.
+__device__ __forceinline__ void finish_plain(const LinArgs& a, float (&z)[32], const uint4 (&res)[4], size_t row, int col,
+                                             int nrows, int ncols, uint8_t* stg, int lane) {
+  if (a.z) put_chunk(stg, z, a.z + row * a.N + col, a.N, nrows, ncols, lane);
+  if (a.act == kActSilu) apply_act<kActSilu, true>(z, a.form);
+  else if (a.act == kActGelu) apply_act<kActGelu, true>(z, a.form);
+  if (a.residual) add_fetched(stg, z, res, lane);
+  put_chunk(stg, z, static_cast<__nv_bfloat16*>(a.y) + row * a.width + col, a.width, nrows, ncols, lane);
+}
+
 // The group tables: with no lengths given, one group of M rows.
 __device__ __forceinline__ bool lin_scan(const LinArgs& a, int TN, int nct, int32_t* s_off, int32_t* s_tile, int lane) {
   TileCount tc;
@@ -186,17 +208,20 @@ struct LinCall {
   cudaStream_t stream;
 };
 
-// Tensor maps: W as {K, N, G} in boxes of 128 rows, X as {K, M} in boxes of `box` rows, one 128-byte
-// swizzle atom of K wide.
-inline int lin_maps(const LinCall& c, uint32_t box, CUtensorMap* tw, CUtensorMap* tx) {
+// Tensor maps, one 128-byte swizzle atom of K wide: X as {K, M} in boxes of `xbox` rows; W as {K, N, G} in
+// boxes of 128 rows or, with `halves`, as {K, N / 2, 2, G} in boxes of 64 rows of the gate and of the up half.
+inline int lin_maps(const LinCall& c, uint32_t xbox, bool halves, CUtensorMap* tw, CUtensorMap* tx) {
   const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint64_t K = c.a.K, N = c.a.N;
-  const uint64_t dw[3] = {K, N, (uint64_t)c.a.G}, sw[2] = {K * 2, N * K * 2};
-  const uint32_t bw[3] = {kBK, kBN, 1};
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t K = c.a.K, N = c.a.N, G = c.a.G;
+  const uint64_t d3[3] = {K, N, G}, s3[2] = {K * 2, N * K * 2};
+  const uint32_t b3[3] = {kBK, kBN, 1};
+  const uint64_t d4[4] = {K, N / 2, 2, G}, s4[3] = {K * 2, N * K, N * K * 2};
+  const uint32_t b4[4] = {kBK, kBN / 2, 2, 1};
   const uint64_t dx[2] = {K, (uint64_t)c.a.M}, sx[1] = {K * 2};
-  const uint32_t bx[2] = {kBK, box};
-  const int st = encode_tmap(tw, bf, 3, c.W, dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
-  return st ? st : encode_tmap(tx, bf, 2, c.X, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B);
+  const uint32_t bx[2] = {kBK, xbox};
+  const int st = halves ? encode_tmap(tw, bf, 4, c.W, d4, s4, b4, sw) : encode_tmap(tw, bf, 3, c.W, d3, s3, b3, sw);
+  return st ? st : encode_tmap(tx, bf, 2, c.X, dx, sx, bx, sw);
 }
 
 // Launchers of the kernels (linear.cu, linear_pair.cu, linear_split.cu).

@@ -3,6 +3,10 @@
 // columns of W and half of the tile's rows of X -- 32 KB a k-block instead of the 48 of a CTA on its
 // own, which is what the loads from L2 bound there -- and has the accumulators of its own columns.
 //
+// With swiglu a CTA's 128 columns of W are 64 of the gate and the same 64 of the up half, so a tile moves
+// no more bytes than without: the lanes of gate and up of one column are in different warps, which swap
+// half of their rows through shared memory and finish 16 rows of 32 columns each.
+//
 // Both CTAs' loads count their bytes on the leader's barrier, so no thread passes on that a stage has
 // landed; the leader's MMAs free the stage in both CTAs by a multicast commit.  Only a tile's release of
 // its accumulator takes arrivals from the other CTA.
@@ -12,30 +16,60 @@
 namespace pgg {
 namespace {
 
-template <bool GATED>
-struct PairCfg {
-  static constexpr int kTN = GATED ? 128 : 256;  // rows of X a tile; half of them in each CTA
-  static constexpr int kStages = GATED ? 5 : 6;
-  static constexpr int kABytes = (GATED ? 2 : 1) * kBN * kBK * 2;
-  static constexpr int kBBytes = kTN / 2 * kBK * 2;
-  static constexpr int kEpiOff = kStages * (kABytes + kBBytes);
-  static constexpr int kBarOff = kEpiOff + 4 * 4096;
-  static constexpr int kGroupOff = kBarOff + 256;
-  static constexpr int kAcc = (GATED ? 2 : 1) * kTN;
-  static __host__ __device__ constexpr size_t bytes(int G) { return 1024 + (size_t)kGroupOff + 8 * (size_t)(G + 1); }
-};
+constexpr int kPairTN = 256;     // rows of X a tile; half of them in each CTA
+constexpr int kPairStages = 6;
+constexpr int kEpiWarps = 8;     // two for each lane quarter of tensor memory
+constexpr int kPairThreads = 32 * (2 + kEpiWarps);
+constexpr int kPairABytes = kBN * kBK * 2, kPairBBytes = kPairTN / 2 * kBK * 2;
+constexpr int kStgBytes = 3072;  // of an epilogue warp: 2 KB that turn a chunk or go to the partner, 1 KB more
+constexpr int kPairEpiOff = kPairStages * (kPairABytes + kPairBBytes);
+constexpr int kPairBarOff = kPairEpiOff + kEpiWarps * kStgBytes;
+constexpr int kPairGroupOff = kPairBarOff + 256;
+size_t pair_smem(int G) { return 1024 + (size_t)kPairGroupOff + 8 * ((size_t)G + 1); }
+
+// Barrier of the two warps that share 32 columns (64 threads); the form that tells each whether `ok` held in
+// both makes them give up together, so that none is left at a later barrier.
+__device__ __forceinline__ void partner_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool partner_all(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// 16 rows of 32 columns, as put_chunk.
+__device__ __forceinline__ void put_rows16(uint8_t* stg, const float (&v)[16], __nv_bfloat16* dst, size_t ld, int nrows,
+                                           int ncols, int lane) {
+  __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(stg);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3);
+    const uint4 w = reinterpret_cast<const uint4*>(stg)[32 * i + lane];
+    if (r < nrows && c < ncols) *reinterpret_cast<uint4*>(dst + (size_t)r * ld + c) = w;
+  }
+  __syncwarp();
+}
 
 template <bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinArgs a) {
-  using C = PairCfg<GATED>;
-  constexpr int TN = C::kTN, STAGES = C::kStages, kCW = 2 * kBN;
-  static_assert(2 * C::kAcc == 512, "two accumulators fill tensor memory");
+  constexpr int TN = kPairTN, STAGES = kPairStages;
+  constexpr int kCols = GATED ? kBN / 2 : kBN;  // output columns of a CTA
+  constexpr int kCW = 2 * kCols;
   static_assert((2 * STAGES + 5) * 8 + 24 <= 256, "barrier area");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // (the leader's are used)
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBarOff);  // (the leader's are used)
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // (the leader's are used)
@@ -43,7 +77,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   volatile WaitCtl* s_ctl = reinterpret_cast<volatile WaitCtl*>(drain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<WaitCtl*>(s_ctl) + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 1);
-  int32_t* s_off = reinterpret_cast<int32_t*>(smem + C::kGroupOff);
+  int32_t* s_off = reinterpret_cast<int32_t*>(smem + kPairGroupOff);
   int32_t* s_tile = s_off + (a.G + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -57,7 +91,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), 8);  // the epilogue warps of both CTAs
+      mbar_init(smem_u32(&tempty[i]), 2 * kEpiWarps);  // the epilogue warps of both CTAs
     }
     mbar_init(smem_u32(drain), 1);
     s_ctl->abort = 0;
@@ -86,116 +120,158 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   const uint32_t tmem = *s_tmem;
   const int tiles = *s_bad ? 0 : s_tile[a.G];
   const int t0 = (int)cluster_id(), step = (int)cluster_count();
-  const uint32_t smem_a = smem_u32(smem), smem_b = smem_a + STAGES * C::kABytes;
+  const uint32_t smem_a = smem_u32(smem), smem_b = smem_a + STAGES * kPairABytes;
   bool aborted = false;
   GroupCursor cur;
 
+  // The first two roles are one thread each: their loops are short chains of waits and issues, which a
+  // vote or a warp barrier a step would lengthen.
   if (warp == 0) {
     // ------------------------------------------------------------ loads of this CTA's halves
-    const uint32_t full0 = map_rank(smem_u32(full), 0);
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    bool stalled = false;
-    for (int t = t0; t < tiles && !aborted && !stalled; t += step) {
-      const LinTile T_ = lin_tile<kCW>(t, a, TN, nct, s_off, s_tile, cur);
-      const int half = ((T_.rows + 15) & ~15) / 2;  // rows of X in each CTA
-      const int boxes = (half + 63) / 64;
-      const int col = T_.col0 + (int)rank * kBN, row = T_.row0 + (int)rank * half;
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (issued == a.stall_at) { stalled = true; break; }
-        if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
-        if (lane == 0) {
+    if (lane == 0) {
+      const uint32_t full0 = map_rank(smem_u32(full), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool stalled = false;
+      for (int t = t0; t < tiles && !aborted && !stalled; t += step) {
+        const LinTile T_ = lin_tile<kCW, true>(t, a, TN, nct, s_off, s_tile, cur);
+        const int half = ((T_.rows + 15) & ~15) / 2;  // rows of X in each CTA
+        const int col = T_.col0 + (int)rank * kCols, row = T_.row0 + (int)rank * half;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (issued == a.stall_at) { stalled = true; break; }
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           const uint32_t fb = full0 + stage * 8;
-          const uint32_t sa = smem_a + stage * C::kABytes, sb = smem_b + stage * C::kBBytes;
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (C::kABytes + boxes * 64 * 128));
-          tma_load_3d_pair(sa, &tmW, fb, kb * kBK, col, T_.g);
-          if (GATED) tma_load_3d_pair(sa + kBN * 128, &tmW, fb, kb * kBK, a.width + col, T_.g);
-          for (int b = 0; b < boxes; ++b) tma_load_2d_pair(sb + b * 64 * 128, &tmX, fb, kb * kBK, row + b * 64);
+          const uint32_t sa = smem_a + stage * kPairABytes, sb = smem_b + stage * kPairBBytes;
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kPairABytes + kPairBBytes));
+          // one load an operand: each has a cost of its own (X in two of 64 rows and gate and up apart
+          // took 5 and 15% longer)
+          if (GATED) tma_load_4d_pair(sa, &tmW, fb, kb * kBK, col, 0, T_.g);
+          else tma_load_3d_pair(sa, &tmW, fb, kb * kBK, col, T_.g);
+          tma_load_2d_pair(sb, &tmX, fb, kb * kBK, row);
+          ++issued;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-    }
-    // The last stages' commits arrive here before the CTA may go; after an abort the leader sees on its
-    // barriers that the loads have landed.
-    long long n = issued < STAGES ? issued : STAGES;
-    for (long long i = 0; i < n; ++i) {
-      if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
-      if (aborted || stalled) {
-        if (rank == 0 && lane == 0) mbar_wait_drain(smem_u32(&full[stage]), phase);
-        __syncwarp();
-      } else if (!warp_wait(smem_u32(&empty[stage]), phase, s_ctl)) {
-        aborted = true;
+      // The last stages' commits arrive here before the CTA may go; after an abort the leader sees on its
+      // barriers that the loads have landed.
+      const long long n = issued < STAGES ? issued : STAGES;
+      for (long long i = 0; i < n; ++i) {
+        if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
+        if (aborted || stalled) {
+          if (rank == 0) mbar_wait_drain(smem_u32(&full[stage]), phase);
+        } else if (!mbar_wait(smem_u32(&empty[stage]), phase, s_ctl)) {
+          aborted = true;
+        }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products, issued by the leader
-    if (rank == 0) {
+    if (rank == 0 && lane == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       const uint64_t desc_a = smem_desc(smem_a, 16, 1024, kSwizzle128B);
       const uint64_t desc_b = smem_desc(smem_b, 16, 1024, kSwizzle128B);
+      uint64_t da = desc_a, db = desc_b;
       for (int t = t0; t < tiles && !aborted; t += step) {
-        const LinTile T_ = lin_tile<kCW>(t, a, TN, nct, s_off, s_tile, cur);
+        const LinTile T_ = lin_tile<kCW, true>(t, a, TN, nct, s_off, s_tile, cur);
         const uint32_t idesc = idesc_bf16(2 * kBN, (T_.rows + 15) & ~15, false, false);
-        if (!warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
+        if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
         tc_fence_after();
-        const uint32_t d = tmem + acc * C::kAcc;
+        const uint32_t d = tmem + acc * TN;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+          if (!mbar_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t da = desc_a + (uint64_t)(stage * C::kABytes >> 4);
-            const uint64_t db = desc_b + (uint64_t)(stage * C::kBBytes >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kBK / 16; ++ks) {
-              const uint32_t more = kb > 0 || ks > 0 ? 1u : 0u;
-              mma_f16_pair(d, da + 2 * ks, db + 2 * ks, idesc, more);
-              if (GATED) mma_f16_pair(d + TN, da + (kBN * 128 >> 4) + 2 * ks, db + 2 * ks, idesc, more);
-            }
-            mma_commit_pair(smem_u32(&empty[stage]));
-          }
-          __syncwarp();
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          for (int ks = 0; ks < kBK / 16; ++ks) mma_f16_pair(d, da + 2 * ks, db + 2 * ks, idesc, kb > 0 || ks > 0 ? 1u : 0u);
+          mma_commit_pair(smem_u32(&empty[stage]));
+          da += kPairABytes >> 4;
+          db += kPairBBytes >> 4;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; da = desc_a; db = desc_b; }
         }
         if (aborted) break;
-        if (lane == 0) mma_commit_pair(smem_u32(&tfull[acc]));
-        __syncwarp();
+        mma_commit_pair(smem_u32(&tfull[acc]));
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      if (aborted && lane == 0) {
+      if (aborted) {
         mma_commit_pair(smem_u32(drain));
         mbar_wait_drain(smem_u32(drain), 0);
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue of this CTA's columns (warps 2..5)
-    const int q = warp & 3;
-    uint8_t* stg = smem + C::kEpiOff + (warp - 2) * 4096;
+    // ------------------------------------------------------------ epilogue of this CTA's columns (warps 2..9)
+    const int q = warp & 3, share = (warp - 2) >> 2;  // lane quarter; which chunks of 32 rows: share, share + 2, ...
+    uint8_t* stg = smem + kPairEpiOff + (warp - 2) * kStgBytes;
     const uint32_t tempty0 = map_rank(smem_u32(tempty), 0);
+    const bool up = GATED && q >= 2;  // this warp's lanes are columns of the up half
+    const int pair_id = 1 + (q & 1) + 2 * share;
+    const int lane_col = GATED ? (q & 1) * 32 : q * 32;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = t0; t < tiles && !aborted; t += step) {
-      const LinTile T_ = lin_tile<kCW>(t, a, TN, nct, s_off, s_tile, cur);
-      const int col = T_.col0 + (int)rank * kBN + q * 32, n = col + lane;
-      float bg = 0.0f, bu = 0.0f;
-      if (a.bias && n < a.width) {
-        const __nv_bfloat16* b = a.bias + (size_t)T_.g * a.N + n;
-        bg = __bfloat162float(b[0]);
-        if (GATED) bu = __bfloat162float(b[a.width]);
-      }
-      if (!warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl)) { aborted = true; break; }
+      const LinTile T_ = lin_tile<kCW, true>(t, a, TN, nct, s_off, s_tile, cur);
+      const int col = T_.col0 + (int)rank * kCols + lane_col, n = col + lane;
+      const int ncols = min(32, a.width - col);
+      float bias = 0.0f;
+      if (a.bias && n < a.width) bias = __bfloat162float(a.bias[(size_t)T_.g * a.N + (up ? a.width : 0) + n]);
+      uint4 res[4];
+      if (!GATED && a.residual && ncols > 0 && 32 * share < T_.rows)
+        fetch_chunk(res, static_cast<const __nv_bfloat16*>(a.residual) + ((size_t)T_.row0 + 32 * share) * a.width + col,
+                    a.width, T_.rows - 32 * share, ncols, lane);
+      bool ok = warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl);
+      if (GATED) ok = partner_all(pair_id, ok);
+      if (!ok) { aborted = true; break; }
       tc_fence_after();
-      const uint32_t tb = tmem + acc * C::kAcc + ((uint32_t)(q * 32) << 16);
-      if (col < a.width) {
+      const uint32_t tb = tmem + acc * TN + ((uint32_t)(q * 32) << 16);
+      if (ncols > 0) {
 #pragma unroll 1
-        for (int c = 0; c < T_.rows; c += 32) {
-          float z[32], u[32];
-          load_acc(tb + c, z, bg);
-          if (GATED) load_acc(tb + TN + c, u, bu);
-          finish_chunk<GATED, __nv_bfloat16>(a, z, u, (size_t)T_.row0 + c, col, min(32, T_.rows - c), stg, lane);
+        for (int c = 32 * share; c < T_.rows; c += 64) {
+          const size_t row = (size_t)T_.row0 + c;
+          float z[32];
+          load_acc(tb + c, z, bias);
+          if constexpr (GATED) {
+            // rows 0 .. 15 of the chunk are the gate warp's to finish, the others the up warp's
+            float* mine = reinterpret_cast<float*>(stg);
+            const float* theirs =
+                reinterpret_cast<const float*>(smem + kPairEpiOff + (warp - 2 + (up ? 2 : -2)) * kStgBytes);
+            float g[16], u[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) mine[j * 32 + lane] = up ? z[j] : z[16 + j];
+            partner_sync(pair_id);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float o = theirs[j * 32 + lane], k = up ? z[16 + j] : z[j];
+              g[j] = up ? o : k;
+              u[j] = up ? k : o;
+            }
+            partner_sync(pair_id);
+            const int half = up ? 16 : 0, nrows = min(16, T_.rows - c - half);
+            const size_t r0 = row + half;
+            if (nrows > 0) {
+              if (a.z) {
+                put_rows16(stg, g, a.z + r0 * a.N + col, a.N, nrows, ncols, lane);
+                put_rows16(stg + 1024, u, a.z + r0 * a.N + a.width + col, a.N, nrows, ncols, lane);
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) g[j] = swiglu_f<true>(g[j], u[j], a.form);
+              if (a.residual) {
+                const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual) + r0 * a.width + n;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (j < nrows && lane < ncols) g[j] += __bfloat162float(r[(size_t)j * a.width]);
+                __syncwarp();  // (the residual may be Y: every row is read before it is written)
+              }
+              put_rows16(stg, g, static_cast<__nv_bfloat16*>(a.y) + r0 * a.width + col, a.width, nrows, ncols, lane);
+            }
+          } else {
+            uint4 next[4];
+            if (a.residual && c + 64 < T_.rows)
+              fetch_chunk(next, static_cast<const __nv_bfloat16*>(a.residual) + (row + 64) * a.width + col, a.width,
+                          T_.rows - c - 64, ncols, lane);
+            finish_plain(a, z, res, row, col, min(32, T_.rows - c), ncols, stg, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) res[i] = next[i];
+          }
         }
       }
       tc_fence_before();
@@ -218,17 +294,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
 template <bool GATED>
 int launch(const LinCall& c, const DeviceInfo& dev) {
-  using C = PairCfg<GATED>;
   auto kern = linear_pair_kernel<GATED>;
   CUtensorMap tw, tx;
-  const int st = lin_maps(c, 64, &tw, &tx);
+  const int st = lin_maps(c, kPairTN / 2, GATED, &tw, &tx);
   if (st) return st;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::bytes(kMaxGroups));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem(kMaxGroups));
   if (e != cudaSuccess) return cuda_status(e);
-  const int64_t nct = (c.a.width + 2 * kBN - 1) / (2 * kBN);
-  const int64_t tiles = ((c.a.M + C::kTN - 1) / C::kTN + (c.a.group_lens ? c.a.G : 0)) * nct;
+  const int cw = GATED ? kBN : 2 * kBN;
+  const int64_t nct = (c.a.width + cw - 1) / cw;
+  const int64_t tiles = ((c.a.M + kPairTN - 1) / kPairTN + (c.a.group_lens ? c.a.G : 0)) * nct;
   const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(dev.sms / 2, tiles));
-  kern<<<grid, kLinThreads, C::bytes(c.a.G), c.stream>>>(tw, tx, c.a);
+  kern<<<grid, kPairThreads, pair_smem(c.a.G), c.stream>>>(tw, tx, c.a);
   return cuda_status(cudaGetLastError());
 }
 

@@ -27,11 +27,11 @@ template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
 template <>
 __device__ __forceinline__ float4 load4(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
+  return *reinterpret_cast<const float4*>(p);
 }
 template <>
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
   return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
 }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kLinThreads)
   LinTile T_{0, 0, 0, 0};
   if (live) {
     GroupCursor cur;
-    T_ = lin_tile<kBN>(t, a, sa.tn, nct, s_off, s_tile, cur);
+    T_ = lin_tile<kBN, false>(t, a, sa.tn, nct, s_off, s_tile, cur);
   }
   const int k_begin = (int)((long long)nkb * rank / splits), k_end = (int)((long long)nkb * (rank + 1) / splits);
   const int run = live ? k_end - k_begin : 0;
@@ -256,7 +256,7 @@ int launch(const LinCall& c, int tn, int splits) {
   constexpr int H = GATED ? 2 : 1;
   auto kern = linear_split_kernel<GATED, T>;
   CUtensorMap tw, tx;
-  int st = lin_maps(c, (uint32_t)tn, &tw, &tx);
+  int st = lin_maps(c, (uint32_t)tn, false, &tw, &tx);
   if (st) return st;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)split_smem(kMaxGroups));
   if (e != cudaSuccess) return cuda_status(e);

@@ -326,3 +326,18 @@ def test_linear_wait_expiry(M, N, K, G, act, stall_at):
     assert pgg.read_error(err) == 0
     want = float(og.swiglu_fwd(np.full((1, 2), float(K)))[0, 0]) if act else float(K)
     assert (Y.float() == torch.tensor(want).to(BF).float().item()).all()
+
+
+@pytest.mark.parametrize("act", list(FORMS))
+@pytest.mark.parametrize("lens", [[1100, 0, 515, 2000], [513, 700], [4096 + 17]])
+def test_linear_long_groups(lens, act):
+    # groups of several row tiles, ragged at their ends; column tiles that end inside a CTA pair's columns
+    lens = np.array(lens, dtype=np.int32)
+    for N, K in ((336, 200), (176, 72), (1296, 64)):
+        X, W, b, r = _inputs(int(lens.sum()), N, K, lens, N, act=act)
+        Y, Z = pgg.grouped_linear(X.to(DEV), W.to(DEV), torch.from_numpy(lens).to(DEV), bias=_dev(b), residual=_dev(r),
+                                  act=act, save_z=True, **FORMS[act])
+        _check(Y, Z, X, W, lens, b, r, act, FORMS[act])
+        again, z2 = pgg.grouped_linear(X.to(DEV), W.to(DEV), torch.from_numpy(lens).to(DEV), bias=_dev(b), residual=_dev(r),
+                                       act=act, save_z=True, **FORMS[act])
+        assert torch.equal(Y, again) and torch.equal(Z, z2)
