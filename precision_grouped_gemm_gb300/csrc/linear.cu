@@ -1,4 +1,7 @@
 // grouped_linear: the persistent kernel of one CTA per SM, the choice of a kernel, and the entry points.
+#include <cmath>
+
+#include "cluster.cuh"
 #include "linear.cuh"
 
 namespace pgg {
@@ -89,58 +92,53 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    bool stalled = false;
-    for (int t = blockIdx.x; t < tiles && !aborted && !stalled; t += gridDim.x) {
-      const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (issued == a.stall_at) { stalled = true; break; }
-        if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
-        if (lane == 0) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool stalled = false;
+      for (int t = blockIdx.x; t < tiles && !aborted && !stalled; t += gridDim.x) {
+        const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (issued == a.stall_at) { stalled = true; break; }
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
           const uint32_t fb = smem_u32(&full[stage]);
           const uint32_t sa = smem_a + stage * L::kABytes, sb = smem_b + stage * L::kBBytes;
           mbar_arrive_expect_tx(fb, L::kStageBytes);
           tma_load_3d(sa, &tmW, fb, kb * kBK, T_.col0, T_.g);
           if (GATED) tma_load_3d(sa + kBN * 128, &tmW, fb, kb * kBK, a.width + T_.col0, T_.g);
           tma_load_2d(sb, &tmX, fb, kb * kBK, T_.row0);
+          ++issued;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-    }
-    if (aborted && lane == 0) {
-      // the loads still in flight land before the block's shared memory goes away
-      long long n = issued < STAGES ? issued : STAGES;
-      int s = stage;
-      uint32_t p = phase;
-      for (long long i = 0; i < n; ++i) {
-        if (--s < 0) { s = STAGES - 1; p ^= 1u; }
-        mbar_wait_drain(smem_u32(&full[s]), p);
+      if (aborted) {
+        // the loads still in flight land before the block's shared memory goes away
+        for (long long i = 0, n = issued < STAGES ? issued : STAGES; i < n; ++i) {
+          if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
+          mbar_wait_drain(smem_u32(&full[stage]), phase);
+        }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    const uint64_t desc_a = smem_desc(smem_a, 16, 1024, kSwizzle128B);
-    const uint64_t desc_b = smem_desc(smem_b, 16, 1024, kSwizzle128B);
-    for (int t = blockIdx.x; t < tiles && !aborted; t += gridDim.x) {
-      const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
-      const uint32_t idesc = idesc_bf16(kBN, (T_.rows + 15) & ~15, false, false);
-      for (int k0 = 0; k0 < nkb && !aborted; k0 += kWide ? kChunk : nkb) {
-        const int k1 = kWide ? min(nkb, k0 + kChunk) : nkb;
-        if (!warp_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
-        tc_fence_after();
-        const uint32_t d = tmem + acc * kAcc;
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+    if (elect_one()) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      const uint64_t desc_a = smem_desc(smem_a, 16, 1024, kSwizzle128B);
+      const uint64_t desc_b = smem_desc(smem_b, 16, 1024, kSwizzle128B);
+      uint64_t da = desc_a, db = desc_b;
+      for (int t = blockIdx.x; t < tiles && !aborted; t += gridDim.x) {
+        const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
+        const uint32_t idesc = idesc_bf16(kBN, (T_.rows + 15) & ~15, false, false);
+        for (int k0 = 0; k0 < nkb && !aborted; k0 += kWide ? kChunk : nkb) {
+          const int k1 = kWide ? min(nkb, k0 + kChunk) : nkb;
+          if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t da = desc_a + (uint64_t)(stage * L::kABytes >> 4);
-            const uint64_t db = desc_b + (uint64_t)(stage * L::kBBytes >> 4);
+          const uint32_t d = tmem + acc * kAcc;
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+            tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < kBK / 16; ++ks) {
               const uint32_t more = kb > k0 || ks > 0 ? 1u : 0u;
@@ -148,19 +146,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               if (GATED) mma_f16(d + TN, da + (kBN * 128 >> 4) + 2 * ks, db + 2 * ks, idesc, more);
             }
             mma_commit(smem_u32(&empty[stage]));
+            da += L::kABytes >> 4;
+            db += L::kBBytes >> 4;
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; da = desc_a; db = desc_b; }
           }
-          __syncwarp();
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (aborted) break;
+          mma_commit(smem_u32(&tfull[acc]));
+          if (++acc == kBufs) { acc = 0; acc_phase ^= 1u; }
         }
-        if (aborted) break;
-        if (lane == 0) mma_commit(smem_u32(&tfull[acc]));
-        __syncwarp();
-        if (++acc == kBufs) { acc = 0; acc_phase ^= 1u; }
       }
-    }
-    if (aborted && lane == 0) {
-      mma_commit(smem_u32(drain));
-      mbar_wait_drain(smem_u32(drain), 0);
+      if (aborted) {
+        mma_commit(smem_u32(drain));
+        mbar_wait_drain(smem_u32(drain), 0);
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..5)
@@ -230,7 +228,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   }
 
-  if (aborted && lane == 0) set_error(a.err, kErrTimeout);
+  if (aborted) set_error(a.err, kErrTimeout);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -257,27 +256,62 @@ int launch(const LinCall& c, const DeviceInfo& dev) {
   return cuda_status(cudaGetLastError());
 }
 
-// Which kernel: few rows of X in few tiles split the reduction over a cluster; bf16 results of long
-// groups take CTA pairs; the rest the persistent kernel, with narrow row tiles where groups are short.
+// Which kernel, by an estimate of its time in microseconds from what each was measured to take: a k-block's
+// stage at 95 KB a microsecond and SM (TMA from L2), its products at the tensor cores' rate, a start and an
+// end.  Groups are taken to be of equal length.
+struct Plan {
+  enum Kind { kSplit, kOne, kPair } kind;
+  int tn, splits;
+  double us;
+};
+Plan choose(const LinCall& c, const DeviceInfo& dev) {
+  const bool gated = c.a.act == kActSwiglu;
+  const int H = gated ? 2 : 1, nkb = ceil_div(c.a.K, kBK);
+  const double live = c.a.group_lens ? (double)std::min<int64_t>(c.a.G, c.a.M) : 1;  // groups that can have rows
+  const double rows = (double)c.a.M / live;
+  const double nct = ceil_div(c.a.width, kBN), sms = dev.sms;
+  auto tiles = [&](int tn) { return live * std::ceil(rows / tn) * nct; };
+  auto block = [&](int tn) { return std::max((H * kBN + tn) * 128 / 95e3, H * std::min<double>(tn, rows) * 0.34 / 256); };
+  Plan best{Plan::kOne, 0, 1, 1e30};
+  auto offer = [&](Plan p) {
+    if (p.us < best.us) best = p;
+  };
+  for (int tn : {32, gated && c.f32 ? 64 : 128}) {
+    const double waves = std::ceil(tiles(tn) / sms);
+    offer({Plan::kOne, tn, 1, 4 + waves * nkb * block(tn) + 0.02 * std::min<double>(tn, rows)});
+  }
+  if (!c.f32) {
+    // the two CTAs' stages: the same bytes for each
+    const double t = live * std::ceil(rows / 256) * std::ceil(c.a.width / (gated ? 128.0 : 256.0));
+    const double kb = std::max(32768 / 110e3, std::min(256.0, rows) * 0.34 / 256);
+    offer({Plan::kPair, 256, 1, 6 + std::ceil(t / (dev.sms / 2)) * nkb * kb});
+  }
+  for (int tn : {16, 32, 64, 128}) {
+    if (gated && tn > 64) continue;
+    for (int splits : {2, 4, 8}) {
+      // the launch has a cluster for every tile that the lengths may make
+      const int64_t most = ((c.a.M + tn - 1) / tn + (c.a.group_lens ? (int64_t)live - 1 : 0)) * (int64_t)nct;
+      const double ctas = tiles(tn) * splits;
+      if (most * splits > 4 * dev.sms || ctas > 2 * sms || nkb < 2 * splits || (tn > 32 && ctas > sms)) continue;
+      const int run = ceil_div(nkb, splits), accs = std::min(run, 256 / (H * tn));
+      if (c.f32 && run > kChunk * accs) continue;  // (sums in fp32: see linear_kernel)
+      offer({Plan::kSplit, tn, splits, 4.5 + run * block(tn) * (ctas > sms ? 2 : 1) + 0.02 * tn});
+    }
+  }
+  return best;
+}
+
 int dispatch(const LinCall& c, const DeviceInfo& dev) {
   const bool gated = c.a.act == kActSwiglu;
-  const int nct = ceil_div(c.a.width, kBN), nkb = ceil_div(c.a.K, kBK);
-  const int64_t live = c.a.group_lens ? std::min<int64_t>(c.a.G, c.a.M) : 1;  // groups that can have rows
-  const int tn = c.a.M <= 16 ? 16 : 32;
-  const int64_t tiles = ((c.a.M + tn - 1) / tn + (c.a.group_lens ? live - 1 : 0)) * nct;
-  if (tiles * 2 <= dev.sms && nkb >= 4) {
-    int splits = 2;
-    while (splits < 8 && tiles * splits * 2 <= 2 * dev.sms && nkb >= splits * 4) splits *= 2;
-    return launch_linear_split(c, dev, tn, splits);
-  }
-  const int64_t rows = c.a.M / live;  // of a group, on average
+  const Plan p = choose(c, dev);
+  if (p.kind == Plan::kSplit) return launch_linear_split(c, dev, p.tn, p.splits);
+  if (p.kind == Plan::kPair) return launch_linear_pair(c, dev);
   if (c.f32) {
-    if (gated) return rows <= 16 ? launch<true, 32, 5, float>(c, dev) : launch<true, 64, 5, float>(c, dev);
-    return rows <= 16 ? launch<false, 32, 9, float>(c, dev) : launch<false, 128, 6, float>(c, dev);
+    if (gated) return p.tn == 32 ? launch<true, 32, 5, float>(c, dev) : launch<true, 64, 5, float>(c, dev);
+    return p.tn == 32 ? launch<false, 32, 9, float>(c, dev) : launch<false, 128, 6, float>(c, dev);
   }
-  if (rows >= 512) return launch_linear_pair(c, dev);
-  if (gated) return rows <= 16 ? launch<true, 32, 5, __nv_bfloat16>(c, dev) : launch<true, 128, 4, __nv_bfloat16>(c, dev);
-  return rows <= 16 ? launch<false, 32, 9, __nv_bfloat16>(c, dev) : launch<false, 128, 6, __nv_bfloat16>(c, dev);
+  if (gated) return p.tn == 32 ? launch<true, 32, 5, __nv_bfloat16>(c, dev) : launch<true, 128, 4, __nv_bfloat16>(c, dev);
+  return p.tn == 32 ? launch<false, 32, 9, __nv_bfloat16>(c, dev) : launch<false, 128, 6, __nv_bfloat16>(c, dev);
 }
 
 int linear_impl(const void* X, const void* W, const int32_t* group_lens, const void* bias, const void* residual,

@@ -128,7 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   // vote or a warp barrier a step would lengthen.
   if (warp == 0) {
     // ------------------------------------------------------------ loads of this CTA's halves
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t full0 = map_rank(smem_u32(full), 0);
       int stage = 0;
       uint32_t phase = 0;
@@ -167,7 +167,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products, issued by the leader
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       const uint64_t desc_a = smem_desc(smem_a, 16, 1024, kSwizzle128B);
@@ -281,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   }
 
-  if (aborted && lane == 0) set_error(a.err, kErrTimeout);
+  if (aborted) set_error(a.err, kErrTimeout);
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -1,26 +1,30 @@
 // grouped_linear for few rows of X: a cluster of CTAs shares one tile (128 output columns by up to TN
 // rows) and cuts its reduction, so that the weights of a small product are read by the whole GPU.  Each
-// CTA multiplies its run of K, leaves its sums in its shared memory, and finishes a share of the rows:
-// it reads the cluster's sums of them through distributed shared memory, in the order of K, and applies
-// the epilogue.  Nothing goes through global memory, so the call needs no workspace.
+// CTA multiplies its run of K and sends its sums to the CTA that finishes the row, through distributed
+// shared memory; that CTA adds them in the order of K and applies the epilogue.  Nothing goes through
+// global memory, so the call needs no workspace.  Nobody reads another's memory, so that one barrier of the
+// cluster is enough where the sums have a place of their own; many rows' sums take the place of the stages
+// instead, when every CTA of the cluster has done with its own.
 #include "cluster.cuh"
 #include "linear.cuh"
 
 namespace pgg {
 namespace {
 
-constexpr int kMaxStages = 8;
-constexpr int kRing = 104 * 1024;  // shared memory of the stages: two CTAs an SM
-constexpr int kBarOff = kRing;
-constexpr int kGroupOff = kBarOff + 256;
-// Columns of tensor memory a CTA may take: two CTAs are resident on an SM, and one that waited for columns
+constexpr int kMaxStages = 12;
+// Shared memory: the ring of stages, the sums that this CTA receives (tn > 32: in the ring), barriers,
+// group tables.  With more
+// CTAs than SMs two share an SM, else one has it, so that its whole run of K can be in flight at once.
+constexpr int kSmemTwo = 112 * 1024, kSmemOne = 216 * 1024, kSmemLeast = 80 * 1024;  // (at most two an SM)
+// Columns of tensor memory a CTA may take: where two CTAs are resident on an SM, one that waited for columns
 // of another cluster's CTA, which waits for its own cluster, would wait for ever.
-constexpr int kCols = 256;
-size_t split_smem(int G) { return 1024 + (size_t)kGroupOff + 8 * ((size_t)G + 1); }
+constexpr int kColsTwo = 256;
 
 struct SplitArgs {
   LinArgs a;
   int tn, stages, stage_bytes, accs;  // accs: accumulators that the CTA's run of K is spread over
+  int own;                            // rows of the tile that a CTA finishes, at most
+  int in_ring;                        // the sums are received in the place of the stages
 };
 
 template <typename T>
@@ -52,17 +56,20 @@ __global__ void __launch_bounds__(kLinThreads)
   const LinArgs& a = sa.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  const int ring_bytes = sa.stages * sa.stage_bytes, recv_bytes = (int)cluster_size() * sa.own * H * kBN * 4;
+  float* recv = reinterpret_cast<float*>(smem + (sa.in_ring ? 0 : ring_bytes));  // [splits][own][H][128]
+  uint64_t* full =
+      reinterpret_cast<uint64_t*>(smem + (sa.in_ring ? max(ring_bytes, recv_bytes) : ring_bytes + recv_bytes));
   uint64_t* empty = full + kMaxStages;
   uint64_t* done = empty + kMaxStages;
   volatile WaitCtl* s_ctl = reinterpret_cast<volatile WaitCtl*>(done + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<WaitCtl*>(s_ctl) + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 1);
-  int32_t* s_off = reinterpret_cast<int32_t*>(smem + kGroupOff);
+  int32_t* s_off = reinterpret_cast<int32_t*>(s_bad + 1);
   int32_t* s_tile = s_off + (a.G + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank(), splits = (int)cluster_size();
+  const int rank = (int)cluster_rank(), splits = (int)cluster_size(), lg = 31 - __clz(splits);
   const int nct = (a.width + kBN - 1) / kBN, nkb = (a.K + kBK - 1) / kBK;
   const int cols = sa.accs * H * sa.tn;  // of tensor memory: a power of two from 32 on
 
@@ -92,6 +99,7 @@ __global__ void __launch_bounds__(kLinThreads)
   }
   tc_fence_before();
   __syncthreads();
+  if (!sa.in_ring) cluster_arrive();  // (waited for before the first access to another CTA's memory: it has to be there)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const int t = (int)cluster_id();
@@ -110,169 +118,177 @@ __global__ void __launch_bounds__(kLinThreads)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    int stage = 0;
-    uint32_t phase = 0;
-    int issued = 0;
-    for (int i = 0; i < run; ++i) {
-      if (a.stall_at >= 0 && k_begin + i >= a.stall_at) break;
-      if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
-      if (lane == 0) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      for (int i = 0; i < run; ++i) {
+        if (a.stall_at >= 0 && k_begin + i >= a.stall_at) break;
+        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
         const uint32_t fb = smem_u32(&full[stage]), s = ring + stage * sa.stage_bytes;
         const int k = (k_begin + i) * kBK;
         mbar_arrive_expect_tx(fb, sa.stage_bytes);
         tma_load_3d(s, &tmW, fb, k, T_.col0, T_.g);
         if (GATED) tma_load_3d(s + kBN * 128, &tmW, fb, k, a.width + T_.col0, T_.g);
         tma_load_2d(s + a_bytes, &tmX, fb, k, T_.row0);
+        ++issued;
+        if (++stage == sa.stages) { stage = 0; phase ^= 1u; }
       }
-      __syncwarp();
-      ++issued;
-      if (++stage == sa.stages) { stage = 0; phase ^= 1u; }
-    }
-    if (aborted && lane == 0) {
-      int n = min(issued, sa.stages), s = stage;
-      uint32_t p = phase;
-      for (int i = 0; i < n; ++i) {
-        if (--s < 0) { s = sa.stages - 1; p ^= 1u; }
-        mbar_wait_drain(smem_u32(&full[s]), p);
+      if (aborted) {
+        for (int i = 0, n = min(issued, sa.stages); i < n; ++i) {
+          if (--stage < 0) { stage = sa.stages - 1; phase ^= 1u; }
+          mbar_wait_drain(smem_u32(&full[stage]), phase);
+        }
       }
     }
   } else if (warp == 1 && run > 0) {
     // ------------------------------------------------------------ products
-    const uint32_t idesc = idesc_bf16(kBN, (T_.rows + 15) & ~15, false, false);
-    const uint64_t desc = smem_desc(ring, 16, 1024, kSwizzle128B);
-    int stage = 0;
-    uint32_t phase = 0;
-    for (int i = 0; i < run; ++i) {
-      if (!warp_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t da = desc + (uint64_t)(stage * sa.stage_bytes >> 4), db = da + (a_bytes >> 4);
-        const uint32_t d = tmem + (i / per) * H * sa.tn;
+    if (elect_one()) {
+      const uint32_t idesc = idesc_bf16(kBN, (T_.rows + 15) & ~15, false, false);
+      const uint64_t desc = smem_desc(ring, 16, 1024, kSwizzle128B);
+      int stage = 0, left = per;  // k-blocks that the accumulator still takes
+      uint32_t phase = 0, d = tmem;
+      uint64_t da = desc;
+      for (int i = 0; i < run; ++i) {
+        if (!mbar_wait(smem_u32(&full[stage]), phase, s_ctl)) { aborted = true; break; }
+        tc_fence_after();
+        const uint64_t db = da + (a_bytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBK / 16; ++ks) {
-          const uint32_t more = i % per > 0 || ks > 0 ? 1u : 0u;
+          const uint32_t more = left < per || ks > 0 ? 1u : 0u;
           mma_f16(d, da + 2 * ks, db + 2 * ks, idesc, more);
           if (GATED) mma_f16(d + sa.tn, da + (kBN * 128 >> 4) + 2 * ks, db + 2 * ks, idesc, more);
         }
         mma_commit(smem_u32(&empty[stage]));
+        da += sa.stage_bytes >> 4;
+        if (++stage == sa.stages) { stage = 0; phase ^= 1u; da = desc; }
+        if (--left == 0) { left = per; d += H * sa.tn; }
       }
-      __syncwarp();
-      if (++stage == sa.stages) { stage = 0; phase ^= 1u; }
+      // every MMA is complete before the sums are read, or, after an abort, before the CTA goes
+      mma_commit(smem_u32(done));
+      if (aborted) mbar_wait_drain(smem_u32(done), 0);
     }
-    // every MMA is complete before the sums are read, or, after an abort, before the CTA goes
-    if (lane == 0) mma_commit(smem_u32(done));
-    __syncwarp();
-    if (aborted && lane == 0) mbar_wait_drain(smem_u32(done), 0);
   } else if (warp >= 2 && run > 0) {
-    // ------------------------------------------------------------ this CTA's sums: [half][row][128 columns]
+    // ------------------------------------------------------------ this CTA's sums: row r to CTA r % splits
     const int q = warp & 3;
     if (!warp_wait(smem_u32(done), 0, s_ctl) || s_ctl->abort) aborted = true;
     aborted = __any_sync(0xffffffffu, aborted);
+    if (sa.in_ring) cluster_arrive();
+    cluster_wait();
     if (!aborted) {
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
       const int used = (run + per - 1) / per;
-      float* part = reinterpret_cast<float*>(smem);  // (every stage has been read)
 #pragma unroll 1
       for (int h = 0; h < H; ++h)
 #pragma unroll 1
         for (int c = 0; c < T_.rows; c += 16) {
           float v[16];
+          uint32_t r[16];
+          tmem_ld16(tb + h * sa.tn + c, r);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
 #pragma unroll 1
-          for (int i = 0; i < used; ++i) {
-            uint32_t r[16];
+          for (int i = 1; i < used; i += 2) {
+            uint32_t r2[16];
             tmem_ld16(tb + (i * H + h) * sa.tn + c, r);
+            if (i + 1 < used) tmem_ld16(tb + ((i + 1) * H + h) * sa.tn + c, r2);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j) {
+              v[j] += __uint_as_float(r[j]);
+              if (i + 1 < used) v[j] += __uint_as_float(r2[j]);
+            }
           }
+          const uint32_t at = smem_u32(recv + (rank * sa.own * H + h) * kBN + q * 32 + lane);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(h * sa.tn + c + j) * kBN + q * 32 + lane] = v[j];
+          for (int j = 0; j < 16; ++j)
+            if (c + j < T_.rows)  // (splits is a power of two)
+              st_cluster(map_rank(at + ((c + j) >> lg) * (H * kBN * 4), (c + j) & (splits - 1)), v[j]);
         }
     }
   }
   __syncwarp();
-  cluster_sync();
-  // ------------------------------------------------------------ rows rank, rank + splits, ... of the tile
-  if (warp >= 2 && run > 0 && !aborted) {
-    const int col = T_.col0 + 4 * lane;  // a warp takes a row, a lane four columns
-    if (col < a.width) {
-      float4 bg = make_float4(0, 0, 0, 0), bu = bg;
-      if (a.bias) {
-        const __nv_bfloat16* b = a.bias + (size_t)T_.g * a.N + col;
-        bg = load4(b);
-        if (GATED) bu = load4(b + a.width);
-      }
-      for (int r = rank + (warp - 2) * splits; r < T_.rows; r += 4 * splits) {
-        const size_t row = (size_t)T_.row0 + r;
-        float4 z = bg, u = bu, res = make_float4(0, 0, 0, 0);
-        if (a.residual) res = load4(static_cast<const T*>(a.residual) + row * a.width + col);
-#pragma unroll 1
-        for (int s0 = 0; s0 < splits; s0 += 4) {
-          float4 p[4], o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (s0 + i < splits) {
-              const uint32_t at = map_rank(ring + (r * kBN + 4 * lane) * 4, s0 + i);
-              p[i] = ld_cluster4(at);
-              if (GATED) o[i] = ld_cluster4(at + sa.tn * kBN * 4);
-            }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (s0 + i < splits) {
-              z.x += p[i].x; z.y += p[i].y; z.z += p[i].z; z.w += p[i].w;
-              if (GATED) { u.x += o[i].x; u.y += o[i].y; u.z += o[i].z; u.w += o[i].w; }
-            }
-        }
-        if (a.z) {
-          store4(a.z + row * a.N + col, z);
-          if (GATED) store4(a.z + row * a.N + a.width + col, u);
-        }
-        if (GATED) {
-          z = make_float4(swiglu_f<kFast>(z.x, u.x, a.form), swiglu_f<kFast>(z.y, u.y, a.form), swiglu_f<kFast>(z.z, u.z, a.form),
-                          swiglu_f<kFast>(z.w, u.w, a.form));
-        } else if (a.act != kActNone) {
-          z = make_float4(act_any<kFast>(z.x, a), act_any<kFast>(z.y, a), act_any<kFast>(z.z, a), act_any<kFast>(z.w, a));
-        }
-        z.x += res.x; z.y += res.y; z.z += res.z; z.w += res.w;
-        store4(static_cast<T*>(a.y) + row * a.width + col, z);
-      }
-    }
+  if (warp < 2 || run == 0) {
+    if (sa.in_ring) cluster_arrive();
+    cluster_wait();
   }
-  if (aborted && lane == 0) set_error(a.err, kErrTimeout);
+  // what the epilogue reads besides the sums: the bias, and the residual of this warp's first row
+  const int col = T_.col0 + 4 * lane;  // a warp finishes a row, a lane four columns
+  const bool mine = warp >= 2 && run > 0 && !aborted && col < a.width;
+  float4 bg = make_float4(0, 0, 0, 0), bu = bg;
+  if (mine && a.bias) {
+    const __nv_bfloat16* b = a.bias + (size_t)T_.g * a.N + col;
+    bg = load4(b);
+    if (GATED) bu = load4(b + a.width);
+  }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();  // the other CTAs have read this one's sums
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, cols < 32 ? 32 : cols);
   }
+  if (mine) {
+    for (int i = warp - 2; i * splits + rank < T_.rows; i += 4) {
+      const size_t row = (size_t)T_.row0 + i * splits + rank;
+      float4 z = bg, u = bu, res = make_float4(0, 0, 0, 0);
+      if (a.residual) res = load4(static_cast<const T*>(a.residual) + row * a.width + col);
+      const float4* from = reinterpret_cast<const float4*>(recv) + i * H * (kBN / 4) + lane;
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s, from += sa.own * H * (kBN / 4)) {
+        const float4 p = from[0];
+        z.x += p.x; z.y += p.y; z.z += p.z; z.w += p.w;
+        if (GATED) {
+          const float4 o = from[kBN / 4];
+          u.x += o.x; u.y += o.y; u.z += o.z; u.w += o.w;
+        }
+      }
+      if (a.z) {
+        store4(a.z + row * a.N + col, z);
+        if (GATED) store4(a.z + row * a.N + a.width + col, u);
+      }
+      if (GATED) {
+        z = make_float4(swiglu_f<kFast>(z.x, u.x, a.form), swiglu_f<kFast>(z.y, u.y, a.form),
+                        swiglu_f<kFast>(z.z, u.z, a.form), swiglu_f<kFast>(z.w, u.w, a.form));
+      } else if (a.act != kActNone) {
+        z = make_float4(act_any<kFast>(z.x, a), act_any<kFast>(z.y, a), act_any<kFast>(z.z, a), act_any<kFast>(z.w, a));
+      }
+      z.x += res.x; z.y += res.y; z.z += res.z; z.w += res.w;
+      store4(static_cast<T*>(a.y) + row * a.width + col, z);
+    }
+  }
+  if (aborted) set_error(a.err, kErrTimeout);
 }
 
 template <bool GATED, typename T>
-int launch(const LinCall& c, int tn, int splits) {
+int launch(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
   constexpr int H = GATED ? 2 : 1;
   auto kern = linear_split_kernel<GATED, T>;
   CUtensorMap tw, tx;
   int st = lin_maps(c, (uint32_t)tn, false, &tw, &tx);
   if (st) return st;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)split_smem(kMaxGroups));
-  if (e != cudaSuccess) return cuda_status(e);
-  SplitArgs a{c.a, tn, 0, (H * kBN + tn) * 128, 1};
-  a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
-  if (c.f32) {  // as many accumulators as there is room for: each takes fewer steps (see linear_kernel)
-    const int most = (int)((c.a.K + kBK * splits - 1) / (kBK * splits));
-    while (a.accs * 2 * H * tn <= kCols && a.accs < most) a.accs *= 2;
-  }
   const int64_t nct = (c.a.width + kBN - 1) / kBN;
   const int64_t live = c.a.group_lens ? std::min<int64_t>(c.a.G, c.a.M) : 1;
   const int64_t tiles = ((c.a.M + tn - 1) / tn + (c.a.group_lens ? live - 1 : 0)) * nct;
+  const bool one = tiles * splits <= dev.sms;
+  const int recv = splits * ((tn + splits - 1) / splits) * H * kBN * 4;
+  const bool in_ring = tn > 32;
+  const int room = one ? kSmemOne : kSmemTwo;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+  if (e != cudaSuccess) return cuda_status(e);
+  SplitArgs a{c.a, tn, 0, (H * kBN + tn) * 128, 1, (tn + splits - 1) / splits, in_ring};
+  const int fixed = 1024 + (in_ring ? 0 : recv) + (2 * kMaxStages + 1) * 8 + 32 + 8 * (c.a.G + 1);
+  const int nkb = (c.a.K + kBK - 1) / kBK;
+  a.stages = std::min(std::min(kMaxStages, (nkb + splits - 1) / splits), (room - fixed) / a.stage_bytes);
+  const int smem = std::max(fixed + std::max(a.stages * a.stage_bytes, in_ring ? recv : 0), kSmemLeast);
+  if (c.f32)  // as many accumulators as there is room for: each takes fewer steps (see linear_kernel)
+    while (a.accs * 2 * H * tn <= kColsTwo && a.accs * splits < nkb) a.accs *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * splits));
   cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = split_smem(c.a.G);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = c.stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -286,10 +302,10 @@ int launch(const LinCall& c, int tn, int splits) {
 
 }  // namespace
 
-int launch_linear_split(const LinCall& c, const DeviceInfo&, int tn, int splits) {
+int launch_linear_split(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
   if (c.a.act == kActSwiglu)
-    return c.f32 ? launch<true, float>(c, tn, splits) : launch<true, __nv_bfloat16>(c, tn, splits);
-  return c.f32 ? launch<false, float>(c, tn, splits) : launch<false, __nv_bfloat16>(c, tn, splits);
+    return c.f32 ? launch<true, float>(c, dev, tn, splits) : launch<true, __nv_bfloat16>(c, dev, tn, splits);
+  return c.f32 ? launch<false, float>(c, dev, tn, splits) : launch<false, __nv_bfloat16>(c, dev, tn, splits);
 }
 
 }  // namespace pgg
