@@ -256,9 +256,11 @@ int launch(const LinCall& c, const DeviceInfo& dev) {
   return cuda_status(cudaGetLastError());
 }
 
-// Which kernel, by an estimate of its time in microseconds from what each was measured to take: a k-block's
-// stage at 95 KB a microsecond and SM (TMA from L2), its products at the tensor cores' rate, a start and an
-// end.  Groups are taken to be of equal length.
+// Which kernel, by an estimate of its time in microseconds.  Groups are taken to be of equal length.  The
+// constants are what the kernels were measured to take: a k-block's stage at 150 KB a microsecond and SM or
+// its products at the tensor cores' rate, a start and an end.  (Times of split / one / pair: 1 x 4096 x 4096
+// 10.1 / 12.9 / 24; 256 x 4096 x 4096 17.3 / 17.5 / 24.8; 512 x 4096 x 4096 - / 18.0 / 25.1; 1024 x 4096 x 4096
+// - / 29.6 / 26.0; 4000 rows of 16 groups, 2048 x 2048: - / 41 / 37.)
 struct Plan {
   enum Kind { kSplit, kOne, kPair } kind;
   int tn, splits;
@@ -270,32 +272,34 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
   const double live = c.a.group_lens ? (double)std::min<int64_t>(c.a.G, c.a.M) : 1;  // groups that can have rows
   const double rows = (double)c.a.M / live;
   const double nct = ceil_div(c.a.width, kBN), sms = dev.sms;
+  const double memory =
+      (2.0 * live * c.a.N * c.a.K + (double)c.a.M * (2.0 * c.a.K + (c.f32 ? 4.0 : 2.0) * c.a.width)) / 6.7e6;
   auto tiles = [&](int tn) { return live * std::ceil(rows / tn) * nct; };
-  auto block = [&](int tn) { return std::max((H * kBN + tn) * 128 / 95e3, H * std::min<double>(tn, rows) * 0.34 / 256); };
+  auto block = [&](int tn) { return std::max((H * kBN + tn) * 128 / 150e3, H * std::min<double>(tn, rows) * 0.31 / 256); };
   Plan best{Plan::kOne, 0, 1, 1e30};
   auto offer = [&](Plan p) {
     if (p.us < best.us) best = p;
   };
-  for (int tn : {32, gated && c.f32 ? 64 : 128}) {
-    const double waves = std::ceil(tiles(tn) / sms);
-    offer({Plan::kOne, tn, 1, 4 + waves * nkb * block(tn) + 0.02 * std::min<double>(tn, rows)});
-  }
+  auto both = [](double a, double b) { return std::max(a, b) + 0.2 * std::min(a, b); };  // they overlap, not wholly
+  for (int tn : {32, gated && c.f32 ? 64 : 128})
+    offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.01 * tn});
   if (!c.f32) {
-    // the two CTAs' stages: the same bytes for each
     const double t = live * std::ceil(rows / 256) * std::ceil(c.a.width / (gated ? 128.0 : 256.0));
-    const double kb = std::max(32768 / 110e3, std::min(256.0, rows) * 0.34 / 256);
-    offer({Plan::kPair, 256, 1, 6 + std::ceil(t / (dev.sms / 2)) * nkb * kb});
+    offer({Plan::kPair, 256, 1,
+           7 + both(std::ceil(t / (dev.sms / 2)) * nkb * std::max(0.25, std::min(256.0, rows) * 0.31 / 256), memory)});
   }
   for (int tn : {16, 32, 64, 128}) {
     if (gated && tn > 64) continue;
     for (int splits : {2, 4, 8}) {
       // the launch has a cluster for every tile that the lengths may make
       const int64_t most = ((c.a.M + tn - 1) / tn + (c.a.group_lens ? (int64_t)live - 1 : 0)) * (int64_t)nct;
-      const double ctas = tiles(tn) * splits;
-      if (most * splits > 4 * dev.sms || ctas > 2 * sms || nkb < 2 * splits || (tn > 32 && ctas > sms)) continue;
+      if (nkb < 2 * splits || most > 4 * dev.sms) continue;
+      const bool one = most * splits <= dev.sms;  // CTAs an SM
+      if (tiles(tn) > linear_split_clusters(dev, splits, one) || (tn > 32 && !one)) continue;
       const int run = ceil_div(nkb, splits), accs = std::min(run, 256 / (H * tn));
       if (c.f32 && run > kChunk * accs) continue;  // (sums in fp32: see linear_kernel)
-      offer({Plan::kSplit, tn, splits, 4.5 + run * block(tn) * (ctas > sms ? 2 : 1) + 0.02 * tn});
+      offer({Plan::kSplit, tn, splits,
+             (c.a.group_lens ? 6.5 : 5.0) + both(run * block(tn) * (one ? 1 : 2), memory) + 0.02 * tn});
     }
   }
   return best;

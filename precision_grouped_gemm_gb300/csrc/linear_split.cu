@@ -5,6 +5,8 @@
 // global memory, so the call needs no workspace.  Nobody reads another's memory, so that one barrier of the
 // cluster is enough where the sums have a place of their own; many rows' sums take the place of the stages
 // instead, when every CTA of the cluster has done with its own.
+#include <atomic>
+
 #include "cluster.cuh"
 #include "linear.cuh"
 
@@ -262,6 +264,20 @@ __global__ void __launch_bounds__(kLinThreads)
   if (aborted) set_error(a.err, kErrTimeout);
 }
 
+cudaLaunchConfig_t config(unsigned grid, int splits, int smem, cudaStream_t stream, cudaLaunchAttribute* at) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = (unsigned)splits;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 template <bool GATED, typename T>
 int launch(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
   constexpr int H = GATED ? 2 : 1;
@@ -285,22 +301,33 @@ int launch(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
   const int smem = std::max(fixed + std::max(a.stages * a.stage_bytes, in_ring ? recv : 0), kSmemLeast);
   if (c.f32)  // as many accumulators as there is room for: each takes fewer steps (see linear_kernel)
     while (a.accs * 2 * H * tn <= kColsTwo && a.accs * splits < nkb) a.accs *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * splits));
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = c.stream;
   cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)splits;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = config((unsigned)(tiles * splits), splits, smem, c.stream, &at);
   e = cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
   return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 }  // namespace
+
+// A cluster's CTAs are on the SMs of one GPC, so this is less than the SMs would hold.  The same on every
+// device that the library runs on, and asked for once.
+int linear_split_clusters(const DeviceInfo& dev, int splits, bool one) {
+  static std::atomic<int> known[9][2];
+  std::atomic<int>& slot = known[splits][one];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  auto kern = linear_split_kernel<false, __nv_bfloat16>;
+  const int smem = one ? kSmemOne : kSmemTwo;
+  cudaLaunchAttribute at{};
+  const cudaLaunchConfig_t cfg = config((unsigned)(dev.sms * splits), splits, smem, nullptr, &at);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 1;
+  }
+  slot.store(n, std::memory_order_relaxed);
+  return n;
+}
 
 int launch_linear_split(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
   if (c.a.act == kActSwiglu)
