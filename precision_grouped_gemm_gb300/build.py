@@ -78,8 +78,9 @@ if __name__ == "__main__":
 # Kernel families with DRAM counters in profiles/traffic.json, and the sources each one's
 # kernels cannot depend on (separate translation units): a family's counters stay valid
 # while the sources it is built from are unchanged.
-_BLOCK = ("block.cuh", "norm.cu", "moe_route.cu", "moe_decode.cu", "act.cuh", "cluster.cuh", "linear.cuh",
-          "linear.cu", "linear_pair.cu", "linear_split.cu", "linear_bwd.cu", "join.cu")  # the operators around the grouped GEMMs
+_BLOCK = ("block.cuh", "norm.cu", "moe_route.cu", "moe_decode.cu", "act.cuh", "cluster.cuh", "packed.cuh", "linear.cuh",
+          "linear.cu", "linear_pair.cu", "linear_split.cu", "linear_bwd.cu",
+          "join.cu")  # the operators around the grouped GEMMs
 DIGEST_EXCLUDE = {
     "bf16": ("gemm_mx.cu", "mx_quant.cu", "moe_glue.cu") + _BLOCK,    # BF16 grouped GEMM family
     "mx": ("gemm_bf16.cu", "gemm_bf16.cuh", "moe_glue.cu") + _BLOCK,  # block-scaled GEMM + MX quantizers

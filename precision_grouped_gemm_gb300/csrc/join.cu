@@ -22,26 +22,39 @@
 #include <atomic>
 
 #include "block.cuh"
+#include "packed.cuh"
 
 namespace pgg {
 namespace {
 
-// Sums of N values over the block, in a fixed order, in every thread.  s: one buffer of a pair that
-// successive sums alternate between, so that one barrier a sum is enough.
-template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[32], int nwarps) {
+// Sum over the block, in a fixed order, in every thread.  s: one of two buffers that successive sums
+// alternate between, so that one barrier a sum is enough.
+__device__ __forceinline__ float block_sum(float v, float* s, int nwarps) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  // (at most 16 warps)
+  v = (threadIdx.x & 15) < nwarps ? s[threadIdx.x & 15] : 0.0f;
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The same for three sums at once.
+__device__ __forceinline__ void block_sums(float (&v)[3], float (*s)[16], int nwarps) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
     if ((threadIdx.x & 31) == 0) s[i][threadIdx.x >> 5] = v[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = (threadIdx.x & 31) < nwarps ? s[i][threadIdx.x & 31] : 0.0f;
+  for (int i = 0; i < 3; ++i) {
+    v[i] = (threadIdx.x & 15) < nwarps ? s[i][threadIdx.x & 15] : 0.0f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    for (int d = 8; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
   }
 }
 
@@ -76,17 +89,19 @@ __device__ __forceinline__ uint4 philox(uint64_t block, const Key& key) {
   return make_uint4(x0, x1, x2, x3);
 }
 // Element e of the 8-element piece number `piece` of the tensor becomes 0 where it is dropped.
-__device__ __forceinline__ void drop8(float (&t)[8], int64_t piece, const Drop& d, const Key& key) {
+__device__ __forceinline__ void drop8(f2 (&t)[4], int64_t piece, const Drop& d, const Key& key) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint4 w = philox((uint64_t)piece * 2 + i, key);
-    t[4 * i] = w.x >= d.below ? t[4 * i] : 0.0f;
-    t[4 * i + 1] = w.y >= d.below ? t[4 * i + 1] : 0.0f;
-    t[4 * i + 2] = w.z >= d.below ? t[4 * i + 2] : 0.0f;
-    t[4 * i + 3] = w.w >= d.below ? t[4 * i + 3] : 0.0f;
+    float a, b;
+    split2(t[2 * i], a, b);
+    t[2 * i] = make2(w.x >= d.below ? a : 0.0f, w.y >= d.below ? b : 0.0f);
+    split2(t[2 * i + 1], a, b);
+    t[2 * i + 1] = make2(w.z >= d.below ? a : 0.0f, w.w >= d.below ? b : 0.0f);
   }
 }
-// Bit e: element e of that piece is kept.
+
+// Bit e: element e of that piece is kept; and what is not kept made 0.
 __device__ __forceinline__ uint32_t keep8(int64_t piece, const Drop& d, const Key& key) {
   uint32_t m = 0;
 #pragma unroll
@@ -97,14 +112,22 @@ __device__ __forceinline__ uint32_t keep8(int64_t piece, const Drop& d, const Ke
   }
   return m;
 }
+__device__ __forceinline__ void keep_only(f2 (&t)[4], uint32_t keep) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    split2(t[i], a, b);
+    t[i] = make2(keep & (1u << (2 * i)) ? a : 0.0f, keep & (2u << (2 * i)) ? b : 0.0f);
+  }
+}
 
 // Piece v of a row of bf16 factors in fp32: ones where there are none, zeros past the row's end.
-__device__ __forceinline__ void load_factors(const uint4* p, int v, int nvec, float (&f)[8]) {
+__device__ __forceinline__ void load_factors(const uint4* p, int v, int nvec, f2 (&f)[4]) {
   if (p && v < nvec) {
-    unpack8(__ldg(p + v), f);
+    unpack2(__ldg(p + v), f);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = v < nvec ? 1.0f : 0.0f;
+    for (int e = 0; e < 4; ++e) f[e] = both(v < nvec ? 1.0f : 0.0f);
   }
 }
 
@@ -132,23 +155,24 @@ struct JoinArgs {
 // load, one row ahead, to its outputs: every byte moves once.
 template <int V, int FMT>
 __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
-  __shared__ float s_sum[2][1][32];
+  __shared__ float s_sum[2][32];
   const int nwarps = blockDim.x >> 5;
   Key key{};
   if (a.drop.rng) key = load_key(a.drop);
-  float g1[V][8], g2[V][8];
+  f2 g1[V][4], g2[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
     load_factors(a.gamma1, v, a.nvec, g1[j]);
     load_factors(a.gamma2, v, a.nvec, g2[j]);
     if (a.gate_col) {
-      float c[8];
+      f2 c[4];
       load_factors(a.gate_col, v, a.nvec, c);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g1[j][e] *= c[e];
+      for (int e = 0; e < 4; ++e) g1[j][e] = mul2(g1[j][e], c[e]);
     }
   }
+  const f2 ra = both(a.ra);
   uint4 xn[V], rn[V];  // the next row's pieces (zeros past the row's end)
   auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -174,51 +198,53 @@ __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
     float k = a.rb * a.drop.inv * (a.gate_row ? __ldg(a.gate_row + row) : 1.0f);
     fetch(row + gridDim.x);  // (h may be x or residual: other rows than the one that is written)
     if (a.gamma1) {
-      float q[1] = {0.0f};
+      f2 t = both(0.0f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float f[8];
-        unpack8(xv[j], f);
+        f2 f[4];
+        unpack2(xv[j], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[0] += f[e] * f[e];
+        for (int e = 0; e < 4; ++e) t = fma2(f[e], f[e], t);
       }
-      block_sums(q, s_sum[par], nwarps);
+      const float q = block_sum(sum2(t), s_sum[par], nwarps);
       par ^= 1;
-      const float rstd1 = rsqrtf(q[0] * a.inv_c + a.eps);
+      const float rstd1 = rsqrtf(q * a.inv_c + a.eps);
       if (a.rstd1 && threadIdx.x == 0) a.rstd1[row] = rstd1;
       k *= rstd1;
     }
-    float s[V][8];
-    float q[1] = {0.0f};
+    f2 s[V][4], t2 = both(0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
-      float t[8], r[8];
-      unpack8(xv[j], t);
-      unpack8(rv[j], r);
+      f2 t[4], r[4];
+      unpack2(xv[j], t);
+      unpack2(rv[j], r);
       if (a.drop.rng) drop8(t, base + v, a.drop, key);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s[j][e] = fmaf(a.ra, r[e], t[e] * g1[j][e] * k);
-        q[0] = fmaf(s[j][e], s[j][e], q[0]);
+      for (int e = 0; e < 4; ++e) {
+        s[j][e] = fma2(ra, r[e], mul2(mul2(t[e], g1[j][e]), both(k)));
+        t2 = fma2(s[j][e], s[j][e], t2);
       }
-      if (a.h && v < a.nvec) a.h[base + v] = pack8(s[j]);
+      if (a.h && v < a.nvec) a.h[base + v] = round8(s[j]);
     }
     if (!a.gamma2) continue;
-    block_sums(q, s_sum[par], nwarps);
+    const float q2 = block_sum(sum2(t2), s_sum[par], nwarps);
     par ^= 1;
-    const float rstd2 = rsqrtf(q[0] * a.inv_c + a.eps);
+    const float rstd2 = rsqrtf(q2 * a.inv_c + a.eps);
     if (a.rstd2 && threadIdx.x == 0) a.rstd2[row] = rstd2;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       // the four lanes of an MX block are in range together: nvec is a multiple of 4 with FMT
       const bool in = v < a.nvec;
-      float y[8];
+      f2 o[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = s[j][e] * rstd2 * g2[j][e];
-      if (a.y && in) a.y[base + v] = pack8(y);
+      for (int e = 0; e < 4; ++e) o[e] = mul2(mul2(s[j][e], both(rstd2)), g2[j][e]);
+      if (a.y && in) a.y[base + v] = round8(o);
       if (FMT) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2(o[e], y[2 * e], y[2 * e + 1]);
         uint32_t am = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(y[e]) & 0x7FFFFFFFu);
@@ -273,32 +299,35 @@ struct JoinBwdArgs {
 // rows are registers, written once per block.  A thread copies its pieces of coming rows into its own
 // places of shared memory, DEPTH - 1 rows ahead (no thread reads another's).
 //
-// With dk = d where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none), all the
-// gradients of the branch come from two sums of dk x: over the rows S = sum gate_row rstd1 dk x, over the
-// row q = sum gg dk x.  With f = rb / (1 - p):
+// Instructions bound it before memory does, so the sums over a row are arranged to need one barrier.  With
+// e = dh + rstd2 u, xk = x where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none):
+//   d = e + c h,  c = -rstd2^3 mean(u h)
+//   q = sum gg xk d = sum gg xk e + c sum gg xk h
+// and all the gradients of the branch come from q and, over the rows, S = sum gate_row rstd1 xk d.  With
+// f = rb / (1 - p):
 //   dgamma1 = f gate_col S    dgate_col = f gamma1 S    dgate_row = f rstd1 q
-//   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C)
+//   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C),  dk = d where it is kept, else 0
 template <int V, int DEPTH, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwdArgs a) {
   extern __shared__ uint4 s_row[];  // [DEPTH][4][V][blockDim]
-  __shared__ float s_sum[2][1][32];
+  __shared__ float s_sum[2][3][16];
   const int nwarps = blockDim.x >> 5;
   Key key{};
   if (a.drop.rng) key = load_key(a.drop);
-  float sum_b[V][8], sum_2[V][8], gg[V][8], g2[V][8];
+  f2 sum_b[V][4], sum_2[V][4], gg[V][4], g2[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
     load_factors(a.gamma1, v, a.nvec, gg[j]);
     load_factors(a.gamma2, v, a.nvec, g2[j]);
     if (a.gate_col) {
-      float c[8];
+      f2 c[4];
       load_factors(a.gate_col, v, a.nvec, c);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) gg[j][e] *= c[e];
+      for (int e = 0; e < 4; ++e) gg[j][e] = mul2(gg[j][e], c[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum_b[j][e] = sum_2[j][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) sum_b[j][e] = sum_2[j][e] = both(0.0f);
   }
   auto place = [&](int slot, int which, int j) {
     return s_row + ((slot * 4 + which) * V + j) * blockDim.x + threadIdx.x;
@@ -331,117 +360,106 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
   };
 #pragma unroll
   for (int i = 0; i < DEPTH - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+  const float f = a.rb * a.drop.inv;
   int par = 0, slot = 0;
-  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
-    const int64_t base = row * a.nvec;
+  float rstd1_next, rstd2_next, gate_next;
+  auto fetch_row = [&](int64_t row) {
+    const bool in = row < a.R;
+    rstd1_next = a.gamma1 && in ? __ldg(a.rstd1 + row) : 1.0f;
+    rstd2_next = a.gamma2 && in ? __ldg(a.rstd2 + row) : 0.0f;
+    gate_next = a.gate_row && in ? __ldg(a.gate_row + row) : 1.0f;
+  };
+  fetch_row(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, par ^= 1) {
+    const int64_t base = row * a.nvec + threadIdx.x;
+    const float rstd1 = rstd1_next, rstd2 = rstd2_next, scale = gate_next * rstd1_next;
+    fetch_row(row + gridDim.x);
     fetch(row + (int64_t)(DEPTH - 1) * gridDim.x, slot == 0 ? DEPTH - 1 : slot - 1);
     uint32_t keep[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
-    const float rstd1 = a.gamma1 ? __ldg(a.rstd1 + row) : 1.0f, rstd2 = a.gamma2 ? __ldg(a.rstd2 + row) : 0.0f;
-    const float gate = a.gate_row ? __ldg(a.gate_row + row) : 1.0f;
+    for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + j * blockDim.x, a.drop, key) : 0xFFu;
     cp_async_wait<DEPTH - 1>();
-    // d = dh + rstd2 u + c h, with the sum over the row in c
-    float c = 0.0f;
-    if (a.gamma2) {
-      float q[1] = {0.0f};
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float hv[8], dy[8];
-        unpack8(*place(slot, 0, j), hv);
-        unpack8(*place(slot, 1, j), dy);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float t = dy[e] * hv[e];
-          sum_2[j][e] = fmaf(t, rstd2, sum_2[j][e]);
-          q[0] = fmaf(t, g2[j][e], q[0]);
-        }
-      }
-      block_sums(q, s_sum[par], nwarps);
-      par ^= 1;
-      c = -rstd2 * rstd2 * (q[0] * rstd2 * a.inv_c);
-    }
-    const float scale = gate * rstd1;
-    float dk[V][8];
-    float q[1] = {0.0f};
+    f2 e[V][4], t_uh = both(0.0f), t_xe = t_uh, t_xh = t_uh;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int v = threadIdx.x + j * blockDim.x;
-      float d[8], x[8];
-      unpack8(*place(slot, 2, j), d);
-      if (a.gamma2) {
-        float hv[8], dy[8];
-        unpack8(*place(slot, 0, j), hv);
-        unpack8(*place(slot, 1, j), dy);
+      f2 hv[4], dy[4], x[4];
+      unpack2(*place(slot, 0, j), hv);
+      unpack2(*place(slot, 1, j), dy);
+      unpack2(*place(slot, 2, j), e[j]);
+      unpack2(*place(slot, 3, j), x);
+      if (a.drop.rng) keep_only(x, keep[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = fmaf(c, hv[e], fmaf(dy[e] * g2[j][e], rstd2, d[e]));
-      }
-      if (a.dres && v < a.nvec) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = a.ra * d[e];
-        a.dres[base + v] = pack8(o);
-      }
-      unpack8(*place(slot, 3, j), x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool kept = (keep[j] >> e) & 1u;
-        const float t = kept ? d[e] * x[e] : 0.0f;
-        dk[j][e] = kept ? gg[j][e] * d[e] : 0.0f;
-        sum_b[j][e] = fmaf(t, scale, sum_b[j][e]);
-        q[0] = fmaf(t, gg[j][e], q[0]);
+      for (int i = 0; i < 4; ++i) {
+        const f2 u = mul2(dy[i], g2[j][i]), gx = mul2(x[i], gg[j][i]);
+        sum_2[j][i] = fma2(mul2(dy[i], hv[i]), both(rstd2), sum_2[j][i]);
+        e[j][i] = fma2(u, both(rstd2), e[j][i]);
+        t_uh = fma2(u, hv[i], t_uh);
+        t_xe = fma2(gx, e[j][i], t_xe);
+        t_xh = fma2(gx, hv[i], t_xh);
       }
     }
-    const float f = a.rb * a.drop.inv;
-    float m = 0.0f;
-    if (a.gamma1 || a.dgate_row) {
-      block_sums(q, s_sum[par], nwarps);
-      par ^= 1;
-      if (a.dgate_row && threadIdx.x == 0) a.dgate_row[row] = f * rstd1 * q[0];
-      m = a.gamma1 ? -rstd1 * rstd1 * (q[0] * a.inv_c) : 0.0f;
-    }
+    float q[3] = {sum2(t_uh), sum2(t_xe), sum2(t_xh)};
+    block_sums(q, s_sum[par], nwarps);
+    const float c = -rstd2 * rstd2 * (q[0] * rstd2 * a.inv_c);
+    const float qx = fmaf(c, q[2], q[1]);
+    if (a.dgate_row && threadIdx.x == 0) a.dgate_row[row] = f * rstd1 * qx;
+    const float m = a.gamma1 ? -rstd1 * rstd1 * (qx * a.inv_c) : 0.0f, fs = f * scale;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int v = threadIdx.x + j * blockDim.x;
-      if (v < a.nvec) {
-        float o[8];
-        if (a.gamma1) {
-          float x[8];
-          unpack8(*place(slot, 3, j), x);
+      const bool in = threadIdx.x + j * blockDim.x < a.nvec;
+      f2 hv[4], x[4], o[4];
+      unpack2(*place(slot, 0, j), hv);
+      unpack2(*place(slot, 3, j), x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = f * scale * fmaf(x[e], m, dk[j][e]);
-        } else {
+      for (int i = 0; i < 4; ++i) e[j][i] = fma2(both(c), hv[i], e[j][i]);  // d
+      if (a.dres && in) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = f * scale * dk[j][e];
-        }
-        a.dx[base + v] = pack8(o);
+        for (int i = 0; i < 4; ++i) o[i] = mul2(both(a.ra), e[j][i]);
+        a.dres[base + j * blockDim.x] = round8(o);
       }
+      if (a.drop.rng) keep_only(e[j], keep[j]);  // dk
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = mul2(gg[j][i], e[j][i]);
+      if (a.gamma1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], both(m), o[i]);
+      } else if (a.drop.rng) {
+        keep_only(x, keep[j]);  // (with the norm a value that is not finite has the whole row)
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum_b[j][i] = fma2(mul2(e[j][i], x[i]), both(scale), sum_b[j][i]);
+        o[i] = mul2(both(fs), o[i]);
+      }
+      if (in) a.dx[base + j * blockDim.x] = round8(o);
     }
     if (++slot == DEPTH) slot = 0;
   }
-  const float f = a.rb * a.drop.inv;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
     if (v < a.nvec) {
       const int64_t plane = (int64_t)gridDim.x * a.nvec * 2;
       float4* p = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.nvec + v) * 2;
-      auto put = [&](float4* dst, const float (&o)[8]) {
-        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+      auto put = [&](float4* dst, const f2 (&o)[4]) {
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2(o[e], w[2 * e], w[2 * e + 1]);
+        dst[0] = make_float4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_float4(w[4], w[5], w[6], w[7]);
       };
-      float fac[8];
+      f2 fac[4];
       if (a.gamma1) {
         load_factors(a.gate_col, v, a.nvec, fac);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) fac[e] *= f * sum_b[j][e];
+        for (int e = 0; e < 4; ++e) fac[e] = mul2(fac[e], mul2(both(f), sum_b[j][e]));
         put(p, fac);
       }
       if (a.gamma2) put(p + plane, sum_2[j]);
       if (a.gate_col) {
         load_factors(a.gamma1, v, a.nvec, fac);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) fac[e] *= f * sum_b[j][e];
+        for (int e = 0; e < 4; ++e) fac[e] = mul2(fac[e], mul2(both(f), sum_b[j][e]));
         put(p + 2 * plane, fac);
       }
     }
