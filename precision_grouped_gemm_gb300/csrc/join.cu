@@ -41,21 +41,28 @@ __device__ __forceinline__ float block_sum(float v, float* s, int nwarps) {
   return v;
 }
 
-// The same for three sums at once.
-__device__ __forceinline__ void block_sums(float (&v)[3], float (*s)[16], int nwarps) {
+// The same for up to four sums at once: the first two steps halve the sums that a lane carries, so that
+// five steps of one value each are left of four times five.
+__device__ __forceinline__ void block_sums(float (&v)[4], float (*s)[16], int nwarps) {
+  const int lane = threadIdx.x & 31;
+  const bool h = lane & 16, l = lane & 8;
+  float a = h ? v[2] : v[0], b = h ? v[3] : v[1];
+  a += __shfl_xor_sync(0xffffffffu, h ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xffffffffu, h ? v[1] : v[3], 16);
+  float c = l ? b : a;
+  c += __shfl_xor_sync(0xffffffffu, l ? a : b, 8);  // the sum number lane / 8
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-    if ((threadIdx.x & 31) == 0) s[i][threadIdx.x >> 5] = v[i];
-  }
+  for (int d = 4; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+  if ((lane & 7) == 0) s[lane >> 3][threadIdx.x >> 5] = c;
   __syncthreads();
+  // lane 8 i + k adds the sums i of the warps k and k + 8
+  const int k = lane & 7;
+  c = k < nwarps ? s[lane >> 3][k] : 0.0f;
+  if (nwarps > 8) c += k + 8 < nwarps ? s[lane >> 3][k + 8] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    v[i] = (threadIdx.x & 15) < nwarps ? s[i][threadIdx.x & 15] : 0.0f;
+  for (int d = 4; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, 8 * i);
 }
 
 struct Drop {
@@ -310,8 +317,9 @@ struct JoinBwdArgs {
 template <int V, int DEPTH, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwdArgs a) {
   extern __shared__ uint4 s_row[];  // [DEPTH][4][V][blockDim]
-  __shared__ float s_sum[2][3][16];
+  __shared__ float s_sum[2][4][16];
   const int nwarps = blockDim.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Key key{};
   if (a.drop.rng) key = load_key(a.drop);
   f2 sum_b[V][4], sum_2[V][4], gg[V][4], g2[V][4];
@@ -329,30 +337,29 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum_b[j][e] = sum_2[j][e] = both(0.0f);
   }
-  auto place = [&](int slot, int which, int j) {
-    return s_row + ((slot * 4 + which) * V + j) * blockDim.x + threadIdx.x;
-  };
+  constexpr int kRow = 4 * V;
+  uint4* mine = s_row + threadIdx.x;  // place i of a row: mine[i * blockDim.x]
   // places that no row is copied to read as zeros: those past the row's end, and of operands that are not given
 #pragma unroll
-  for (int i = 0; i < DEPTH * 4; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool given = i % 4 == 3 || (i % 4 == 2 ? a.dh != nullptr : a.gamma2 != nullptr);
-      if (!given || threadIdx.x + j * blockDim.x >= a.nvec) *place(0, i, j) = make_uint4(0, 0, 0, 0);
-    }
+  for (int i = 0; i < DEPTH * kRow; ++i) {
+    const int which = i % kRow / V, j = i % V;
+    const bool given = which == 3 || (which == 2 ? a.dh != nullptr : a.gamma2 != nullptr);
+    if (!given || threadIdx.x + j * blockDim.x >= a.nvec) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+  }
   auto fetch = [&](int64_t row, int slot) {
     if (row < a.R) {
-      const int64_t base = row * a.nvec;
+      const uint32_t step = blockDim.x * 16, dst = smem_u32(mine) + slot * kRow * step;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int v = threadIdx.x + j * blockDim.x;
+        const int64_t at = row * a.nvec + v;
         if (v < a.nvec) {
           if (a.gamma2) {
-            cp_async_16(smem_u32(place(slot, 0, j)), a.h + base + v);
-            cp_async_16(smem_u32(place(slot, 1, j)), a.dy + base + v);
+            cp_async_16(dst + j * step, a.h + at);
+            cp_async_16(dst + (V + j) * step, a.dy + at);
           }
-          if (a.dh) cp_async_16(smem_u32(place(slot, 2, j)), a.dh + base + v);
-          cp_async_16(smem_u32(place(slot, 3, j)), a.x + base + v);
+          if (a.dh) cp_async_16(dst + (2 * V + j) * step, a.dh + at);
+          cp_async_16(dst + (3 * V + j) * step, a.x + at);
         }
       }
     }
@@ -379,14 +386,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
 #pragma unroll
     for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + j * blockDim.x, a.drop, key) : 0xFFu;
     cp_async_wait<DEPTH - 1>();
+    const uint4* cur = mine + slot * kRow * blockDim.x;
     f2 e[V][4], t_uh = both(0.0f), t_xe = t_uh, t_xh = t_uh;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       f2 hv[4], dy[4], x[4];
-      unpack2(*place(slot, 0, j), hv);
-      unpack2(*place(slot, 1, j), dy);
-      unpack2(*place(slot, 2, j), e[j]);
-      unpack2(*place(slot, 3, j), x);
+      unpack2(cur[j * blockDim.x], hv);
+      unpack2(cur[(V + j) * blockDim.x], dy);
+      unpack2(cur[(2 * V + j) * blockDim.x], e[j]);
+      unpack2(cur[(3 * V + j) * blockDim.x], x);
       if (a.drop.rng) keep_only(x, keep[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
         t_xh = fma2(gx, hv[i], t_xh);
       }
     }
-    float q[3] = {sum2(t_uh), sum2(t_xe), sum2(t_xh)};
+    float q[4] = {sum2(t_uh), sum2(t_xe), sum2(t_xh), 0.0f};
     block_sums(q, s_sum[par], nwarps);
     const float c = -rstd2 * rstd2 * (q[0] * rstd2 * a.inv_c);
     const float qx = fmaf(c, q[2], q[1]);
@@ -408,8 +416,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
     for (int j = 0; j < V; ++j) {
       const bool in = threadIdx.x + j * blockDim.x < a.nvec;
       f2 hv[4], x[4], o[4];
-      unpack2(*place(slot, 0, j), hv);
-      unpack2(*place(slot, 3, j), x);
+      unpack2(cur[j * blockDim.x], hv);
+      unpack2(cur[(3 * V + j) * blockDim.x], x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) e[j][i] = fma2(both(c), hv[i], e[j][i]);  // d
       if (a.dres && in) {
@@ -466,8 +474,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
   }
 }
 
-// Columns of the three sums: n partial rows each, added in a fixed order; a block has eight columns
-// (a 32-byte sector of each row) of one of them.
+// Columns of the three sums: n partial rows each, added in a fixed order; a block has 32 columns of one of
+// them, each warp every 16th row.  It is launched while the kernel above runs and waits for its rows.
 struct JoinReduce {
   const float* part;
   int n, C;
@@ -476,25 +484,24 @@ struct JoinReduce {
 };
 constexpr int kReduceThreads = 512;
 __global__ void __launch_bounds__(kReduceThreads) join_reduce_kernel(const JoinReduce a) {
-  constexpr int kWarps = kReduceThreads / 32, kGroups = kReduceThreads / 8;
-  __shared__ float s[kWarps][8];
-  const int c = threadIdx.x & 7, i0 = threadIdx.x >> 3, w = threadIdx.x >> 5;
+  constexpr int kWarps = kReduceThreads / 32;
+  __shared__ float s[kWarps][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   const int which = a.which[blockIdx.y];
-  const float* p = a.part + (int64_t)which * a.n * a.C + blockIdx.x * 8 + c;
+  const float* p = a.part + (int64_t)which * a.n * a.C + c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float t = 0.0f;
-#pragma unroll 4
-  for (int i = i0; i < a.n; i += kGroups) t += p[(int64_t)i * a.C];
-  t += __shfl_xor_sync(0xffffffffu, t, 8);
-  t += __shfl_xor_sync(0xffffffffu, t, 16);
-  if ((threadIdx.x & 31) < 8) s[w][c] = t;
+  if (c < a.C) {
+#pragma unroll 8
+    for (int i = w; i < a.n; i += kWarps) t += p[(int64_t)i * a.C];
+  }
+  s[w][lane] = t;
   __syncthreads();
-  if (w == 0) {
+  if (w == 0 && c < a.C) {
     t = 0.0f;
-    for (int k = threadIdx.x >> 3; k < kWarps; k += 4) t += s[k][c];
-    t += __shfl_xor_sync(0xffffffffu, t, 8);
-    t += __shfl_xor_sync(0xffffffffu, t, 16);
-    if (threadIdx.x < 8) a.out[which][blockIdx.x * 8 + c] = t;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) t += s[k][lane];
+    a.out[which][c] = t;
   }
 }
 
@@ -619,22 +626,22 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
                 col ? static_cast<const uint4*>(gate) : nullptr, make_drop(rng, p), R, nvec, 1.0f / (float)C,
                 residual_scale, branch_scale, static_cast<uint4*>(dx), static_cast<uint4*>(dresidual),
                 col ? nullptr : dgate, static_cast<float*>(ws)};
-  auto kern = V == 1 ? join_bwd_kernel<1, 3, 256, 3> : V == 2 ? join_bwd_kernel<2, 3, 512, 1> : join_bwd_kernel<4, 1, 512, 1>;
-  const int depth = V == 4 ? 1 : 3;
-  const size_t row = (size_t)4 * V * threads * sizeof(uint4);
+  auto kern = V == 1 ? join_bwd_kernel<1, 3, 256, 3> : V == 2 ? join_bwd_kernel<2, 2, 512, 1> : join_bwd_kernel<4, 1, 512, 1>;
+  const int depth = V == 4 ? 1 : V == 2 ? 2 : 3;
+  const size_t smem = (size_t)depth * 4 * V * threads * sizeof(uint4);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)(depth * 4 * V * 512 * sizeof(uint4)));
   static std::atomic<int> resident[5][17];
   std::atomic<int>& known = resident[V][threads / 32];
   int per_sm = known.load(std::memory_order_relaxed);
   if (e == cudaSuccess && per_sm == 0) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, depth * row);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
     per_sm = std::max(1, per_sm);
     if (e == cudaSuccess) known.store(per_sm, std::memory_order_relaxed);
   }
   if (e != cudaSuccess) return cuda_status(e);
   const int grid = std::min(bwd_blocks(R, nvec), dev.sms * per_sm);
-  kern<<<grid, threads, depth * row, s>>>(a);
+  kern<<<grid, threads, smem, s>>>(a);
   if ((st = cuda_status(cudaGetLastError()))) return st;
   JoinReduce r{a.part, grid, (int)C, {dgamma_post, dgamma, col ? dgate : nullptr}, {0, 0, 0}};
   int sums = 0;
@@ -642,7 +649,7 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
     if (r.out[i]) r.which[sums++] = i;
   if (!sums) return PGG_OK;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)nvec, (unsigned)sums);
+  cfg.gridDim = dim3((unsigned)((C + 31) / 32), (unsigned)sums);
   cfg.blockDim = dim3(kReduceThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};

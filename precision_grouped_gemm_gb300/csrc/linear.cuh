@@ -149,6 +149,14 @@ __device__ __forceinline__ void add_acc(uint32_t taddr, float (&v)[32]) {
 
 template <int ACT, bool FAST>
 __device__ __forceinline__ void apply_act(float (&v)[32], const ActForm& f) {
+  if (ACT == kActGelu && FAST) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const f2 z = make2(v[j], v[j + 1]);
+      split2(mul2(z, normal_cdf_f2(z, gauss_f2(z))), v[j], v[j + 1]);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] = act_f<ACT, FAST>(v[j], f);
 }

@@ -14,6 +14,7 @@
 
 #include "act.cuh"
 #include "block.cuh"
+#include "packed.cuh"
 #include "sched.cuh"
 
 namespace pgg {
@@ -95,11 +96,11 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) linear_bwd_kernel(const LinB
   for (int64_t r0 = r_begin; r0 < r_end; ++g) {
     const int64_t r1 = min(r_end, (int64_t)s_off[g + 1]);
     if (r1 <= r0) continue;  // an empty group
-    float sum[H][8];
+    f2 sum[H][4];
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[h][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) sum[h][e] = both(0.0f);
     if (in) {
       for (int64_t r = r0 + warp; r < r1; r += (int64_t)kWarps * UNROLL) {
         uint4 dy[UNROLL], z[UNROLL], u[UNROLL];
@@ -116,20 +117,20 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) linear_bwd_kernel(const LinB
         for (int i = 0; i < UNROLL; ++i) {
           const int64_t row = r + i * kWarps;
           if (row < r1) {
-            float d[8], zz[8], uu[8], o[8], o2[8];
-            unpack8(dy[i], d);
-            if (ACT != kActNone) unpack8(z[i], zz);
-            if (GATED) unpack8(u[i], uu);
+            f2 d[4], zz[4], uu[4], o[4], o2[4];
+            unpack2(dy[i], d);
+            if (ACT != kActNone) unpack2(z[i], zz);
+            if (GATED) unpack2(u[i], uu);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (GATED) swiglu_bwd_f(d[e], zz[e], uu[e], a.form, o[e], o2[e]);
-              else o[e] = ACT == kActNone ? d[e] : act_bwd_f<ACT>(d[e], zz[e], a.form);
-              sum[0][e] += o[e];
-              if (GATED) sum[H - 1][e] += o2[e];
+            for (int e = 0; e < 4; ++e) {
+              if (GATED) swiglu_bwd_f2(d[e], zz[e], uu[e], a.form, o[e], o2[e]);
+              else o[e] = ACT == kActNone ? d[e] : act_bwd_f2<ACT>(d[e], zz[e], a.form);
+              sum[0][e] = add2(sum[0][e], o[e]);
+              if (GATED) sum[H - 1][e] = add2(sum[H - 1][e], o2[e]);
             }
             if (ACT != kActNone && a.dz) {
-              a.dz[row * H * a.nvec + v] = pack8(o);
-              if (GATED) a.dz[row * H * a.nvec + a.nvec + v] = pack8(o2);
+              a.dz[row * H * a.nvec + v] = round8(o);
+              if (GATED) a.dz[row * H * a.nvec + a.nvec + v] = round8(o2);
             }
           }
         }
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) linear_bwd_kernel(const LinB
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s_sum[warp][h * 8 + e][lane] = sum[h][e];
+      for (int e = 0; e < 4; ++e) split2(sum[h][e], s_sum[warp][h * 8 + 2 * e][lane], s_sum[warp][h * 8 + 2 * e + 1][lane]);
     __syncthreads();
     const bool first = s_off[g] < r_begin, last = s_off[g + 1] > r_end;  // divided before, behind this run
     float* dst = !first && !last ? a.db + (int64_t)g * N : a.part + (int64_t)(run * 2 + (first ? 0 : 1)) * N;
@@ -200,7 +201,10 @@ __global__ void __launch_bounds__(32 * kRedWarps) bias_grad_reduce_kernel(const 
 struct Cut {
   int nvec, per, slabs, runs, run_rows;
 };
-constexpr int per_sm(int act) { return act == kActSwiglu ? 3 : act == kActNone ? 5 : 3; }
+// Resident blocks an SM, with the rows that a thread loads ahead (UNROLL): 32768 x 5760 with swiglu, 944 MB, 4
+// blocks of one row 171 us, 3 of two 179, 5 of one (fewer registers than it needs) 208; gelu 4 of two 146, 3 of
+// four 148, 5 of two 160; silu 3 of four 156, 4 of two 159.
+constexpr int per_sm(int act) { return act == kActNone ? 5 : act == kActSilu ? 3 : 4; }
 Cut cut(int64_t M, int64_t N, int act) {
   const int64_t width = act == kActSwiglu ? N / 2 : N;
   Cut c;
@@ -268,8 +272,8 @@ int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_l
   switch (act) {
     case PGG_ACT_NONE: linear_bwd_kernel<kActNone, 4, per_sm(kActNone)><<<grid, kThreads, smem, s>>>(a); break;
     case PGG_ACT_SILU: linear_bwd_kernel<kActSilu, 4, per_sm(kActSilu)><<<grid, kThreads, smem, s>>>(a); break;
-    case PGG_ACT_GELU: linear_bwd_kernel<kActGelu, 4, per_sm(kActGelu)><<<grid, kThreads, smem, s>>>(a); break;
-    default: linear_bwd_kernel<kActSwiglu, 2, per_sm(kActSwiglu)><<<grid, kThreads, smem, s>>>(a);
+    case PGG_ACT_GELU: linear_bwd_kernel<kActGelu, 2, per_sm(kActGelu)><<<grid, kThreads, smem, s>>>(a); break;
+    default: linear_bwd_kernel<kActSwiglu, 1, per_sm(kActSwiglu)><<<grid, kThreads, smem, s>>>(a);
   }
   if ((st = cuda_status(cudaGetLastError()))) return st;
   cudaLaunchConfig_t cfg{};
