@@ -10,6 +10,15 @@ the MX operand of its tokens itself.
     logits = y gate^T                          grouped_gemm_fwd with one group
     ids, w = top-k of the logits               moe_route
     out = sum_j w_j expert_{ids_j}(y)          moe_permute ... moe_combine, or moe_decode
+
+A block may have more parts, each left out unless it is given:
+
+    biases b1, b2 of the experts, and a SwiGLU g sigmoid(alpha g) (u + offset)     grouped_linear
+    a shared expert S1, S2 that every token takes, added to out                    grouped_linear
+    s = residual_scale residual + branch_scale gate dropout(rmsnorm(x) gamma_post) block_join
+
+with their gradients (grouped_linear_bwd, block_join_bwd).  The few-token layer has no biases: a block
+with them decodes the long way, on bf16 weights.
 """
 from __future__ import annotations
 
@@ -43,10 +52,26 @@ class MoeBlock:
     swiglu_limit: float = 0.0
     eps: float = 1e-6
     fmt: str = None            # decode weights: None (bf16), "e4m3" or "e2m1"
+    b1: torch.Tensor = None    # [E, 2I] bf16: the experts' biases
+    b2: torch.Tensor = None    # [E, H] bf16
+    alpha: float = 1.0         # of the SwiGLU, as in grouped_linear
+    offset: float = 0.0
+    S1: torch.Tensor = None    # [2S, H] bf16 (gate | up): a shared expert, with the same SwiGLU
+    S2: torch.Tensor = None    # [H, S] bf16
+    gamma_post: torch.Tensor = None  # [H] bf16: the norm of x before it joins the residual stream
+    residual_scale: float = 1.0
+    branch_scale: float = 1.0
+    dropout: float = 0.0       # of x, in training
 
     def __post_init__(self):
         E, I2, H = self.W1.shape
         self.sizes = E, H, I2 // 2
+        # (a form that the few-token layer and the fused expert products do not have)
+        self._biased = self.b1 is not None or self.b2 is not None or self.alpha != 1.0 or self.offset != 0.0
+        if self._biased and self.fmt is not None:
+            raise ValueError("MX decode weights go with neither biases nor alpha and offset")
+        if (self.S1 is None) != (self.S2 is None):
+            raise ValueError("a shared expert needs S1 and S2")
         self._mx = self._mx_of = self._ws = None
         self._err = torch.zeros(1, dtype=torch.int32, device=self.W1.device)
         self.quantize_weights()
@@ -59,37 +84,106 @@ class MoeBlock:
         ids, w = B.moe_route(logits, self.k, self.bias, self.score, self.renormalize, self.scale)
         return logits, ids, w
 
-    def forward(self, x, residual=None):
-        """-> (out [T,H], h [T,H]: the new residual stream, saved tensors for `backward`)."""
+    def _form(self):
+        return {"act": "swiglu", "alpha": self.alpha, "offset": self.offset, "limit": self.swiglu_limit}
+
+    def _joined(self, gate):
+        return (gate is not None or self.gamma_post is not None or self.residual_scale != 1.0 or self.branch_scale != 1.0
+                or self.dropout)
+
+    def _join(self, gate, rng=None):
+        """block_join's arguments besides the tensors that flow; rng None: no dropout."""
+        return {"gamma_post": self.gamma_post, "gamma": self.gamma, "gate": gate, "residual_scale": self.residual_scale,
+                "branch_scale": self.branch_scale, "p": 0.0 if rng is None else self.dropout, "rng": rng}
+
+    def _experts(self, Xs, lens, save, err=None):
+        """The experts' outputs for the permuted batch -> (Ys, A, Hs)."""
+        if self._biased:
+            A, Hs = B.grouped_linear(Xs, self.W1, lens, bias=self.b1, save_z=save, err=err, **self._form())
+            return B.grouped_linear(A, self.W2, lens, bias=self.b2, err=err)[0], A, Hs
+        A, Hs = B.grouped_fc1_swiglu(Xs, self.W1, lens, swiglu_limit=self.swiglu_limit, save_h=save, err=err)
+        return B.grouped_gemm_fwd(A, self.W2, lens, err=err), A, Hs
+
+    def _shared(self, y, out, save, err=None):
+        """Adds the shared expert's output to `out`, in place -> (As, Zs)."""
+        if self.S1 is None:
+            return None, None
+        As, Zs = B.grouped_linear(y, self.S1, save_z=save, err=err, **self._form())
+        B.grouped_linear(As, self.S2, residual=out, Y=out, err=err)
+        return As, Zs
+
+    def forward(self, x, residual=None, gate=None, rng=None):
+        """-> (out [T,H], h [T,H]: the new residual stream, saved tensors for `backward`).
+
+        gate: fp32 [T] or bf16 [H], of x; rng: int64 [2] on the device, (seed, offset) of the dropout, which
+        `backward` reads again."""
         E, _, _ = self.sizes
-        h, y, _, _, rstd = B.add_rmsnorm(x, residual, self.gamma, self.eps)
+        if self.dropout and rng is None:
+            raise ValueError("dropout needs rng")
+        if self._joined(gate):
+            h, y, _, _, rstd_post, rstd = B.block_join(x, residual, eps=self.eps, **self._join(gate, rng))
+        else:
+            rstd_post = None
+            h, y, _, _, rstd = B.add_rmsnorm(x, residual, self.gamma, self.eps)
         logits, ids, w = self._route(y)
         Xs, lens, pos = B.moe_permute(ids, y, E)
-        A, Hs = B.grouped_fc1_swiglu(Xs, self.W1, lens, swiglu_limit=self.swiglu_limit)
-        Ys = B.grouped_gemm_fwd(A, self.W2, lens)
-        return B.moe_combine(Ys, pos, w), h, (h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys)
+        Ys, A, Hs = self._experts(Xs, lens, True)
+        out = B.moe_combine(Ys, pos, w)
+        As, Zs = self._shared(y, out, True)
+        return out, h, (h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys, x, rstd_post, gate, rng, As, Zs)
 
     def backward(self, dout, dh, saved):
-        """Gradients of `forward` -> dict: dx (of x and of residual), dgamma, dgate, dW1, dW2."""
-        h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys = saved
+        """Gradients of `forward` -> dict: dx, dresidual (dx itself in a block that only adds the two), dgamma,
+        dgate, dW1, dW2, and of the parts that the block has: db1, db2, dS1, dS2, dgamma_post, and dgate_in of
+        forward's gate."""
+        h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys, x, rstd_post, gate, rng, As, Zs = saved
         one = self._one_group(y.shape[0], y.device)
+        g = {}
         dYs, dw = B.moe_combine_bwd(dout, Ys, pos, w)
-        dH = B.grouped_fc2_dgrad_swiglu_bwd(dYs, self.W2, Hs, lens, swiglu_limit=self.swiglu_limit)
-        dW2 = B.grouped_gemm_wgrad(A, dYs, lens)
-        dW1 = B.grouped_gemm_wgrad(Xs, dH, lens)
+        if self._biased:
+            dH, db1 = B.grouped_linear_bwd(B.grouped_gemm_dgrad(dYs, self.W2, lens), Hs, lens, **self._form())
+            if self.b1 is not None:
+                g["db1"] = db1
+            if self.b2 is not None:
+                g["db2"] = B.grouped_linear_bwd(dYs, group_lens=lens)[1]
+        else:
+            dH = B.grouped_fc2_dgrad_swiglu_bwd(dYs, self.W2, Hs, lens, swiglu_limit=self.swiglu_limit)
+        g["dW2"] = B.grouped_gemm_wgrad(A, dYs, lens)
+        g["dW1"] = B.grouped_gemm_wgrad(Xs, dH, lens)
         dy = B.moe_combine(B.grouped_gemm_dgrad(dH, self.W1, lens), pos)
+        if self.S1 is not None:
+            dZs, _ = B.grouped_linear_bwd(B.grouped_gemm_dgrad(dout, self.S2[None], one), Zs, **self._form())
+            g["dS2"] = B.grouped_gemm_wgrad(As, dout, one)[0]
+            g["dS1"] = B.grouped_gemm_wgrad(y, dZs, one)[0]
+            dy += B.grouped_gemm_dgrad(dZs, self.S1[None], one)
         dlogits = B.moe_route_bwd(logits, ids, dw, self.bias, self.score, self.renormalize, self.scale)
-        dgate = B.grouped_gemm_wgrad(y, dlogits, one)[0]
+        g["dgate"] = B.grouped_gemm_wgrad(y, dlogits, one)[0]
         dy += B.grouped_gemm_dgrad(dlogits, self.gate[None], one)
-        dx, dgamma = B.add_rmsnorm_bwd(dy, dh, h, self.gamma, rstd)
-        return {"dx": dx, "dgamma": dgamma, "dgate": dgate, "dW1": dW1, "dW2": dW2}
+        if self._joined(gate):
+            g["dx"], g["dresidual"], dgp, g["dgamma"], dgi = B.block_join_bwd(dy, dh, x, h, rstd_post, rstd,
+                                                                              **self._join(gate, rng))
+            if dgp is not None:
+                g["dgamma_post"] = dgp
+            if dgi is not None:
+                g["dgate_in"] = dgi
+        else:
+            g["dx"], g["dgamma"] = B.add_rmsnorm_bwd(dy, dh, h, self.gamma, rstd)
+            g["dresidual"] = g["dx"]
+        return g
 
-    def decode(self, x, residual=None, err=None):
-        """`forward` for up to 128 tokens, inference only -> (out, h).  A block has one workspace, so its
+    def decode(self, x, residual=None, err=None, gate=None):
+        """`forward` for up to 128 tokens, inference only (no dropout) -> (out, h).  A block has one workspace, so its
         decode calls run in the order of one stream.  err: the caller's error word; without one the block's
         own, which `check_decode` reads.  A first call inside a graph's capture has a workspace of the
         graph's, zeroed at every replay: call `prepare_decode` before the capture to avoid that."""
         err = self._err if err is None else err
+        if self._biased:
+            h, y, _, _ = self._entry(x, residual, gate)
+            _, ids, w = self._route(y)
+            Xs, lens, pos = B.moe_permute(ids, y, self.sizes[0], err=err)
+            out = B.moe_combine(self._experts(Xs, lens, False, err)[0], pos, w)
+            self._shared(y, out, False, err)
+            return out, h
         ws = self._ws
         if ws is None:
             # (memory of a graph's pool is the graph's: eager calls and other graphs get their own)
@@ -99,12 +193,20 @@ class MoeBlock:
             if not self._current():
                 # (a capture quantizes into its own memory, at every replay)
                 mx = self._quantized() if torch.cuda.is_current_stream_capturing() else self.quantize_weights()
-        h, y, codes, scales, _ = B.add_rmsnorm(x, residual, self.gamma, self.eps, fmt=self.fmt, save_rstd=False)
+        h, y, codes, scales = self._entry(x, residual, gate)
         _, ids, w = self._route(y)
         if self.fmt is None:
-            return B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=ws, err=err), h
-        return B.mx_moe_decode(self.fmt, codes, scales, ids, w, *mx, swiglu_limit=self.swiglu_limit, ws=ws,
-                               err=err), h
+            out = B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=ws, err=err)
+        else:
+            out = B.mx_moe_decode(self.fmt, codes, scales, ids, w, *mx, swiglu_limit=self.swiglu_limit, ws=ws, err=err)
+        self._shared(y, out, False, err)
+        return out, h
+
+    def _entry(self, x, residual, gate):
+        """What stands in front of a decoding block's gate -> (h, y, codes, scales)."""
+        if self._joined(gate):
+            return B.block_join(x, residual, eps=self.eps, fmt=self.fmt, save_rstd=False, **self._join(gate))[:4]
+        return B.add_rmsnorm(x, residual, self.gamma, self.eps, fmt=self.fmt, save_rstd=False)[:4]
 
     def _quantized(self, into=(None,) * 4):
         E, H, I = self.sizes
