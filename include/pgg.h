@@ -499,7 +499,8 @@ typedef enum { PGG_ACT_NONE = 0, PGG_ACT_SILU = 1, PGG_ACT_GELU = 2, PGG_ACT_SWI
  *   z = [g | u]: g sigmoid(alpha g) (u + offset), with limit > 0 g <- min(g, limit) and u <-
  *   clamp(u, -limit, limit) first.  alpha, offset and limit are not read where act has no use for them,
  *   but must be finite, limit >= 0.  alpha = 1, offset = 0 is the SwiGLU of pgg_grouped_fc1_swiglu.
- *   Z is fp32 up to Y; Z, Y are each rounded once.  N % 8 == 0 (swiglu: % 16), K % 8 == 0.
+ *   Z is fp32 up to Y; Z, Y are each rounded once.  N % 8 == 0 (swiglu: % 16), K % 8 == 0,
+ *   M <= 2^31 - 4097.
  * The result of a row does not depend on its group's other rows beyond the order in which K is summed
  * up, which follows the sizes of the call; it is deterministic. */
 int pgg_grouped_linear(const void* X, const void* W, const int32_t* group_lens, const void* bias, const void* residual,
@@ -515,7 +516,8 @@ int pgg_grouped_linear_bwd_workspace_size(int64_t M, int64_t N, int G, int act, 
  *   dY [M, N] bf16 (PGG_ACT_SWIGLU: [M, N/2]), Z [M, N] bf16 as saved; dZ [M, N] bf16 (out; NULL: the
  *   bias' gradient alone; may be Z, and dY where they have one shape); dbias [G, N] fp32 (out).
  *   PGG_ACT_NONE: Z and dZ are NULL (dZ is dY).  No gradient passes where a clamp is active.
- *   ws: device scratch, 16-byte aligned; it holds nothing between calls.  M == 0 writes dbias = 0.
+ *   ws: device scratch, 16-byte aligned; it holds nothing between calls, and calls that may overlap need
+ *   one each.  M == 0 writes dbias = 0.
  *   Bad group_lens set *err and write nothing. */
 int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_lens, void* dZ, float* dbias, int64_t M,
                            int64_t N, int G, int act, float alpha, float offset, float limit, void* ws,
@@ -565,7 +567,8 @@ int pgg_block_join_bwd_workspace_size(int64_t R, int64_t C, size_t* bytes);
  *   that call's.  dx [R, C] bf16; dresidual [R, C] bf16 or NULL; dgamma_post, dgamma [C], dgate [R] or
  *   [C] fp32, each given where its operand is, summed up in a fixed order.
  *   dx and dresidual may be dy, dh, x or h (not the same of them).  ws: device scratch, 16-byte
- *   aligned; it holds nothing between calls.  R == 0 writes zero sums. */
+ *   aligned; it holds nothing between calls, and calls that may overlap need one each.  R == 0 writes
+ *   zero sums. */
 int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void* h, const float* rstd_post,
                        const float* rstd, const void* gamma_post, const void* gamma, const void* gate, int gate_kind,
                        const int64_t* rng, int64_t R, int64_t C, double p, float residual_scale, float branch_scale,

@@ -653,6 +653,21 @@ def mx_moe_decode(fmt, X, SX, ids, w, W1, SW1, W2, SW2, out=None, swiglu_limit=0
     return out
 
 
+def _here(*ts):
+    """_dev, and on the current device, whose stream the call goes to."""
+    here = None
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("tensors must live on the CUDA device")
+            if here is None:
+                here = torch.cuda.current_device() if _raw_device is None else _raw_device()
+            if t.get_device() != here:
+                raise ValueError("tensors must live on the current CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+
+
 _ACT = {None: 0, "silu": 1, "gelu": 2, "swiglu": 3}
 
 
@@ -697,7 +712,7 @@ def grouped_linear(X, W, group_lens=None, bias=None, residual=None, act=None, al
     if save_z or Z is not None:
         Z, pz = _out(Z, "Z", _BF, (M, N), X.device, stream)
     pe = None if err is None else _in(err, "err", _I, err.shape)
-    _dev(*given)
+    _here(*given)
     _check(lib().pgg_grouped_linear(px, pw, pl, pb, pr, py, _DTYPE[out_dtype], pz, M, N, K, G, kind, alpha, offset, limit,
                                     pe, _stream(stream)), "pgg_grouped_linear")
     return Y, Z
@@ -732,7 +747,7 @@ def grouped_linear_bwd(dY, Z=None, group_lens=None, act=None, alpha=1.0, offset=
     if ws is None:
         ws = _new(torch.empty, max(16, grouped_linear_bwd_workspace_size(M, N, G, act)), _U8, dY.device, stream)
     pe = None if err is None else _in(err, "err", _I, err.shape)
-    _dev(*given)
+    _here(*given)
     _check(lib().pgg_grouped_linear_bwd(py, pz, pl, pd, pb, M, N, G, kind, alpha, offset, limit, *_scratch(ws), pe,
                                         _stream(stream)), "pgg_grouped_linear_bwd")
     return (dZ if kind else dY), dbias
@@ -791,7 +806,7 @@ def block_join(x, residual, gamma_post=None, gamma=None, gate=None, residual_sca
         rstd_post, pd1 = _out(rstd_post, "rstd_post", _F, (R,), dev, stream)
     if gamma is not None and (save_rstd or rstd is not None):
         rstd, pd2 = _out(rstd, "rstd", _F, (R,), dev, stream)
-    _dev(*given)
+    _here(*given)
     _check(lib().pgg_block_join(px, pr, p1, p2, pg, kind, pn, R, C, p, residual_scale, branch_scale, eps, f, ph, py, pc,
                                 ps, pd1, pd2, _stream(stream)), "pgg_block_join")
     return h, y, codes, scales, rstd_post, rstd
@@ -839,7 +854,7 @@ def block_join_bwd(dy, dh, x, h=None, rstd_post=None, rstd=None, gamma_post=None
         dgate, pdg = _out(dgate, "dgate", _F, gate.shape, dev, stream)
     if ws is None:
         ws = _new(torch.empty, max(16, block_join_bwd_workspace_size(R, C)), _U8, dev, stream)
-    _dev(*given)
+    _here(*given)
     _check(lib().pgg_block_join_bwd(py, pd, px, ph, q1, q2, p1, p2, pg, kind, pn, R, C, p, residual_scale, branch_scale,
                                     pdx, pdr, pd1, pd2, pdg, *_scratch(ws), _stream(stream)), "pgg_block_join_bwd")
     return dx, dresidual, dgamma_post, dgamma, dgate

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     mbar_init(smem_u32(drain), 1);
     s_ctl->abort = 0;
-    s_ctl->limit_ns = a.wait_ns ? a.wait_ns : kWaitTimeoutNs;
+    s_ctl->limit_ns = a.wait_ns;
     fence_mbar_init();
     fence_proxy_async_smem();
     prefetch_tmap(&tmW);
@@ -323,7 +323,7 @@ int linear_impl(const void* X, const void* W, const int32_t* group_lens, const v
                 float offset, float limit, unsigned long long wait_ns, long long stall_at, int32_t* err,
                 void* stream) {
   if (G < 1 || G > kMaxGroups || (!group_lens && G != 1)) return PGG_ERR_INVALID_ARG;
-  if (M < 0 || M >= ((int64_t)1 << 31)) return PGG_ERR_INVALID_ARG;
+  if (M < 0 || M > INT32_MAX - 4096) return PGG_ERR_INVALID_ARG;
   if (act < PGG_ACT_NONE || act > PGG_ACT_SWIGLU) return PGG_ERR_INVALID_ARG;
   if (dtype != PGG_DTYPE_F32 && dtype != PGG_DTYPE_BF16) return PGG_ERR_INVALID_ARG;
   const int mult = act == PGG_ACT_SWIGLU ? 16 : 8;
@@ -341,6 +341,8 @@ int linear_impl(const void* X, const void* W, const int32_t* group_lens, const v
   DeviceInfo dev;
   int st = current_device(&dev);
   if (st != PGG_OK) return st;
+  // (a tile's loads are waited for in one piece by its epilogue: the longest reductions need more than the default)
+  if (wait_ns == 0) wait_ns = kWaitTimeoutNs + 2000ull * (unsigned long long)ceil_div(K, kBK);
   LinCall c{X, W, {}, dtype == PGG_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)};
   c.a = {group_lens, G, M, (int)N, (int)K, (int)(act == PGG_ACT_SWIGLU ? N / 2 : N), act, {alpha, offset, limit},
          static_cast<const __nv_bfloat16*>(bias), residual, Y, static_cast<__nv_bfloat16*>(Z), err, wait_ns, stall_at};

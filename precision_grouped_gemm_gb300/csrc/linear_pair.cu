@@ -95,7 +95,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(smem_u32(drain), 1);
     s_ctl->abort = 0;
-    s_ctl->limit_ns = a.wait_ns ? a.wait_ns : kWaitTimeoutNs;
+    s_ctl->limit_ns = a.wait_ns;
     fence_mbar_init();
     fence_proxy_async_smem();
     prefetch_tmap(&tmW);

@@ -19,7 +19,8 @@ constexpr int kMaxStages = 12;
 // CTAs than SMs two share an SM, else one has it, so that its whole run of K can be in flight at once.
 constexpr int kSmemTwo = 112 * 1024, kSmemOne = 216 * 1024, kSmemLeast = 80 * 1024;  // (at most two an SM)
 // Columns of tensor memory a CTA may take: where two CTAs are resident on an SM, one that waited for columns
-// of another cluster's CTA, which waits for its own cluster, would wait for ever.
+// of another cluster's CTA, which waits for its own cluster, would wait for ever.  (No other kernel here whose
+// CTAs wait for one another fits beside kSmemLeast.)
 constexpr int kColsTwo = 256;
 
 struct SplitArgs {
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kLinThreads)
     }
     mbar_init(smem_u32(done), 1);
     s_ctl->abort = 0;
-    s_ctl->limit_ns = a.wait_ns ? a.wait_ns : kWaitTimeoutNs;
+    s_ctl->limit_ns = a.wait_ns;
     fence_mbar_init();
     fence_proxy_async_smem();
     prefetch_tmap(&tmW);

@@ -341,3 +341,37 @@ def test_linear_long_groups(lens, act):
         again, z2 = pgg.grouped_linear(X.to(DEV), W.to(DEV), torch.from_numpy(lens).to(DEV), bias=_dev(b), residual=_dev(r),
                                        act=act, save_z=True, **FORMS[act])
         assert torch.equal(Y, again) and torch.equal(Z, z2)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    from precision_grouped_gemm_gb300 import _binding
+    x, w = torch.ones(2, 64, dtype=BF, device=DEV), torch.ones(32, 64, dtype=BF, device=DEV)
+    pgg.grouped_linear(x, w)
+    monkeypatch.setattr(_binding, "_raw_device", lambda: 1)   # as if another device were the current one
+    for call in (lambda: pgg.grouped_linear(x, w), lambda: pgg.grouped_linear_bwd(x), lambda: pgg.block_join(x, x),
+                 lambda: pgg.block_join_bwd(None, x, x)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
+def test_linear_on_four_streams_at_once():
+    # calls of every kernel (few rows, short and long groups, both types) that overlap
+    cases = []
+    for i, (M, N, K, G, act, out) in enumerate([(1, 2048, 2048, 1, None, BF), (40, 1024, 2048, 1, "swiglu", BF),
+                                                (700, 512, 512, 5, "gelu", BF), (3000, 1024, 512, 2, "swiglu", BF),
+                                                (37, 256, 2048, 1, None, torch.float32), (900, 512, 512, 3, "silu", torch.float32)]):
+        lens = _split(np.random.default_rng(i), M, G)
+        X, W, b, r = (_dev(t) for t in _inputs(M, N, K, lens, i, act=act, out=out))
+        gl = torch.from_numpy(lens).to(DEV)
+        kw = dict(bias=b, residual=r, act=act, out_dtype=out, **FORMS[act])
+        cases.append((X, W, gl, kw, pgg.grouped_linear(X, W, gl, **kw)[0]))
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for n in range(30):
+        for j, s in enumerate(streams):
+            X, W, gl, kw, ref = cases[(n + j) % len(cases)]
+            with torch.cuda.stream(s):
+                got.append((pgg.grouped_linear(X, W, gl, **kw)[0], ref))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
