@@ -158,41 +158,42 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) linear_bwd_kernel(const LinB
   }
 }
 
-// db_g of the groups that runs divide, and zeros for the empty ones: a block has 32 columns and walks
-// the groups with a stride; 16 warps share out the runs of a group.
+// db_g of the groups that runs divide, and zeros for the empty ones, launched while the kernel above runs.
+// A warp has 32 columns; SHARE: the block's warps share out the runs of one group (few long groups), else each
+// warp has groups of its own (32 groups of 1092 rows, 5760 columns: 4 us instead of 15.6).
 constexpr int kRedWarps = 16;
+template <bool SHARE>
 __global__ void __launch_bounds__(32 * kRedWarps) bias_grad_reduce_kernel(const int32_t* __restrict__ offs,
                                                                           const float* __restrict__ part, int G,
                                                                           int run_rows, int64_t N,
                                                                           float* __restrict__ db) {
-  __shared__ float s[kRedWarps][32];
+  __shared__ float s[SHARE ? kRedWarps : 1][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (offs[G + 1]) return;
-  for (int g = blockIdx.y; g < G; g += gridDim.y) {
+  const int step = SHARE ? 1 : kRedWarps;
+  for (int g = blockIdx.y * step + (SHARE ? 0 : warp); g < G; g += gridDim.y * step) {
     const int o0 = offs[g], o1 = offs[g + 1];
     const int p0 = o0 / run_rows, p1 = (o1 - 1) / run_rows;
-    if (o0 == o1) {
-      if (warp == 0 && c < N) db[(int64_t)g * N + c] = 0.0f;
-      continue;
-    }
-    if (p0 == p1) continue;
+    if (o0 != o1 && p0 == p1) continue;
     float t = 0.0f;
-    if (c < N) {
+    if (c < N && o0 != o1) {
 #pragma unroll 4
-      for (int p = p0 + warp; p <= p1; p += kRedWarps)
+      for (int p = p0 + (SHARE ? warp : 0); p <= p1; p += SHARE ? kRedWarps : 1)
         t += part[(int64_t)(p * 2 + (o0 < p * run_rows ? 0 : 1)) * N + c];
     }
-    s[warp][lane] = t;
-    __syncthreads();
-    if (warp == 0 && c < N) {
+    if (SHARE) {
+      s[warp][lane] = t;
+      __syncthreads();
       t = 0.0f;
+      if (warp == 0) {
 #pragma unroll
-      for (int w = 0; w < kRedWarps; ++w) t += s[w][lane];
-      db[(int64_t)g * N + c] = t;
+        for (int w = 0; w < kRedWarps; ++w) t += s[SHARE ? w : 0][lane];
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    if ((!SHARE || warp == 0) && c < N) db[(int64_t)g * N + c] = t;
   }
 }
 
@@ -277,7 +278,8 @@ int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_l
   }
   if ((st = cuda_status(cudaGetLastError()))) return st;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((N + 31) / 32), (unsigned)std::min(G, 16));
+  const bool share = c.runs > 4 * G;
+  cfg.gridDim = dim3((unsigned)((N + 31) / 32), (unsigned)(share ? std::min(G, 16) : (G + kRedWarps - 1) / kRedWarps));
   cfg.blockDim = dim3(32 * kRedWarps);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -285,7 +287,8 @@ int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_l
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, bias_grad_reduce_kernel, (const int32_t*)offs, (const float*)part, G,
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, share ? bias_grad_reduce_kernel<true> : bias_grad_reduce_kernel<false>,
+                                           (const int32_t*)offs, (const float*)part, G,
                                            c.run_rows, N, dbias);
   return cuda_status(e != cudaSuccess ? e : cudaGetLastError());
 }
