@@ -159,7 +159,9 @@ struct JoinArgs {
 
 // A block walks rows with a grid stride; thread t owns the row's 8-element pieces t, t + blockDim, ...
 // (V of them) in all of them, so gamma1 gate_col and gamma2 stay in registers, and each row from its
-// load, one row ahead, to its outputs: every byte moves once.
+// load, one row ahead, to its outputs: every byte moves once.  16384 x 4096 with y and e4m3 codes (606 MB): 101 us,
+// 88% of the copy rate; with dropout and without codes (537 MB) 105 us, 75%: instructions bound it then, 330 a
+// piece of eight elements, of which the generator has 120.
 template <int V, int FMT>
 __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
   __shared__ float s_sum[2][32];
@@ -314,6 +316,7 @@ struct JoinBwdArgs {
 // f = rb / (1 - p):
 //   dgamma1 = f gate_col S    dgate_col = f gamma1 S    dgate_row = f rstd1 q
 //   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C),  dk = d where it is kept, else 0
+// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 54 us, with dropout 68.
 template <int V, int DEPTH, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwdArgs a) {
   extern __shared__ uint4 s_row[];  // [DEPTH][4][V][blockDim]

@@ -10,6 +10,9 @@
 // accumulator row is an output column, an accumulator column a row of X.  So a tile takes as many
 // MMA columns as the group has rows left, in steps of 16 -- a ragged tail costs what it holds -- a
 // thread's bias is one number, and a few rows of X stream the weights through the same code.
+//
+// Three kernels: linear_pair.cu (long groups, bf16 results), linear.cu (one CTA per SM), linear_split.cu
+// (few rows); linear.cu chooses.
 #pragma once
 #include <algorithm>
 #include <type_traits>
