@@ -260,7 +260,9 @@ int launch(const LinCall& c, const DeviceInfo& dev) {
   return cuda_status(cudaGetLastError());
 }
 
-// Which kernel, by an estimate of its time in microseconds.  Groups are taken to be of equal length.  The
+// Which kernel, by an estimate of its time in microseconds.  The host knows the rows of all groups together,
+// so row tiles are taken as the mean of equal groups and of one that has half of the rows (64 groups of 2048
+// rows, 4096 x 2048, by Zipf's law: 168 us with 128 rows a tile, 189 with 32; equal: 167, 165).  The
 // constants are what the kernels were measured to take: a k-block's stage at 150 KB a microsecond and SM or
 // its products at the tensor cores' rate, a start and an end.  (Times of split / one / pair: 1 x 4096 x 4096
 // 10.1 / 12.9 / 24; 256 x 4096 x 4096 17.3 / 17.5 / 24.8; 512 x 4096 x 4096 - / 18.0 / 25.1; 1024 x 4096 x 4096
@@ -278,17 +280,25 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
   const double nct = ceil_div(c.a.width, kBN), sms = dev.sms;
   const double memory =
       (2.0 * live * c.a.N * c.a.K + (double)c.a.M * (2.0 * c.a.K + (c.f32 ? 4.0 : 2.0) * c.a.width)) / 6.7e6;
-  auto tiles = [&](int tn) { return live * std::ceil(rows / tn) * nct; };
+  auto row_tiles = [&](int tn) {
+    const double even = live * std::ceil(rows / tn);
+    if (live < 2) return even;
+    const double half = 0.5 * (double)c.a.M, rest = live - 1;
+    return 0.5 * (even + std::ceil(half / tn) + rest * std::ceil(half / rest / tn));
+  };
+  auto tiles = [&](int tn) { return row_tiles(tn) * nct; };
   auto block = [&](int tn) { return std::max((H * kBN + tn) * 128 / 150e3, H * std::min<double>(tn, rows) * 0.31 / 256); };
   Plan best{Plan::kOne, 0, 1, 1e30};
   auto offer = [&](Plan p) {
     if (p.us < best.us) best = p;
   };
   auto both = [](double a, double b) { return std::max(a, b) + 0.2 * std::min(a, b); };  // they overlap, not wholly
-  for (int tn : {32, gated && c.f32 ? 64 : 128})
-    offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.01 * tn});
+  for (int tn : {32, gated && c.f32 ? 64 : 128}) {
+    if (tn == 32 && live > 1 && rows >= 32) continue;  // (as fast at best, and slow for a long group among them)
+    offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.003 * tn});
+  }
   if (!c.f32) {
-    const double t = live * std::ceil(rows / 256) * std::ceil(c.a.width / (gated ? 128.0 : 256.0));
+    const double t = row_tiles(256) * std::ceil(c.a.width / (gated ? 128.0 : 256.0));
     offer({Plan::kPair, 256, 1,
            7 + both(std::ceil(t / (dev.sms / 2)) * nkb * std::max(0.25, std::min(256.0, rows) * 0.31 / 256), memory)});
   }
