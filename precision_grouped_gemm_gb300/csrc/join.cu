@@ -160,7 +160,7 @@ struct JoinArgs {
 // A block walks rows with a grid stride; thread t owns the row's 8-element pieces t, t + blockDim, ...
 // (V of them) in all of them, so gamma1 gate_col and gamma2 stay in registers, and each row from its
 // load, one row ahead, to its outputs: every byte moves once.  16384 x 4096 with y and e4m3 codes (606 MB): 101 us,
-// 88% of the copy rate; with dropout and without codes (537 MB) 105 us, 75%: instructions bound it then, 330 a
+// 88% of the copy rate; with dropout and without codes (537 MB) 107 us, 74%: instructions bound it then, 330 a
 // piece of eight elements, of which the generator has 120.
 template <int V, int FMT>
 __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
@@ -228,10 +228,14 @@ __global__ void __launch_bounds__(512) join_kernel(const JoinArgs a) {
       f2 t[4], r[4];
       unpack2(xv[j], t);
       unpack2(rv[j], r);
+      // (before the mask: a row's NaN does not come into its dropped elements; nor past the row's end)
+      const f2 kv = both(v < a.nvec ? k : 0.0f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = mul2(t[e], kv);
       if (a.drop.rng) drop8(t, base + v, a.drop, key);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[j][e] = fma2(ra, r[e], mul2(mul2(t[e], g1[j][e]), both(k)));
+        s[j][e] = fma2(ra, r[e], mul2(t[e], g1[j][e]));
         t2 = fma2(s[j][e], s[j][e], t2);
       }
       if (a.h && v < a.nvec) a.h[base + v] = round8(s[j]);

@@ -163,6 +163,33 @@ def test_join_dropped_places_hold_nothing():
     assert torch.isfinite(dx).all() and (dx[bad] == 0).all()
 
 
+def test_join_dropped_places_of_a_row_without_a_norm():
+    # a NaN or an infinity in a row that is normed: its kept elements have no value, its dropped ones are 0
+    R, C, p = 24, 264, 0.5
+    t, d, n, _, mask = _case(R, C, True, "token", p, None, 12)
+    x = d["x"].clone()
+    x[3, 7], x[4, 9], x[5, 250] = float("nan"), float("inf"), float("-inf")
+    form = {k: d[k] for k in ("gamma_post", "gate", "rng")} | {"p": p}
+    h, *_ = pgg.block_join(x, d["residual"], **form)
+    ref, *_ = pgg.block_join(d["x"], d["residual"], **form)
+    keep = torch.from_numpy(mask).to(DEV)
+    assert torch.equal(h[~keep], d["residual"][~keep])
+    assert torch.isnan(h[3][keep[3]]).all()
+    rest = torch.ones(R, dtype=torch.bool, device=DEV)
+    rest[3:6] = False
+    assert torch.equal(h[rest], ref[rest])
+    # a row that the mask empties is the residual's, and so is its norm
+    p, x, res = 0.9, d["x"][:, :8].contiguous(), d["residual"][:, :8].contiguous()
+    keep = torch.from_numpy(ol.keep(R, 8, p, t["rng"].tolist())).to(DEV)
+    empty = ~keep.any(dim=1)
+    assert empty.any()
+    x[empty, 5] = float("nan")
+    one = torch.ones(8, dtype=BF, device=DEV)
+    h, y, *_ = pgg.block_join(x, res, gamma_post=one, gamma=one, p=p, rng=d["rng"])
+    assert torch.equal(h[empty], res[empty])
+    assert torch.equal(y[empty], pgg.block_join(torch.zeros_like(x), res, gamma=one)[1][empty])
+
+
 def test_join_rows_of_zeros_and_special_values():
     x = torch.zeros(4, 64, dtype=BF, device=DEV)
     x[1, 3], x[2, 5] = float("inf"), float("nan")
