@@ -41,28 +41,36 @@ __device__ __forceinline__ float block_sum(float v, float* s, int nwarps) {
   return v;
 }
 
-// The same for up to four sums at once: the first two steps halve the sums that a lane carries, so that
-// five steps of one value each are left of four times five.
-__device__ __forceinline__ void block_sums(float (&v)[4], float (*s)[16], int nwarps) {
+// The same for N = 4 or 8 sums at once: the first steps halve the sums that a lane carries, so that of N
+// times five steps fewer than N + 4 are left.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[16], int nwarps) {
+  constexpr int kSpan = 32 / N;  // lanes of one sum
   const int lane = threadIdx.x & 31;
-  const bool h = lane & 16, l = lane & 8;
-  float a = h ? v[2] : v[0], b = h ? v[3] : v[1];
-  a += __shfl_xor_sync(0xffffffffu, h ? v[0] : v[2], 16);
-  b += __shfl_xor_sync(0xffffffffu, h ? v[1] : v[3], 16);
-  float c = l ? b : a;
-  c += __shfl_xor_sync(0xffffffffu, l ? a : b, 8);  // the sum number lane / 8
 #pragma unroll
-  for (int d = 4; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
-  if ((lane & 7) == 0) s[lane >> 3][threadIdx.x >> 5] = c;
+  for (int n = N, d = 16; n > 1; n >>= 1, d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float give = up ? v[i] : v[i + n / 2], own = up ? v[i + n / 2] : v[i];
+      v[i] = own + __shfl_xor_sync(0xffffffffu, give, d);
+    }
+  }
+  float c = v[0];  // the sum number lane / kSpan
+#pragma unroll
+  for (int d = kSpan / 2; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+  const int i = lane / kSpan, k = lane % kSpan;
+  if (k == 0) s[i][threadIdx.x >> 5] = c;
   __syncthreads();
-  // lane 8 i + k adds the sums i of the warps k and k + 8
-  const int k = lane & 7;
-  c = k < nwarps ? s[lane >> 3][k] : 0.0f;
-  if (nwarps > 8) c += k + 8 < nwarps ? s[lane >> 3][k + 8] : 0.0f;
+  // lane k of a sum's adds those of the warps k, k + kSpan, ...
+  c = 0.0f;
 #pragma unroll
-  for (int d = 4; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+  for (int w = 0; w < 16; w += kSpan)
+    if (w + k < nwarps) c += s[i][w + k];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, 8 * i);
+  for (int d = kSpan / 2; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = __shfl_sync(0xffffffffu, c, kSpan * j);
 }
 
 struct Drop {
@@ -310,7 +318,8 @@ struct JoinBwdArgs {
 
 // The same ownership: a thread's columns stay its own over all rows of the block, so the sums over
 // rows are registers, written once per block.  A thread copies its pieces of coming rows into its own
-// places of shared memory, DEPTH - 1 rows ahead (no thread reads another's).
+// places of shared memory, DEPTH - 1 steps ahead (no thread reads another's).  A step is ROWS rows, of which
+// one's arithmetic fills the waits of another's sums.
 //
 // Instructions bound it before memory does, so the sums over a row are arranged to need one barrier.  With
 // e = dh + rstd2 u, xk = x where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none):
@@ -320,11 +329,11 @@ struct JoinBwdArgs {
 // f = rb / (1 - p):
 //   dgamma1 = f gate_col S    dgate_col = f gamma1 S    dgate_row = f rstd1 q
 //   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C),  dk = d where it is kept, else 0
-// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 54 us, with dropout 68.
-template <int V, int DEPTH, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwdArgs a) {
-  extern __shared__ uint4 s_row[];  // [DEPTH][4][V][blockDim]
-  __shared__ float s_sum[2][4][16];
+// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 52 us, with dropout 65.
+template <int V, int ROWS, int DEPTH, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs a) {
+  extern __shared__ uint4 s_row[];  // [DEPTH][ROWS][4][V][blockDim]
+  __shared__ float s_sum[2][4 * ROWS][16];
   const int nwarps = blockDim.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Key key{};
@@ -348,32 +357,41 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
   uint4* mine = s_row + threadIdx.x;  // place i of a row: mine[i * blockDim.x]
   // places that no row is copied to read as zeros: those past the row's end, and of operands that are not given
 #pragma unroll
-  for (int i = 0; i < DEPTH * kRow; ++i) {
+  for (int i = 0; i < DEPTH * ROWS * kRow; ++i) {
     const int which = i % kRow / V, j = i % V;
     const bool given = which == 3 || (which == 2 ? a.dh != nullptr : a.gamma2 != nullptr);
     if (!given || threadIdx.x + j * blockDim.x >= a.nvec) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
   }
-  auto fetch = [&](int64_t row, int slot) {
-    if (row < a.R) {
-      const uint32_t step = blockDim.x * 16, dst = smem_u32(mine) + slot * kRow * step;
+  const int64_t grid = gridDim.x;
+  auto fetch = [&](int64_t first, int slot) {
+    const uint32_t step = blockDim.x * 16;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
-        const int64_t at = row * a.nvec + v;
-        if (v < a.nvec) {
-          if (a.gamma2) {
-            cp_async_16(dst + j * step, a.h + at);
-            cp_async_16(dst + (V + j) * step, a.dy + at);
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t row = first + k * grid;
+      const uint32_t dst = smem_u32(mine) + (slot * ROWS + k) * kRow * step;
+      if (row < a.R) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int v = threadIdx.x + j * blockDim.x;
+          const int64_t at = row * a.nvec + v;
+          if (v < a.nvec) {
+            if (a.gamma2) {
+              cp_async_16(dst + j * step, a.h + at);
+              cp_async_16(dst + (V + j) * step, a.dy + at);
+            }
+            if (a.dh) cp_async_16(dst + (2 * V + j) * step, a.dh + at);
+            cp_async_16(dst + (3 * V + j) * step, a.x + at);
           }
-          if (a.dh) cp_async_16(dst + (2 * V + j) * step, a.dh + at);
-          cp_async_16(dst + (3 * V + j) * step, a.x + at);
         }
+      } else if (k > 0) {  // a last row without its fellows: zeros, which change no sum
+#pragma unroll
+        for (int i = 0; i < kRow; ++i) mine[((slot * ROWS + k) * kRow + i) * blockDim.x] = make_uint4(0, 0, 0, 0);
       }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < DEPTH - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+  for (int i = 0; i < DEPTH - 1; ++i) fetch(blockIdx.x + i * ROWS * grid, i);
   const float f = a.rb * a.drop.inv;
   int par = 0, slot = 0;
   // The rows' three numbers, of the block's next 32 rows one a lane: a load a row, with rows a grid apart,
@@ -381,77 +399,94 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) join_bwd_kernel(const JoinBwd
   const int lane = threadIdx.x & 31;
   float rstd1_of = 1.0f, rstd2_of = 0.0f, gate_of = 1.0f;
   int nth = 0;
-  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, par ^= 1, ++nth) {
-    const int64_t base = row * a.nvec + threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.R; row += ROWS * grid, par ^= 1, nth += ROWS) {
     if ((nth & 31) == 0) {
-      const int64_t of = row + (int64_t)lane * gridDim.x;
-      if (of < a.R) {
-        if (a.gamma1) rstd1_of = __ldg(a.rstd1 + of);
-        if (a.gamma2) rstd2_of = __ldg(a.rstd2 + of);
-        if (a.gate_row) gate_of = __ldg(a.gate_row + of);
-      }
+      const int64_t of = row + lane * grid;
+      const bool is = of < a.R;
+      rstd1_of = is && a.gamma1 ? __ldg(a.rstd1 + of) : 1.0f;
+      rstd2_of = is && a.gamma2 ? __ldg(a.rstd2 + of) : 0.0f;
+      gate_of = is && a.gate_row ? __ldg(a.gate_row + of) : 1.0f;
     }
-    const float rstd1 = __shfl_sync(0xffffffffu, rstd1_of, nth & 31), rstd2 = __shfl_sync(0xffffffffu, rstd2_of, nth & 31);
-    const float scale = __shfl_sync(0xffffffffu, gate_of, nth & 31) * rstd1;
-    fetch(row + (int64_t)(DEPTH - 1) * gridDim.x, slot == 0 ? DEPTH - 1 : slot - 1);
-    uint32_t keep[V];
+    fetch(row + (DEPTH - 1) * ROWS * grid, slot == 0 ? DEPTH - 1 : slot - 1);
+    float rstd1[ROWS], rstd2[ROWS], scale[ROWS];
+    uint32_t keep[ROWS][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) keep[j] = a.drop.rng ? keep8(base + j * blockDim.x, a.drop, key) : 0xFFu;
+    for (int k = 0; k < ROWS; ++k) {
+      rstd1[k] = __shfl_sync(0xffffffffu, rstd1_of, (nth + k) & 31);
+      rstd2[k] = __shfl_sync(0xffffffffu, rstd2_of, (nth + k) & 31);
+      scale[k] = __shfl_sync(0xffffffffu, gate_of, (nth + k) & 31) * rstd1[k];
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        keep[k][j] = a.drop.rng ? keep8((row + k * grid) * a.nvec + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
+    }
     cp_async_wait<DEPTH - 1>();
-    const uint4* cur = mine + slot * kRow * blockDim.x;
-    f2 e[V][4], t_uh = both(0.0f), t_xe = t_uh, t_xh = t_uh;
+    const uint4* cur = mine + slot * ROWS * kRow * blockDim.x;  // row k's place i: cur[(k * kRow + i) * blockDim.x]
+    f2 e[ROWS][V][4];
+    float q[4 * ROWS];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      f2 hv[4], dy[4], x[4];
-      unpack2(cur[j * blockDim.x], hv);
-      unpack2(cur[(V + j) * blockDim.x], dy);
-      unpack2(cur[(2 * V + j) * blockDim.x], e[j]);
-      unpack2(cur[(3 * V + j) * blockDim.x], x);
-      if (a.drop.rng) keep_only(x, keep[j]);
+    for (int k = 0; k < ROWS; ++k) {
+      f2 t_uh = both(0.0f), t_xe = t_uh, t_xh = t_uh;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f2 u = mul2(dy[i], g2[j][i]), gx = mul2(x[i], gg[j][i]);
-        sum_2[j][i] = fma2(mul2(dy[i], hv[i]), both(rstd2), sum_2[j][i]);
-        e[j][i] = fma2(u, both(rstd2), e[j][i]);
-        t_uh = fma2(u, hv[i], t_uh);
-        t_xe = fma2(gx, e[j][i], t_xe);
-        t_xh = fma2(gx, hv[i], t_xh);
+      for (int j = 0; j < V; ++j) {
+        f2 hv[4], dy[4], x[4];
+        unpack2(cur[(k * kRow + j) * blockDim.x], hv);
+        unpack2(cur[(k * kRow + V + j) * blockDim.x], dy);
+        unpack2(cur[(k * kRow + 2 * V + j) * blockDim.x], e[k][j]);
+        unpack2(cur[(k * kRow + 3 * V + j) * blockDim.x], x);
+        if (a.drop.rng) keep_only(x, keep[k][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 u = mul2(dy[i], g2[j][i]), gx = mul2(x[i], gg[j][i]);
+          sum_2[j][i] = fma2(mul2(dy[i], hv[i]), both(rstd2[k]), sum_2[j][i]);
+          e[k][j][i] = fma2(u, both(rstd2[k]), e[k][j][i]);
+          t_uh = fma2(u, hv[i], t_uh);
+          t_xe = fma2(gx, e[k][j][i], t_xe);
+          t_xh = fma2(gx, hv[i], t_xh);
+        }
       }
+      q[k] = sum2(t_uh);
+      q[ROWS + k] = sum2(t_xe);
+      q[2 * ROWS + k] = sum2(t_xh);
+      q[3 * ROWS + k] = 0.0f;
     }
-    float q[4] = {sum2(t_uh), sum2(t_xe), sum2(t_xh), 0.0f};
-    block_sums(q, s_sum[par], nwarps);
-    const float c = -rstd2 * rstd2 * (q[0] * rstd2 * a.inv_c);
-    const float qx = fmaf(c, q[2], q[1]);
-    if (a.dgate_row && threadIdx.x == 0) a.dgate_row[row] = f * rstd1 * qx;
-    const float m = a.gamma1 ? -rstd1 * rstd1 * (qx * a.inv_c) : 0.0f, fs = f * scale;
+    block_sums<4 * ROWS>(q, s_sum[par], nwarps);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool in = threadIdx.x + j * blockDim.x < a.nvec;
-      f2 hv[4], x[4], o[4];
-      unpack2(cur[j * blockDim.x], hv);
-      unpack2(cur[(3 * V + j) * blockDim.x], x);
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t base = (row + k * grid) * a.nvec + threadIdx.x;
+      const bool is = k == 0 || row + k * grid < a.R;
+      const float c = -rstd2[k] * rstd2[k] * (q[k] * rstd2[k] * a.inv_c);
+      const float qx = fmaf(c, q[2 * ROWS + k], q[ROWS + k]);
+      if (a.dgate_row && threadIdx.x == 0 && is) a.dgate_row[row + k * grid] = f * rstd1[k] * qx;
+      const float m = a.gamma1 ? -rstd1[k] * rstd1[k] * (qx * a.inv_c) : 0.0f, fs = f * scale[k];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[j][i] = fma2(both(c), hv[i], e[j][i]);  // d
-      if (a.dres && in) {
+      for (int j = 0; j < V; ++j) {
+        const bool in = is && threadIdx.x + j * blockDim.x < a.nvec;
+        f2 hv[4], x[4], o[4];
+        unpack2(cur[(k * kRow + j) * blockDim.x], hv);
+        unpack2(cur[(k * kRow + 3 * V + j) * blockDim.x], x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = mul2(both(a.ra), e[j][i]);
-        a.dres[base + j * blockDim.x] = round8(o);
+        for (int i = 0; i < 4; ++i) e[k][j][i] = fma2(both(c), hv[i], e[k][j][i]);  // d
+        if (a.dres && in) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mul2(both(a.ra), e[k][j][i]);
+          a.dres[base + j * blockDim.x] = round8(o);
+        }
+        if (a.drop.rng) keep_only(e[k][j], keep[k][j]);  // dk
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = mul2(gg[j][i], e[k][j][i]);
+        if (a.gamma1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], both(m), o[i]);
+        } else if (a.drop.rng) {
+          keep_only(x, keep[k][j]);  // (with the norm a value that is not finite has the whole row)
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum_b[j][i] = fma2(mul2(e[k][j][i], x[i]), both(scale[k]), sum_b[j][i]);
+          o[i] = mul2(both(fs), o[i]);
+        }
+        if (in) a.dx[base + j * blockDim.x] = round8(o);
       }
-      if (a.drop.rng) keep_only(e[j], keep[j]);  // dk
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = mul2(gg[j][i], e[j][i]);
-      if (a.gamma1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], both(m), o[i]);
-      } else if (a.drop.rng) {
-        keep_only(x, keep[j]);  // (with the norm a value that is not finite has the whole row)
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum_b[j][i] = fma2(mul2(e[j][i], x[i]), both(scale), sum_b[j][i]);
-        o[i] = mul2(both(fs), o[i]);
-      }
-      if (in) a.dx[base + j * blockDim.x] = round8(o);
     }
     if (++slot == DEPTH) slot = 0;
   }
@@ -638,18 +673,16 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
                 col ? static_cast<const uint4*>(gate) : nullptr, make_drop(rng, p), R, nvec, 1.0f / (float)C,
                 residual_scale, branch_scale, static_cast<uint4*>(dx), static_cast<uint4*>(dresidual),
                 col ? nullptr : dgate, static_cast<float*>(ws)};
-  // Up to 384 threads (8192 x 2880): with dropout one block an SM of more registers, 68.5 us instead of 71.8,
-  // without it two, 54.5 instead of 60.0.  (Two pieces a thread there: 74.6 and 60.9.)
-  const bool drop = a.drop.rng != nullptr;
-  auto kern = V == 1   ? (drop ? join_bwd_kernel<1, 2, 384, 1> : join_bwd_kernel<1, 2, 384, 2>)
-              : V == 2 ? join_bwd_kernel<2, 2, 512, 1>
-                       : join_bwd_kernel<4, 1, 512, 1>;
-  const int depth = V == 4 ? 1 : 2;
-  const size_t smem = (size_t)depth * 4 * V * threads * sizeof(uint4);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(depth * 4 * V * 512 * sizeof(uint4)));
-  static std::atomic<int> resident[5][17][2];
-  std::atomic<int>& known = resident[V][threads / 32][drop];
+  // Up to 384 threads two rows at a time, on one block an SM of more registers (8192 x 2880, without dropout: 52.1
+  // us, with 64.8; one row 53.4 and 69, with two blocks an SM 54.5 and 71.8; four rows 52.8 and 69.2).
+  auto kern = V == 1   ? join_bwd_kernel<1, 2, 2, 384>
+              : V == 2 ? join_bwd_kernel<2, 1, 2, 512>
+                       : join_bwd_kernel<4, 1, 1, 512>;
+  const size_t place = 16 * sizeof(uint4);  // a thread's shared memory: 16 pieces with each of the three
+  const size_t smem = place * threads;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(place * 512));
+  static std::atomic<int> resident[5][17];
+  std::atomic<int>& known = resident[V][threads / 32];
   int per_sm = known.load(std::memory_order_relaxed);
   if (e == cudaSuccess && per_sm == 0) {
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
