@@ -22,6 +22,7 @@
 #include <atomic>
 
 #include "block.cuh"
+#include "cluster.cuh"
 #include "packed.cuh"
 
 namespace pgg {
@@ -42,9 +43,10 @@ __device__ __forceinline__ float block_sum(float v, float* s, int nwarps) {
 }
 
 // The same for N = 4 or 8 sums at once: the first steps halve the sums that a lane carries, so that of N
-// times five steps fewer than N + 4 are left.
-template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[16], int nwarps) {
+// times five steps fewer than N + 4 are left.  CL > 1: over the CTAs of a cluster, which write each other's
+// buffers; the buffers' turns keep a sum's writes behind the reads of the one before the last.
+template <int N, int CL>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[16 * CL], int nwarps) {
   constexpr int kSpan = 32 / N;  // lanes of one sum
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -60,13 +62,22 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*s)[16], int nw
 #pragma unroll
   for (int d = kSpan / 2; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
   const int i = lane / kSpan, k = lane % kSpan;
-  if (k == 0) s[i][threadIdx.x >> 5] = c;
-  __syncthreads();
+  if (CL == 1) {
+    if (k == 0) s[i][threadIdx.x >> 5] = c;
+    __syncthreads();
+  } else {
+    const uint32_t to = smem_u32(&s[i][16 * (blockIdx.x % CL) + (threadIdx.x >> 5)]);
+    if (k < CL) st_cluster(map_rank(to, k), c);
+    __syncwarp();
+    cluster_sync();
+  }
   // lane k of a sum's adds those of the warps k, k + kSpan, ...
   c = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 16; w += kSpan)
-    if (w + k < nwarps) c += s[i][w + k];
+  for (int r = 0; r < CL; ++r)
+#pragma unroll
+    for (int w = 0; w < 16; w += kSpan)
+      if (w + k < nwarps) c += s[i][16 * r + w + k];
 #pragma unroll
   for (int d = kSpan / 2; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
 #pragma unroll
@@ -318,35 +329,41 @@ struct JoinBwdArgs {
 
 // The same ownership: a thread's columns stay its own over all rows of the block, so the sums over
 // rows are registers, written once per block.  A thread copies its pieces of coming rows into its own
-// places of shared memory, DEPTH - 1 steps ahead (no thread reads another's).  A step is ROWS rows, of which
-// one's arithmetic fills the waits of another's sums.
+// places of shared memory, a step ahead (no thread reads another's).  A step is ROWS rows, of which
+// one's arithmetic fills the waits of another's sums.  The longest rows are shared out over CL CTAs.
 //
-// Instructions bound it before memory does, so the sums over a row are arranged to need one barrier.  With
-// e = dh + rstd2 u, xk = x where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none):
+// The chain of a row's steps bounds it before memory does (with dropout 56% of the issue slots taken), so the
+// sums over a row are arranged to need one barrier.  With e = dh + rstd2 u, xk = x where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none):
 //   d = e + c h,  c = -rstd2^3 mean(u h)
 //   q = sum gg xk d = sum gg xk e + c sum gg xk h
 // and all the gradients of the branch come from q and, over the rows, S = sum gate_row rstd1 xk d.  With
 // f = rb / (1 - p):
 //   dgamma1 = f gate_col S    dgate_col = f gamma1 S    dgate_row = f rstd1 q
 //   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C),  dk = d where it is kept, else 0
-// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 52 us, with dropout 65.
-template <int V, int ROWS, int DEPTH, int THREADS>
+// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 52 us, with dropout 66; 16384 x 4096 with
+// dropout (805 MB) 151.
+template <int V, int ROWS, int CL, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs a) {
   extern __shared__ uint4 s_row[];  // [DEPTH][ROWS][4][V][blockDim]
-  __shared__ float s_sum[2][4 * ROWS][16];
+  __shared__ float s_sum[2][4 * ROWS][16 * CL];
+  constexpr int DEPTH = 2;
   const int nwarps = blockDim.x >> 5;
+  // the row's pieces that this CTA has: all of them, or its share
+  const int own = CL == 1 ? a.nvec : (a.nvec + CL - 1) / CL, rank = blockIdx.x % CL, block = blockIdx.x / CL;
+  const int v0 = rank * own, v1 = min(a.nvec, v0 + own);
+  if (CL > 1) cluster_sync();  // (the other CTAs' shared memory is there)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Key key{};
   if (a.drop.rng) key = load_key(a.drop);
   f2 sum_b[V][4], sum_2[V][4], gg[V][4], g2[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int v = threadIdx.x + j * blockDim.x;
-    load_factors(a.gamma1, v, a.nvec, gg[j]);
-    load_factors(a.gamma2, v, a.nvec, g2[j]);
+    const int v = v0 + threadIdx.x + j * blockDim.x;
+    load_factors(a.gamma1, v, v1, gg[j]);
+    load_factors(a.gamma2, v, v1, g2[j]);
     if (a.gate_col) {
       f2 c[4];
-      load_factors(a.gate_col, v, a.nvec, c);
+      load_factors(a.gate_col, v, v1, c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) gg[j][e] = mul2(gg[j][e], c[e]);
     }
@@ -360,9 +377,9 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
   for (int i = 0; i < DEPTH * ROWS * kRow; ++i) {
     const int which = i % kRow / V, j = i % V;
     const bool given = which == 3 || (which == 2 ? a.dh != nullptr : a.gamma2 != nullptr);
-    if (!given || threadIdx.x + j * blockDim.x >= a.nvec) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+    if (!given || v0 + (int)threadIdx.x + j * (int)blockDim.x >= v1) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
   }
-  const int64_t grid = gridDim.x;
+  const int64_t grid = gridDim.x / CL;
   auto fetch = [&](int64_t first, int slot) {
     const uint32_t step = blockDim.x * 16;
 #pragma unroll
@@ -372,9 +389,9 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
       if (row < a.R) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int v = threadIdx.x + j * blockDim.x;
+          const int v = v0 + threadIdx.x + j * blockDim.x;
           const int64_t at = row * a.nvec + v;
-          if (v < a.nvec) {
+          if (v < v1) {
             if (a.gamma2) {
               cp_async_16(dst + j * step, a.h + at);
               cp_async_16(dst + (V + j) * step, a.dy + at);
@@ -391,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < DEPTH - 1; ++i) fetch(blockIdx.x + i * ROWS * grid, i);
+  for (int i = 0; i < DEPTH - 1; ++i) fetch(block + i * ROWS * grid, i);
   const float f = a.rb * a.drop.inv;
   int par = 0, slot = 0;
   // The rows' three numbers, of the block's next 32 rows one a lane: a load a row, with rows a grid apart,
@@ -399,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
   const int lane = threadIdx.x & 31;
   float rstd1_of = 1.0f, rstd2_of = 0.0f, gate_of = 1.0f;
   int nth = 0;
-  for (int64_t row = blockIdx.x; row < a.R; row += ROWS * grid, par ^= 1, nth += ROWS) {
+  for (int64_t row = block; row < a.R; row += ROWS * grid, par ^= 1, nth += ROWS) {
     if ((nth & 31) == 0) {
       const int64_t of = row + lane * grid;
       const bool is = of < a.R;
@@ -417,7 +434,8 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
       scale[k] = __shfl_sync(0xffffffffu, gate_of, (nth + k) & 31) * rstd1[k];
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        keep[k][j] = a.drop.rng ? keep8((row + k * grid) * a.nvec + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
+        keep[k][j] =
+            a.drop.rng ? keep8((row + k * grid) * a.nvec + v0 + threadIdx.x + j * blockDim.x, a.drop, key) : 0xFFu;
     }
     cp_async_wait<DEPTH - 1>();
     const uint4* cur = mine + slot * ROWS * kRow * blockDim.x;  // row k's place i: cur[(k * kRow + i) * blockDim.x]
@@ -449,18 +467,18 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
       q[2 * ROWS + k] = sum2(t_xh);
       q[3 * ROWS + k] = 0.0f;
     }
-    block_sums<4 * ROWS>(q, s_sum[par], nwarps);
+    block_sums<4 * ROWS, CL>(q, s_sum[par], nwarps);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      const int64_t base = (row + k * grid) * a.nvec + threadIdx.x;
+      const int64_t base = (row + k * grid) * a.nvec + v0 + threadIdx.x;
       const bool is = k == 0 || row + k * grid < a.R;
       const float c = -rstd2[k] * rstd2[k] * (q[k] * rstd2[k] * a.inv_c);
       const float qx = fmaf(c, q[2 * ROWS + k], q[ROWS + k]);
-      if (a.dgate_row && threadIdx.x == 0 && is) a.dgate_row[row + k * grid] = f * rstd1[k] * qx;
+      if (a.dgate_row && threadIdx.x == 0 && rank == 0 && is) a.dgate_row[row + k * grid] = f * rstd1[k] * qx;
       const float m = a.gamma1 ? -rstd1[k] * rstd1[k] * (qx * a.inv_c) : 0.0f, fs = f * scale[k];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const bool in = is && threadIdx.x + j * blockDim.x < a.nvec;
+        const bool in = is && v0 + (int)threadIdx.x + j * (int)blockDim.x < v1;
         f2 hv[4], x[4], o[4];
         unpack2(cur[(k * kRow + j) * blockDim.x], hv);
         unpack2(cur[(k * kRow + 3 * V + j) * blockDim.x], x);
@@ -492,10 +510,10 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int v = threadIdx.x + j * blockDim.x;
-    if (v < a.nvec) {
-      const int64_t plane = (int64_t)gridDim.x * a.nvec * 2;
-      float4* p = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.nvec + v) * 2;
+    const int v = v0 + threadIdx.x + j * blockDim.x;
+    if (v < v1) {
+      const int64_t plane = grid * a.nvec * 2;
+      float4* p = reinterpret_cast<float4*>(a.part) + ((int64_t)block * a.nvec + v) * 2;
       auto put = [&](float4* dst, const f2 (&o)[4]) {
         float w[8];
 #pragma unroll
@@ -505,14 +523,14 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
       };
       f2 fac[4];
       if (a.gamma1) {
-        load_factors(a.gate_col, v, a.nvec, fac);
+        load_factors(a.gate_col, v, v1, fac);
 #pragma unroll
         for (int e = 0; e < 4; ++e) fac[e] = mul2(fac[e], mul2(both(f), sum_b[j][e]));
         put(p, fac);
       }
       if (a.gamma2) put(p + plane, sum_2[j]);
       if (a.gate_col) {
-        load_factors(a.gamma1, v, a.nvec, fac);
+        load_factors(a.gamma1, v, v1, fac);
 #pragma unroll
         for (int e = 0; e < 4; ++e) fac[e] = mul2(fac[e], mul2(both(f), sum_b[j][e]));
         put(p + 2 * plane, fac);
@@ -554,13 +572,16 @@ __global__ void __launch_bounds__(kReduceThreads) join_reduce_kernel(const JoinR
 
 int threads_of(int nvec, int V) { return std::max(32, ((nvec + V - 1) / V + 31) / 32 * 32); }
 int join_v(int nvec) { return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4; }
-int bwd_v(int nvec) { return nvec <= 384 ? 1 : nvec <= 1024 ? 2 : 4; }
+int bwd_v(int nvec) { return nvec <= 384 ? 1 : 2; }
+// CTAs, a cluster, that share a row: four pieces a thread would not stay in registers (4096 x 16384 with dropout:
+// 264 us, two CTAs 186, four 187; without 243, 171, 158; 4096 x 10240 with dropout 197, 141, 125).
+int bwd_ctas(int nvec) { return nvec <= 1024 ? 1 : 4; }
 
 // Blocks of the backward pass: at most as many as are resident at once, which this bounds for the
 // workspace.
 int bwd_blocks(int64_t R, int nvec) {
-  const int threads = threads_of(nvec, bwd_v(nvec));
-  return (int)std::min<int64_t>(R, 160 * std::max(1, std::min(8, 768 / threads)));
+  const int threads = threads_of(nvec, bwd_v(nvec) * bwd_ctas(nvec));
+  return (int)std::min<int64_t>(R, 160 / bwd_ctas(nvec) * std::max(1, std::min(8, 768 / threads)));
 }
 
 template <int V>
@@ -665,7 +686,8 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
   if (!aligned_to(rstd_post, 4) || !aligned_to(rstd, 4)) return PGG_ERR_ALIGNMENT;
   DeviceInfo dev;
   if ((st = current_device(&dev)) != PGG_OK) return st;
-  const int nvec = (int)(C / 8), V = bwd_v(nvec), threads = threads_of(nvec, V);
+  const int nvec = (int)(C / 8), V = bwd_v(nvec), ctas = bwd_ctas(nvec);
+  const int threads = threads_of((nvec + ctas - 1) / ctas, V);
   JoinBwdArgs a{static_cast<const uint4*>(dy), static_cast<const uint4*>(dh), static_cast<const uint4*>(x),
                 static_cast<const uint4*>(h), rstd_post, rstd, static_cast<const uint4*>(gamma_post),
                 static_cast<const uint4*>(gamma),
@@ -674,25 +696,39 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
                 residual_scale, branch_scale, static_cast<uint4*>(dx), static_cast<uint4*>(dresidual),
                 col ? nullptr : dgate, static_cast<float*>(ws)};
   // Up to 384 threads two rows at a time, on one block an SM of more registers (8192 x 2880, without dropout: 52.1
-  // us, with 64.8; one row 53.4 and 69, with two blocks an SM 54.5 and 71.8; four rows 52.8 and 69.2).
-  auto kern = V == 1   ? join_bwd_kernel<1, 2, 2, 384>
-              : V == 2 ? join_bwd_kernel<2, 1, 2, 512>
-                       : join_bwd_kernel<4, 1, 1, 512>;
+  // us, with 65.8; one row 53.4 and 69, with two blocks an SM 54.5 and 71.8; four rows 52.8 and 69.2).
+  auto kern = V == 1      ? join_bwd_kernel<1, 2, 1, 384>
+              : ctas == 1 ? join_bwd_kernel<2, 1, 1, 512>
+                          : join_bwd_kernel<2, 1, 4, 512>;
   const size_t place = 16 * sizeof(uint4);  // a thread's shared memory: 16 pieces with each of the three
   const size_t smem = place * threads;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(place * 512));
-  static std::atomic<int> resident[5][17];
-  std::atomic<int>& known = resident[V][threads / 32];
-  int per_sm = known.load(std::memory_order_relaxed);
-  if (e == cudaSuccess && per_sm == 0) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
-    per_sm = std::max(1, per_sm);
-    if (e == cudaSuccess) known.store(per_sm, std::memory_order_relaxed);
+  cudaLaunchConfig_t run{};
+  run.blockDim = dim3((unsigned)threads);
+  run.dynamicSmemBytes = smem;
+  run.stream = s;
+  cudaLaunchAttribute pair{};
+  pair.id = cudaLaunchAttributeClusterDimension;
+  pair.val.clusterDim.x = (unsigned)ctas;
+  pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+  run.attrs = &pair;
+  run.numAttrs = ctas > 1 ? 1 : 0;
+  // blocks, or clusters of them, that run at one time
+  static std::atomic<int> resident[3][5][17];
+  std::atomic<int>& known = resident[V][ctas][threads / 32];
+  int most = known.load(std::memory_order_relaxed);
+  if (e == cudaSuccess && most == 0) {
+    run.gridDim = dim3((unsigned)(dev.sms * ctas));
+    e = ctas == 1 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&most, kern, threads, smem)
+                  : cudaOccupancyMaxActiveClusters(&most, kern, &run);
+    most = std::max(1, ctas == 1 ? most * dev.sms : most);
+    if (e == cudaSuccess) known.store(most, std::memory_order_relaxed);
   }
   if (e != cudaSuccess) return cuda_status(e);
-  const int grid = std::min(bwd_blocks(R, nvec), dev.sms * per_sm);
-  kern<<<grid, threads, smem, s>>>(a);
-  if ((st = cuda_status(cudaGetLastError()))) return st;
+  const int grid = std::min(bwd_blocks(R, nvec), most);
+  run.gridDim = dim3((unsigned)(grid * ctas));
+  e = cudaLaunchKernelEx(&run, kern, a);
+  if ((st = cuda_status(e != cudaSuccess ? e : cudaGetLastError()))) return st;
   JoinReduce r{a.part, grid, (int)C, {dgamma_post, dgamma, col ? dgate : nullptr}, {0, 0, 0}};
   int sums = 0;
   for (int i = 0; i < 3; ++i)

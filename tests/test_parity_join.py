@@ -104,6 +104,14 @@ def test_join_and_its_gradients(R, C, post, gate, p, fmt):
         assert torch.equal(got[name], again[name]), name
 
 
+@pytest.mark.parametrize("R,C,post,gate,p,fmt", [
+    (90, 8200, True, "channel", 0.1, None), (301, 8200, False, "token", 0.0, None), (170, 16384, True, "token", 0.0, None),
+    (307, 2888, True, "token", 0.0, None), (601, 520, True, "channel", 0.0, None)])
+def test_join_many_rows_a_block(R, C, post, gate, p, fmt):
+    # each block, or pair of them (C > 8192), has some rows in turn, the last without a fellow in some
+    test_join_and_its_gradients(R, C, post, gate, p, fmt)
+
+
 def test_join_plain_is_the_norm():
     # no norm of x, no gate, no dropout: the residual's addition and the norm that the framework has
     rng = np.random.default_rng(1)
