@@ -20,15 +20,19 @@ struct ActForm {
   float alpha, offset, limit;  // limit 0: no clamp
 };
 
-// 1 / (1 + e^-x).  FAST: the short exponential and quotient, whose error (some 2^-20 at |x| = 10) stays
-// far inside the rounding to bf16; fp32 results take the full ones.
+// e^x.  FAST: the short exponential, whose error (some 2^-20 at |x| = 10) stays far inside the rounding to
+// bf16; fp32 results take the full one.
+template <bool FAST>
+__device__ __forceinline__ float exp_f(float x) {
+  return FAST ? __expf(x) : expf(x);
+}
+// 1 / (1 + e^-x), the quotient to two units of the last place.
 template <bool FAST = true>
 __device__ __forceinline__ float sigmoid_f(float x) {
-  return FAST ? __fdividef(1.0f, 1.0f + __expf(-x)) : 1.0f / (1.0f + expf(-x));
+  return __fdividef(1.0f, 1.0f + exp_f<FAST>(-x));
 }
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
 
-// The normal distribution function for bf16 results, two at a time, from e = exp(-z^2 / 2): Phi(-|z|) / e =
+// The normal distribution function, two at a time, from e = exp(-z^2 / 2): Phi(-|z|) / e =
 // erfcx(|z| / sqrt 2) / 2 is t P(t) with t = 1 / (1 + 0.3 |z|) and a polynomial P fitted to it over |z| <= 14 (the
 // relative error is below 1.5e-7, 4.5e-7 in fp32 arithmetic, in the tail too).
 __device__ __forceinline__ f2 normal_cdf_f2(f2 z, f2 e) {
@@ -47,10 +51,11 @@ __device__ __forceinline__ f2 normal_cdf_f2(f2 z, f2 e) {
   return make2(a < 0.0f ? c : 1.0f - c, b < 0.0f ? d : 1.0f - d);
 }
 // exp(-z^2 / 2)
+template <bool FAST = true>
 __device__ __forceinline__ f2 gauss_f2(f2 z) {
   float a, b;
   split2(mul2(mul2(z, z), both(-0.5f)), a, b);
-  return make2(__expf(a), __expf(b));
+  return make2(exp_f<FAST>(a), exp_f<FAST>(b));
 }
 
 // Minimum and maximum that a NaN goes through.
@@ -68,13 +73,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_f(float z, const ActForm& f) {
   if (ACT == kActSilu) return z * sigmoid_f<FAST>(f.alpha * z);
-  if (ACT == kActGelu && FAST) {
+  if (ACT == kActGelu) {
     const f2 v = both(z);
     float lo, hi;
-    split2(mul2(v, normal_cdf_f2(v, gauss_f2(v))), lo, hi);
+    split2(mul2(v, normal_cdf_f2(v, gauss_f2<FAST>(v))), lo, hi);
     return lo;
   }
-  if (ACT == kActGelu) return z * normal_cdf(z);
   return z;
 }
 template <bool FAST>

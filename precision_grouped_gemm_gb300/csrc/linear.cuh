@@ -27,6 +27,7 @@ namespace pgg {
 constexpr int kBN = 128;     // output columns of a tile (of each half with swiglu): TMEM lanes
 constexpr int kBK = 64;      // one 128-byte swizzle atom of the reduction
 constexpr int kLinThreads = 192;
+constexpr int kChunk = 4;    // fp32 results: k-blocks that one accumulator takes
 constexpr int kBand = 8;     // row tiles that take their turns at one column tile
 
 struct LinArgs {
@@ -150,18 +151,18 @@ __device__ __forceinline__ void add_acc(uint32_t taddr, float (&v)[32]) {
   for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
 }
 
-template <int ACT, bool FAST>
-__device__ __forceinline__ void apply_act(float (&v)[32], const ActForm& f) {
-  if (ACT == kActGelu && FAST) {
+template <int ACT, bool FAST, int N>
+__device__ __forceinline__ void apply_act(float (&v)[N], const ActForm& f) {
+  if constexpr (ACT == kActGelu) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
+    for (int j = 0; j < N; j += 2) {
       const f2 z = make2(v[j], v[j + 1]);
-      split2(mul2(z, normal_cdf_f2(z, gauss_f2(z))), v[j], v[j + 1]);
+      split2(mul2(z, normal_cdf_f2(z, gauss_f2<FAST>(z))), v[j], v[j + 1]);
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = act_f<ACT, FAST>(v[j], f);
+    for (int j = 0; j < N; ++j) v[j] = act_f<ACT, FAST>(v[j], f);
+  }
 }
 
 // One chunk of 32 rows: z (and u, the other half) with the bias already in them -> Z, Y.
