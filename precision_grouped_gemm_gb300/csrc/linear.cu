@@ -7,10 +7,8 @@
 namespace pgg {
 namespace {
 
-constexpr int kChunk = 4;  // fp32 results: k-blocks that one accumulator takes
-
-// Shared memory: the ring of stages (weights | rows of X), a 4 KB staging buffer per epilogue warp,
-// the barriers, the group tables.
+// Shared memory: the ring of stages (weights | rows of X), a staging buffer per epilogue warp (4 KB, or 2 of
+// eight warps), the barriers, the group tables.
 template <bool GATED, int TN, int STAGES>
 struct LinSmem {
   static constexpr int kABytes = (GATED ? 2 : 1) * kBN * kBK * 2;
@@ -22,23 +20,67 @@ struct LinSmem {
   static __host__ __device__ constexpr size_t bytes(int G) { return 1024 + (size_t)kGroupOff + 8 * (size_t)(G + 1); }
 };
 
-// One CTA per SM walks the tiles: one thread loads, one multiplies, four warps finish, with two
-// accumulators so that a tile's epilogue and the next one's products overlap.  For short groups, whose
-// weights are read once for few rows: memory bounds it.  256 experts of 96 rows, 4096 x 2048 (4.6 GB): 668 us,
-// the plain copy rate; 128 rows over 32 experts, 5760 x 2880 with swiglu (985 MB): 145 us, the same.
-template <bool GATED, int TN, int STAGES, typename T>
-__global__ void __launch_bounds__(kLinThreads, 1)
+// One chunk of 32 rows of fp32 results, 16 rows at a time (registers, and half the staging of finish_chunk).
+template <bool GATED>
+__device__ __forceinline__ void finish_halves(const LinArgs& a, const float (&z)[32], const float (&u)[32], size_t row,
+                                              int col, int nrows, uint8_t* stg, int lane) {
+  const int ncols = min(32, a.width - col);
+#pragma unroll
+  for (int h = 0; h < 32; h += 16) {
+    if (h >= nrows) break;
+    const size_t r0 = row + h;
+    float v[16], w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      v[j] = z[h + j];
+      w[j] = GATED ? u[h + j] : 0.0f;
+    }
+    if (a.z) {
+      put_rows16(stg, v, a.z + r0 * a.N + col, a.N, nrows - h, ncols, lane);
+      if (GATED) put_rows16(stg, w, a.z + r0 * a.N + a.width + col, a.N, nrows - h, ncols, lane);
+    }
+    if (GATED) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = swiglu_f<false>(v[j], w[j], a.form);
+    } else if (a.act == kActSilu) {
+      apply_act<kActSilu, false>(v, a.form);
+    } else if (a.act == kActGelu) {
+      apply_act<kActGelu, false>(v, a.form);
+    }
+    if (a.residual && lane < ncols) {
+      const float* r = static_cast<const float*>(a.residual) + r0 * a.width + col + lane;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (h + j < nrows) v[j] += r[(size_t)j * a.width];
+    }
+    __syncwarp();  // (the residual may be Y: every row is read before it is written)
+    put_rows16(stg, v, static_cast<float*>(a.y) + r0 * a.width + col, a.width, nrows - h, ncols, lane);
+  }
+}
+
+// One CTA per SM walks the tiles: one thread loads, one multiplies, four or eight warps finish, with two or
+// four accumulators so that a tile's epilogue and the next one's products overlap.
+//
+// bf16 results of short groups, whose weights are read once for few rows: memory bounds it.  256 experts of 96
+// rows, 4096 x 2048 (4.6 GB): 668 us, the plain copy rate; 128 rows over 32 experts, 5760 x 2880 with swiglu
+// (985 MB): 145 us, the same.  fp32 results: the loads from L2 bound it, 8192 x 4096 x 4096 199 us, 1380 TFLOP/s;
+// with swiglu 204 us, 1349.
+template <bool GATED, int TN, int STAGES, typename T, int SHARES>
+__global__ void __launch_bounds__(64 + 128 * SHARES, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinArgs a) {
   using L = LinSmem<GATED, TN, STAGES>;
   // fp32 results: the tensor core's own accumulation drops bits at each step (a sum over 4096 was off by
   // 3.4e-6 of its norm, a chain of fp32 additions by 1.5e-7), so the accumulators hold kChunk k-blocks and
-  // the epilogue adds them up in registers
+  // the epilogue adds them up in registers.  SHARES 2: eight epilogue warps, which have room for the sums of twice
+  // the rows and hide each other's latencies (16384 x 4096 x 1024 with silu 239 -> 145 us; swiglu with tiles of 128
+  // rows, 32 experts of 1024 rows, 5760 x 2880: 841 us, with 64 rows a tile 1086, bound by the loads from L2).
   constexpr bool kWide = std::is_same<T, float>::value;
-  constexpr int kBufs = kWide ? 4 : 2;              // accumulators in turn
   constexpr int kAcc = (GATED ? 2 : 1) * TN;        // columns of an accumulator
+  constexpr int kBufs = kWide && kAcc <= 128 ? 4 : 2;  // accumulators in turn
   constexpr uint32_t kTmemCols = kBufs * kAcc;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert((2 * STAGES + 2 * kBufs + 1) * 8 + 24 <= 256, "barrier area");
+  static_assert(kWide || SHARES == 1, "bf16 results: four epilogue warps");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -63,7 +105,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), 128);
+      mbar_init(smem_u32(&tempty[i]), 128 * SHARES);
     }
     mbar_init(smem_u32(drain), 1);
     s_ctl->abort = 0;
@@ -102,7 +144,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       long long issued = 0;
       bool stalled = false;
       for (int t = blockIdx.x; t < tiles && !aborted && !stalled; t += gridDim.x) {
-        const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
+        const LinTile T_ = lin_tile<kBN>(t, a, TN, nct, s_off, s_tile, cur);
         for (int kb = 0; kb < nkb; ++kb) {
           if (issued == a.stall_at) { stalled = true; break; }
           if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, s_ctl)) { aborted = true; break; }
@@ -133,7 +175,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const uint64_t desc_b = smem_desc(smem_b, 16, 1024, kSwizzle128B);
       uint64_t da = desc_a, db = desc_b;
       for (int t = blockIdx.x; t < tiles && !aborted; t += gridDim.x) {
-        const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
+        const LinTile T_ = lin_tile<kBN>(t, a, TN, nct, s_off, s_tile, cur);
         const uint32_t idesc = idesc_bf16(kBN, (T_.rows + 15) & ~15, false, false);
         for (int k0 = 0; k0 < nkb && !aborted; k0 += kWide ? kChunk : nkb) {
           const int k1 = kWide ? min(nkb, k0 + kChunk) : nkb;
@@ -165,13 +207,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5)
+    // ------------------------------------------------------------ epilogue (warps 2 on)
     const int q = warp & 3;  // the lane quarter of tensor memory that this warp may read
-    uint8_t* stg = smem + L::kEpiOff + (warp - 2) * 4096;
+    uint8_t* stg = smem + L::kEpiOff + (warp - 2) * (4096 / SHARES);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = blockIdx.x; t < tiles && !aborted; t += gridDim.x) {
-      const LinTile T_ = lin_tile<kBN, false>(t, a, TN, nct, s_off, s_tile, cur);
+      const LinTile T_ = lin_tile<kBN>(t, a, TN, nct, s_off, s_tile, cur);
       const int col = T_.col0 + q * 32, n = col + lane;
       float bg = 0.0f, bu = 0.0f;
       if (a.bias && n < a.width) {
@@ -179,10 +221,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         bg = __bfloat162float(b[0]);
         if (GATED) bu = __bfloat162float(b[a.width]);
       }
-      if (kWide) {
-        float z[TN / 32][32], u[GATED ? TN / 32 : 1][32];
+      if constexpr (kWide) {
+        // this warp's chunks of 32 rows: share, share + SHARES, ...
+        constexpr int kStep = 32 * SHARES, kRuns = TN / kStep;
+        const int r0 = 32 * ((warp - 2) >> 2);
+        float z[kRuns][32], u[GATED ? kRuns : 1][32];
 #pragma unroll
-        for (int i = 0; i < TN / 32; ++i)
+        for (int i = 0; i < kRuns; ++i)
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             z[i][j] = bg;
@@ -192,12 +237,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int k0 = 0; k0 < nkb; k0 += kChunk) {
           if (!warp_wait(smem_u32(&tfull[acc]), acc_phase, s_ctl)) { aborted = true; break; }
           tc_fence_after();
-          const uint32_t tb = tmem + acc * kAcc + ((uint32_t)(q * 32) << 16);
+          const uint32_t tb = tmem + acc * kAcc + ((uint32_t)(q * 32) << 16) + r0;
 #pragma unroll
-          for (int i = 0; i < TN / 32; ++i) {
-            if (i * 32 < T_.rows) {  // (the accumulator's columns past the rows hold nothing)
-              add_acc(tb + i * 32, z[i]);
-              if (GATED) add_acc(tb + TN + i * 32, u[GATED ? i : 0]);
+          for (int i = 0; i < kRuns; ++i) {
+            if (r0 + i * kStep < T_.rows) {  // (the accumulator's columns past the rows hold nothing)
+              add_acc(tb + i * kStep, z[i]);
+              if (GATED) add_acc(tb + TN + i * kStep, u[GATED ? i : 0]);
             }
           }
           tc_fence_before();
@@ -207,10 +252,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (aborted) break;
         if (col < a.width) {
 #pragma unroll
-          for (int i = 0; i < TN / 32; ++i)
-            if (i * 32 < T_.rows)
-              finish_chunk<GATED, T>(a, z[i], u[GATED ? i : 0], (size_t)T_.row0 + i * 32, col, min(32, T_.rows - i * 32),
-                                     stg, lane);
+          for (int i = 0; i < kRuns; ++i) {
+            const int c = r0 + i * kStep;
+            if (c < T_.rows) {
+              if constexpr (SHARES == 1)
+                finish_chunk<GATED, T>(a, z[i], u[GATED ? i : 0], (size_t)T_.row0 + c, col, T_.rows - c, stg, lane);
+              else
+                finish_halves<GATED>(a, z[i], u[GATED ? i : 0], (size_t)T_.row0 + c, col, T_.rows - c, stg, lane);
+            }
+          }
         }
         continue;
       }
@@ -244,10 +294,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <bool GATED, int TN, int STAGES, typename T>
+template <bool GATED, int TN, int STAGES, typename T, int SHARES = 1>
 int launch(const LinCall& c, const DeviceInfo& dev) {
   using L = LinSmem<GATED, TN, STAGES>;
-  auto kern = linear_kernel<GATED, TN, STAGES, T>;
+  auto kern = linear_kernel<GATED, TN, STAGES, T, SHARES>;
   CUtensorMap tw, tx;
   const int st = lin_maps(c, TN, false, &tw, &tx);
   if (st) return st;
@@ -256,7 +306,7 @@ int launch(const LinCall& c, const DeviceInfo& dev) {
   if (e != cudaSuccess) return cuda_status(e);
   const int64_t tiles = ((c.a.M + TN - 1) / TN + (c.a.group_lens ? c.a.G : 0)) * ceil_div(c.a.width, kBN);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(dev.sms, tiles));
-  kern<<<grid, kLinThreads, L::bytes(c.a.G), c.stream>>>(tw, tx, c.a);
+  kern<<<grid, 64 + 128 * SHARES, L::bytes(c.a.G), c.stream>>>(tw, tx, c.a);
   return cuda_status(cudaGetLastError());
 }
 
@@ -293,7 +343,8 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
     if (p.us < best.us) best = p;
   };
   auto both = [](double a, double b) { return std::max(a, b) + 0.2 * std::min(a, b); };  // they overlap, not wholly
-  for (int tn : {32, gated && c.f32 ? 64 : 128}) {
+  for (int tn : {32, 64, 128}) {
+    if (tn == 64 && !(gated && c.f32)) continue;  // (elsewhere 128 is as fast)
     if (tn == 32 && live > 1 && rows >= 32) continue;  // (as fast at best, and slow for a long group among them)
     offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.003 * tn});
   }
@@ -325,8 +376,11 @@ int dispatch(const LinCall& c, const DeviceInfo& dev) {
   if (p.kind == Plan::kSplit) return launch_linear_split(c, dev, p.tn, p.splits);
   if (p.kind == Plan::kPair) return launch_linear_pair(c, dev);
   if (c.f32) {
-    if (gated) return p.tn == 32 ? launch<true, 32, 5, float>(c, dev) : launch<true, 64, 5, float>(c, dev);
-    return p.tn == 32 ? launch<false, 32, 9, float>(c, dev) : launch<false, 128, 6, float>(c, dev);
+    if (gated)
+      return p.tn == 32   ? launch<true, 32, 5, float>(c, dev)
+             : p.tn == 64 ? launch<true, 64, 5, float, 2>(c, dev)
+                          : launch<true, 128, 4, float, 2>(c, dev);
+    return p.tn == 32 ? launch<false, 32, 9, float>(c, dev) : launch<false, 128, 6, float, 2>(c, dev);
   }
   if (gated) return p.tn == 32 ? launch<true, 32, 5, __nv_bfloat16>(c, dev) : launch<true, 128, 4, __nv_bfloat16>(c, dev);
   return p.tn == 32 ? launch<false, 32, 9, __nv_bfloat16>(c, dev) : launch<false, 128, 6, __nv_bfloat16>(c, dev);

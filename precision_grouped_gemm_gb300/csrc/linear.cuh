@@ -53,9 +53,10 @@ struct LinTile {
 
 // Tile t: up to TN rows by CW columns, nct column tiles.  Within a group, up to kBand row tiles take turns
 // at one column tile, so that what runs at one time shares a band of X and a few column tiles of W in L2.
-// EVEN: a short group's rows are shared out evenly over its tiles (in steps of 16), so that its last tile
-// is not a small one that costs the weights' loads of a full one.
-template <int CW, bool EVEN>
+// A short group's rows are shared out evenly over its tiles (in steps of 16), so that its last tile is not a
+// small one that costs the weights' loads of a full one; and CTAs take every 152nd tile, so that with two tiles a
+// group one half of them would have all the small ones (64 groups of 150 rows in tiles of 128: 338 -> 244 us).
+template <int CW>
 __device__ __forceinline__ LinTile lin_tile(int t, const LinArgs& a, int TN, int nct, const int32_t* s_off,
                                             const int32_t* s_tile, GroupCursor& cur) {
   cur.at(s_tile, s_off, nullptr, a.G, t);
@@ -63,8 +64,8 @@ __device__ __forceinline__ LinTile lin_tile(int t, const LinArgs& a, int TN, int
   const int band = local / (kBand * nct), in = local - band * kBand * nct;
   const int bm = min(kBand, nmt - band * kBand);
   const int ct = in / bm, mt = band * kBand + in - ct * bm;
-  // (with at most 8 tiles the steps of 16 leave none without rows)
-  const int per = EVEN && nmt <= 8 ? ((cur.len + nmt - 1) / nmt + 15) & ~15 : TN;
+  // (with at most 8 tiles of up to 256 rows the steps of 16 leave none without rows)
+  const int per = nmt <= 8 ? ((cur.len + nmt - 1) / nmt + 15) & ~15 : TN;
   return {cur.g, cur.off + mt * per, min(per, cur.len - mt * per), ct * CW};
 }
 
@@ -103,6 +104,36 @@ __device__ __forceinline__ void put_chunk(uint8_t* stg, const float (&v)[32], fl
   }
   __syncwarp();
 }
+// 16 rows of 32 columns, as put_chunk.
+__device__ __forceinline__ void put_rows16(uint8_t* stg, const float (&v)[16], __nv_bfloat16* dst, size_t ld, int nrows,
+                                           int ncols, int lane) {
+  __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(stg);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3);
+    const uint4 w = reinterpret_cast<const uint4*>(stg)[32 * i + lane];
+    if (r < nrows && c < ncols) *reinterpret_cast<uint4*>(dst + (size_t)r * ld + c) = w;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void put_rows16(uint8_t* stg, const float (&v)[16], float* dst, size_t ld, int nrows, int ncols,
+                                           int lane) {
+  float* s = reinterpret_cast<float*>(stg);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s[j * 32 + lane] = v[j];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7);
+    const uint4 w = reinterpret_cast<const uint4*>(stg)[32 * i + lane];
+    if (r < nrows && c < ncols) *reinterpret_cast<uint4*>(dst + (size_t)r * ld + c) = w;
+  }
+  __syncwarp();
+}
+
 // The chunk's residual in the order of its 16-byte pieces, zeros outside; and v[j] += its row j at this
 // lane's column.
 __device__ __forceinline__ void fetch_chunk(uint4 (&w)[4], const __nv_bfloat16* src, size_t ld, int nrows, int ncols,

@@ -47,22 +47,6 @@ __device__ __forceinline__ bool partner_all(int id, bool ok) {
   return r != 0;
 }
 
-// 16 rows of 32 columns, as put_chunk.
-__device__ __forceinline__ void put_rows16(uint8_t* stg, const float (&v)[16], __nv_bfloat16* dst, size_t ld, int nrows,
-                                           int ncols, int lane) {
-  __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(stg);
-#pragma unroll
-  for (int j = 0; j < 16; ++j) s[j * 32 + lane] = __float2bfloat16_rn(v[j]);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3);
-    const uint4 w = reinterpret_cast<const uint4*>(stg)[32 * i + lane];
-    if (r < nrows && c < ncols) *reinterpret_cast<uint4*>(dst + (size_t)r * ld + c) = w;
-  }
-  __syncwarp();
-}
-
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinArgs a) {
@@ -139,7 +123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       long long issued = 0;
       bool stalled = false;
       for (int t = t0; t < tiles && !aborted && !stalled; t += step) {
-        const LinTile T_ = lin_tile<kCW, true>(t, a, TN, nct, s_off, s_tile, cur);
+        const LinTile T_ = lin_tile<kCW>(t, a, TN, nct, s_off, s_tile, cur);
         const int half = ((T_.rows + 15) & ~15) / 2;  // rows of X in each CTA
         const int col = T_.col0 + (int)rank * kCols, row = T_.row0 + (int)rank * half;
         for (int kb = 0; kb < nkb; ++kb) {
@@ -178,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint64_t desc_b = smem_desc(smem_b, 16, 1024, kSwizzle128B);
       uint64_t da = desc_a, db = desc_b;
       for (int t = t0; t < tiles && !aborted; t += step) {
-        const LinTile T_ = lin_tile<kCW, true>(t, a, TN, nct, s_off, s_tile, cur);
+        const LinTile T_ = lin_tile<kCW>(t, a, TN, nct, s_off, s_tile, cur);
         const uint32_t idesc = idesc_bf16(2 * kBN, (T_.rows + 15) & ~15, false, false);
         if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, s_ctl)) { aborted = true; break; }
         tc_fence_after();
@@ -213,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = t0; t < tiles && !aborted; t += step) {
-      const LinTile T_ = lin_tile<kCW, true>(t, a, TN, nct, s_off, s_tile, cur);
+      const LinTile T_ = lin_tile<kCW>(t, a, TN, nct, s_off, s_tile, cur);
       const int col = T_.col0 + (int)rank * kCols + lane_col, n = col + lane;
       const int ncols = min(32, a.width - col);
       float bias = 0.0f;

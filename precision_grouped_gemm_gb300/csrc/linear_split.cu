@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kLinThreads)
   LinTile T_{0, 0, 0, 0};
   if (live) {
     GroupCursor cur;
-    T_ = lin_tile<kBN, false>(t, a, sa.tn, nct, s_off, s_tile, cur);
+    T_ = lin_tile<kBN>(t, a, sa.tn, nct, s_off, s_tile, cur);
   }
   const int k_begin = (int)((long long)nkb * rank / splits), k_end = (int)((long long)nkb * (rank + 1) / splits);
   const int run = live ? k_end - k_begin : 0;

@@ -209,14 +209,22 @@ def test_join_rows_of_zeros_and_special_values():
 
 
 def test_join_in_place():
-    t, d, n, _, mask = _case(300, 520, True, "channel", 0.2, None, 21)
+    _in_place(300, 520)
+
+
+def test_join_in_place_on_clusters():
+    _in_place(130, 8264)
+
+
+def _in_place(R, C):
+    t, d, n, _, mask = _case(R, C, True, "channel", 0.2, None, 21)
     form = {k: d[k] for k in ("gamma_post", "gamma", "gate", "rng")} | {"p": 0.2}
     h, y, _, _, r1, r2 = pgg.block_join(d["x"], d["residual"], **form)
     for name in ("x", "residual"):
         a = {k: d[k].clone() for k in ("x", "residual")}
         h2, y2, *_ = pgg.block_join(a["x"], a["residual"], h=a[name], **form)
         assert torch.equal(h, h2) and torch.equal(y, y2)
-    dy, dh = (_bf(np.random.default_rng(s), 300, 520).to(DEV) for s in (1, 2))
+    dy, dh = (_bf(np.random.default_rng(s), R, C).to(DEV) for s in (1, 2))
     ref = pgg.block_join_bwd(dy, dh, d["x"], h, r1, r2, **form)
     for first, second in (("dy", "dh"), ("x", "h"), ("dh", "dy"), ("h", "x")):
         a = {"dy": dy.clone(), "dh": dh.clone(), "x": d["x"].clone(), "h": h.clone()}
@@ -263,6 +271,35 @@ def test_join_on_another_stream_and_empty():
     assert h.shape == (0, 64)
     dx, dr, d1, d2, dg = pgg.block_join_bwd(e, e, e, h, z, z, gamma_post=gm, gamma=gm, gate=gm)
     assert (d1 == 0).all() and (d2 == 0).all() and (dg == 0).all() and dg.shape == (64,)
+
+
+def test_join_on_three_streams_at_once():
+    # rows of a thread's one, of two pieces, and of a cluster; with a product between them
+    work = []
+    for seed, (R, C) in enumerate(((700, 520), (500, 4096), (400, 8200))):
+        rng = np.random.default_rng(seed)
+        t = {k: _bf(rng, R, C).to(DEV) for k in ("x", "residual", "dy", "dh")}
+        w = _bf(rng, 64, C, scale=C ** -0.5).to(DEV)
+        form = {"gamma_post": _bf(rng, C).to(DEV), "gamma": _bf(rng, C).to(DEV), "gate": _bf(rng, C).to(DEV), "p": 0.1,
+                "rng": torch.tensor([seed, 5], device=DEV)}
+        work.append((t, w, form))
+
+    def run(t, w, form):
+        h, y, _, _, r1, r2 = pgg.block_join(t["x"], t["residual"], **form)
+        z, _ = pgg.grouped_linear(y[:24], w)
+        return (h, y, z, *pgg.block_join_bwd(t["dy"], t["dh"], t["x"], h, r1, r2, **form))
+
+    ref = [run(*a) for a in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = []
+    for _ in range(6):
+        for st, a in zip(streams, work):
+            with torch.cuda.stream(st):
+                got.append(run(*a))
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert all(torch.equal(u, v) for u, v in zip(out, ref[i % 3]))
 
 
 def test_join_mask_past_32_bits_of_elements():

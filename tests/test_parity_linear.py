@@ -124,6 +124,24 @@ def test_linear_one_long_group_among_short_ones():
         _check(Y, Z, X, W, lens, b, r, act, FORMS[act])
 
 
+@pytest.mark.parametrize("act", list(FORMS))
+@pytest.mark.parametrize("N,K,lens", [
+    (2064, 328, [3000]), (1040, 520, [700]), (544, 1096, [1, 2, 0, 15, 16, 17, 33, 65, 97, 129, 193, 257, 0, 385, 513]),
+    (4112, 200, [150] * 16), (4112, 200, [1030, 0, 22])])
+def test_linear_fp32_in_tiles_of_every_height(N, K, lens, act):
+    # long and short groups, whose rows are shared out evenly over their tiles; the residual in place
+    lens = np.array(lens, dtype=np.int32)
+    M, width = int(lens.sum()), N // 2 if act == "swiglu" else N
+    X, W, b, r = _inputs(M, N, K, lens, N + K, act=act, out=torch.float32)
+    buf = torch.full((M + 9, width), 7.0, device=DEV)
+    buf[:M] = r.to(DEV)
+    gl = None if len(lens) == 1 else torch.from_numpy(lens).to(DEV)
+    Y, Z = pgg.grouped_linear(X.to(DEV), W.to(DEV), gl, bias=_dev(b), residual=buf[:M], Y=buf[:M], act=act, save_z=True,
+                              **FORMS[act])
+    assert (buf[M:] == 7).all()
+    _check(Y, Z, X, W, lens, b, r, act, FORMS[act])
+
+
 def test_linear_equals_the_swiglu_layer():
     lens = np.array([70, 0, 200, 33], dtype=np.int32)
     X, W, _, _ = _inputs(303, 256, 192, lens, 9, act="swiglu")
