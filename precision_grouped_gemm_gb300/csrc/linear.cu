@@ -20,6 +20,8 @@ struct LinSmem {
   static __host__ __device__ constexpr size_t bytes(int G) { return 1024 + (size_t)kGroupOff + 8 * (size_t)(G + 1); }
 };
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // One chunk of 32 rows of fp32 results, 16 rows at a time (registers, and half the staging of finish_chunk).
 template <bool GATED>
 __device__ __forceinline__ void finish_halves(const LinArgs& a, const float (&z)[32], const float (&u)[32], size_t row,
@@ -64,16 +66,15 @@ __device__ __forceinline__ void finish_halves(const LinArgs& a, const float (&z)
 // bf16 results of short groups, whose weights are read once for few rows: memory bounds it.  256 experts of 96
 // rows, 4096 x 2048 (4.6 GB): 668 us, the plain copy rate; 128 rows over 32 experts, 5760 x 2880 with swiglu
 // (985 MB): 145 us, the same.  fp32 results: the loads from L2 bound it, 8192 x 4096 x 4096 199 us, 1380 TFLOP/s;
-// with swiglu 204 us, 1349.
+// with swiglu, whose tiles are half as high, 270 us, 1019.
 template <bool GATED, int TN, int STAGES, typename T, int SHARES>
 __global__ void __launch_bounds__(64 + 128 * SHARES, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinArgs a) {
   using L = LinSmem<GATED, TN, STAGES>;
   // fp32 results: the tensor core's own accumulation drops bits at each step (a sum over 4096 was off by
   // 3.4e-6 of its norm, a chain of fp32 additions by 1.5e-7), so the accumulators hold kChunk k-blocks and
-  // the epilogue adds them up in registers.  SHARES 2: eight epilogue warps, which have room for the sums of twice
-  // the rows and hide each other's latencies (16384 x 4096 x 1024 with silu 239 -> 145 us; swiglu with tiles of 128
-  // rows, 32 experts of 1024 rows, 5760 x 2880: 841 us, with 64 rows a tile 1086, bound by the loads from L2).
+  // the epilogue adds them up in registers (64 sums a thread at most: none are spilled).  SHARES 2: eight epilogue
+  // warps, which hide each other's latencies (16384 x 4096 x 1024 with silu 239 -> 145 us).
   constexpr bool kWide = std::is_same<T, float>::value;
   constexpr int kAcc = (GATED ? 2 : 1) * TN;        // columns of an accumulator
   constexpr int kBufs = kWide && kAcc <= 128 ? 4 : 2;  // accumulators in turn
@@ -225,6 +226,18 @@ __global__ void __launch_bounds__(64 + 128 * SHARES, 1)
         // this warp's chunks of 32 rows: share, share + SHARES, ...
         constexpr int kStep = 32 * SHARES, kRuns = TN / kStep;
         const int r0 = 32 * ((warp - 2) >> 2);
+        if (SHARES > 1 && a.residual && col < a.width) {
+          // the residual's rows come to L2 meanwhile: registers to hold them are not left
+#pragma unroll
+          for (int i = 0; i < kRuns; ++i) {
+            const int r = r0 + i * kStep + lane;
+            if (r < T_.rows) {
+              const float* row = static_cast<const float*>(a.residual) + ((size_t)T_.row0 + r) * a.width;
+              prefetch_l2(row + col);
+              prefetch_l2(row + min(col + 31, a.width - 1));
+            }
+          }
+        }
         float z[kRuns][32], u[GATED ? kRuns : 1][32];
 #pragma unroll
         for (int i = 0; i < kRuns; ++i)
@@ -343,8 +356,7 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
     if (p.us < best.us) best = p;
   };
   auto both = [](double a, double b) { return std::max(a, b) + 0.2 * std::min(a, b); };  // they overlap, not wholly
-  for (int tn : {32, 64, 128}) {
-    if (tn == 64 && !(gated && c.f32)) continue;  // (elsewhere 128 is as fast)
+  for (int tn : {32, gated && c.f32 ? 64 : 128}) {
     if (tn == 32 && live > 1 && rows >= 32) continue;  // (as fast at best, and slow for a long group among them)
     offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.003 * tn});
   }
@@ -376,10 +388,7 @@ int dispatch(const LinCall& c, const DeviceInfo& dev) {
   if (p.kind == Plan::kSplit) return launch_linear_split(c, dev, p.tn, p.splits);
   if (p.kind == Plan::kPair) return launch_linear_pair(c, dev);
   if (c.f32) {
-    if (gated)
-      return p.tn == 32   ? launch<true, 32, 5, float>(c, dev)
-             : p.tn == 64 ? launch<true, 64, 5, float, 2>(c, dev)
-                          : launch<true, 128, 4, float, 2>(c, dev);
+    if (gated) return p.tn == 32 ? launch<true, 32, 5, float>(c, dev) : launch<true, 64, 5, float, 2>(c, dev);
     return p.tn == 32 ? launch<false, 32, 9, float>(c, dev) : launch<false, 128, 6, float, 2>(c, dev);
   }
   if (gated) return p.tn == 32 ? launch<true, 32, 5, __nv_bfloat16>(c, dev) : launch<true, 128, 4, __nv_bfloat16>(c, dev);
