@@ -264,6 +264,27 @@ def test_linear_bwd(M, N, G, empty, act):
         assert torch.equal(buf, dz)
 
 
+@pytest.mark.parametrize("act", [None, "silu", "swiglu"])
+@pytest.mark.parametrize("lens", [[1] * 70, [0] * 31 + [3, 0, 9, 8, 7, 1, 600, 0, 2, 40] + [1, 2, 0] * 20 + [33] + [0] * 30,
+                                  [5000] + [0, 1, 12] * 80, [2] * 1024])
+def test_linear_bwd_of_groups_with_few_rows(lens, act):
+    # groups inside a run, over the ends of runs and over many of them; empty ones before, between and behind
+    lens = np.array(lens, dtype=np.int32)
+    M, N, form = int(lens.sum()), 528, FORMS[act]
+    rng = np.random.default_rng(M)
+    Z, dY = _bf(rng, M, N, scale=1.5), _bf(rng, M, N // 2 if act == "swiglu" else N)
+    dz, db = pgg.grouped_linear_bwd(dY.to(DEV), Z.to(DEV) if act else None, torch.from_numpy(lens).to(DEV), act=act, **form)
+    one, rb1 = pgg.grouped_linear_bwd(dY.to(DEV), Z.to(DEV) if act else None, None, act=act, **form)
+    assert torch.equal(dz, one)  # (an element's gradient is its own; test_linear_bwd checks it)
+    rz, rb, _ = ol.linear_bwd(util.f64(dY), util.f64(Z), lens, act, **form)
+    # dZ's own error, 2^-18 of its terms: |dY| (1 + 1.7 |g|) (|u| + 1) <= 11 |dY| for |g|, |u| <= 1.5, or 1 + 2 |z|
+    dy = np.abs(util.f64(dY))
+    terms = np.tile(11 * dy, 2) if act == "swiglu" else dy * (1 + 2 * np.abs(util.f64(Z))) if act else dy
+    ends = np.concatenate([[0], np.cumsum(lens)])
+    mag = np.array([terms[ends[i]:ends[i + 1]].sum(0) for i in range(len(lens))])
+    _near(db, rb, ((2.0 ** -18 if act else 0.0) + (lens[:, None] / 8 + 32) * 2.0 ** -24) * mag, "dbias")
+
+
 def test_linear_gradients_by_differences_through_the_framework():
     """dX, dW, dbias and the residual's gradient from the calls that a training step makes, against
     central differences of the fp64 oracle along random directions."""
