@@ -49,11 +49,12 @@ __device__ __forceinline__ void finish_halves(const LinArgs& a, const float (&z)
     } else if (a.act == kActGelu) {
       apply_act<kActGelu, false>(v, a.form);
     }
-    if (a.residual && lane < ncols) {
-      const float* r = static_cast<const float*>(a.residual) + r0 * a.width + col + lane;
+    if (a.residual) {
+      const float* r = static_cast<const float*>(a.residual) + r0 * a.width + col + min(lane, ncols - 1);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (h + j < nrows) v[j] += r[(size_t)j * a.width];
+      for (int j = 0; j < 16; ++j) w[j] = r[(size_t)min(j, nrows - h - 1) * a.width];  // (see add_chunk)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += w[j];
     }
     __syncwarp();  // (the residual may be Y: every row is read before it is written)
     put_rows16(stg, v, static_cast<float*>(a.y) + r0 * a.width + col, a.width, nrows - h, ncols, lane);

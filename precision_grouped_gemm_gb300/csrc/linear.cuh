@@ -161,9 +161,15 @@ __device__ __forceinline__ void add_chunk(uint8_t* stg, float (&v)[32], const __
 }
 __device__ __forceinline__ void add_chunk(uint8_t* stg, float (&v)[32], const float* src, size_t ld, int nrows,
                                           int ncols, int lane) {
+  // (places that are not there read the last that is: loads without a branch between them, whose latencies
+  // would follow one another)
+  const float* p = src + min(lane, ncols - 1);
+  float w[32];
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < nrows && lane < ncols) v[j] += src[(size_t)j * ld + lane];
+  for (int j = 0; j < 32; ++j) w[j] = p[(size_t)min(j, nrows - 1) * ld];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] += w[j];
+  __syncwarp();  // (the residual may be Y: every row is read before it is written)
 }
 
 // 32 accumulator columns of this thread's lane, plus the bias; or added to what is there.

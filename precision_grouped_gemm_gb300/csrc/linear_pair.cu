@@ -243,10 +243,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) g[j] = swiglu_f<true>(g[j], u[j], a.form);
               if (a.residual) {
-                const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual) + r0 * a.width + n;
+                const __nv_bfloat16* r =
+                    static_cast<const __nv_bfloat16*>(a.residual) + r0 * a.width + min(n, a.width - 1);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (j < nrows && lane < ncols) g[j] += __bfloat162float(r[(size_t)j * a.width]);
+                for (int j = 0; j < 16; ++j) u[j] = __bfloat162float(r[(size_t)min(j, nrows - 1) * a.width]);  // (see add_chunk)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) g[j] += u[j];
                 __syncwarp();  // (the residual may be Y: every row is read before it is written)
               }
               put_rows16(stg, g, static_cast<__nv_bfloat16*>(a.y) + r0 * a.width + col, a.width, nrows, ncols, lane);
