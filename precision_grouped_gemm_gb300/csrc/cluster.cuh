@@ -116,5 +116,9 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// Arrive on the barrier of this CTA alone.
+__device__ __forceinline__ void mma_commit_pair_own(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 }  // namespace pgg

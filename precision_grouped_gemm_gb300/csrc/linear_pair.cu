@@ -182,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (aborted) {
-        mma_commit_pair(smem_u32(drain));
+        mma_commit_pair_own(smem_u32(drain));  // (nobody waits in the other CTA, which may go before it arrived)
         mbar_wait_drain(smem_u32(drain), 0);
       }
     }
