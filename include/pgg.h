@@ -527,6 +527,20 @@ int pgg_grouped_linear_bwd(const void* dY, const void* Z, const int32_t* group_l
 int pgg_test_stalled_linear(const void* X, const void* W, const int32_t* group_lens, void* Y, int64_t M, int64_t N,
                             int64_t K, int G, int act, int64_t stall_at, uint64_t wait_ns, int32_t* err, void* stream);
 
+/* Test hooks: which kernel pgg_grouped_linear takes for these sizes (grouped: with group_lens), and the
+ * call with a kernel of the tests' choice.
+ *   plan[0]: 0 clusters that share a tile's reduction, 1 one CTA per SM, 2 pairs of CTAs; plan[1]: rows of X
+ *   in a tile; plan[2]: CTAs that share a reduction (else 1); plan[3]: CTAs an SM.  sms: the SMs to plan
+ *   for, 0: the current device's.
+ *   A kernel that the sizes do not have is PGG_ERR_INVALID_ARG.  stall_at -1: no stall; wait_ns 0: the
+ *   call's own limit; else as in pgg_test_stalled_linear. */
+int pgg_test_linear_plan(int64_t M, int64_t N, int64_t K, int G, int grouped, int act, int dtype, int sms,
+                         int32_t* plan);
+int pgg_test_planned_linear(int kind, int tn, int splits, const void* X, const void* W, const int32_t* group_lens,
+                            const void* bias, const void* residual, void* Y, int dtype, void* Z, int64_t M, int64_t N,
+                            int64_t K, int G, int act, float alpha, float offset, float limit, int64_t stall_at,
+                            uint64_t wait_ns, int32_t* err, void* stream);
+
 /* Forms of a block's gate. */
 typedef enum { PGG_GATE_NONE = 0, PGG_GATE_TOKEN = 1, PGG_GATE_CHANNEL = 2 } pgg_gate;
 

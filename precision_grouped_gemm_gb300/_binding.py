@@ -63,6 +63,9 @@ SIGNATURES = {
     "pgg_grouped_linear_bwd": [_P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _F32, _F32, _F32, _P, ctypes.c_size_t, _P,
                                _P],
     "pgg_test_stalled_linear": [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I64, ctypes.c_uint64, _P, _P],
+    "pgg_test_linear_plan": [_I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P],
+    "pgg_test_planned_linear": [_I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _I32, _I32, _F32,
+                                _F32, _F32, _I64, ctypes.c_uint64, _P, _P],
     "pgg_block_join": [_P, _P, _P, _P, _P, _I32, _P, _I64, _I64, ctypes.c_double, _F32, _F32, _F32, _I32, _P, _P, _P,
                        _P, _P, _P, _P],
     "pgg_block_join_bwd_workspace_size": [_I64, _I64, _P],

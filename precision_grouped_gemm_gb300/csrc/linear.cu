@@ -336,6 +336,22 @@ struct Plan {
   int tn, splits;
   double us;
 };
+// Rows of the high tiles of linear_kernel.
+int one_rows(const LinCall& c) { return c.f32 && c.a.act == kActSwiglu ? 64 : 128; }
+// CTAs of a split product's launch: a cluster for every tile that the lengths may make.
+int64_t split_ctas(const LinCall& c, int tn, int splits) {
+  const int64_t live = c.a.group_lens ? std::min<int64_t>(c.a.G, c.a.M) : 1;
+  return ((c.a.M + tn - 1) / tn + live - 1) * ceil_div(c.a.width, kBN) * splits;
+}
+// Whether these tiles and cuts are a form of the split kernel for the sizes.
+bool split_has(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
+  const int H = c.a.act == kActSwiglu ? 2 : 1, nkb = ceil_div(c.a.K, kBK);
+  const int64_t ctas = split_ctas(c, tn, splits);
+  if ((H == 2 && tn > 64) || nkb < 2 * splits || ctas > 4 * (int64_t)dev.sms * splits) return false;
+  if (tn > 32 && ctas > dev.sms) return false;  // (two CTAs an SM have not the room)
+  const int run = ceil_div(nkb, splits), accs = std::min(run, 256 / (H * tn));
+  return !c.f32 || run <= kChunk * accs;  // (sums in fp32: see linear_kernel)
+}
 Plan choose(const LinCall& c, const DeviceInfo& dev) {
   const bool gated = c.a.act == kActSwiglu;
   const int H = gated ? 2 : 1, nkb = ceil_div(c.a.K, kBK);
@@ -357,7 +373,7 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
     if (p.us < best.us) best = p;
   };
   auto both = [](double a, double b) { return std::max(a, b) + 0.2 * std::min(a, b); };  // they overlap, not wholly
-  for (int tn : {32, gated && c.f32 ? 64 : 128}) {
+  for (int tn : {32, one_rows(c)}) {
     if (tn == 32 && live > 1 && rows >= 32) continue;  // (as fast at best, and slow for a long group among them)
     offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.003 * tn});
   }
@@ -367,15 +383,11 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
            7 + both(std::ceil(t / (dev.sms / 2)) * nkb * std::max(0.25, std::min(256.0, rows) * 0.31 / 256), memory)});
   }
   for (int tn : {16, 32, 64, 128}) {
-    if (gated && tn > 64) continue;
     for (int splits : {2, 4, 8}) {
-      // the launch has a cluster for every tile that the lengths may make
-      const int64_t most = ((c.a.M + tn - 1) / tn + (c.a.group_lens ? (int64_t)live - 1 : 0)) * (int64_t)nct;
-      if (nkb < 2 * splits || most > 4 * dev.sms) continue;
-      const bool one = most * splits <= dev.sms;  // CTAs an SM
-      if (tiles(tn) > linear_split_clusters(dev, splits, one) || (tn > 32 && !one)) continue;
-      const int run = ceil_div(nkb, splits), accs = std::min(run, 256 / (H * tn));
-      if (c.f32 && run > kChunk * accs) continue;  // (sums in fp32: see linear_kernel)
+      if (!split_has(c, dev, tn, splits)) continue;
+      const bool one = split_ctas(c, tn, splits) <= dev.sms;  // CTAs an SM
+      if (tiles(tn) > linear_split_clusters(dev, splits, one)) continue;
+      const int run = ceil_div(nkb, splits);
       offer({Plan::kSplit, tn, splits,
              (c.a.group_lens ? 6.5 : 5.0) + both(run * block(tn) * (one ? 1 : 2), memory) + 0.02 * tn});
     }
@@ -383,9 +395,16 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
   return best;
 }
 
-int dispatch(const LinCall& c, const DeviceInfo& dev) {
+// Whether a plan is one that `choose` can give for the sizes.
+bool plan_has(const LinCall& c, const DeviceInfo& dev, const Plan& p) {
+  if (p.kind == Plan::kPair) return !c.f32 && p.tn == 256 && p.splits == 1;
+  if (p.kind == Plan::kOne) return (p.tn == 32 || p.tn == one_rows(c)) && p.splits == 1;
+  return p.kind == Plan::kSplit && (p.tn == 16 || p.tn == 32 || p.tn == 64 || p.tn == 128) &&
+         (p.splits == 2 || p.splits == 4 || p.splits == 8) && split_has(c, dev, p.tn, p.splits);
+}
+
+int run_plan(const LinCall& c, const DeviceInfo& dev, const Plan& p) {
   const bool gated = c.a.act == kActSwiglu;
-  const Plan p = choose(c, dev);
   if (p.kind == Plan::kSplit) return launch_linear_split(c, dev, p.tn, p.splits);
   if (p.kind == Plan::kPair) return launch_linear_pair(c, dev);
   if (c.f32) {
@@ -396,18 +415,22 @@ int dispatch(const LinCall& c, const DeviceInfo& dev) {
   return p.tn == 32 ? launch<false, 32, 9, __nv_bfloat16>(c, dev) : launch<false, 128, 6, __nv_bfloat16>(c, dev);
 }
 
-int linear_impl(const void* X, const void* W, const int32_t* group_lens, const void* bias, const void* residual,
-                void* Y, int dtype, void* Z, int64_t M, int64_t N, int64_t K, int G, int act, float alpha,
-                float offset, float limit, unsigned long long wait_ns, long long stall_at, int32_t* err,
-                void* stream) {
-  if (G < 1 || G > kMaxGroups || (!group_lens && G != 1)) return PGG_ERR_INVALID_ARG;
+int check_sizes(int64_t M, int64_t N, int64_t K, int G, bool grouped, int act, int dtype) {
+  if (G < 1 || G > kMaxGroups || (!grouped && G != 1)) return PGG_ERR_INVALID_ARG;
   if (M < 0 || M > INT32_MAX - 4096) return PGG_ERR_INVALID_ARG;
   if (act < PGG_ACT_NONE || act > PGG_ACT_SWIGLU) return PGG_ERR_INVALID_ARG;
   if (dtype != PGG_DTYPE_F32 && dtype != PGG_DTYPE_BF16) return PGG_ERR_INVALID_ARG;
-  const int mult = act == PGG_ACT_SWIGLU ? 16 : 8;
   for (int64_t d : {N, K})
     if (d < 8 || d >= ((int64_t)1 << 30)) return PGG_ERR_INVALID_ARG;
-  if (N % mult || K % 8) return PGG_ERR_ALIGNMENT;
+  return N % (act == PGG_ACT_SWIGLU ? 16 : 8) || K % 8 ? PGG_ERR_ALIGNMENT : PGG_OK;
+}
+
+int linear_impl(const void* X, const void* W, const int32_t* group_lens, const void* bias, const void* residual,
+                void* Y, int dtype, void* Z, int64_t M, int64_t N, int64_t K, int G, int act, float alpha,
+                float offset, float limit, unsigned long long wait_ns, long long stall_at, int32_t* err,
+                void* stream, const Plan* plan = nullptr) {
+  int st = check_sizes(M, N, K, G, group_lens != nullptr, act, dtype);
+  if (st) return st;
   const float big = 3.0e38f;
   if (!(alpha >= -big && alpha <= big) || !(offset >= -big && offset <= big) || !(limit >= 0.0f && limit <= big))
     return PGG_ERR_INVALID_ARG;
@@ -417,14 +440,14 @@ int linear_impl(const void* X, const void* W, const int32_t* group_lens, const v
     if (!aligned_to(p, 16)) return PGG_ERR_ALIGNMENT;
   if (!aligned_to(group_lens, 4) || !aligned_to(err, 4)) return PGG_ERR_ALIGNMENT;
   DeviceInfo dev;
-  int st = current_device(&dev);
-  if (st != PGG_OK) return st;
+  if ((st = current_device(&dev)) != PGG_OK) return st;
   // (a tile's loads are waited for in one piece by its epilogue: the longest reductions need more than the default)
   if (wait_ns == 0) wait_ns = kWaitTimeoutNs + 2000ull * (unsigned long long)ceil_div(K, kBK);
   LinCall c{X, W, {}, dtype == PGG_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)};
   c.a = {group_lens, G, M, (int)N, (int)K, (int)(act == PGG_ACT_SWIGLU ? N / 2 : N), act, {alpha, offset, limit},
          static_cast<const __nv_bfloat16*>(bias), residual, Y, static_cast<__nv_bfloat16*>(Z), err, wait_ns, stall_at};
-  return dispatch(c, dev);
+  if (plan && !plan_has(c, dev, *plan)) return PGG_ERR_INVALID_ARG;
+  return run_plan(c, dev, plan ? *plan : choose(c, dev));
 }
 
 }  // namespace
@@ -446,6 +469,42 @@ int pgg_test_stalled_linear(const void* X, const void* W, const int32_t* group_l
   if (stall_at < 0 || wait_ns < 100000ull || wait_ns > 1000000000ull) return PGG_ERR_INVALID_ARG;
   return linear_impl(X, W, group_lens, nullptr, nullptr, Y, PGG_DTYPE_BF16, nullptr, M, N, K, G, act, 1.0f, 0.0f, 0.0f,
                      wait_ns, stall_at, err, stream);
+}
+
+int pgg_test_linear_plan(int64_t M, int64_t N, int64_t K, int G, int grouped, int act, int dtype, int sms,
+                         int32_t* plan) {
+  int st = check_sizes(M, N, K, G, grouped != 0, act, dtype);
+  if (st) return st;
+  if (!plan || M < 1 || sms < 0) return PGG_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (sms) dev.sms = sms;
+  else if ((st = current_device(&dev)) != PGG_OK) return st;
+  LinCall c{nullptr, nullptr, {}, dtype == PGG_DTYPE_F32, nullptr};
+  static const int32_t some = 0;  // (the choice asks whether there are lengths, not for them)
+  c.a.group_lens = grouped ? &some : nullptr;
+  c.a.G = G;
+  c.a.M = M;
+  c.a.N = (int)N;
+  c.a.K = (int)K;
+  c.a.width = (int)(act == PGG_ACT_SWIGLU ? N / 2 : N);
+  c.a.act = act;
+  const Plan p = choose(c, dev);
+  plan[0] = p.kind;
+  plan[1] = p.tn;
+  plan[2] = p.splits;
+  plan[3] = p.kind == Plan::kSplit && split_ctas(c, p.tn, p.splits) > dev.sms ? 2 : 1;
+  return PGG_OK;
+}
+
+int pgg_test_planned_linear(int kind, int tn, int splits, const void* X, const void* W, const int32_t* group_lens,
+                            const void* bias, const void* residual, void* Y, int dtype, void* Z, int64_t M, int64_t N,
+                            int64_t K, int G, int act, float alpha, float offset, float limit, int64_t stall_at,
+                            uint64_t wait_ns, int32_t* err, void* stream) {
+  if (kind < Plan::kSplit || kind > Plan::kPair || stall_at < -1) return PGG_ERR_INVALID_ARG;
+  if (wait_ns != 0 && (wait_ns < 100000ull || wait_ns > 1000000000ull)) return PGG_ERR_INVALID_ARG;
+  const Plan p{static_cast<Plan::Kind>(kind), tn, splits, 0.0};
+  return linear_impl(X, W, group_lens, bias, residual, Y, dtype, Z, M, N, K, G, act, alpha, offset, limit, wait_ns,
+                     stall_at, err, stream, &p);
 }
 
 }  // extern "C"
