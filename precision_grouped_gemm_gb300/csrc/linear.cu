@@ -324,13 +324,13 @@ int launch(const LinCall& c, const DeviceInfo& dev) {
   return cuda_status(cudaGetLastError());
 }
 
-// Which kernel, by an estimate of its time in microseconds.  The host knows the rows of all groups together,
-// so row tiles are taken as the mean of equal groups and of one that has half of the rows (64 groups of 2048
-// rows, 4096 x 2048, by Zipf's law: 168 us with 128 rows a tile, 189 with 32; equal: 167, 165).  The
-// constants are what the kernels were measured to take: a k-block's stage at 150 KB a microsecond and SM or
-// its products at the tensor cores' rate, a start and an end.  (Times of split / one / pair: 1 x 4096 x 4096
-// 10.1 / 12.9 / 24; 256 x 4096 x 4096 17.3 / 17.5 / 24.8; 512 x 4096 x 4096 - / 18.0 / 25.1; 1024 x 4096 x 4096
-// - / 29.6 / 26.0; 4000 rows of 16 groups, 2048 x 2048: - / 41 / 37.)
+// Which kernel, by an estimate of its time in microseconds.  The host knows the rows of all groups together, so
+// the work is taken as that of groups whose lengths vary about their mean as a routed batch's do, and to a quarter
+// of a batch with half of its rows in one group (64 groups of 2048 rows, 4096 x 2048, by Zipf's law: 168 us with 128
+// rows a tile, 189 with 32).  The constants are what the kernels were measured to take: a k-block's stage, or its
+// products at the tensor cores' rate, a start and an end.  (Times of split / one / pair: 1 x 4096 x 4096 10.1 / 12.9 /
+// 24; 256 x 4096 x 4096 17.3 / 17.5 / 24.8; 512 x 4096 x 4096 - / 18.0 / 25.1; 1024 x 4096 x 4096 - / 29.6 / 26.0;
+// 4000 rows of 16 groups, 2048 x 2048: - / 40 / 43; 32768 rows of 32, 5760 x 2880 with swiglu: - / 706 / 636.)
 struct Plan {
   enum Kind { kSplit, kOne, kPair } kind;
   int tn, splits;
@@ -368,6 +368,26 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
   };
   auto tiles = [&](int tn) { return row_tiles(tn) * nct; };
   auto block = [&](int tn) { return std::max((H * kBN + tn) * 128 / 150e3, H * std::min<double>(tn, rows) * 0.31 / 256); };
+  // Waves of row tiles by `columns` column tiles over `at_once` places, times a mean tile's time a k-block, of
+  // which `cost` is one with so many rows (shared out evenly: see lin_tile).
+  auto walk = [&](int tn, double columns, double at_once, auto cost) {
+    double n = 0, t = 0;
+    auto add = [&](double groups, double len) {
+      double each = std::ceil(len / tn);
+      if (live > 1) {  // lengths vary by the root of their mean: past a whole number of tiles by chance
+        const double k = std::floor(len / tn + 0.5);
+        each = k < 1 ? 1 : k + 0.5 * std::erfc((k * tn - len) / std::sqrt(2 * len));
+      }
+      n += groups * each;
+      t += groups * each * cost(std::min<double>(tn, len / each + (len > 16 ? 8 : 0)));
+    };
+    add(live < 2 ? 1 : 0.75 * live, rows);
+    if (live > 1) {
+      add(0.25, 0.5 * (double)c.a.M);
+      add(0.25 * (live - 1), 0.5 * (double)c.a.M / (live - 1));
+    }
+    return std::max(1.0, std::ceil(n * columns / at_once - 0.02)) * t / n;
+  };
   Plan best{Plan::kOne, 0, 1, 1e30};
   auto offer = [&](Plan p) {
     if (p.us < best.us) best = p;
@@ -375,12 +395,14 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
   auto both = [](double a, double b) { return std::max(a, b) + 0.2 * std::min(a, b); };  // they overlap, not wholly
   for (int tn : {32, one_rows(c)}) {
     if (tn == 32 && live > 1 && rows >= 32) continue;  // (as fast at best, and slow for a long group among them)
-    offer({Plan::kOne, tn, 1, 4.5 + both(std::ceil(tiles(tn) / sms) * nkb * block(tn), memory) + 0.003 * tn});
+    const double load = tn < 128 || c.f32 ? (H * kBN + tn) * 128 / 150e3 : gated ? 0.36 : 0.21;
+    const double t = walk(tn, nct, sms, [&](double r) { return std::max(load, H * r * 0.31 / 256); });
+    offer({Plan::kOne, tn, 1, 4.5 + both(nkb * t, memory) + 0.003 * tn});
   }
   if (!c.f32) {
-    const double t = row_tiles(256) * std::ceil(c.a.width / (gated ? 128.0 : 256.0));
-    offer({Plan::kPair, 256, 1,
-           7 + both(std::ceil(t / (dev.sms / 2)) * nkb * std::max(0.25, std::min(256.0, rows) * 0.31 / 256), memory)});
+    const double t = walk(256, std::ceil(c.a.width / (gated ? 128.0 : 256.0)), dev.sms / 2,
+                          [](double r) { return std::max(0.22, r * 0.31 / 256); });
+    offer({Plan::kPair, 256, 1, 6 + both(nkb * t, memory)});
   }
   for (int tn : {16, 32, 64, 128}) {
     for (int splits : {2, 4, 8}) {

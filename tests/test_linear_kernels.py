@@ -67,7 +67,10 @@ def test_plan_refusals():
     (8192, 4096, 4096, 1, "swiglu", F32, (ONE, 64, 1, 1)), (715, 232, 5928, 1, None, F32, (ONE, 32, 1, 1)),
     # long ones
     (16384, 4096, 2048, 1, None, BF, (PAIR, 256, 1, 1)), (4096, 2048, 1024, 1, None, BF, (PAIR, 256, 1, 1)),
-    (32768, 2880, 2880, 32, None, BF, (PAIR, 256, 1, 1))])
+    (32768, 2880, 2880, 32, None, BF, (PAIR, 256, 1, 1)),
+    # with swiglu, whose tiles of 128 rows cost more loads: in pairs down to some 250 rows a group
+    (32768, 5760, 2880, 32, "swiglu", BF, (PAIR, 256, 1, 1)), (32768, 4096, 2048, 64, "swiglu", BF, (PAIR, 256, 1, 1)),
+    (8192, 4096, 2048, 8, "swiglu", BF, (PAIR, 256, 1, 1)), (24576, 4096, 2048, 256, "swiglu", BF, (ONE, 128, 1, 1))])
 def test_sizes_take_their_kernel(M, N, K, G, act, out, plan):
     assert _plan(M, N, K, G, G > 1, act, out) == (0, plan)
 
