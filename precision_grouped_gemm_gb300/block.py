@@ -115,11 +115,12 @@ class MoeBlock:
     def forward(self, x, residual=None, gate=None, rng=None):
         """-> (out [T,H], h [T,H]: the new residual stream, saved tensors for `backward`).
 
-        gate: fp32 [T] or bf16 [H], of x; rng: int64 [2] on the device, (seed, offset) of the dropout, which
-        `backward` reads again."""
+        gate: fp32 [T] or bf16 [H], of x; rng: int64 [2] on the device, (seed, offset) of the dropout, of which
+        `saved` has a copy: the caller may step it on before `backward`."""
         E, _, _ = self.sizes
         if self.dropout and rng is None:
             raise ValueError("dropout needs rng")
+        rng = rng.clone() if self.dropout else None
         if self._joined(gate):
             h, y, _, _, rstd_post, rstd = B.block_join(x, residual, eps=self.eps, **self._join(gate, rng))
         else:
