@@ -121,7 +121,8 @@ class MoeBlock:
         if self.dropout and rng is None:
             raise ValueError("dropout needs rng")
         rng = rng.clone() if self.dropout else None
-        if self._joined(gate):
+        joined = self._joined(gate)
+        if joined:
             h, y, _, _, rstd_post, rstd = B.block_join(x, residual, eps=self.eps, **self._join(gate, rng))
         else:
             rstd_post = None
@@ -131,7 +132,9 @@ class MoeBlock:
         Ys, A, Hs = self._experts(Xs, lens, True)
         out = B.moe_combine(Ys, pos, w)
         As, Zs = self._shared(y, out, True)
-        return out, h, (h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys, x, rstd_post, gate, rng, As, Zs)
+        # (a block that only adds x keeps it no longer than the caller does)
+        return out, h, (h, y, rstd, logits, ids, w, Xs, lens, pos, A, Hs, Ys, x if joined else None, rstd_post, gate, rng,
+                        As, Zs)
 
     def backward(self, dout, dh, saved):
         """Gradients of `forward` -> dict: dx, dresidual (dx itself in a block that only adds the two), dgamma,

@@ -62,3 +62,15 @@ def test_both_passes_in_a_graph_that_steps_the_state_between_them():
         o, _, s = b.forward(x, res, rng=torch.tensor([9, 30 + i], device=DEV))
         ref = b.backward(dout, dh, s)
         assert torch.equal(out, o) and all(torch.equal(ref[n], grads[n]) for n in ref)
+
+
+def test_a_plain_block_keeps_only_what_its_backward_reads():
+    rng, b = _block(20, join=False)
+    x, res, dout, dh = (_t(rng, 24, H) for _ in range(4))
+    ref = b.backward(dout, dh, b.forward(x, res)[2])
+    at = x.data_ptr()
+    out, h, saved = b.forward(x, res)
+    assert all(t is None or t.data_ptr() != at for t in saved)
+    x.fill_(float("nan"))   # (as if its memory were another's by now)
+    got = b.backward(dout, dh, saved)
+    assert all(torch.equal(ref[n], got[n]) for n in ref)
