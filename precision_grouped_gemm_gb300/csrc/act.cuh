@@ -97,12 +97,16 @@ __device__ __forceinline__ f2 sigmoid_f2(f2 x) {
   split2(add2(make2(__expf(-a), __expf(-b)), both(1.0f)), a, b);
   return make2(__fdividef(1.0f, a), __fdividef(1.0f, b));
 }
+// The derivative of v s, s = sigmoid(alpha v), from s and p = v s: s + alpha (p (1 - s)).  In this order nothing that is not
+// finite comes up where alpha v passes fp32's range, as 1 + alpha v (1 - s) and its product with s would there.
+__device__ __forceinline__ f2 silu_slope_f2(f2 p, f2 s, float alpha) {
+  return fma2(both(alpha), mul2(p, fma2(s, both(-1.0f), both(1.0f))), s);
+}
 template <int ACT>
 __device__ __forceinline__ f2 act_bwd_f2(f2 dy, f2 z, const ActForm& f) {
   if (ACT == kActSilu) {
-    const f2 az = mul2(z, both(f.alpha)), s = sigmoid_f2(az);
-    // s (1 + az (1 - s))
-    return mul2(dy, mul2(s, fma2(az, fma2(s, both(-1.0f), both(1.0f)), both(1.0f))));
+    const f2 s = sigmoid_f2(mul2(z, both(f.alpha)));
+    return mul2(dy, silu_slope_f2(mul2(z, s), s, f.alpha));
   }
   const f2 e = gauss_f2(z);
   return mul2(dy, fma2(mul2(z, both(0.39894228040143268f)), e, normal_cdf_f2(z, e)));
@@ -120,9 +124,9 @@ __device__ __forceinline__ void swiglu_bwd_f2(f2 dy, f2 g, f2 u, const ActForm& 
     g = make2(min_nan(g0, f.limit), min_nan(g1, f.limit));
     u = make2(max_nan(min_nan(u0, f.limit), -f.limit), max_nan(min_nan(u1, f.limit), -f.limit));
   }
-  const f2 ag = mul2(g, both(f.alpha)), s = sigmoid_f2(ag), ds = mul2(dy, s);
-  dg = mul2(mul2(ds, add2(u, both(f.offset))), fma2(ag, fma2(s, both(-1.0f), both(1.0f)), both(1.0f)));
-  du = mul2(ds, g);
+  const f2 s = sigmoid_f2(mul2(g, both(f.alpha))), p = mul2(g, s);
+  dg = mul2(mul2(dy, add2(u, both(f.offset))), silu_slope_f2(p, s, f.alpha));
+  du = mul2(dy, p);
   if (f.limit > 0.0f) {
     split2(dg, a, b);
     dg = make2(og0 ? 0.0f : a, og1 ? 0.0f : b);
