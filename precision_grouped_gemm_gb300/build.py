@@ -9,6 +9,7 @@ library needs (tensor-map encoding) is fetched at run time.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -24,6 +25,23 @@ SOURCES = ["pgg_api.cu", "gemm_bf16.cu", "mx_quant.cu", "gemm_mx.cu", "moe_glue.
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]
+
+# Files whose kernels hold their sums in registers beside tensor memory: they are built without a spilled register
+# or not at all (one that spilled some of 128 sums ended in an illegal instruction, and why was not found).
+NO_SPILLS = ("linear.cu", "linear_pair.cu", "linear_split.cu")
+
+
+def spilled(log: str) -> list:
+    """The kernels of a ptxas -v log that spill registers: [(mangled name, bytes stored)]."""
+    found, name = [], None
+    for line in log.splitlines():
+        m = re.search(r"(?:Compiling entry function|Function properties for) '?([\w$.]+)", line)
+        if m:
+            name = m.group(1)
+        m = re.search(r"(\d+) bytes spill stores, (\d+) bytes spill loads", line)
+        if m and (int(m.group(1)) or int(m.group(2))):
+            found.append((name, int(m.group(1))))
+    return found
 
 
 def nvcc() -> str:
@@ -57,6 +75,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
             f.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr[-4000:]}")
+        bad = spilled(r.stdout + r.stderr) if src in NO_SPILLS else []
+        if bad:
+            os.remove(o)
+            raise RuntimeError(f"{src}: kernels that spill registers: {bad}")
         if verbose:
             print(r.stderr)
         return o

@@ -54,7 +54,7 @@ __device__ __forceinline__ float act_any(float z, const LinArgs& a) {
 }
 
 template <bool GATED, typename T>
-__global__ void __launch_bounds__(kLinThreads)
+__global__ void __launch_bounds__(kLinThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ SplitArgs sa) {
   constexpr int H = GATED ? 2 : 1;
