@@ -38,7 +38,11 @@ __device__ __forceinline__ uint32_t cluster_count() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Its two halves, which order no memory: every thread arrives, and waits before it arrives again.
+// Its two halves: every thread arrives, and waits before it arrives again.  A release orders what the thread read and
+// wrote before what another writes after its wait; a relaxed arrival orders nothing.
+__device__ __forceinline__ void cluster_arrive_release() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of CTA `rank`'s counterpart of this CTA's shared-memory address.

@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     const int q = warp & 3;
     if (!warp_wait(smem_u32(done), 0, s_ctl) || s_ctl->abort) aborted = true;
     aborted = __any_sync(0xffffffffu, aborted);
-    if (sa.in_ring) cluster_arrive();
+    // (the stages, whose products are complete, before the sums that others write in their place)
+    if (sa.in_ring) cluster_arrive_release();
     cluster_wait();
     if (!aborted) {
       tc_fence_after();
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
   }
   __syncwarp();
   if (warp < 2 || run == 0) {
-    if (sa.in_ring) cluster_arrive();
+    if (sa.in_ring) cluster_arrive_release();
     cluster_wait();
   }
   // what the epilogue reads besides the sums: the bias, and the residual of this warp's first row
