@@ -352,7 +352,7 @@ bool split_has(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
   const int run = ceil_div(nkb, splits), accs = std::min(run, 256 / (H * tn));
   return !c.f32 || run <= kChunk * accs;  // (sums in fp32: see linear_kernel)
 }
-Plan choose(const LinCall& c, const DeviceInfo& dev) {
+int choose(const LinCall& c, const DeviceInfo& dev, Plan* plan) {
   const bool gated = c.a.act == kActSwiglu;
   const int H = gated ? 2 : 1, nkb = ceil_div(c.a.K, kBK);
   const double live = c.a.group_lens ? (double)std::min<int64_t>(c.a.G, c.a.M) : 1;  // groups that can have rows
@@ -408,13 +408,17 @@ Plan choose(const LinCall& c, const DeviceInfo& dev) {
     for (int splits : {2, 4, 8}) {
       if (!split_has(c, dev, tn, splits)) continue;
       const bool one = split_ctas(c, tn, splits) <= dev.sms;  // CTAs an SM
-      if (tiles(tn) > linear_split_clusters(dev, splits, one)) continue;
+      int clusters;
+      const int st = linear_split_clusters(dev, splits, one, &clusters);
+      if (st) return st;
+      if (tiles(tn) > clusters) continue;
       const int run = ceil_div(nkb, splits);
       offer({Plan::kSplit, tn, splits,
              (c.a.group_lens ? 6.5 : 5.0) + both(run * block(tn) * (one ? 1 : 2), memory) + 0.02 * tn});
     }
   }
-  return best;
+  *plan = best;
+  return PGG_OK;
 }
 
 // Whether a plan is one that `choose` can give for the sizes.
@@ -468,8 +472,10 @@ int linear_impl(const void* X, const void* W, const int32_t* group_lens, const v
   LinCall c{X, W, {}, dtype == PGG_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)};
   c.a = {group_lens, G, M, (int)N, (int)K, (int)(act == PGG_ACT_SWIGLU ? N / 2 : N), act, {alpha, offset, limit},
          static_cast<const __nv_bfloat16*>(bias), residual, Y, static_cast<__nv_bfloat16*>(Z), err, wait_ns, stall_at};
-  if (plan && !plan_has(c, dev, *plan)) return PGG_ERR_INVALID_ARG;
-  return run_plan(c, dev, plan ? *plan : choose(c, dev));
+  if (plan) return plan_has(c, dev, *plan) ? run_plan(c, dev, *plan) : PGG_ERR_INVALID_ARG;
+  Plan chosen;
+  st = choose(c, dev, &chosen);
+  return st ? st : run_plan(c, dev, chosen);
 }
 
 }  // namespace
@@ -510,7 +516,8 @@ int pgg_test_linear_plan(int64_t M, int64_t N, int64_t K, int G, int grouped, in
   c.a.K = (int)K;
   c.a.width = (int)(act == PGG_ACT_SWIGLU ? N / 2 : N);
   c.a.act = act;
-  const Plan p = choose(c, dev);
+  Plan p;
+  if ((st = choose(c, dev, &p))) return st;
   plan[0] = p.kind;
   plan[1] = p.tn;
   plan[2] = p.splits;

@@ -276,7 +276,7 @@ inline int lin_maps(const LinCall& c, uint32_t xbox, bool halves, CUtensorMap* t
 // Launchers of the kernels (linear.cu, linear_pair.cu, linear_split.cu).
 int launch_linear_pair(const LinCall& c, const DeviceInfo& dev);
 int launch_linear_split(const LinCall& c, const DeviceInfo& dev, int tn, int splits);
-// Clusters of `splits` CTAs that run at one time, with one CTA an SM or two.
-int linear_split_clusters(const DeviceInfo& dev, int splits, bool one);
+// Clusters of `splits` CTAs that run at one time, with one CTA an SM or two, into *count.
+int linear_split_clusters(const DeviceInfo& dev, int splits, bool one, int* count);
 
 }  // namespace pgg

@@ -316,22 +316,23 @@ int launch(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {
 
 // A cluster's CTAs are on the SMs of one GPC, so this is less than the SMs would hold.  The same on every
 // device that the library runs on, and asked for once.
-int linear_split_clusters(const DeviceInfo& dev, int splits, bool one) {
+int linear_split_clusters(const DeviceInfo& dev, int splits, bool one, int* count) {
   static std::atomic<int> known[9][2];
   std::atomic<int>& slot = known[splits][one];
-  int n = slot.load(std::memory_order_relaxed);
-  if (n > 0) return n;
+  *count = slot.load(std::memory_order_relaxed);
+  if (*count > 0) return PGG_OK;
   auto kern = linear_split_kernel<false, __nv_bfloat16>;
   const int smem = one ? kSmemOne : kSmemTwo;
   cudaLaunchAttribute at{};
   const cudaLaunchConfig_t cfg = config((unsigned)(dev.sms * splits), splits, smem, nullptr, &at);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return 1;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(count, kern, &cfg);
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // (told by the status, not by the next launch too)
+    return cuda_status(e);
   }
-  slot.store(n, std::memory_order_relaxed);
-  return n;
+  slot.store(*count = std::max(1, *count), std::memory_order_relaxed);
+  return PGG_OK;
 }
 
 int launch_linear_split(const LinCall& c, const DeviceInfo& dev, int tn, int splits) {

@@ -54,6 +54,16 @@ def test_plan_refusals():
     assert run(ns=50_000) == INVALID and run(ns=2_000_000_000) == INVALID
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="asks a machine without a device")
+def test_no_plan_where_the_device_does_not_answer():
+    # the clusters that fit are asked of the device: an answer that fails is the call's, not taken as one cluster
+    from precision_grouped_gemm_gb300 import build
+    build.build()
+    for _ in range(2):
+        assert _plan(1, 4096, 4096, sms=152)[0] not in (0, INVALID)
+    assert _plan(4096, 2048, 72, sms=152)[0] == 0   # (too short to cut: nothing to ask)
+
+
 # ---------------------------------------------------------------- what the sizes take
 
 @pytest.mark.gpu
