@@ -580,6 +580,7 @@ int pgg_block_join_bwd_workspace_size(int64_t R, int64_t C, size_t* bytes);
  *   forward call (h and rstd NULL without gamma, rstd_post without gamma_post); the other arguments are
  *   that call's.  dx [R, C] bf16; dresidual [R, C] bf16 or NULL; dgamma_post, dgamma [C], dgate [R] or
  *   [C] fp32, each given where its operand is, summed up in a fixed order.
+ *   What the mask drops passes nothing on, whatever it, its row's norm and a row's gate hold.
  *   dx and dresidual may be dy, dh, x or h (not the same of them).  ws: device scratch, 16-byte
  *   aligned; it holds nothing between calls, and calls that may overlap need one each.  R == 0 writes
  *   zero sums. */

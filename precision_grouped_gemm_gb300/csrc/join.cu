@@ -475,7 +475,9 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
       const float c = -rstd2[k] * rstd2[k] * (q[k] * rstd2[k] * a.inv_c);
       const float qx = fmaf(c, q[2 * ROWS + k], q[ROWS + k]);
       if (a.dgate_row && threadIdx.x == 0 && rank == 0 && is) a.dgate_row[row + k * grid] = f * rstd1[k] * qx;
-      const float m = a.gamma1 ? -rstd1[k] * rstd1[k] * (qx * a.inv_c) : 0.0f, fs = f * scale[k];
+      const float m = a.gamma1 ? -rstd1[k] * rstd1[k] * (qx * a.inv_c) * scale[k] : 0.0f;
+      // x itself is masked where it is not normed, and of a row whose norm is not finite (rstd NaN or 0)
+      const bool mask_x = a.drop.rng && !(a.gamma1 && rstd1[k] > 0.0f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const bool in = is && v0 + (int)threadIdx.x + j * (int)blockDim.x < v1;
@@ -489,19 +491,21 @@ __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs 
           for (int i = 0; i < 4; ++i) o[i] = mul2(both(a.ra), e[k][j][i]);
           a.dres[base + j * blockDim.x] = round8(o);
         }
-        if (a.drop.rng) keep_only(e[k][j], keep[k][j]);  // dk
+        // scale dk, masked behind the factor: a row's gate or norm does not come into its dropped places
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[k][j][i] = mul2(e[k][j][i], both(scale[k]));
+        if (a.drop.rng) keep_only(e[k][j], keep[k][j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = mul2(gg[j][i], e[k][j][i]);
         if (a.gamma1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] = fma2(x[i], both(m), o[i]);
-        } else if (a.drop.rng) {
-          keep_only(x, keep[k][j]);  // (with the norm a value that is not finite has the whole row)
         }
+        if (mask_x) keep_only(x, keep[k][j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sum_b[j][i] = fma2(mul2(e[k][j][i], x[i]), both(scale[k]), sum_b[j][i]);
-          o[i] = mul2(both(fs), o[i]);
+          sum_b[j][i] = fma2(e[k][j][i], x[i], sum_b[j][i]);
+          o[i] = mul2(both(f), o[i]);
         }
         if (in) a.dx[base + j * blockDim.x] = round8(o);
       }
