@@ -7,7 +7,7 @@ operands, quantized when the block is made and again when W1 or W2 have changed,
 the MX operand of its tokens itself.
 
     s = x + residual, y = rmsnorm(s) gamma     add_rmsnorm
-    logits = y gate^T                          grouped_gemm_fwd with one group
+    logits = y gate^T, in fp32                 grouped_linear
     ids, w = top-k of the logits               moe_route
     out = sum_j w_j expert_{ids_j}(y)          moe_permute ... moe_combine, or moe_decode
 
@@ -79,8 +79,9 @@ class MoeBlock:
     def _one_group(self, rows, device):
         return torch.full((1,), rows, dtype=torch.int32, device=device)
 
-    def _route(self, y):
-        logits = B.grouped_gemm_fwd(y, self.gate[None], self._one_group(y.shape[0], y.device))
+    def _route(self, y, err=None):
+        # (fp32: rounded to bf16, logits tie, and move an expert's weight by 2^-8 of the logit)
+        logits, _ = B.grouped_linear(y, self.gate, out_dtype=torch.float32, err=err)
         ids, w = B.moe_route(logits, self.k, self.bias, self.score, self.renormalize, self.scale)
         return logits, ids, w
 
@@ -160,7 +161,7 @@ class MoeBlock:
             g["dS2"] = B.grouped_gemm_wgrad(As, dout, one)[0]
             g["dS1"] = B.grouped_gemm_wgrad(y, dZs, one)[0]
             dy += B.grouped_gemm_dgrad(dZs, self.S1[None], one)
-        dlogits = B.moe_route_bwd(logits, ids, dw, self.bias, self.score, self.renormalize, self.scale)
+        dlogits = B.moe_route_bwd(logits, ids, dw, self.bias, self.score, self.renormalize, self.scale).bfloat16()
         g["dgate"] = B.grouped_gemm_wgrad(y, dlogits, one)[0]
         dy += B.grouped_gemm_dgrad(dlogits, self.gate[None], one)
         if self._joined(gate):
@@ -183,7 +184,7 @@ class MoeBlock:
         err = self._err if err is None else err
         if self._biased:
             h, y, _, _ = self._entry(x, residual, gate)
-            _, ids, w = self._route(y)
+            _, ids, w = self._route(y, err)
             Xs, lens, pos = B.moe_permute(ids, y, self.sizes[0], err=err)
             out = B.moe_combine(self._experts(Xs, lens, False, err)[0], pos, w)
             self._shared(y, out, False, err)
@@ -198,7 +199,7 @@ class MoeBlock:
                 # (a capture quantizes into its own memory, at every replay)
                 mx = self._quantized() if torch.cuda.is_current_stream_capturing() else self.quantize_weights()
         h, y, codes, scales = self._entry(x, residual, gate)
-        _, ids, w = self._route(y)
+        _, ids, w = self._route(y, err)
         if self.fmt is None:
             out = B.moe_decode(y, ids, w, self.W1, self.W2, swiglu_limit=self.swiglu_limit, ws=ws, err=err)
         else:
