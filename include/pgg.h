@@ -556,8 +556,8 @@ typedef enum { PGG_GATE_NONE = 0, PGG_GATE_TOKEN = 1, PGG_GATE_CHANNEL = 2 } pgg
  *   call runs (a replayed graph takes what it holds then).  Element i of the row-major tensor is kept
  *   where word i % 4 of Philox4x32-10 with the counter (i / 4, offset), low words first, and the key
  *   seed is at least floor(p 2^32); a dropped element is 0 whatever it, its row's norm and a row's gate
- *   hold.  Calls with other offsets have independent masks.  The mask is not stored: pgg_block_join_bwd computes it again from the same
- *   rng and p.
+ *   hold.  Calls with other offsets have independent masks.  The mask is not stored: pgg_block_join_bwd
+ *   computes it again from the same rng and p.
  *   Outputs, each optional (NULL), at least one given: h, y [R, C] bf16, rstd_post, rstd [R] fp32, and
  *   with fmt codes and scales as in pgg_add_rmsnorm.  8 <= C <= PGG_NORM_MAX_COLS, C % 8 == 0, with codes
  *   C % 32 == 0; eps >= 0.  h may be x or residual (in place).  R == 0 is a no-op.  Sums of squares are

@@ -1,8 +1,8 @@
 // Activations of the products with biases (grouped_linear) and their derivatives, in fp32:
 //
 //   silu     z sigmoid(alpha z)
-//   gelu     z Phi(z), Phi the normal distribution function (the exact form, by erfc: no
-//            cancellation in the lower tail)
+//   gelu     z Phi(z), Phi the normal distribution function (the exact form; by e^(-z^2/2) times a fitted
+//            polynomial, normal_cdf_f2: no cancellation in the lower tail)
 //   swiglu   g sigmoid(alpha g) (u + offset) of the halves [g | u] of z, with limit > 0 clamped
 //            first: g <- min(g, limit), u <- clamp(u, -limit, limit)
 //
@@ -21,7 +21,8 @@ struct ActForm {
 };
 
 // e^x.  FAST: the short exponential, whose error (some 2^-20 at |x| = 10) stays far inside the rounding to
-// bf16; fp32 results take the full one.
+// bf16; fp32 Y takes the full one.  The gradient has the short one throughout, its fp32 sums too: a term is off by
+// 2^-22 |dY| from it (e^-x is largest where its share of the sigmoid is smallest), no more than the sum's own additions.
 template <bool FAST>
 __device__ __forceinline__ float exp_f(float x) {
   return FAST ? __expf(x) : expf(x);
@@ -33,8 +34,9 @@ __device__ __forceinline__ float sigmoid_f(float x) {
 }
 
 // The normal distribution function, two at a time, from e = exp(-z^2 / 2): Phi(-|z|) / e =
-// erfcx(|z| / sqrt 2) / 2 is t P(t) with t = 1 / (1 + 0.3 |z|) and a polynomial P fitted to it over |z| <= 14 (the
-// relative error is below 1.5e-7, 4.5e-7 in fp32 arithmetic, in the tail too).
+// erfcx(|z| / sqrt 2) / 2 is t P(t) with t = 1 / (1 + 0.3 |z|) and a polynomial P fitted to it over |z| <= 14.  The
+// relative error of the fit is below 1.7e-7; in fp32 arithmetic 4.3e-7, and 8e-7 with a quotient that is off by its two
+// units, in the tail too.
 __device__ __forceinline__ f2 normal_cdf_f2(f2 z, f2 e) {
   float a, b, c, d;
   split2(z, a, b);
@@ -97,8 +99,8 @@ __device__ __forceinline__ f2 sigmoid_f2(f2 x) {
   split2(add2(make2(__expf(-a), __expf(-b)), both(1.0f)), a, b);
   return make2(__fdividef(1.0f, a), __fdividef(1.0f, b));
 }
-// The derivative of v s, s = sigmoid(alpha v), from s and p = v s: s + alpha (p (1 - s)).  In this order nothing that is not
-// finite comes up where alpha v passes fp32's range, as 1 + alpha v (1 - s) and its product with s would there.
+// The derivative of v s, s = sigmoid(alpha v), from s and p = v s: s + alpha (p (1 - s)).  In this order nothing that is
+// not finite comes up where alpha v passes fp32's range, as 1 + alpha v (1 - s) and its product with s would there.
 __device__ __forceinline__ f2 silu_slope_f2(f2 p, f2 s, float alpha) {
   return fma2(both(alpha), mul2(p, fma2(s, both(-1.0f), both(1.0f))), s);
 }

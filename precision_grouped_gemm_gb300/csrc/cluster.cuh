@@ -7,7 +7,7 @@ namespace pgg {
 // True in one thread of a converged warp.  A role that one thread plays is entered by this: the compiler
 // then knows that one thread is there, and the operands that TMA and the tensor cores take from uniform
 // registers need no loop over the warp's lanes (with `lane == 0` a k-block's four MMAs and commit took
-// some 0.3 us to issue, and 16384 x 4096 x 2048 165 us instead of 145).
+// some 0.3 us to issue, and 16384 x 4096 x 2048 175 us instead of 157).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));

@@ -333,15 +333,16 @@ struct JoinBwdArgs {
 // one's arithmetic fills the waits of another's sums.  The longest rows are shared out over CL CTAs.
 //
 // The chain of a row's steps bounds it before memory does (with dropout 56% of the issue slots taken), so the
-// sums over a row are arranged to need one barrier.  With e = dh + rstd2 u, xk = x where it is kept, else 0, and gg = gamma1 gate_col (ones where there are none):
+// sums over a row are arranged to need one barrier.  With e = dh + rstd2 u, xk = x where it is kept, else 0, and
+// gg = gamma1 gate_col (ones where there are none):
 //   d = e + c h,  c = -rstd2^3 mean(u h)
 //   q = sum gg xk d = sum gg xk e + c sum gg xk h
 // and all the gradients of the branch come from q and, over the rows, S = sum gate_row rstd1 xk d.  With
 // f = rb / (1 - p):
 //   dgamma1 = f gate_col S    dgate_col = f gamma1 S    dgate_row = f rstd1 q
-//   dx = f gate_row rstd1 (gg dk - x rstd1^2 q / C),  dk = d where it is kept, else 0
-// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 52 us, with dropout 66; 16384 x 4096 with
-// dropout (805 MB) 151.
+//   dx = f (gg g - x gate_row rstd1^3 q / C),  g = gate_row rstd1 d where it is kept, else 0
+// 8192 x 2880 (283 MB, 41.8 us at the copy rate): 52 us, with dropout 67; 16384 x 4096 with
+// dropout (805 MB) 150.
 template <int V, int ROWS, int CL, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) join_bwd_kernel(const JoinBwdArgs a) {
   extern __shared__ uint4 s_row[];  // [DEPTH][ROWS][4][V][blockDim]
@@ -699,8 +700,9 @@ int pgg_block_join_bwd(const void* dy, const void* dh, const void* x, const void
                 col ? static_cast<const uint4*>(gate) : nullptr, make_drop(rng, p), R, nvec, 1.0f / (float)C,
                 residual_scale, branch_scale, static_cast<uint4*>(dx), static_cast<uint4*>(dresidual),
                 col ? nullptr : dgate, static_cast<float*>(ws)};
-  // Up to 384 threads two rows at a time, on one block an SM of more registers (8192 x 2880, without dropout: 52.1
-  // us, with 65.8; one row 53.4 and 69, with two blocks an SM 54.5 and 71.8; four rows 52.8 and 69.2).
+  // Up to 384 threads two rows at a time, on one block an SM of more registers (8192 x 2880, without dropout 52.1
+  // us and with 65.8 when it was chosen, 52.3 and 66.9 now; one row 53.4 and 69, with two blocks an SM 54.5 and
+  // 71.8; four rows 52.8 and 69.2).
   auto kern = V == 1      ? join_bwd_kernel<1, 2, 1, 384>
               : ctas == 1 ? join_bwd_kernel<2, 1, 1, 512>
                           : join_bwd_kernel<2, 1, 4, 512>;

@@ -66,16 +66,16 @@ __device__ __forceinline__ void finish_halves(const LinArgs& a, const float (&z)
 //
 // bf16 results of short groups, whose weights are read once for few rows: memory bounds it.  256 experts of 96
 // rows, 4096 x 2048 (4.6 GB): 668 us, the plain copy rate; 128 rows over 32 experts, 5760 x 2880 with swiglu
-// (985 MB): 145 us, the same.  fp32 results: the loads from L2 bound it, 8192 x 4096 x 4096 199 us, 1380 TFLOP/s;
-// with swiglu, whose tiles are half as high, 270 us, 1019.
+// (985 MB): 145 us, the same.  fp32 results: the loads from L2 bound it, 8192 x 4096 x 4096 199 to 206 us by
+// GPU, 1380 TFLOP/s; with swiglu, whose tiles are half as high, 270 to 288 us, 1019.
 template <bool GATED, int TN, int STAGES, typename T, int SHARES>
 __global__ void __launch_bounds__(64 + 128 * SHARES, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinArgs a) {
   using L = LinSmem<GATED, TN, STAGES>;
   // fp32 results: the tensor core's own accumulation drops bits at each step (a sum over 4096 was off by
   // 3.4e-6 of its norm, a chain of fp32 additions by 1.5e-7), so the accumulators hold kChunk k-blocks and
-  // the epilogue adds them up in registers (64 sums a thread at most: none are spilled).  SHARES 2: eight epilogue
-  // warps, which hide each other's latencies (16384 x 4096 x 1024 with silu 239 -> 145 us).
+  // the epilogue adds them up in registers (64 sums a thread at most; the build fails where one is spilled).
+  // SHARES 2: eight epilogue warps, which hide each other's latencies (16384 x 4096 x 1024 with silu 239 -> 145 us).
   constexpr bool kWide = std::is_same<T, float>::value;
   constexpr int kAcc = (GATED ? 2 : 1) * TN;        // columns of an accumulator
   constexpr int kBufs = kWide && kAcc <= 128 ? 4 : 2;  // accumulators in turn

@@ -327,8 +327,8 @@ struct Cut {
   int nvec, per, slabs, runs, run_rows;
 };
 // Resident blocks an SM, with the rows that a thread loads ahead (UNROLL): 32768 x 5760 with swiglu, 944 MB, 4
-// blocks of one row 171 us, 3 of two 179, 5 of one (fewer registers than it needs) 208; gelu 4 of two 146, 3 of
-// four 148, 5 of two 160; silu 3 of four 156, 4 of two 159.
+// blocks of one row 171 us when it was chosen (162 now), 3 of two 179, 5 of one (fewer registers than it needs) 208;
+// 32768 x 4096 with gelu 4 of two 146, 3 of four 148, 5 of two 160; with silu 3 of four 127.5, 4 of two 128.
 constexpr int per_sm(int act) { return act == kActNone ? 5 : act == kActSilu ? 3 : 4; }
 Cut cut(int64_t M, int64_t N, int G, int act) {
   const int64_t width = act == kActSwiglu ? N / 2 : N;

@@ -12,8 +12,8 @@
 // its accumulator takes arrivals from the other CTA.
 //
 // The tensor cores bound it: 16384 x 4096 x 2048 with a residual 154 us, 1786 TFLOP/s, pipes 86% busy (13.5 waves
-// of tiles in 14); 32 experts of 1092 rows, 5760 x 2880 with swiglu and Z 638 us, 1703 TFLOP/s, 91% (700
-// on other GPUs).  Over seconds the power cap lowers the clock to 1.33 to 1.48 GHz: 179 and 740 us.
+// of tiles in 14); 32 experts of 1092 rows, 5760 x 2880 with swiglu and Z 619 to 638 us by GPU, 1703 TFLOP/s, 91%.  Over
+// seconds the power cap lowers the clock to 1.33 to 1.48 GHz: 179 and 732 to 758 us.
 #include "cluster.cuh"
 #include "linear.cuh"
 

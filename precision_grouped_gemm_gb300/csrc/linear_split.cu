@@ -6,8 +6,8 @@
 // cluster is enough where the sums have a place of their own; many rows' sums take the place of the stages
 // instead, when every CTA of the cluster has done with its own.
 //
-// Latency bounds it: 1 x 4096 x 4096 10.9 us on 5.0 of bytes, of which 2.5 are before the first load has landed
-// and 2 behind the last one (sums out, the cluster's barrier, the rows); 37 x 256 x 4096 7.4 us.
+// Latency bounds it: 1 x 4096 x 4096 10.8 us on 5.0 of bytes, of which 2.5 are before the first load has landed
+// and 2 behind the last one (sums out, the cluster's barrier, the rows); 37 x 256 x 4096 6.4 us.
 #include <atomic>
 
 #include "cluster.cuh"

@@ -7,7 +7,7 @@ derivative in fp32 is the biases' gradient of groups of one row.
 Tolerances, u = 2^-24, from the arithmetic.  An exponential of -x: the argument alpha v is rounded, x u; the full one has 2
 units, 4 u, the short one 2 + 1.173 x units, (4 + 2.4 x) u, by their documented bounds: at most (4 + 3.4 x) u.  A sigmoid is
 1 / (1 + e) or e / (1 + e): sum and quotient (two units) 5 u, a product u, and the exponential's error times its share
-sigmoid(-v): (10 + 3.4 |v| sigmoid(-v)) u.  1 - s has the error of s and u, which a derivative multiplies by |v| s.  Phi(-|z|): the exponential's argument z^2 / 2 is rounded, z^2 u; the fit 1.5e-7 = 3 u; its variable 5 u, to which the fit's
+sigmoid(-v): (10 + 3.4 |v| sigmoid(-v)) u.  1 - s has the error of s and u, which a derivative multiplies by |v| s.  Phi(-|z|): the exponential's argument z^2 / 2 is rounded, z^2 u; the fit 1.7e-7 = 3 u; its variable 5 u, to which the fit's
 relative slope is 2.7 at most; its own eight steps 4 u: 24 u + z^2 u, twice the last with the short exponential.  A product
 after that is u each.  A number below 2^-126 is off by 2^-149 (a rounding there is half of that, the short exponential's
 flush of its last bit one), times what it is multiplied with; the fp32 result itself by 2^-149 too.  bf16 results add
