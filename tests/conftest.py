@@ -12,3 +12,10 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103) and the built library")
     config.addinivalue_line("markers", "deterministic: bitwise run-to-run reproducibility")
     config.addinivalue_line("markers", "slow: larger CPU cases")
+
+
+@pytest.fixture(autouse=True)
+def _seeded():
+    """torch's own generators start every test alike: a test that draws from them has the same inputs in every run."""
+    import torch
+    torch.manual_seed(0)
